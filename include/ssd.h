@@ -93,8 +93,12 @@ typedef enum {
     SSD_ERR_NO_MEMORY = 4,   /* workspace allocation failed (ssd_forward) */
     SSD_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up (see ssd_get_device_error) */
     SSD_ERR_SCRATCH_TOO_SMALL = 6, /* ssd_forward_noalloc: workload larger than its fixed scratch */
-    SSD_ERR_RANGE = 7        /* a float16 tensor-core operand left float16's range (see ssd_get_device_error) */
+    SSD_ERR_RANGE = 7,       /* a float16 tensor-core operand left float16's range (see ssd_get_device_error) */
+    SSD_ERR_SLOT = 8         /* a slot index past its state pool (see ssd_get_device_error) */
 } ssd_status;
+
+/* Element types of the layer operators (ssd_conv_*, ssd_selective_*, ssd_layer_norm_*). */
+typedef enum { SSD_BF16 = 0, SSD_F16 = 1, SSD_F32 = 2 } ssd_dtype;
 
 /* Size in bytes of the fixed device scratch array used by ssd_forward_noalloc. */
 #define SSD_NOALLOC_SCRATCH_BYTES (64u << 20)
@@ -425,14 +429,163 @@ SSD_API int ssd_step_ex(const void* x, const float* dt, const float* A, const vo
                         int dstate, const ssd_input_options* options, void* y, cudaStream_t stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * The layer operators around a scan: a short causal convolution, the selective
+ * scan with one decay per channel and state entry, and the layer norm.  The
+ * pages describe none of them; they are what a layer runs next to the scan
+ * (and, for the second, in its place).  Common to all:
+ *
+ *  * `dtype` is the element type of the tensors declared as void* (x, y, their
+ *    gradients, B, C, dt, z, the convolution's states); everything else is
+ *    float32.  All arithmetic is float32; a void* output is rounded once, to
+ *    nearest even.  Pointers are aligned to their element; 16-byte aligned
+ *    rows are read and written in vectors.
+ *  * Strides count elements and are not negative; the innermost dimension is
+ *    dense.  So the inputs may be column slices of a projection's rows.
+ *  * lengths: (batch) int32 or NULL.  Row b then holds lengths[b] tokens (held
+ *    to [0, seqlen]); what lies past them is not used, whatever it is, their
+ *    outputs and gradients are zero, and the final state is the one after the
+ *    row's own last token (the initial state where the length is 0).
+ *  * slots: (batch) int32 or NULL, for the single-token calls: row b works on
+ *    state slots[b] of a pool of nslots states.  A negative slot is an idle
+ *    row: its output is zero and no state is touched.  A slot >= nslots is
+ *    idle too and raises the flag that ssd_get_device_error() reports as
+ *    SSD_ERR_SLOT.  Two rows of one call may not share a slot.  With NULL row
+ *    b works on state b (nslots >= batch).
+ *  * Outputs may not overlap inputs, except the states updated in place.
+ *  * Workspaces come stream-ordered from the library's pool, as in
+ *    ssd_forward.  Deterministic: no atomics, sums in a fixed order.
+ *  * Limits: batch <= 65535, seqlen <= 4194240, channels and width <= 2^20
+ *    (SSD_ERR_UNSUPPORTED beyond).
+ */
+
+/*
+ * ssd_conv_forward -- causal depthwise convolution of `width` taps (2 to 4):
+ *     pre[b,t,c] = bias[c] + sum_k weight[c,k] * x[b, t - (width-1) + k, c]
+ *     y = pre * sigmoid(pre) if silu, else pre
+ * x at t < 0 is init_state (the width-1 inputs before the row; zeros if NULL).
+ *   x            (batch, seqlen, channels) at the given strides
+ *   weight       (channels, width) f32; bias (channels) f32 or NULL
+ *   init_state, final_state (batch, width-1, channels), oldest input first, or NULL
+ *   y0, y1, y2   the output's channels in up to three dense tensors,
+ *                (batch, seqlen, n_i) with n0 + n1 + n2 == channels (unused ones
+ *                NULL and 0, last): for instance a scan's x, B and C
+ */
+SSD_API int ssd_conv_forward(int dtype, const void* x, long long x_batch_stride, long long x_token_stride,
+                             const float* weight, const float* bias, const void* init_state, const int* lengths,
+                             int batch, int seqlen, int channels, int width, int silu, void* y0, int n0, void* y1,
+                             int n1, void* y2, int n2, void* final_state, cudaStream_t stream);
+
+/*
+ * ssd_conv_backward -- gradients through ssd_conv_forward from dLoss/dy (in the
+ * same pieces; f32_i != 0: piece i is float32 whatever dtype is, as ssd_backward
+ * returns dB and dC) and dLoss/dfinal_state (dfinal, or NULL).  pre is computed
+ * again from x.
+ *   dx       (batch, seqlen, channels) at the given strides (rows may not overlap)
+ *   dweight  (channels, width) f32 or NULL; dbias (channels) f32 or NULL
+ *   dinit    (batch, width-1, channels) or NULL
+ */
+SSD_API int ssd_conv_backward(int dtype, const void* x, long long x_batch_stride, long long x_token_stride,
+                              const float* weight, const float* bias, const void* init_state, const int* lengths,
+                              int batch, int seqlen, int channels, int width, int silu, const void* dy0, int n0,
+                              int f32_0, const void* dy1, int n1, int f32_1, const void* dy2, int n2, int f32_2,
+                              const void* dfinal, void* dx, long long dx_batch_stride, long long dx_token_stride,
+                              float* dweight, float* dbias, void* dinit, cudaStream_t stream);
+
+/*
+ * ssd_conv_step -- ssd_conv_forward for one token of every row, its state
+ * (nslots, width-1, channels) updated in place.  x is (batch, channels) at a row
+ * stride; the outputs are (batch, n_i).
+ */
+SSD_API int ssd_conv_step(int dtype, const void* x, long long x_row_stride, const float* weight, const float* bias,
+                          void* state, const int* slots, int nslots, int batch, int channels, int width, int silu,
+                          void* y0, int n0, void* y1, int n1, void* y2, int n2, cudaStream_t stream);
+
+/* Strides of the selective scan's inputs in elements, per row and per token (a
+ * NULL pointer: all dense).  B and C are (ngroups, dstate) dense within a token;
+ * ssd_selective_step reads the *_batch members only. */
+typedef struct ssd_selective_strides {
+    long long x_batch, x_token, dt_batch, dt_token, z_batch, z_token, B_batch, B_token, C_batch, C_token;
+} ssd_selective_strides;
+
+/*
+ * ssd_selective_forward -- the selective scan with one dt per channel and one
+ * decay per channel and state entry (group g = c / (channels / ngroups)):
+ *     h[c,n] <- exp(dt[b,t,c] * A[c,n]) * h[c,n] + dt[b,t,c] * x[b,t,c] * B[b,t,g,n]
+ *     y[b,t,c] = sum_n C[b,t,g,n] * h[c,n] + D[c] * x[b,t,c]
+ * with ssd_input_options around it: dt_bias (channels), dt_softplus, dt_limit
+ * act on dt, and y <- y * z * sigmoid(z) with z shaped like x; D_per_channel is
+ * not read (D is one weight per channel here).
+ *   x, dt, z     (batch, seqlen, channels); B, C (batch, seqlen, ngroups, dstate)
+ *   A            (channels, dstate) f32; D (channels) f32 or NULL
+ *   init_state, final_state (batch, channels, dstate) f32 or NULL
+ *   y            (batch, seqlen, channels) dense
+ * Value domain: A <= 0 and an effective dt >= 0, as for ssd_forward.  dstate is
+ * 1 to 128 (SSD_ERR_UNSUPPORTED beyond).
+ */
+SSD_API int ssd_selective_forward(int dtype, const void* x, const void* dt, const float* A, const void* B,
+                                  const void* C, const float* D, const float* init_state, const int* lengths,
+                                  const ssd_selective_strides* strides, int batch, int seqlen, int channels,
+                                  int ngroups, int dstate, const ssd_input_options* options, void* y,
+                                  float* final_state, cudaStream_t stream);
+
+/*
+ * ssd_selective_backward -- gradients through ssd_selective_forward from dy
+ * (dense, y's layout) and dfinal (f32, or NULL).  Everything is computed again
+ * from the inputs.  Outputs, dense and fully written:
+ *   dx, ddt   (batch, seqlen, channels): ddt is that of the raw dt input (through
+ *             softplus; zero where dt_limit cut the value)
+ *   dA        (channels, dstate) f32; dB, dC (batch, seqlen, ngroups, dstate) f32
+ *   dD        (channels) f32 or NULL; ddt_bias (channels) f32 or NULL
+ *   dz        (batch, seqlen, channels), given exactly when options->z is
+ *   dinit     (batch, channels, dstate) f32 or NULL
+ */
+SSD_API int ssd_selective_backward(int dtype, const void* x, const void* dt, const float* A, const void* B,
+                                   const void* C, const float* D, const float* init_state, const int* lengths,
+                                   const ssd_selective_strides* strides, int batch, int seqlen, int channels,
+                                   int ngroups, int dstate, const ssd_input_options* options, const void* dy,
+                                   const float* dfinal, void* dx, void* ddt, float* dA, float* dB, float* dC,
+                                   float* dD, void* dz, float* ddt_bias, float* dinit, cudaStream_t stream);
+
+/*
+ * ssd_selective_step -- ssd_selective_forward for one token of every row: x, dt,
+ * z, y (batch, channels), B, C (batch, ngroups, dstate), state (nslots, channels,
+ * dstate) f32 updated in place.
+ */
+SSD_API int ssd_selective_step(int dtype, const void* x, const void* dt, const float* A, const void* B, const void* C,
+                               const float* D, float* state, const int* slots, int nslots,
+                               const ssd_selective_strides* strides, int batch, int channels, int ngroups, int dstate,
+                               const ssd_input_options* options, void* y, cudaStream_t stream);
+
+/*
+ * ssd_layer_norm_forward -- y = (x - mean) * rstd * weight + bias over rows of
+ * `width`, rstd = 1 / sqrt(mean((x - mean)^2) + eps).  x at a row stride, y
+ * dense; weight and bias (width) f32, NULL for ones and zeros; mean and rstd
+ * (rows) f32, NULL where they are not wanted.
+ */
+SSD_API int ssd_layer_norm_forward(int dtype, const void* x, long long x_row_stride, const float* weight,
+                                   const float* bias, float eps, long long rows, int width, void* y, float* mean,
+                                   float* rstd, cudaStream_t stream);
+
+/*
+ * ssd_layer_norm_backward -- dx (dense), and dweight and dbias ((width) f32, or
+ * NULL) summed over the rows, from dy, x and the forward pass's mean and rstd.
+ */
+SSD_API int ssd_layer_norm_backward(int dtype, const void* x, long long x_row_stride, const float* weight,
+                                    const float* mean, const float* rstd, const void* dy, long long dy_row_stride,
+                                    long long rows, int width, void* dx, float* dweight, float* dbias,
+                                    cudaStream_t stream);
+
+/*
  * ssd_get_device_error -- reads and clears the library's device error words
  * on the current device (synchronizes with the device).  Returns SSD_OK;
  * SSD_ERR_TIMEOUT if a kernel's bounded wait gave up since the last read
  * (the kernel then skipped the rest of its work and returned, so the outputs
  * of that call are incomplete while the device stays usable); otherwise
  * SSD_ERR_RANGE if a value converted to a float16 tensor-core operand was
- * outside float16's finite range since the last read; or SSD_ERR_CUDA if the
- * read itself failed.
+ * outside float16's finite range since the last read; otherwise SSD_ERR_SLOT
+ * if a single-token call (ssd_conv_step, ssd_selective_step) met a slot index
+ * past its pool since the last read; or SSD_ERR_CUDA if the read itself failed.
  */
 SSD_API int ssd_get_device_error(void);
 
@@ -463,7 +616,8 @@ SSD_API int ssd_debug_stall(int kinds);
  * microseconds between launches, so a timed loop can select only the kernel
  * it needs.  ssd_profile_read() waits for those
  * events and returns, per kernel kind (see ssd_kernel_name), the summed
- * device time in milliseconds and the launch count since the last reset.
+ * device time in milliseconds and the launch count since the last reset;
+ * *n_kinds is the number of kinds written, at most max_kinds.
  * ssd_launch_count() counts every kernel the library has launched since load
  * (profiling enabled or not).
  */

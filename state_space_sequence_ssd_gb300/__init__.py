@@ -12,6 +12,10 @@ CUDA kernels.  Inputs must be contiguous CUDA tensors:
     chunk_states / states (batch, nchunks, H, P, N) f32.
 
 ``stream`` is a torch.cuda.Stream (default: the current stream).
+
+The operators that a layer runs around the scan (short convolution, selective
+scan with one decay per channel, layer norm) are in layer.py; they also take
+strided rows and other element types.
 """
 from __future__ import annotations
 
@@ -19,10 +23,23 @@ from . import _ffi
 
 __all__ = ["ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan", "ssd_forward",
            "ssd_forward_noalloc", "ssd_forward_heads", "ssd_partition_heads", "ssd_forward_plan", "ssd_step",
-           "ssd_step_multi", "ssd_forward_ex", "ssd_step_ex", "ssd_backward", "ssd_get_device_error", "SSDError", "library_path"]
+           "ssd_step_multi", "ssd_forward_ex", "ssd_step_ex", "ssd_backward", "ssd_get_device_error", "SSDError", "library_path",
+           "ssd_conv_forward", "ssd_conv_backward", "ssd_conv_step", "ssd_selective_forward", "ssd_selective_backward",
+           "ssd_selective_step", "ssd_layer_norm_forward", "ssd_layer_norm_backward"]
+_LAYER = frozenset(n for n in __all__ if n.startswith(("ssd_conv_", "ssd_selective_", "ssd_layer_norm_")))
 
 SSDError = _ffi.SSDError
 library_path = _ffi.LIB_PATH
+
+
+def __getattr__(name):
+    """The layer operators, looked up when they are first used (their module imports torch)."""
+    if name in _LAYER:
+        from . import layer
+        for n in _LAYER:
+            globals()[n] = getattr(layer, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():
@@ -403,5 +420,6 @@ def ssd_forward_plan(batch, seqlen, nheads, headdim, ngroups, dstate, chunk_size
 
 
 def ssd_get_device_error():
-    """SSD_OK (0) or SSD_ERR_TIMEOUT (5) if a bounded device wait gave up since the last read."""
+    """SSD_OK (0), SSD_ERR_TIMEOUT (5) if a bounded device wait gave up since the last read, SSD_ERR_RANGE (7) if a
+    float16 operand left its range, or SSD_ERR_SLOT (8) if a single-token call met a slot past its pool."""
     return _ffi.lib().ssd_get_device_error()

@@ -20,10 +20,13 @@ SSD_ERR_NO_MEMORY = 4
 SSD_ERR_TIMEOUT = 5
 SSD_ERR_SCRATCH_TOO_SMALL = 6
 SSD_ERR_RANGE = 7
+SSD_ERR_SLOT = 8
+SSD_BF16, SSD_F16, SSD_F32 = 0, 1, 2  # ssd_dtype
 SSD_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 # name -> (restype, argtypes); the exported surface of include/ssd.h
 _p, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p
+_l = ctypes.c_longlong
 SIGNATURES = {
     "ssd_status_string": (ctypes.c_char_p, [_i]),
     "ssd_chunk_cumsum": (_i, [_p, _p, _i, _i, _i, _i, _p, _p, _p]),
@@ -40,6 +43,14 @@ SIGNATURES = {
     "ssd_forward_ex": (_i, [_p] * 7 + [_i] * 7 + [_p, _p, _p, _p]),
     "ssd_step_ex": (_i, [_p] * 7 + [_i] * 5 + [_p, _p, _p]),
     "ssd_backward": (_i, [_p] * 9 + [_i] * 7 + [_p] * 8),
+    "ssd_conv_forward": (_i, [_i, _p, _l, _l, _p, _p, _p, _p] + [_i] * 5 + [_p, _i] * 3 + [_p, _p]),
+    "ssd_conv_backward": (_i, [_i, _p, _l, _l, _p, _p, _p, _p] + [_i] * 5 + [_p, _i, _i] * 3 + [_p, _p, _l, _l] + [_p] * 4),
+    "ssd_conv_step": (_i, [_i, _p, _l, _p, _p, _p, _p] + [_i] * 5 + [_p, _i] * 3 + [_p]),
+    "ssd_selective_forward": (_i, [_i] + [_p] * 9 + [_i] * 5 + [_p] * 4),
+    "ssd_selective_backward": (_i, [_i] + [_p] * 9 + [_i] * 5 + [_p] * 13),
+    "ssd_selective_step": (_i, [_i] + [_p] * 8 + [_i, _p] + [_i] * 4 + [_p] * 3),
+    "ssd_layer_norm_forward": (_i, [_i, _p, _l, _p, _p, ctypes.c_float, _l, _i] + [_p] * 4),
+    "ssd_layer_norm_backward": (_i, [_i, _p, _l, _p, _p, _p, _p, _l, _l, _i] + [_p] * 4),
     "ssd_get_device_error": (_i, []),
     "ssd_debug_set_wait_limit_ns": (_i, [ctypes.c_ulonglong]),
     "ssd_debug_stall": (_i, [_i]),
@@ -57,6 +68,11 @@ class InputOptions(ctypes.Structure):
     _fields_ = [("dt_bias", ctypes.c_void_p), ("dt_softplus", ctypes.c_int), ("dt_limit", ctypes.c_int),
                 ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float), ("D_per_channel", ctypes.c_int),
                 ("z", ctypes.c_void_p)]
+
+
+class SelectiveStrides(ctypes.Structure):
+    """struct ssd_selective_strides."""
+    _fields_ = [(f"{name}_{dim}", ctypes.c_longlong) for name in ("x", "dt", "z", "B", "C") for dim in ("batch", "token")]
 
 
 _lock = threading.Lock()

@@ -46,7 +46,9 @@ cudaEvent_t take_event() {
 }
 
 const char* const kKindNames[kNumKinds] = {"chunk_cumsum", "chunk_state", "state_passing", "chunk_scan",
-                                           "bc_to_f16", "step", "bwd_chunk", "bwd_reduce"};
+                                           "bc_to_f16", "step", "bwd_chunk", "bwd_reduce",
+                                           "conv", "conv_bwd", "conv_step", "selective", "selective_bwd",
+                                           "selective_step", "layer_norm", "layer_norm_bwd"};
 
 }  // namespace
 
@@ -149,8 +151,8 @@ Dims make_dims(int batch, int seqlen, int nheads, int headdim, int ngroups, int 
 
 }  // namespace
 
-// device error words: [0] the code of a bounded wait that gave up, [1] the float16 range flag
-__device__ int g_ssd_device_error[2] = {0, 0};
+// device error words: [0] the code of a bounded wait that gave up, [1] the float16 range flag, [2] the slot flag
+__device__ int g_ssd_device_error[3] = {0, 0, 0};
 
 namespace {
 
@@ -454,6 +456,14 @@ int forward_pooled(const Dims& d, const void* x, const float* dt, const float* A
 
 }  // namespace
 
+namespace ssd {
+
+int take_workspace(void** ptr, size_t bytes, cudaStream_t s) { return workspace_alloc(ptr, bytes, s); }
+int* error_words() { return device_error_ptr(); }
+int multiprocessors() { return device_sms(); }
+
+}  // namespace ssd
+
 extern "C" {
 
 const char* ssd_status_string(int status) {
@@ -467,6 +477,8 @@ const char* ssd_status_string(int status) {
         case SSD_ERR_RANGE:
             return "SSD_ERR_RANGE: a value converted to a float16 tensor-core operand exceeded float16's range "
                    "(|v| > 65504); that call's results are not reliable";
+        case SSD_ERR_SLOT:
+            return "SSD_ERR_SLOT: a single-token call met a slot index past its state pool; that row was left idle";
         case SSD_ERR_SCRATCH_TOO_SMALL:
             return "SSD_ERR_SCRATCH_TOO_SMALL: the workload needs more than the fixed scratch of ssd_forward_noalloc "
                    "(SSD_NOALLOC_SCRATCH_BYTES); use ssd_forward";
@@ -748,13 +760,15 @@ int ssd_step_multi(const void* x, const float* dt, const float* A, const void* B
 }
 
 int ssd_get_device_error(void) {
-    int v[2] = {0, 0};
-    const int zero[2] = {0, 0};
+    int v[3] = {0, 0, 0};
+    const int zero[3] = {0, 0, 0};
     if (cudaMemcpyFromSymbol(v, g_ssd_device_error, sizeof(v)) != cudaSuccess) return SSD_ERR_CUDA;
-    if ((v[0] != 0 || v[1] != 0) && cudaMemcpyToSymbol(g_ssd_device_error, zero, sizeof(zero)) != cudaSuccess)
+    if ((v[0] != 0 || v[1] != 0 || v[2] != 0) &&
+        cudaMemcpyToSymbol(g_ssd_device_error, zero, sizeof(zero)) != cudaSuccess)
         return SSD_ERR_CUDA;
     if (v[0] != 0) return SSD_ERR_TIMEOUT;
-    return v[1] != 0 ? SSD_ERR_RANGE : SSD_OK;
+    if (v[1] != 0) return SSD_ERR_RANGE;
+    return v[2] != 0 ? SSD_ERR_SLOT : SSD_OK;
 }
 
 int ssd_debug_set_wait_limit_ns(unsigned long long ns) {
@@ -806,7 +820,7 @@ int ssd_profile_read(float* total_ms, int* launches, int max_kinds, int* n_kinds
         if (total_ms) total_ms[k] = (float)g_prof_ms[k];
         if (launches) launches[k] = g_prof_count[k];
     }
-    if (n_kinds) *n_kinds = kNumKinds;
+    if (n_kinds) *n_kinds = n > 0 ? n : 0;
     return status;
 }
 
