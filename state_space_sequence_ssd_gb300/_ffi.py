@@ -88,6 +88,8 @@ class SSDError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libssd_gb300.so once; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

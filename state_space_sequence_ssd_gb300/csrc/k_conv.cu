@@ -21,16 +21,42 @@ namespace {
 
 constexpr int kWarps = 8;
 
+// The taps and biases of V channels as pairs.  Tap 3 is the current token's: a narrower kernel's taps end there and its
+// first ones are unused (never multiplied: zero times an infinite input would be NaN).
 template <int V>
 __device__ __forceinline__ void load_taps(const float* __restrict__ weight, const float* __restrict__ bias, int W, int c,
-                                          int valid, float (&w)[4][V], float (&b)[V]) {
-    // tap 3 is the current token's: a narrower kernel's taps end there and its first ones are unused (never
-    // multiplied: zero times an infinite input would be NaN)
+                                          int valid, f32x2 (&w)[4][(V + 1) / 2], f32x2 (&b)[(V + 1) / 2]) {
+    float wf[4][V + 1] = {}, bf[V + 1] = {};
+    const bool rows = W == 4 && (reinterpret_cast<uintptr_t>(weight) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        b[i] = (bias != nullptr && i < valid) ? bias[c + i] : 0.f;
+        if (i >= valid) continue;
+        if (rows) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(weight) + c + i);
+            wf[0][i] = q.x; wf[1][i] = q.y; wf[2][i] = q.z; wf[3][i] = q.w;
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k][i] = (k >= 4 - W && i < valid) ? weight[(int64_t)(c + i) * W + k - (4 - W)] : 0.f;
+            for (int k = 0; k < 4; ++k)
+                if (k >= 4 - W) wf[k][i] = __ldg(weight + (int64_t)(c + i) * W + k - (4 - W));
+        }
+        if (bias != nullptr) bf[i] = __ldg(bias + c + i);
+    }
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) {
+        b[i] = pk(bf[2 * i], bf[2 * i + 1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k][i] = pk(wf[k][2 * i], wf[k][2 * i + 1]);
+    }
+}
+
+// The convolution at one token: taps times the last four inputs (x[3] the newest), and the activation.
+template <int W, int P>
+__device__ __forceinline__ void taps_times(const f32x2 (&w)[4][P], const f32x2 (&b)[P], const f32x2 (*x)[P], f32x2 (&pre)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        pre[i] = b[i];
+#pragma unroll
+        for (int k = 4 - W; k < 4; ++k) pre[i] = fma2(w[k][i], x[k][i], pre[i]);
     }
 }
 
@@ -46,9 +72,7 @@ __device__ __forceinline__ T* piece_at(const Pieces& y, int64_t row, int c) {
 // x at token t of row b (t < 0: the initial state's rows; past the length: zero)
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> input_at(const ConvArgs& a, int b, int t, int len, int c, int valid, bool vec) {
-    Vec<T, V> z;
-#pragma unroll
-    for (int i = 0; i < V; ++i) z.e[i] = from_f32<T>(0.f);
+    const Vec<T, V> z = Vec<T, V>::zero();
     if (t >= len) return z;
     if (t >= 0) return load_vec<T, V>(static_cast<const T*>(a.x) + b * a.x_batch + t * a.x_token + c, valid, vec);
     if (a.init == nullptr || t < -(a.width - 1)) return z;
@@ -56,186 +80,212 @@ __device__ __forceinline__ Vec<T, V> input_at(const ConvArgs& a, int b, int t, i
                           valid, vec);
 }
 
-// A warp: 32 V channels of `run` consecutive tokens.
-template <typename T, int V, int RUN>
+// A warp: 32 V channels of RUN consecutive tokens, STEP of them loaded at a time so that a warp keeps that many loads
+// in flight.
+template <typename T, int V, int W, int RUN>
 __global__ void __launch_bounds__(32 * kWarps) conv_forward_kernel(ConvArgs a, Pieces y, T* __restrict__ final_state,
                                                                    bool vec) {
+    constexpr int P = (V + 1) / 2, STEP = RUN < 8 ? RUN : 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.z, c = (blockIdx.x * 32 + lane) * V;
     const int valid = min(V, a.channels - c);
     if (valid <= 0) return;
     const int len = row_length(a.lengths, b, a.seqlen);
     const int64_t row0 = (int64_t)b * a.seqlen;
-    if (final_state != nullptr && blockIdx.y == 0 && warp < a.width - 1) {
-        const Vec<T, V> v = input_at<T, V>(a, b, len - (a.width - 1) + warp, len, c, valid, vec);
-        store_vec<T, V>(final_state + ((int64_t)b * (a.width - 1) + warp) * a.channels + c, v, valid, vec);
+    if (final_state != nullptr && blockIdx.y == 0 && warp < W - 1) {
+        const Vec<T, V> v = input_at<T, V>(a, b, len - (W - 1) + warp, len, c, valid, vec);
+        store_vec<T, V>(final_state + ((int64_t)b * (W - 1) + warp) * a.channels + c, v, valid, vec);
     }
     const int t0 = (blockIdx.y * kWarps + warp) * RUN;
     if (t0 >= a.seqlen) return;
-    float w[4][V], bias[V];
-    load_taps<V>(a.weight, a.bias, a.width, c, valid, w, bias);
-    Vec<T, V> past[3];
+    Vec<T, V> in[STEP];
+    f32x2 x[STEP + 3][P];  // the inputs of this step's tokens, after the three before them
 #pragma unroll
-    for (int k = 0; k < 3; ++k) past[k] = input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, vec);
-    constexpr int STEP = RUN < 8 ? RUN : 8;  // tokens whose loads are in flight together
+    for (int k = 0; k < 3; ++k) {
+        const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, vec) : Vec<T, V>::zero();
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[k][i] = v.pair(i);
+    }
+    f32x2 w[4][P], bias[P];
+    load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
+    const int64_t xt = a.x_token;
+    const T* xp = static_cast<const T*>(a.x) + b * a.x_batch + t0 * xt + c;
+    int piece = c < y.n[0] ? 0 : c - y.n[0] < y.n[1] ? 1 : 2;
+    const int wide = piece == 0 ? y.n[0] : piece == 1 ? y.n[1] : y.n[2];
+    T* yp = piece_at<T>(y, row0 + t0, c);
 #pragma unroll 1
     for (int s = 0; s < RUN; s += STEP) {
-        Vec<T, V> in[STEP + 3];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) in[k] = past[k];
+        for (int i = 0; i < STEP; ++i) in[i] = load_vec<T, V>(xp + i * xt, t0 + s + i < len ? valid : 0, vec);
+        xp += STEP * xt;
 #pragma unroll
-        for (int i = 0; i < STEP; ++i) in[3 + i] = input_at<T, V>(a, b, t0 + s + i, len, c, valid, vec);
+        for (int i = 0; i < STEP; ++i)
+#pragma unroll
+            for (int j = 0; j < P; ++j) x[3 + i][j] = in[i].pair(j);
 #pragma unroll
         for (int i = 0; i < STEP; ++i) {
             const int t = t0 + s + i;
             if (t >= a.seqlen) return;
-            Vec<T, V> out;
+            f32x2 pre[P];
+            taps_times<W, P>(w, bias, x + i, pre);
+            if (a.silu) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float v = bias[e];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k >= 4 - a.width) v = fmaf(w[k][e], to_f32<T>(in[i + k].e[e]), v);
-                if (a.silu) v *= sigmoid(v);
-                out.e[e] = from_f32<T>(t < len ? v : 0.f);
+                for (int j = 0; j < P; ++j) pre[j] = mul2(pre[j], sigmoid2(pre[j]));
             }
-            store_vec<T, V>(piece_at<T>(y, row0 + t, c), out, valid, vec);
+            store_vec<T, V>(yp, t < len ? Vec<T, V>::of_pairs(pre) : Vec<T, V>::zero(), valid, vec);
+            yp += wide;
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) past[k] = in[STEP + k];
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int j = 0; j < P; ++j) x[k][j] = x[STEP + k][j];
     }
 }
 
-// dLoss/dpre at token t from dLoss/dy and pre
-__device__ __forceinline__ float through_silu(float dy, float pre, int silu) {
-    if (!silu) return dy;
-    const float s = sigmoid(pre);
-    return dy * s * fmaf(pre, 1.f - s, 1.f);
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void grad_at(const Pieces& dy, int64_t row, int c, int valid, bool vec, float (&g)[V]) {
-    int p = 0, at = c;
-    if (at >= dy.n[0]) { at -= dy.n[0]; p = 1; if (at >= dy.n[1]) { at -= dy.n[1]; p = 2; } }
-    const void* base = p == 0 ? dy.p[0] : p == 1 ? dy.p[1] : dy.p[2];
-    const int n = p == 0 ? dy.n[0] : p == 1 ? dy.n[1] : dy.n[2];
-    const int f32 = p == 0 ? dy.f32[0] : p == 1 ? dy.f32[1] : dy.f32[2];
-    if (f32) {
-        const Vec<float, V> r = load_vec<float, V>(static_cast<const float*>(base) + row * n + at, valid, vec);
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = r.e[i];
-    } else {
-        const Vec<T, V> r = load_vec<T, V>(static_cast<const T*>(base) + row * n + at, valid, vec);
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = to_f32<T>(r.e[i]);
-    }
+// The gradient's piece that holds channel c: its base, its width, the channel's place in it.
+struct GradPiece {
+    const void* p;
+    int wide, at;
+    bool f32;
+};
+__device__ __forceinline__ GradPiece grad_piece(const Pieces& dy, int c) {
+    if (c < dy.n[0]) return {dy.p[0], dy.n[0], c, dy.f32[0] != 0};
+    c -= dy.n[0];
+    if (c < dy.n[1]) return {dy.p[1], dy.n[1], c, dy.f32[1] != 0};
+    return {dy.p[2], dy.n[2], c - dy.n[1], dy.f32[2] != 0};
 }
 
 constexpr int kBwdRun = 32;  // tokens a warp of the backward kernel walks
 
-// A warp: 32 V channels of kBwdRun consecutive tokens, their dx and their part of dweight and dbias.  dx[t]
-// needs dLoss/dpre up to W-1 tokens on, so the walk goes that far past the run (those tokens' pre again).
-// The block's eight warps' sums of one channel are joined in shared memory in warp order and written as one
-// row of `partial`, (rows, width + 1, channels).
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * kWarps) conv_backward_kernel(ConvArgs a, Pieces dy, const T* __restrict__ dfinal,
+// A warp: 32 V channels of kBwdRun consecutive tokens, their dx and their part of dweight and dbias.  dx[t] needs
+// dLoss/dpre up to W-1 tokens on, so the walk goes that far past the run (those tokens' pre again).  Tokens are taken
+// four at a time: their x and dy are loaded together, one group ahead of their use.  The block's eight warps' sums of
+// one channel are joined in shared memory in warp order and written as one row of `partial`,
+// (rows, width + 1, channels).
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(32 * kWarps, 2) conv_backward_kernel(ConvArgs a, Pieces dy, const T* __restrict__ dfinal,
                                                                     T* __restrict__ dx, int64_t dx_batch, int64_t dx_token,
                                                                     T* __restrict__ dinit, float* __restrict__ partial,
                                                                     bool vec, bool vec_dx) {
-    __shared__ float sums[kWarps][5][32 * V];
+    constexpr int P = (V + 1) / 2, S = 4;
+    __shared__ float sums[kWarps][W + 1][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.z, c = (blockIdx.x * 32 + lane) * V, W = a.width;
+    const int b = blockIdx.z, c = (blockIdx.x * 32 + lane) * V;
     const int valid = max(0, min(V, a.channels - c));
     const int len = row_length(a.lengths, b, a.seqlen);
-    const int64_t row0 = (int64_t)b * a.seqlen;
     const int t0 = (blockIdx.y * kWarps + warp) * kBwdRun;
-    float w[4][V], bias[V], dw[4][V], db[V];
+    f32x2 dw[W][P], db[P];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        db[e] = 0.f;
+    for (int j = 0; j < P; ++j) {
+        db[j] = 0ull;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dw[k][e] = 0.f;
+        for (int k = 0; k < W; ++k) dw[k][j] = 0ull;
     }
-    if (valid > 0) load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
     if (valid > 0 && t0 < a.seqlen) {
-        // the run itself; block row 0 also walks the initial state's tokens, which have no output of their own
+        f32x2 w[4][P], bias[P];
+        load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
+        // the run itself; the first one also gives the initial state's tokens, which have no output of their own
         const int first = (t0 == 0 && dinit != nullptr) ? -(W - 1) : t0;
         const int last = min(t0 + kBwdRun, a.seqlen);
-        float x[4][V], g[4][V];  // the last four inputs and dLoss/dpre values, newest at [3]
+        const GradPiece gr = grad_piece(dy, c);
+        const int64_t g0 = (int64_t)b * a.seqlen * gr.wide + gr.at;
+        const T* gp = static_cast<const T*>(gr.p) + g0;
+        const float* gf = static_cast<const float*>(gr.p) + g0;
+        const T* xp = static_cast<const T*>(a.x) + b * a.x_batch + c;
+        f32x2 x[S + 3][P], g[S + 3][P];  // inputs and dLoss/dpre of this group's tokens, after the three before them
 #pragma unroll
-        for (int e = 0; e < V; ++e)
+        for (int k = 0; k < 3; ++k) {
+            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, vec) : Vec<T, V>::zero();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) g[k][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const Vec<T, V> r = input_at<T, V>(a, b, t0 - 4 + k, len, c, valid, vec);
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[k][e] = to_f32<T>(r.e[e]);
+            for (int j = 0; j < P; ++j) { x[k][j] = v.pair(j); g[k][j] = 0ull; }
         }
-#pragma unroll 4
-        for (int t = t0; t < last + W - 1; ++t) {
-            // token t enters; token t - (W-1) has all its gradients and leaves
-            const Vec<T, V> r = input_at<T, V>(a, b, t, len, c, valid, vec);
-            float gy[V];
-            const bool live = t < len;
-            if (live) grad_at<T, V>(dy, row0 + t, c, valid, vec, gy);
+        Vec<T, V> nx[S], ng[S];
+        Vec<float, V> nf[S];
+        auto fetch = [&](int t) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
+            for (int i = 0; i < S; ++i) {
+                const int got = t + i < min(len, last + W - 1) ? valid : 0;
+                nx[i] = load_vec<T, V>(xp + (int64_t)(t + i) * a.x_token, got, vec);
+                if (gr.f32) nf[i] = load_vec<float, V>(gf + (int64_t)(t + i) * gr.wide, got, vec);
+                else ng[i] = load_vec<T, V>(gp + (int64_t)(t + i) * gr.wide, got, vec);
+            }
+        };
+        fetch(t0);
+        for (int t = t0; t < last + W - 1; t += S) {
+            f32x2 gy[S][P];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) { x[k][e] = x[k + 1][e]; g[k][e] = g[k + 1][e]; }
-                x[3][e] = to_f32<T>(r.e[e]);
-                float pre = bias[e];
+            for (int i = 0; i < S; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k >= 4 - W) pre = fmaf(w[k][e], x[k][e], pre);
-                g[3][e] = live ? through_silu(gy[e], pre, a.silu) : 0.f;
-                if (t < last) {
-                    db[e] += g[3][e];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) dw[k][e] = fmaf(g[3][e], x[k][e], dw[k][e]);
+                for (int j = 0; j < P; ++j) {
+                    x[3 + i][j] = nx[i].pair(j);
+                    gy[i][j] = gr.f32 ? nf[i].pair(j) : ng[i].pair(j);
                 }
-            }
-            const int o = t - (W - 1);
-            if (o < first || o >= last) continue;
-            // g[3] is token t's: tap 3 - j of token o's own later outputs, at distance j
-            float d[V];
+            if (t + S < last + W - 1) fetch(t + S);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                d[e] = 0.f;
-                if (W == 4) d[e] = w[3][e] * g[0][e] + w[2][e] * g[1][e] + w[1][e] * g[2][e] + w[0][e] * g[3][e];
-                else if (W == 3) d[e] = w[3][e] * g[1][e] + w[2][e] * g[2][e] + w[1][e] * g[3][e];
-                else d[e] = w[3][e] * g[2][e] + w[2][e] * g[3][e];
-            }
-            const int j = o + W - 1 - len;  // the final state's row that holds token o
-            if (dfinal != nullptr && j >= 0 && j < W - 1) {
-                const Vec<T, V> f = load_vec<T, V>(dfinal + ((int64_t)b * (W - 1) + j) * a.channels + c, valid, vec);
+            for (int i = 0; i < S; ++i) {
+                // token t + i enters; token t + i - (W-1) then has all its gradients and leaves
+                f32x2 pre[P];
+                taps_times<W, P>(w, bias, x + i, pre);
+                const bool live = t + i < len;
 #pragma unroll
-                for (int e = 0; e < V; ++e) d[e] += to_f32<T>(f.e[e]);
-            }
-            Vec<T, V> out;
+                for (int j = 0; j < P; ++j) {
+                    f32x2 q = gy[i][j];
+                    if (a.silu) {  // times s (1 + pre (1 - s))
+                        const f32x2 s = sigmoid2(pre[j]), one = pk(1.f, 1.f);
+                        q = mul2(mul2(q, s), fma2(pre[j], fma2(s, pk(-1.f, -1.f), one), one));
+                    }
+                    g[3 + i][j] = live ? q : 0ull;
+                    if (t + i < last) {
+                        db[j] = add2(db[j], g[3 + i][j]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) out.e[e] = from_f32<T>((o < len) ? d[e] : 0.f);
-            if (o >= 0)
-                store_vec<T, V>(dx + b * dx_batch + o * dx_token + c, out, valid, vec_dx);
-            else
-                store_vec<T, V>(dinit + ((int64_t)b * (W - 1) + o + W - 1) * a.channels + c, out, valid, vec);
+                        for (int k = 0; k < W; ++k) dw[k][j] = fma2(g[3 + i][j], x[4 - W + k + i][j], dw[k][j]);
+                    }
+                }
+                const int o = t + i - (W - 1);
+                if (o < first || o >= last) continue;
+                f32x2 d[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    d[j] = mul2(w[3][j], g[4 - W + i][j]);  // its own output's, through the newest tap
+#pragma unroll
+                    for (int k = 1; k < W; ++k) d[j] = fma2(w[3 - k][j], g[4 - W + k + i][j], d[j]);
+                }
+                const int r = o + W - 1 - len;  // the final state's row that holds token o
+                if (dfinal != nullptr && r >= 0 && r < W - 1) {
+                    const Vec<T, V> f = load_vec<T, V>(dfinal + ((int64_t)b * (W - 1) + r) * a.channels + c, valid, vec);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) d[j] = add2(d[j], f.pair(j));
+                }
+                const Vec<T, V> out = o < len ? Vec<T, V>::of_pairs(d) : Vec<T, V>::zero();
+                if (o >= 0)
+                    store_vec<T, V>(dx + b * dx_batch + o * dx_token + c, out, valid, vec_dx);
+                else
+                    store_vec<T, V>(dinit + ((int64_t)b * (W - 1) + o + W - 1) * a.channels + c, out, valid, vec);
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) { x[k][j] = x[S + k][j]; g[k][j] = g[S + k][j]; }
         }
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+    for (int k = 0; k <= W; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sums[warp][k][lane * V + e] = dw[k][e];
-        sums[warp][4][lane * V + e] = db[e];
-    }
+        for (int j = 0; j < P; ++j) {
+            float lo, hi;
+            unpk(k < W ? dw[k < W ? k : 0][j] : db[j], lo, hi);
+            sums[warp][k][lane * V + 2 * j] = lo;
+            if (2 * j + 1 < V) sums[warp][k][lane * V + 2 * j + 1] = hi;
+        }
     __syncthreads();
     const int64_t row = (int64_t)b * gridDim.y + blockIdx.y;
-    for (int i = threadIdx.x; i < 5 * 32 * V; i += blockDim.x) {
+    for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += blockDim.x) {
         const int k = i / (32 * V), cc = blockIdx.x * 32 * V + i % (32 * V);
-        if (cc >= a.channels || k < 4 - W) continue;
+        if (cc >= a.channels) continue;
         float s = 0.f;
 #pragma unroll
         for (int q = 0; q < kWarps; ++q) s += sums[q][k][i % (32 * V)];
-        partial[(row * (W + 1) + k - (4 - W)) * a.channels + cc] = s;
+        partial[(row * (W + 1) + k) * a.channels + cc] = s;
     }
 }
 
@@ -266,41 +316,51 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* __restric
     }
 }
 
-// One token: a thread holds V channels of one row, reads the slot's W-1 inputs, and writes them back moved on
-// by one.  An idle row (slot -1) writes zeros and leaves every slot alone.
-template <typename T, int V>
+// One token: a thread holds V channels of R rows, whose inputs it loads together; the taps are read once for them.  The
+// slot's W-1 inputs are written back moved on by one.  An idle row (slot -1) writes zeros and leaves every slot alone.
+template <typename T, int V, int W, int R>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, T* __restrict__ state, const int* __restrict__ slots,
                                                         int nslots, Pieces y, int* err, bool vec) {
-    const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V, b = blockIdx.y;
+    constexpr int P = (V + 1) / 2;
+    const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V, b0 = blockIdx.y * R;
     const int valid = min(V, a.channels - c);
     if (valid <= 0) return;
-    const int W = a.width, slot = row_slot(slots, b, nslots, err);
-    Vec<T, V> out;
+    int slot[R];
+    Vec<T, V> in[R][4];
 #pragma unroll
-    for (int e = 0; e < V; ++e) out.e[e] = from_f32<T>(0.f);
-    if (slot >= 0) {
-        T* st = state + (int64_t)slot * (W - 1) * a.channels + c;
-        Vec<T, V> in[4];
-        in[3] = load_vec<T, V>(static_cast<const T*>(a.x) + b * a.x_batch + c, valid, vec);
+    for (int r = 0; r < R; ++r) slot[r] = b0 + r < a.batch ? row_slot(slots, b0 + r, nslots, err) : -1;
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-            in[k] = k >= 4 - W ? load_vec<T, V>(st + (int64_t)(k - (4 - W)) * a.channels, valid, vec) : out;
-        float w[4][V], bias[V];
-        load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
+    for (int r = 0; r < R; ++r) {
+        const int got = slot[r] >= 0 ? valid : 0;
+        const T* st = state + (int64_t)slot[r] * (W - 1) * a.channels + c;
+        in[r][3] = load_vec<T, V>(static_cast<const T*>(a.x) + (b0 + r) * a.x_batch + c, got, vec);
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-            if (k >= 4 - W) store_vec<T, V>(st + (int64_t)(k - (4 - W)) * a.channels, in[k + 1], valid, vec);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float v = bias[e];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k >= 4 - W) v = fmaf(w[k][e], to_f32<T>(in[k].e[e]), v);
-            if (a.silu) v *= sigmoid(v);
-            out.e[e] = from_f32<T>(v);
-        }
+        for (int k = 4 - W; k < 3; ++k) in[r][k] = load_vec<T, V, true>(st + (int64_t)(k - (4 - W)) * a.channels, got, vec);
     }
-    store_vec<T, V>(piece_at<T>(y, b, c), out, valid, vec);
+    f32x2 w[4][P], bias[P];
+    load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (b0 + r >= a.batch) return;
+        Vec<T, V> out = Vec<T, V>::zero();
+        if (slot[r] >= 0) {
+            T* st = state + (int64_t)slot[r] * (W - 1) * a.channels + c;
+#pragma unroll
+            for (int k = 4 - W; k < 3; ++k) store_vec<T, V>(st + (int64_t)(k - (4 - W)) * a.channels, in[r][k + 1], valid, vec);
+            f32x2 x[4][P], pre[P];
+#pragma unroll
+            for (int k = 4 - W; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) x[k][j] = in[r][k].pair(j);
+            taps_times<W, P>(w, bias, x, pre);
+            if (a.silu) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) pre[j] = mul2(pre[j], sigmoid2(pre[j]));
+            }
+            out = Vec<T, V>::of_pairs(pre);
+        }
+        store_vec<T, V>(piece_at<T>(y, b0 + r, c), out, valid, vec);
+    }
 }
 
 bool on(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -317,29 +377,27 @@ bool whole_vectors(const ConvArgs& a, const Pieces& y, const void* s1, const voi
     return true;
 }
 
-template <typename T, int V>
-void run_forward(const ConvArgs& a, const Pieces& y, void* final_state, bool vec, cudaStream_t s) {
+template <typename T, int V, int W>
+void run_forward(const ConvArgs& a, const Pieces& y, void* final_state, cudaStream_t s) {
     const int tiles = ceil_div(a.channels, 32 * V);
-    // long runs read the halo of W-1 tokens rarely; short ones fill the SMs on short prompts
-    const bool many = (int64_t)tiles * a.batch * ceil_div(a.seqlen, kWarps * 16) >= 304;
-    if (many)
-        conv_forward_kernel<T, V, 16><<<dim3(tiles, ceil_div(a.seqlen, kWarps * 16), a.batch), 32 * kWarps, 0, s>>>(
-            a, y, static_cast<T*>(final_state), vec);
+    T* f = static_cast<T*>(final_state);
+    // long runs read the taps and the halo of W-1 tokens rarely; short ones fill the SMs on short prompts
+    auto blocks = [&](int run) { return dim3(tiles, ceil_div(a.seqlen, kWarps * run), a.batch); };
+    if ((int64_t)tiles * a.batch * ceil_div(a.seqlen, kWarps * 32) >= 304)
+        conv_forward_kernel<T, V, W, 32><<<blocks(32), 32 * kWarps, 0, s>>>(a, y, f, true);
     else
-        conv_forward_kernel<T, V, 4><<<dim3(tiles, ceil_div(a.seqlen, kWarps * 4), a.batch), 32 * kWarps, 0, s>>>(
-            a, y, static_cast<T*>(final_state), vec);
+        conv_forward_kernel<T, V, W, 4><<<blocks(4), 32 * kWarps, 0, s>>>(a, y, f, true);
 }
 
-template <typename T>
+template <typename T, int W>
 int forward_of(const ConvArgs& a, const Pieces& y, void* final_state, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
     launch_begin(kKindConv, s);
-    if (whole_vectors(a, y, final_state, nullptr, V, sizeof(T))) run_forward<T, V>(a, y, final_state, true, s);
-    else run_forward<T, 1>(a, y, final_state, true, s);
+    if (whole_vectors(a, y, final_state, nullptr, 4, sizeof(T))) run_forward<T, 4, W>(a, y, final_state, s);
+    else run_forward<T, 1, W>(a, y, final_state, s);
     return launch_end(kKindConv, s);
 }
 
-template <typename T>
+template <typename T, int W>
 int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* dx, int64_t dx_batch, int64_t dx_token,
                 float* dweight, float* dbias, void* dinit, float* partial, cudaStream_t s) {
     constexpr int V = 4;
@@ -349,10 +407,10 @@ int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* d
     launch_begin(kKindConvBwd, s);
     if (whole_vectors(a, dy, dfinal, dinit, V, sizeof(T))) {
         const bool vec_dx = dx_batch % V == 0 && dx_token % V == 0 && on(dx, V * sizeof(T));
-        conv_backward_kernel<T, V><<<dim3(ceil_div(a.channels, 32 * V), rows, a.batch), 32 * kWarps, 0, s>>>(
+        conv_backward_kernel<T, V, W><<<dim3(ceil_div(a.channels, 32 * V), rows, a.batch), 32 * kWarps, 0, s>>>(
             a, dy, df, o, dx_batch, dx_token, di, partial, true, vec_dx);
     } else {
-        conv_backward_kernel<T, 1><<<dim3(ceil_div(a.channels, 32), rows, a.batch), 32 * kWarps, 0, s>>>(
+        conv_backward_kernel<T, 1, W><<<dim3(ceil_div(a.channels, 32), rows, a.batch), 32 * kWarps, 0, s>>>(
             a, dy, df, o, dx_batch, dx_token, di, partial, true, true);
     }
     const int r = launch_end(kKindConvBwd, s);
@@ -363,43 +421,56 @@ int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* d
     return launch_end(kKindConvBwd, s);
 }
 
-template <typename T>
-int step_of(const ConvArgs& a, void* state, const int* slots, int nslots, const Pieces& y, int* err, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-    launch_begin(kKindConvStep, s);
-    if (whole_vectors(a, y, state, nullptr, V, sizeof(T)))
-        conv_step_kernel<T, V><<<dim3(ceil_div(a.channels, 128 * V), a.batch), 128, 0, s>>>(a, static_cast<T*>(state), slots,
-                                                                                         nslots, y, err, true);
+template <typename T, int V, int W>
+void run_step(const ConvArgs& a, T* state, const int* slots, int nslots, const Pieces& y, int* err, cudaStream_t s) {
+    const int tiles = ceil_div(a.channels, 128 * V);
+    // four rows a thread where the batch fills the SMs all the same
+    if (a.batch / 4 * tiles >= 152)
+        conv_step_kernel<T, V, W, 4><<<dim3(tiles, ceil_div(a.batch, 4)), 128, 0, s>>>(a, state, slots, nslots, y, err, true);
     else
-        conv_step_kernel<T, 1><<<dim3(ceil_div(a.channels, 128), a.batch), 128, 0, s>>>(a, static_cast<T*>(state), slots,
-                                                                                       nslots, y, err, true);
+        conv_step_kernel<T, V, W, 1><<<dim3(tiles, a.batch), 128, 0, s>>>(a, state, slots, nslots, y, err, true);
+}
+
+template <typename T, int W>
+int step_of(const ConvArgs& a, void* state, const int* slots, int nslots, const Pieces& y, int* err, cudaStream_t s) {
+    T* st = static_cast<T*>(state);
+    launch_begin(kKindConvStep, s);
+    if (whole_vectors(a, y, state, nullptr, 4, sizeof(T))) run_step<T, 4, W>(a, st, slots, nslots, y, err, s);
+    else run_step<T, 1, W>(a, st, slots, nslots, y, err, s);
     return launch_end(kKindConvStep, s);
+}
+
+// Calls f with a value of the element type and the number of taps as a constant.
+template <typename F>
+int by_type_and_width(const ConvArgs& a, F f) {
+    auto widths = [&](auto type) {
+        if (a.width == 2) return f(type, std::integral_constant<int, 2>());
+        if (a.width == 3) return f(type, std::integral_constant<int, 3>());
+        return f(type, std::integral_constant<int, 4>());
+    };
+    if (a.dtype == SSD_BF16) return widths(__nv_bfloat16());
+    if (a.dtype == SSD_F16) return widths(__half());
+    return widths(0.f);
 }
 
 }  // namespace
 
 int launch_conv_forward(const ConvArgs& a, const Pieces& y, void* final_state, cudaStream_t s) {
-    if (a.dtype == SSD_BF16) return forward_of<__nv_bfloat16>(a, y, final_state, s);
-    if (a.dtype == SSD_F16) return forward_of<__half>(a, y, final_state, s);
-    return forward_of<float>(a, y, final_state, s);
+    return by_type_and_width(a, [&](auto type, auto W) { return forward_of<decltype(type), W()>(a, y, final_state, s); });
 }
 
 int conv_backward_rows(const ConvArgs& a) { return a.batch * ceil_div(a.seqlen, kWarps * kBwdRun); }
 
 int launch_conv_backward(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* dx, int64_t dx_batch,
                          int64_t dx_token, float* dweight, float* dbias, void* dinit, float* partial, cudaStream_t s) {
-    if (a.dtype == SSD_BF16)
-        return backward_of<__nv_bfloat16>(a, dy, dfinal, dx, dx_batch, dx_token, dweight, dbias, dinit, partial, s);
-    if (a.dtype == SSD_F16)
-        return backward_of<__half>(a, dy, dfinal, dx, dx_batch, dx_token, dweight, dbias, dinit, partial, s);
-    return backward_of<float>(a, dy, dfinal, dx, dx_batch, dx_token, dweight, dbias, dinit, partial, s);
+    return by_type_and_width(a, [&](auto type, auto W) {
+        return backward_of<decltype(type), W()>(a, dy, dfinal, dx, dx_batch, dx_token, dweight, dbias, dinit, partial, s);
+    });
 }
 
 int launch_conv_step(const ConvArgs& a, void* state, const int* slots, int nslots, const Pieces& y, int* err,
                      cudaStream_t s) {
-    if (a.dtype == SSD_BF16) return step_of<__nv_bfloat16>(a, state, slots, nslots, y, err, s);
-    if (a.dtype == SSD_F16) return step_of<__half>(a, state, slots, nslots, y, err, s);
-    return step_of<float>(a, state, slots, nslots, y, err, s);
+    return by_type_and_width(a, [&](auto type, auto W) { return step_of<decltype(type), W()>(a, state, slots, nslots, y, err, s); });
 }
 
 }  // namespace ssd

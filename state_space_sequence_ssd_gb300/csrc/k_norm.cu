@@ -16,18 +16,52 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sum over the `lanes` threads of one row (a power of two; at most kThreads).  Every thread of the block calls it.
-// `lane` is the thread's place in its row; buf holds one float per warp.
-__device__ __forceinline__ float row_sum(float v, int lanes, float* buf) {
-    for (int o = min(lanes, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sums of two values over the `lanes` threads of one row (a power of two; at most kThreads).  Every thread of the
+// block calls it.  buf holds a pair per warp; calls that follow one another alternate between two of them, so that
+// one barrier a call is enough.
+__device__ __forceinline__ float2 row_sums(float2 v, int lanes, float2* buf) {
+    if (lanes >= 32) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+    } else {
+        for (int o = lanes / 2; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+    }
     if (lanes <= 32) return v;
     const int warp = threadIdx.x >> 5, per = lanes >> 5;
-    __syncthreads();  // buf's last readers are done
     if ((threadIdx.x & 31) == 0) buf[warp] = v;
     __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < per; ++i) v += buf[(warp / per) * per + i];
+    v = make_float2(0.f, 0.f);
+    for (int i = 0; i < per; ++i) {
+        const float2 q = buf[(warp / per) * per + i];
+        v.x += q.x;
+        v.y += q.y;
+    }
     return v;
+}
+__device__ __forceinline__ float row_sum(float v, int lanes, float2* buf) { return row_sums(make_float2(v, 0.f), lanes, buf).x; }
+
+// V columns of a float32 row from column c on (a null row: `otherwise`).  `vec`: 16-byte aligned groups of four.
+template <int V>
+__device__ __forceinline__ void load_columns(const float* p, int c, int width, bool vec, float otherwise, float (&o)[V]) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = otherwise;
+    } else if (V >= 4 && vec) {
+#pragma unroll
+        for (int e = 0; e + 3 < V; e += 4) {
+            const float4 q = c < width ? __ldg(reinterpret_cast<const float4*>(p + c + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[e] = q.x; o[e + 1] = q.y; o[e + 2] = q.z; o[e + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = c + e < width ? __ldg(p + c + e) : 0.f;
+    }
 }
 
 // NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  With NV = 0 the row
@@ -37,38 +71,42 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restr
                                                                 const float* __restrict__ weight,
                                                                 const float* __restrict__ bias, float eps, int64_t rows,
                                                                 int width, int lanes, T* __restrict__ y,
-                                                                float* __restrict__ mean, float* __restrict__ rstd) {
-    __shared__ float buf[kThreads / 32];
-    const int lane = threadIdx.x % lanes;
+                                                                float* __restrict__ mean, float* __restrict__ rstd, bool vecw) {
+    __shared__ float2 buf[2][kThreads / 32];
+    const int lane = threadIdx.x & (lanes - 1);
     const int64_t row = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
     const bool live = row < rows;
     const T* xr = x + (live ? row : 0) * x_row;
     const float inv = 1.f / (float)width;
-    float v[NV > 0 ? NV : 1][V];
+    Vec<T, V> r[NV > 0 ? NV : 1];
     float s = 0.f;
     if constexpr (NV > 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + lanes * i) * V;
-            const Vec<T, V> r = load_vec<T, V>(xr + c, live ? width - c : 0, true);
-#pragma unroll
-            for (int e = 0; e < V; ++e) { v[i][e] = to_f32<T>(r.e[e]); s += v[i][e]; }
+            r[i] = load_vec<T, V>(xr + c, live ? width - c : 0, true);
         }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += r[i].get(e);
     } else if (live) {
         for (int c = lane; c < width; c += lanes) s += to_f32<T>(xr[c]);
     }
-    const float m = row_sum(s, lanes, buf) * inv;
+    const float m = row_sum(s, lanes, buf[0]) * inv;
     float q = 0.f;
     if constexpr (NV > 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if ((lane + lanes * i) * V + e < width) { v[i][e] -= m; q = fmaf(v[i][e], v[i][e], q); }
+            for (int e = 0; e < V; ++e) {
+                const float d = r[i].get(e) - m;
+                if (V > 1 ? (lane + lanes * i) * V < width : lane + lanes * i < width) q = fmaf(d, d, q);
+            }
     } else if (live) {
         for (int c = lane; c < width; c += lanes) { const float d = to_f32<T>(xr[c]) - m; q = fmaf(d, d, q); }
     }
-    const float rs = rsqrtf(fmaf(row_sum(q, lanes, buf), inv, eps));
+    const float rs = rsqrtf(fmaf(row_sum(q, lanes, buf[1]), inv, eps));
     if (!live) return;
     if (lane == 0) {
         if (mean != nullptr) mean[row] = m;
@@ -80,13 +118,12 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restr
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + lanes * i) * V;
             if (c >= width) break;
-            Vec<T, V> o;
-            const Vec<float, V> w = weight != nullptr ? load_vec<float, V>(weight + c, width - c, false) : Vec<float, V>();
-            const Vec<float, V> bb = bias != nullptr ? load_vec<float, V>(bias + c, width - c, false) : Vec<float, V>();
+            float o[V], w[V], b[V];
+            load_columns<V>(weight, c, width, vecw, 1.f, w);
+            load_columns<V>(bias, c, width, vecw, 0.f, b);
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                o.e[e] = from_f32<T>(fmaf(v[i][e] * rs, weight != nullptr ? w.e[e] : 1.f, bias != nullptr ? bb.e[e] : 0.f));
-            store_vec<T, V>(yr + c, o, width - c, true);
+            for (int e = 0; e < V; ++e) o[e] = fmaf((r[i].get(e) - m) * rs, w[e], b[e]);
+            store_vec<T, V>(yr + c, Vec<T, V>::of(o), width - c, true);
         }
     } else {
         for (int c = lane; c < width; c += lanes)
@@ -95,90 +132,93 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restr
     }
 }
 
-// A block of `lanes` threads a row, kThreads / lanes rows at a time.  The thread's columns of dweight and dbias
-// stay in registers while the block walks its rows.
+// A block of `lanes` threads a row, kThreads / lanes rows at a time.  The thread's columns of dweight and dbias stay
+// in registers while the block walks its rows, and the next rows' loads are in flight while a row is summed.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __restrict__ x, int64_t x_row,
                                                                  const float* __restrict__ weight,
                                                                  const float* __restrict__ mean,
                                                                  const float* __restrict__ rstd, const T* __restrict__ dy,
                                                                  int64_t dy_row, int64_t rows, int width, int lanes,
-                                                                 T* __restrict__ dx, float* __restrict__ partial) {
+                                                                 T* __restrict__ dx, float* __restrict__ partial, bool vecw) {
     extern __shared__ float sums[];  // (kThreads / lanes) x 2 x width where rows share a block
-    __shared__ float buf[2][kThreads / 32];
-    const int lane = threadIdx.x % lanes, slot = threadIdx.x / lanes, per = kThreads / lanes;
+    __shared__ float2 buf[2][kThreads / 32];
+    const int lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes, per = kThreads / lanes;
     const float inv = 1.f / (float)width;
     float w[NV][V], dw[NV][V], db[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        load_columns<V>(weight, (lane + lanes * i) * V, width, vecw, 1.f, w[i]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int c = (lane + lanes * i) * V + e;
-            w[i][e] = c < width ? (weight != nullptr ? weight[c] : 1.f) : 0.f;
-            dw[i][e] = db[i][e] = 0.f;
-        }
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += (int64_t)gridDim.x * per) {
-        const int64_t row = r0 + slot;
+        for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.f;
+    }
+    Vec<T, V> nx[NV], ng[NV];
+    float nm, nrs;
+    auto fetch = [&](int64_t row) {
         const bool live = row < rows;
-        const T* xr = x + (live ? row : 0) * x_row;
-        const T* gr = dy + (live ? row : 0) * dy_row;
-        const float m = live ? mean[row] : 0.f, rs = live ? rstd[row] : 0.f;
-        float xh[NV][V], g[NV][V];
-        float s1 = 0.f, s2 = 0.f;
+        const int64_t at = live ? row : 0;
+        nm = live ? __ldg(mean + at) : 0.f;
+        nrs = live ? __ldg(rstd + at) : 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + lanes * i) * V;
-            const Vec<T, V> a = load_vec<T, V>(xr + c, live ? width - c : 0, true);
-            const Vec<T, V> d = load_vec<T, V>(gr + c, live ? width - c : 0, true);
+            nx[i] = load_vec<T, V>(x + at * x_row + c, live ? width - c : 0, true);
+            ng[i] = load_vec<T, V>(dy + at * dy_row + c, live ? width - c : 0, true);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * per;
+    int64_t row = (int64_t)blockIdx.x * per + slot;
+    fetch(row);
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += step, row += step, turn ^= 1) {
+        Vec<T, V> cx[NV], cg[NV];
+        const float m = nm, rs = nrs;
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) { cx[i] = nx[i]; cg[i] = ng[i]; }
+        if (r0 + step < rows) fetch(row + step);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float gy = to_f32<T>(d.e[e]);
-                xh[i][e] = (live && c + e < width) ? (to_f32<T>(a.e[e]) - m) * rs : 0.f;
+                const float gy = cg[i].get(e), xh = (cx[i].get(e) - m) * rs;  // gy is zero past the row's end
                 db[i][e] += gy;
-                dw[i][e] = fmaf(gy, xh[i][e], dw[i][e]);
-                g[i][e] = gy * w[i][e];
-                s1 += g[i][e];
-                s2 = fmaf(g[i][e], xh[i][e], s2);
+                dw[i][e] = fmaf(gy, xh, dw[i][e]);
+                s.x = fmaf(gy, w[i][e], s.x);
+                s.y = fmaf(gy * w[i][e], xh, s.y);
             }
-        }
-        s1 = row_sum(s1, lanes, buf[0]) * inv;
-        s2 = row_sum(s2, lanes, buf[1]) * inv;
-        if (!live) continue;
+        s = row_sums(s, lanes, buf[turn]);
+        if (row >= rows) continue;
+        s.x *= inv;
+        s.y *= inv;
         T* o = dx + row * width;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + lanes * i) * V;
             if (c >= width) break;
-            Vec<T, V> out;
+            float out[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) out.e[e] = from_f32<T>(rs * (g[i][e] - s1 - xh[i][e] * s2));
-            store_vec<T, V>(o + c, out, width - c, true);
+            for (int e = 0; e < V; ++e)
+                out[e] = rs * fmaf(-(cx[i].get(e) - m) * rs, s.y, fmaf(cg[i].get(e), w[i][e], -s.x));
+            store_vec<T, V>(o + c, Vec<T, V>::of(out), width - c, true);
         }
     }
     if (partial == nullptr) return;
-    float* row = partial + (int64_t)blockIdx.x * 2 * width;
-    if (per == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int c = (lane + lanes * i) * V + e;
-                if (c < width) { row[c] = dw[i][e]; row[width + c] = db[i][e]; }
-            }
-        return;
-    }
+    float* out = partial + (int64_t)blockIdx.x * 2 * width;
+    float* to = per == 1 ? out : sums + slot * 2 * width;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const int c = (lane + lanes * i) * V + e;
-            if (c < width) { sums[slot * 2 * width + c] = dw[i][e]; sums[slot * 2 * width + width + c] = db[i][e]; }
+            if (c < width) { to[c] = dw[i][e]; to[width + c] = db[i][e]; }
         }
+    if (per == 1) return;
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * width; c += kThreads) {
         float s = 0.f;
         for (int q = 0; q < per; ++q) s += sums[q * 2 * width + c];
-        row[c] = s;
+        out[c] = s;
     }
 }
 
@@ -192,13 +232,14 @@ __global__ void __launch_bounds__(kThreads) norm_backward_wide_kernel(const T* _
                                                                       const T* __restrict__ dy, int64_t dy_row,
                                                                       int64_t rows, int width, T* __restrict__ dx,
                                                                       float* __restrict__ partial) {
-    __shared__ float buf[2][kThreads / 32];
+    __shared__ float2 buf[2][kThreads / 32];
     const float inv = 1.f / (float)width;
+    int turn = 0;
     float* sum = partial == nullptr ? nullptr : partial + (int64_t)blockIdx.x * 2 * width;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T *xr = x + row * x_row, *gr = dy + row * dy_row;
         const float m = mean[row], rs = rstd[row];
-        float s1 = 0.f, s2 = 0.f;
+        float2 s = make_float2(0.f, 0.f);
         for (int c = threadIdx.x; c < width; c += kThreads) {
             const float gy = to_f32<T>(gr[c]), xh = (to_f32<T>(xr[c]) - m) * rs;
             const float g = gy * (weight != nullptr ? weight[c] : 1.f);
@@ -207,11 +248,12 @@ __global__ void __launch_bounds__(kThreads) norm_backward_wide_kernel(const T* _
                 sum[c] = first ? gy * xh : fmaf(gy, xh, sum[c]);
                 sum[width + c] = first ? gy : sum[width + c] + gy;
             }
-            s1 += g;
-            s2 = fmaf(g, xh, s2);
+            s.x += g;
+            s.y = fmaf(g, xh, s.y);
         }
-        s1 = row_sum(s1, kThreads, buf[0]) * inv;
-        s2 = row_sum(s2, kThreads, buf[1]) * inv;
+        s = row_sums(s, kThreads, buf[turn]);
+        turn ^= 1;
+        const float s1 = s.x * inv, s2 = s.y * inv;
         for (int c = threadIdx.x; c < width; c += kThreads) {
             const float g = to_f32<T>(gr[c]) * (weight != nullptr ? weight[c] : 1.f), xh = (to_f32<T>(xr[c]) - m) * rs;
             dx[row * width + c] = from_f32<T>(rs * (g - s1 - xh * s2));
@@ -227,7 +269,7 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restric
     const int i = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (i < 2 * width) {
-#pragma unroll 8
+#pragma unroll 16
         for (int r = warp; r < parts; r += 8) s += partial[(int64_t)r * 2 * width + i];
     }
     part[warp][lane] = s;
@@ -245,29 +287,30 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restric
 
 bool on(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// Threads that share a row of `vecs` vectors, a power of two: one vector each up to a warp, then up to a block's
-// threads so that a thread holds about `want` vectors.
-int row_lanes(int vecs, int want) {
-    int lanes = 1;
-    while (lanes < 32 && lanes < vecs) lanes *= 2;
-    while (lanes < kThreads && lanes * want < vecs) lanes *= 2;
+// Threads that share a row of `vecs` vectors, a power of two: enough that a thread holds at most `most` vectors, more
+// (down to one each) while the rows alone leave the SMs with less than about 1024 threads.
+int row_lanes(int64_t rows, int vecs, int most, int least) {
+    int lanes = least;
+    while (lanes < kThreads && (int64_t)lanes * most < vecs) lanes *= 2;
+    while (lanes < kThreads && lanes < vecs && rows * lanes < 152 * 1024) lanes *= 2;
     return lanes;
 }
 
 template <typename T, int V>
 int forward_of(const void* x, int64_t x_row, const float* weight, const float* bias, float eps, int64_t rows, int width,
                void* y, float* mean, float* rstd, cudaStream_t s) {
+    constexpr int M = V == 1 ? 4 : 1;
     const int vecs = ceil_div(width, V);
-    const int lanes = row_lanes(vecs, V == 1 ? 8 : 2);
+    const int lanes = row_lanes(rows, vecs, 8 * M, 1);
     const int nv = ceil_div(vecs, lanes);
     const int64_t blocks = ceil_div64(rows, kThreads / lanes);
     if (blocks > 2147483647) return SSD_ERR_UNSUPPORTED;
+    const bool vecw = on(weight, 16) && on(bias, 16);
     launch_begin(kKindNorm, s);
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)blocks, kThreads, 0, s>>>(static_cast<const T*>(x), x_row, weight, bias, eps, rows, width, lanes,
-                                                     static_cast<T*>(y), mean, rstd);
+                                                     static_cast<T*>(y), mean, rstd, vecw);
     };
-    constexpr int M = V == 1 ? 4 : 1;
     if (nv <= 1 * M) go(norm_forward_kernel<T, V, 1 * M>);
     else if (nv <= 2 * M) go(norm_forward_kernel<T, V, 2 * M>);
     else if (nv <= 4 * M) go(norm_forward_kernel<T, V, 4 * M>);
@@ -279,17 +322,18 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
 template <typename T, int V>
 int backward_of(const void* x, int64_t x_row, const float* weight, const float* mean, const float* rstd, const void* dy,
                 int64_t dy_row, int64_t rows, int width, void* dx, float* partial, int parts, cudaStream_t s) {
+    constexpr int M = V == 1 ? 4 : 1;
     const int vecs = ceil_div(width, V);
-    const int lanes = row_lanes(vecs, V == 1 ? 8 : 1);
+    const int lanes = row_lanes(rows, vecs, 2 * M, 32);
     const int nv = ceil_div(vecs, lanes);
     const int smem = lanes == kThreads || partial == nullptr ? 0 : kThreads / lanes * 2 * width * 4;
     const T *xt = static_cast<const T*>(x), *gt = static_cast<const T*>(dy);
     T* o = static_cast<T*>(dx);
+    const bool vecw = on(weight, 16);
     launch_begin(kKindNormBwd, s);
     auto go = [&](auto kernel) {
-        kernel<<<parts, kThreads, smem, s>>>(xt, x_row, weight, mean, rstd, gt, dy_row, rows, width, lanes, o, partial);
+        kernel<<<parts, kThreads, smem, s>>>(xt, x_row, weight, mean, rstd, gt, dy_row, rows, width, lanes, o, partial, vecw);
     };
-    constexpr int M = V == 1 ? 4 : 1;
     if (nv <= 1 * M) go(norm_backward_kernel<T, V, 1 * M>);
     else if (nv <= 2 * M) go(norm_backward_kernel<T, V, 2 * M>);
     else if (nv <= 4 * M) go(norm_backward_kernel<T, V, 4 * M>);

@@ -70,16 +70,16 @@ __global__ void __launch_bounds__(kThreads) selective_kernel(SelectiveArgs a, in
     f32x2 A01, A23, h01, h23;
     {
         const Vec<float, 4> A4 = load_vec<float, 4>(a.A + (mine ? ci * N + 4 * q : 0), nvalid, false);
-        A01 = pk(A4.e[0] * kLog2e, A4.e[1] * kLog2e);
-        A23 = pk(A4.e[2] * kLog2e, A4.e[3] * kLog2e);
+        A01 = pk(A4.get(0) * kLog2e, A4.get(1) * kLog2e);
+        A23 = pk(A4.get(2) * kLog2e, A4.get(3) * kLog2e);
         h01 = h23 = 0ull;
         const float* from = nullptr;
         if (!STATE_ONLY && nchunks > 1) from = hops + ((int64_t)b * nchunks + part) * a.channels * N;
         else if (!STATE_ONLY && a.init != nullptr) from = a.init + (int64_t)b * a.channels * N;
         if (from != nullptr) {
             const Vec<float, 4> h4 = load_vec<float, 4>(from + (mine ? ci * N + 4 * q : 0), nvalid, false);
-            h01 = pk(h4.e[0], h4.e[1]);
-            h23 = pk(h4.e[2], h4.e[3]);
+            h01 = pk(h4.get(0), h4.get(1));
+            h23 = pk(h4.get(2), h4.get(3));
         }
     }
     float bias[4] = {0.f, 0.f, 0.f, 0.f}, Dv[4] = {0.f, 0.f, 0.f, 0.f}, dsum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads) selective_kernel(SelectiveArgs a, in
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     // a token past the length keeps the state: dt = 0
-                    const float d = live ? effective(to_f32<T>(rd[i].e[e]), bias[e], a.dto) : 0.f;
-                    const float dx = d * to_f32<T>(rx[i].e[e]);
+                    const float d = live ? effective(rd[i].get(e), bias[e], a.dto) : 0.f;
+                    const float dx = d * rx[i].get(e);
                     s_dt[(idx / CV) * CC + 4 * v0 + (e ^ ((v0 >> 1) & 3))] = make_float4(d, d, dx, dx);
                     if (STATE_ONLY) dsum[e] += d;
                 }
@@ -135,9 +135,9 @@ __global__ void __launch_bounds__(kThreads) selective_kernel(SelectiveArgs a, in
         for (int i = 0; i < K::BI; ++i) {
             const int idx = tid + i * kThreads;
             if (idx < TS * LP) {
-                s_B[idx] = make_float4(to_f32<T>(rB[i].e[0]), to_f32<T>(rB[i].e[1]), to_f32<T>(rB[i].e[2]), to_f32<T>(rB[i].e[3]));
+                s_B[idx] = make_float4(rB[i].get(0), rB[i].get(1), rB[i].get(2), rB[i].get(3));
                 if (!STATE_ONLY)
-                    s_C[idx] = make_float4(to_f32<T>(rC[i].e[0]), to_f32<T>(rC[i].e[1]), to_f32<T>(rC[i].e[2]), to_f32<T>(rC[i].e[3]));
+                    s_C[idx] = make_float4(rC[i].get(0), rC[i].get(1), rC[i].get(2), rC[i].get(3));
             }
         }
         __syncthreads();
@@ -172,20 +172,20 @@ __global__ void __launch_bounds__(kThreads) selective_kernel(SelectiveArgs a, in
             for (int i = 0; i < K::XI; ++i) {
                 const int idx = tid + i * kThreads, t = t0 + idx / CV, valid = nc - 4 * v0;
                 if (idx >= TS * CV || t >= te || valid <= 0) continue;
-                Vec<T, 4> o;
+                float o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = 0.f;
                     if (t < len) {
-                        v = fmaf(Dv[e], to_f32<T>(cx[i].e[e]), s_y[(idx / CV) * CC + 4 * v0 + e]);
+                        v = fmaf(Dv[e], cx[i].get(e), s_y[(idx / CV) * CC + 4 * v0 + e]);
                         if (zp != nullptr) {
-                            const float zv = to_f32<T>(cz[i].e[e]);
+                            const float zv = cz[i].get(e);
                             v *= zv * sigmoid(zv);
                         }
                     }
-                    o.e[e] = from_f32<T>(v);
+                    o[e] = v;
                 }
-                store_vec<T, 4>(y + ((int64_t)b * a.seqlen + t) * a.channels + g0 + cb + 4 * v0, o, valid, vec);
+                store_vec<T, 4>(y + ((int64_t)b * a.seqlen + t) * a.channels + g0 + cb + 4 * v0, Vec<T, 4>::of(o), valid, vec);
             }
         }
     }
@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(kThreads) selective_kernel(SelectiveArgs a, in
     if (STATE_ONLY) to = hops + ((int64_t)b * nchunks + part + 1) * a.channels * N;  // carried into the next chunk
     else if (final_state != nullptr && te == a.seqlen) to = final_state + (int64_t)b * a.channels * N;
     if (to != nullptr && mine) {
-        Vec<float, 4> h4;
-        unpk(h01, h4.e[0], h4.e[1]);
-        unpk(h23, h4.e[2], h4.e[3]);
-        store_vec<float, 4>(to + ci * N + 4 * q, h4, nvalid, N % 4 == 0 && (reinterpret_cast<uintptr_t>(to) & 15) == 0);
+        float h4[4];
+        unpk(h01, h4[0], h4[1]);
+        unpk(h23, h4[2], h4[3]);
+        store_vec<float, 4>(to + ci * N + 4 * q, Vec<float, 4>::of(h4), nvalid, N % 4 == 0 && (reinterpret_cast<uintptr_t>(to) & 15) == 0);
     }
     if (STATE_ONLY) {
         // sum of dt over the chunk, per channel: the threads of one vector's tokens, in shared memory
@@ -275,56 +275,97 @@ int forward_of(const SelectiveArgs& a, int chunks, void* y, float* final_state, 
 }
 
 // ------------------------------------------------------------------------------------------------ one token
-// A lane holds four state entries of one channel and LP lanes share the channel.  Bound by HBM: the state is read
-// and written once.  An idle row (slot -1) writes zeros and leaves every slot alone.
-template <typename T>
-__global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, int lp, float* __restrict__ state,
+// A lane holds four state entries of one channel for R rows, and LP lanes share the channel.  Bound by HBM: the state
+// is read and written once.  The rows' states are loaded together and A once for them; each of the first R lanes
+// forms one row's dt and gate for the others, and ends with that row's output.  An idle row (slot -1) writes zeros
+// and leaves every slot alone.
+template <typename T, int LP, int R>
+__global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, float* __restrict__ state,
                                                              const int* __restrict__ slots, int nslots, T* __restrict__ y,
                                                              int* err, bool vecs, bool vecb) {
-    const int b = blockIdx.y, N = a.dstate, q = threadIdx.x % lp;
-    const int64_t c = (int64_t)blockIdx.x * (256 / lp) + threadIdx.x / lp;
+    const int b0 = blockIdx.y * R, N = a.dstate, q = threadIdx.x % LP;
+    const int64_t c = (int64_t)blockIdx.x * (256 / LP) + threadIdx.x / LP;
     const bool mine = c < a.channels;
-    const int slot = row_slot(slots, b, nslots, err);
     const int nvalid = mine ? max(0, min(4, N - 4 * q)) : 0;
-    float acc = 0.f, xv = 0.f;
-    if (mine && slot >= 0) {
-        float* st = state + ((int64_t)slot * a.channels + c) * N + 4 * q;
-        const Vec<float, 4> h = load_vec<float, 4>(st, nvalid, vecs);
-        const Vec<float, 4> A4 = load_vec<float, 4>(a.A + c * N + 4 * q, nvalid, vecs);
-        const int g = (int)(c / (a.channels / a.ngroups));
-        const Vec<T, 4> Bv = load_vec<T, 4>(static_cast<const T*>(a.B) + b * a.B_batch + (int64_t)g * N + 4 * q, nvalid, vecb);
-        const Vec<T, 4> Cv = load_vec<T, 4>(static_cast<const T*>(a.C) + b * a.C_batch + (int64_t)g * N + 4 * q, nvalid, vecb);
-        xv = to_f32<T>(static_cast<const T*>(a.x)[b * a.x_batch + c]);
-        const float d = effective(to_f32<T>(static_cast<const T*>(a.dt)[b * a.dt_batch + c]),
-                                  a.dto.bias != nullptr ? a.dto.bias[c] : 0.f, a.dto);
-        Vec<float, 4> o;
+    const int g = mine ? (int)(c / (a.channels / a.ngroups)) : 0;
+    int slot[R];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            o.e[e] = fmaf(exp2_fast(d * (A4.e[e] * kLog2e)), h.e[e], d * xv * to_f32<T>(Bv.e[e]));
-            acc = fmaf(to_f32<T>(Cv.e[e]), o.e[e], acc);
-        }
-        store_vec<float, 4>(st, o, nvalid, vecs);
+    for (int r = 0; r < R; ++r) slot[r] = b0 + r < a.batch ? row_slot(slots, b0 + r, nslots, err) : -1;
+    Vec<float, 4> h[R];
+    Vec<T, 4> Bv[R], Cv[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int got = slot[r] >= 0 ? nvalid : 0;
+        h[r] = load_vec<float, 4, true>(state + ((int64_t)slot[r] * a.channels + c) * N + 4 * q, got, vecs);
+        const int64_t bc = (int64_t)g * N + 4 * q;
+        Bv[r] = load_vec<T, 4>(static_cast<const T*>(a.B) + (b0 + r) * a.B_batch + bc, got, vecb);
+        Cv[r] = load_vec<T, 4>(static_cast<const T*>(a.C) + (b0 + r) * a.C_batch + bc, got, vecb);
     }
-    for (int off = lp / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (!mine || q != 0) return;
-    if (slot >= 0) {
-        if (a.D != nullptr) acc = fmaf(a.D[c], xv, acc);
-        if (a.z != nullptr) {
-            const float zv = to_f32<T>(static_cast<const T*>(a.z)[b * a.z_batch + c]);
-            acc *= zv * sigmoid(zv);
-        }
+    // lane q: row b0 + q's scalars
+    const bool own = mine && q < R && b0 + q < a.batch;
+    float xq = 0.f, dq = 0.f, zq = 0.f, Dq = 0.f;
+    if (own) {
+        xq = to_f32<T>(static_cast<const T*>(a.x)[(b0 + q) * a.x_batch + c]);
+        dq = to_f32<T>(static_cast<const T*>(a.dt)[(b0 + q) * a.dt_batch + c]);
+        if (a.z != nullptr) zq = to_f32<T>(static_cast<const T*>(a.z)[(b0 + q) * a.z_batch + c]);
+        if (a.D != nullptr) Dq = __ldg(a.D + c);
     }
-    y[(int64_t)b * a.channels + c] = from_f32<T>(acc);
+    const float bias = a.dto.bias != nullptr && mine ? __ldg(a.dto.bias + c) : 0.f;
+    const Vec<float, 4> A4 = load_vec<float, 4>(a.A + (mine ? c * N + 4 * q : 0), nvalid, vecs);
+    const f32x2 log2e = pk(kLog2e, kLog2e), A01 = mul2(A4.pair(0), log2e), A23 = mul2(A4.pair(1), log2e);
+    dq = effective(dq, bias, a.dto);
+    const float dxq = dq * xq;
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float d = __shfl_sync(0xffffffffu, dq, r, LP), dx = __shfl_sync(0xffffffffu, dxq, r, LP);
+        const f32x2 dd = pk(d, d), dxx = pk(dx, dx);
+        const f32x2 h01 = fma2(exp2_2(mul2(dd, A01)), h[r].pair(0), mul2(dxx, Bv[r].pair(0)));
+        const f32x2 h23 = fma2(exp2_2(mul2(dd, A23)), h[r].pair(1), mul2(dxx, Bv[r].pair(1)));
+        acc[r] = sum2(fma2(Cv[r].pair(1), h23, mul2(Cv[r].pair(0), h01)));
+        const f32x2 o[2] = {h01, h23};
+        if (slot[r] >= 0)
+            store_vec<float, 4>(state + ((int64_t)slot[r] * a.channels + c) * N + 4 * q, Vec<float, 4>::of_pairs(o), nvalid, vecs);
+    }
+    // the rows' sums over the channel's lanes: lane q ends with row `which`
+    int which = 0;
+    float s = fold_lanes<R, LP / 2>(acc, q, which);
+    // that sum belongs to lane `which` of the channel, which holds the row's x and z; LP / R lanes hold each
+    s = __shfl_sync(0xffffffffu, s, (q % R) * (LP / R), LP);
+    if (!own) return;
+    int live = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) live |= (r == q && slot[r] >= 0);
+    s = fmaf(Dq, xq, s);
+    if (a.z != nullptr) s *= zq * sigmoid(zq);
+    y[(int64_t)(b0 + q) * a.channels + c] = from_f32<T>(live ? s : 0.f);
+}
+
+template <typename T, int LP>
+int step_lanes(const SelectiveArgs& a, float* state, const int* slots, int nslots, T* y, int* err, cudaStream_t s) {
+    constexpr int R = LP < 4 ? LP : 4;
+    const bool vecs = a.dstate % 4 == 0 && aligned_to(state, 16) && aligned_to(a.A, 16), vecb = states_of_four(a, sizeof(T));
+    const int tiles = ceil_div(a.channels, 256 / LP);
+    launch_begin(kKindSelectiveStep, s);
+    // several rows a thread where the batch fills the SMs all the same
+    if (a.batch / R * tiles >= 152 * 4)
+        selective_step_kernel<T, LP, R><<<dim3(tiles, ceil_div(a.batch, R)), 256, 0, s>>>(a, state, slots, nslots, y, err, vecs, vecb);
+    else
+        selective_step_kernel<T, LP, 1><<<dim3(tiles, a.batch), 256, 0, s>>>(a, state, slots, nslots, y, err, vecs, vecb);
+    return launch_end(kKindSelectiveStep, s);
 }
 
 template <typename T>
 int step_of(const SelectiveArgs& a, float* state, const int* slots, int nslots, void* y, int* err, cudaStream_t s) {
-    const int lp = selective_lanes(a.dstate);
-    const bool vecs = a.dstate % 4 == 0 && aligned_to(state, 16) && aligned_to(a.A, 16);
-    launch_begin(kKindSelectiveStep, s);
-    selective_step_kernel<T><<<dim3(ceil_div(a.channels, 256 / lp), a.batch), 256, 0, s>>>(
-        a, lp, state, slots, nslots, static_cast<T*>(y), err, vecs, states_of_four(a, sizeof(T)));
-    return launch_end(kKindSelectiveStep, s);
+    T* yt = static_cast<T*>(y);
+    switch (selective_lanes(a.dstate)) {
+        case 2: return step_lanes<T, 2>(a, state, slots, nslots, yt, err, s);
+        case 4: return step_lanes<T, 4>(a, state, slots, nslots, yt, err, s);
+        case 8: return step_lanes<T, 8>(a, state, slots, nslots, yt, err, s);
+        case 16: return step_lanes<T, 16>(a, state, slots, nslots, yt, err, s);
+        case 32: return step_lanes<T, 32>(a, state, slots, nslots, yt, err, s);
+        default: return SSD_ERR_UNSUPPORTED;
+    }
 }
 
 }  // namespace

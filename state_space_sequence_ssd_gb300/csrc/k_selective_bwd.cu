@@ -113,13 +113,13 @@ __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Row<T>
         if (r.z != nullptr) z = load_vec<T, 4>(r.z + t * a.z_token + 4 * v0, valid, vec);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float dt = live ? effective(to_f32<T>(d.e[e]), bias[e], a.dto) : 0.f;
-            float g = to_f32<T>(dy.e[e]);
+            const float dt = live ? effective(d.get(e), bias[e], a.dto) : 0.f;
+            float g = dy.get(e);
             if (r.z != nullptr) {
-                const float zv = to_f32<T>(z.e[e]);
+                const float zv = z.get(e);
                 g *= zv * sigmoid(zv);
             }
-            s_q[(idx / K::CV) * K::CC + 4 * v0 + e] = make_float4(dt, dt * to_f32<T>(x.e[e]), g, 0.f);
+            s_q[(idx / K::CV) * K::CC + 4 * v0 + e] = make_float4(dt, dt * x.get(e), g, 0.f);
             dsum[e] += dt;
         }
     }
@@ -129,21 +129,21 @@ __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Row<T>
         const int valid = (t < r.len && t < r.te) ? max(0, a.dstate - n) : 0;
         const Vec<T, 4> B = load_vec<T, 4>(r.B + t * a.B_token + n, valid, vecb);
         const Vec<T, 4> C = load_vec<T, 4>(r.C + t * a.C_token + n, valid, vecb);
-        s_B[idx] = make_float4(to_f32<T>(B.e[0]), to_f32<T>(B.e[1]), to_f32<T>(B.e[2]), to_f32<T>(B.e[3]));
-        s_C[idx] = make_float4(to_f32<T>(C.e[0]), to_f32<T>(C.e[1]), to_f32<T>(C.e[2]), to_f32<T>(C.e[3]));
+        s_B[idx] = make_float4(B.get(0), B.get(1), B.get(2), B.get(3));
+        s_C[idx] = make_float4(C.get(0), C.get(1), C.get(2), C.get(3));
     }
 }
 
 __device__ __forceinline__ void read4(const float* p, int valid, f32x2& lo, f32x2& hi, float scale = 1.f) {
-    const Vec<float, 4> v = load_vec<float, 4>(p, valid, false);
-    lo = pk(v.e[0] * scale, v.e[1] * scale);
-    hi = pk(v.e[2] * scale, v.e[3] * scale);
+    const Vec<float, 4> v = load_vec<float, 4, true>(p, valid, false);
+    lo = pk(v.get(0) * scale, v.get(1) * scale);
+    hi = pk(v.get(2) * scale, v.get(3) * scale);
 }
 __device__ __forceinline__ void write4(float* p, int valid, f32x2 lo, f32x2 hi) {
-    Vec<float, 4> v;
-    unpk(lo, v.e[0], v.e[1]);
-    unpk(hi, v.e[2], v.e[3]);
-    store_vec<float, 4>(p, v, valid, false);
+    float v[4];
+    unpk(lo, v[0], v[1]);
+    unpk(hi, v[2], v[3]);
+    store_vec<float, 4>(p, Vec<float, 4>::of(v), valid, false);
 }
 
 // Every block's own end state (from zero) into hops[k + 1], its own gradient at its start into mus[k - 1] (block 0's
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) selective_block_kernel(SelectiveArgs
             const int idx = tid + i * kThreads, t = r.tb + idx / K::CV;
             if (idx >= kBlock * K::CV || t >= r.te) break;
             const bool live = t < r.len;
-            Vec<T, 4> ox, od, oz;
+            float ox[4], od[4], oz[4];
             const int got = live ? valid : 0;
             const Vec<T, 4> x = load_vec<T, 4>(r.x + t * a.x_token + 4 * v0, got, vec);
             const Vec<T, 4> d = load_vec<T, 4>(r.dt + t * a.dt_token + 4 * v0, got, vec);
@@ -382,10 +382,10 @@ __global__ void __launch_bounds__(kThreads) selective_block_kernel(SelectiveArgs
                 if (live && e < valid) {
                     const int c = r.c0 + 4 * v0 + e, s = (idx / K::CV) * K::CC + 4 * v0 + e;
                     const float4 w = reinterpret_cast<const float4*>(sm)[s];  // dt, dt x, g
-                    const float xv = to_f32<T>(x.e[e]), Dc = a.D != nullptr ? a.D[c] : 0.f;
+                    const float xv = x.get(e), Dc = a.D != nullptr ? a.D[c] : 0.f;
                     fx = fmaf(w.x, s_sb[s], Dc * w.z);
                     fd = fmaf(xv, s_sb[s], kLn2 * s_sa[s]);
-                    const float raw = to_f32<T>(d.e[e]) + (a.dto.bias != nullptr ? a.dto.bias[c] : 0.f);
+                    const float raw = d.get(e) + (a.dto.bias != nullptr ? a.dto.bias[c] : 0.f);
                     if (a.dto.limit) {
                         const float soft = a.dto.softplus ? softplus(raw) : raw;
                         if (!(soft >= a.dto.lo && soft <= a.dto.hi)) fd = 0.f;
@@ -394,18 +394,18 @@ __global__ void __launch_bounds__(kThreads) selective_block_kernel(SelectiveArgs
                     dD[e] = fmaf(w.z, xv, dD[e]);
                     dbias[e] += fd;
                     if (r.z != nullptr) {
-                        const float zv = to_f32<T>(z.e[e]), sg = sigmoid(zv);
-                        fz = to_f32<T>(gy.e[e]) * fmaf(Dc, xv, s_y[s]) * sg * fmaf(zv, 1.f - sg, 1.f);
+                        const float zv = z.get(e), sg = sigmoid(zv);
+                        fz = gy.get(e) * fmaf(Dc, xv, s_y[s]) * sg * fmaf(zv, 1.f - sg, 1.f);
                     }
                 }
-                ox.e[e] = from_f32<T>(fx);
-                od.e[e] = from_f32<T>(fd);
-                oz.e[e] = from_f32<T>(fz);
+                ox[e] = fx;
+                od[e] = fd;
+                oz[e] = fz;
             }
             const int64_t o = ((int64_t)r.b * a.seqlen + t) * a.channels + r.c0 + 4 * v0;
-            store_vec<T, 4>(dx + o, ox, valid, vec);
-            store_vec<T, 4>(ddt + o, od, valid, vec);
-            if (dz != nullptr) store_vec<T, 4>(dz + o, oz, valid, vec);
+            store_vec<T, 4>(dx + o, Vec<T, 4>::of(ox), valid, vec);
+            store_vec<T, 4>(ddt + o, Vec<T, 4>::of(od), valid, vec);
+            if (dz != nullptr) store_vec<T, 4>(dz + o, Vec<T, 4>::of(oz), valid, vec);
         }
     }
     __syncthreads();

@@ -28,38 +28,184 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
-// V consecutive elements as one access of V * sizeof(T) bytes (at most 16)
+// 2^v by the special function unit (relative error about 2^-22; results below 2^-126 are zero)
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / (1 + exp(-v)).  Past v = -88 the denominator overflows and its reciprocal is 0, the limit.
+__device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.f + exp2_fast(v * -kLog2e)); }
+
+// Two float32 values in one register pair, for sm_100's packed arithmetic (one instruction, each lane rounded as
+// a separate instruction would be; the multiplier takes as long as for two, the issue slot is saved).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pk(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpk(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+    float lo, hi;
+    unpk(v, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 exp2_2(f32x2 v) {
+    float lo, hi;
+    unpk(v, lo, hi);
+    return pk(exp2_fast(lo), exp2_fast(hi));
+}
+__device__ __forceinline__ f32x2 rcp_2(f32x2 v) {
+    float lo, hi;
+    unpk(v, lo, hi);
+    return pk(rcp_fast(lo), rcp_fast(hi));
+}
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
+    return rcp_2(add2(pk(1.f, 1.f), exp2_2(mul2(v, pk(-kLog2e, -kLog2e)))));
+}
+
+// V consecutive elements as they lie in memory.  They stay packed words until get() unpacks one: a load whose halves
+// are taken apart at once would be waited for at once.
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-    T e[V];
+struct Vec {
+    static constexpr int BYTES = sizeof(T) * V, WORDS = (BYTES + 3) / 4;
+    static_assert(BYTES == 2 || BYTES == 4 || BYTES == 8 || BYTES == 16, "one access");
+    uint32_t w[WORDS];
+
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+        else return __half2float(__ushort_as_half((unsigned short)((i & 1) ? (w[i / 2] >> 16) : (w[i / 2] & 0xffffu))));
+    }
+    // each value rounded once
+    __device__ __forceinline__ static Vec of(const float (&v)[V]) {
+        Vec r;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                const float hi = 2 * i + 1 < V ? v[2 * i + 1 < V ? 2 * i + 1 : 0] : 0.f;
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], hi);
+                    r.w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                } else {
+                    const __half2 p = __floats2half2_rn(v[2 * i], hi);
+                    r.w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+            }
+        }
+        return r;
+    }
+    // elements 2 i and 2 i + 1
+    __device__ __forceinline__ f32x2 pair(int i) const;
+    __device__ __forceinline__ static Vec of_pairs(const f32x2 (&v)[(V + 1) / 2]);
+    __device__ __forceinline__ static Vec zero() {
+        Vec r;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r.w[i] = 0u;
+        return r;
+    }
 };
 
-// V elements at p, those from `valid` on taken as zero.  `vec`: p is aligned to the whole vector.
-template <typename T, int V>
+// The bits of one element.
+template <typename T>
+__device__ __forceinline__ uint32_t bits_at(const T* p) {
+    if constexpr (sizeof(T) == 4) return *reinterpret_cast<const uint32_t*>(p);
+    else return *reinterpret_cast<const unsigned short*>(p);
+}
+
+// V elements at p, those from `valid` on taken as zero.  `vec`: p is aligned to the whole vector and either all of
+// its elements are valid or none.  KEEP: the memory may be written by this kernel (else the read-only path).
+template <typename T, int V, bool KEEP = false>
 __device__ __forceinline__ Vec<T, V> load_vec(const T* p, int valid, bool vec) {
-    Vec<T, V> r;
-    if (vec && valid >= V) {
-        r = *reinterpret_cast<const Vec<T, V>*>(p);
+    using R = Vec<T, V>;
+    R r = R::zero();
+    if (vec) {
+        if (valid > 0) {
+            if constexpr (R::BYTES == 16) {
+                const uint4 q = KEEP ? *reinterpret_cast<const uint4*>(p) : __ldg(reinterpret_cast<const uint4*>(p));
+                r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
+            } else if constexpr (R::BYTES == 8) {
+                const uint2 q = KEEP ? *reinterpret_cast<const uint2*>(p) : __ldg(reinterpret_cast<const uint2*>(p));
+                r.w[0] = q.x; r.w[1] = q.y;
+            } else if constexpr (R::BYTES == 4) {
+                r.w[0] = KEEP ? *reinterpret_cast<const uint32_t*>(p) : __ldg(reinterpret_cast<const uint32_t*>(p));
+            } else {
+                r.w[0] = KEEP ? *reinterpret_cast<const unsigned short*>(p) : __ldg(reinterpret_cast<const unsigned short*>(p));
+            }
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) r.e[i] = i < valid ? p[i] : from_f32<T>(0.f);
+        for (int i = 0; i < V; ++i)
+            if (i < valid) r.w[sizeof(T) == 4 ? i : i / 2] |= bits_at(p + i) << ((sizeof(T) == 2 && (i & 1)) ? 16 : 0);
     }
     return r;
 }
 
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& r, int valid, bool vec) {
-    if (vec && valid >= V) {
-        *reinterpret_cast<Vec<T, V>*>(p) = r;
+    using R = Vec<T, V>;
+    if (vec) {
+        if (valid <= 0) return;
+        if constexpr (R::BYTES == 16) *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        else if constexpr (R::BYTES == 8) *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+        else if constexpr (R::BYTES == 4) *reinterpret_cast<uint32_t*>(p) = r.w[0];
+        else *reinterpret_cast<unsigned short*>(p) = (unsigned short)r.w[0];
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i < valid) p[i] = r.e[i];
+            if (i < valid) {
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(p + i) = r.w[i];
+                else *reinterpret_cast<unsigned short*>(p + i) = (unsigned short)((i & 1) ? r.w[i / 2] >> 16 : r.w[i / 2] & 0xffffu);
+            }
     }
 }
 
-// 1 / (1 + exp(-v)).  Past v = -88 the denominator is beyond 2^126 and the approximate quotient 0, the limit.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+template <typename T, int V>
+__device__ __forceinline__ f32x2 Vec<T, V>::pair(int i) const {
+    if constexpr (V == 1) return pk(get(0), 0.f);
+    else if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        return pk(f.x, f.y);
+    } else return pk(get(2 * i), get(2 * i + 1));
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> Vec<T, V>::of_pairs(const f32x2 (&v)[(V + 1) / 2]) {
+    float f[V + 1];
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) unpk(v[i], f[2 * i], f[2 * i + 1]);
+    float g[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = f[i];
+    return of(g);
+}
 
 // A row's length, held to [0, seqlen] (no lengths: the whole row).
 __device__ __forceinline__ int row_length(const int* lengths, int b, int seqlen) {

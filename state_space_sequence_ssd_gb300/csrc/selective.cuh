@@ -1,54 +1,10 @@
-// selective.cuh -- device helpers of the selective scan's kernels: packed float32 pairs, the exponential, the dt
-// transform, and the sum over the lanes that share a channel.
+// selective.cuh -- device helpers of the selective scan's kernels: the dt transform and the sum over the lanes that
+// share a channel.
 #pragma once
 
 #include "ops.cuh"
 
 namespace ssd {
-
-// Two float32 values in one register pair, for sm_100's packed arithmetic (one instruction, each lane rounded as
-// a separate instruction would be; the multiplier takes as long as for two, the issue slot is saved).
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pk(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpk(f32x2 v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ float sum2(f32x2 v) {
-    float lo, hi;
-    unpk(v, lo, hi);
-    return lo + hi;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-// 2^v by the special function unit (relative error about 2^-22; results below 2^-126 are zero)
-__device__ __forceinline__ float exp2_fast(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ f32x2 exp2_2(f32x2 v) {
-    float lo, hi;
-    unpk(v, lo, hi);
-    return pk(exp2_fast(lo), exp2_fast(hi));
-}
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1].  log1p(e) / e is fitted on [0, 1] by a polynomial
 // of degree 8 through the Chebyshev expansion (largest relative error 1.5e-7 with its float32 evaluation), so the

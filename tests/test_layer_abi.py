@@ -155,9 +155,9 @@ def test_binding_refuses_what_is_not_on_the_gpu():
 def test_binding_reads_strides():
     from state_space_sequence_ssd_gb300 import layer
     t = torch.zeros((3, 5, 64))
-    assert layer._strides(t[..., 8:24], "t", 1) == [320, 64]
-    assert layer._strides(t[:1, :, :8], "t", 1) == [0, 64]
-    assert layer._strides(t.unflatten(-1, (4, 16)), "t", 2) == [320, 64]
+    assert list(layer._strides(t[..., 8:24], "t", 1)) == [320, 64]
+    assert list(layer._strides(t[:1, :, :8], "t", 1)) == [0, 64]
+    assert list(layer._strides(t.unflatten(-1, (4, 16)), "t", 2)) == [320, 64]
     with pytest.raises(ValueError, match="dense"):
         layer._strides(t.transpose(1, 2), "t", 1)
     assert layer._flat_rows(t[..., :8], "t", 8)[1:] == (64, 15)
