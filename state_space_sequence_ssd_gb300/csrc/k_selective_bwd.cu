@@ -22,29 +22,6 @@ constexpr int kBlock = 64;  // tokens of a block
 constexpr int kRun = 8;     // tokens whose states are held in registers
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Sums R values over the lanes at offsets OFF, OFF / 2, ..., MIN, halving the values held while more than one is left.
-// The lane keeps the sums number which .. which + (values left) - 1, in v[0 ..].
-template <int R, int OFF, int MIN>
-__device__ __forceinline__ void fold_between(float* v, int lane, int& which) {
-    if constexpr (OFF >= MIN) {
-        if constexpr (R > 1) {
-            constexpr int HALF = R / 2;
-            const bool up = (lane & OFF) != 0;
-#pragma unroll
-            for (int j = 0; j < HALF; ++j) {
-                const float mine = up ? v[j + HALF] : v[j];
-                const float other = up ? v[j] : v[j + HALF];
-                v[j] = mine + __shfl_xor_sync(0xffffffffu, other, OFF);
-            }
-            if (up) which += HALF;
-            fold_between<HALF, OFF / 2, MIN>(v, lane, which);
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], OFF);
-            fold_between<1, OFF / 2, MIN>(v, lane, which);
-        }
-    }
-}
-
 template <int LP>
 struct Blk {
     static constexpr int CW = 32 / LP, CC = kWarps * CW, N4 = 4 * LP, CV = CC / 4;
@@ -111,16 +88,25 @@ __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Row<T>
         const Vec<T, 4> dy = load_vec<T, 4>(r.dy + (int64_t)t * a.channels + 4 * v0, valid, vec);
         Vec<T, 4> z;
         if (r.z != nullptr) z = load_vec<T, 4>(r.z + t * a.z_token + 4 * v0, valid, vec);
+        float dt[4], g[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float dt = live ? effective(d.get(e), bias[e], a.dto) : 0.f;
-            float g = dy.get(e);
-            if (r.z != nullptr) {
+            dt[e] = d.get(e) + bias[e];
+            g[e] = dy.get(e);
+        }
+        effective(dt, a.dto);
+        if (r.z != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
                 const float zv = z.get(e);
-                g *= zv * sigmoid(zv);
+                g[e] *= zv * sigmoid(zv);
             }
-            s_q[(idx / K::CV) * K::CC + 4 * v0 + e] = make_float4(dt, dt * x.get(e), g, 0.f);
-            dsum[e] += dt;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dt[e] = live ? dt[e] : 0.f;
+            s_q[(idx / K::CV) * K::CC + 4 * v0 + e] = make_float4(dt[e], dt[e] * x.get(e), g[e], 0.f);
+            dsum[e] += dt[e];
         }
     }
     float4 *s_B = reinterpret_cast<float4*>(sm + K::OFF_B), *s_C = reinterpret_cast<float4*>(sm + K::OFF_C);

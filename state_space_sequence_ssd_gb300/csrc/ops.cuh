@@ -79,13 +79,10 @@ __device__ __forceinline__ f32x2 exp2_2(f32x2 v) {
     unpk(v, lo, hi);
     return pk(exp2_fast(lo), exp2_fast(hi));
 }
-__device__ __forceinline__ f32x2 rcp_2(f32x2 v) {
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {  // constants: one in a scalar instruction, two moves in a packed one
     float lo, hi;
     unpk(v, lo, hi);
-    return pk(rcp_fast(lo), rcp_fast(hi));
-}
-__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
-    return rcp_2(add2(pk(1.f, 1.f), exp2_2(mul2(v, pk(-kLog2e, -kLog2e)))));
+    return pk(sigmoid(lo), sigmoid(hi));
 }
 
 // V consecutive elements as they lie in memory.  They stay packed words until get() unpacks one: a load whose halves
@@ -260,10 +257,16 @@ struct SelectiveArgs {
     const int* lengths;
     DtOpts dto;
 };
-// Chunks that the forward pass splits the sequence into (1: no split), and the float32 workspace it needs.
-int selective_chunks(const SelectiveArgs& a, int sms);
-size_t selective_workspace(const SelectiveArgs& a, int chunks);
-int launch_selective_forward(const SelectiveArgs& a, int chunks, void* y, float* final_state, float* ws, cudaStream_t s);
+// How the forward pass runs: the width of its lanes, the chunks that the sequence is split into (1: no split); and the
+// workspace in bytes that this takes.
+struct SelectivePlan {
+    bool wide;
+    int chunks;
+};
+SelectivePlan selective_plan(const SelectiveArgs& a, int sms);
+size_t selective_workspace(const SelectiveArgs& a, const SelectivePlan& p);
+int launch_selective_forward(const SelectiveArgs& a, const SelectivePlan& p, void* y, float* final_state, float* ws,
+                             cudaStream_t s);
 
 struct SelectiveGrads {
     const void* dy;       // dense

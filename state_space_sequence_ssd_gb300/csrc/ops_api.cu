@@ -162,11 +162,11 @@ int ssd_selective_forward(int dtype, const void* x, const void* dt, const float*
                            options, &a);
     if (r != SSD_OK) return r;
     if (!y || !on(y, size_of(dtype)) || !on(final_state, 4)) return SSD_ERR_INVALID_ARG;
-    const int chunks = selective_chunks(a, multiprocessors());
-    const size_t bytes = selective_workspace(a, chunks);
+    const SelectivePlan plan = selective_plan(a, multiprocessors());
+    const size_t bytes = selective_workspace(a, plan);
     void* ws = nullptr;
     if (bytes > 0 && take_workspace(&ws, bytes, stream) != SSD_OK) return SSD_ERR_NO_MEMORY;
-    r = launch_selective_forward(a, chunks, y, final_state, static_cast<float*>(ws), stream);
+    r = launch_selective_forward(a, plan, y, final_state, static_cast<float*>(ws), stream);
     return give_back(ws, stream, r);
 }
 

@@ -8,7 +8,8 @@ namespace ssd {
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1].  log1p(e) / e is fitted on [0, 1] by a polynomial
 // of degree 8 through the Chebyshev expansion (largest relative error 1.5e-7 with its float32 evaluation), so the
-// result stays relatively exact where e is small, as a logarithm of 1 + e would not.
+// result stays relatively exact where e is small, as a logarithm of 1 + e would not.  (Not in packed arithmetic: its
+// constants would each take two moves, where a scalar instruction holds one.)
 __device__ __forceinline__ float softplus(float v) {
     const float e = exp2_fast(-fabsf(v) * kLog2e);
     float p = 0.005253457929939032f;
@@ -23,36 +24,41 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(p, e, fmaxf(v, 0.f));
 }
 
-// The effective dt of one channel: bias (already looked up), softplus, limits.
-__device__ __forceinline__ float effective(float v, float bias, const DtOpts& o) {
-    v += bias;
-    if (o.softplus) v = softplus(v);
-    if (o.limit) v = fminf(fmaxf(v, o.lo), o.hi);
-    return v;
+// The effective dt of M values of raw dt with their bias added: softplus, limits.  The options are looked at once for
+// all of them: a branch within each value's chain of dependent instructions would run the chains one after another.
+template <int M>
+__device__ __forceinline__ void effective(float (&v)[M], const DtOpts& o) {
+    if (o.softplus) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = softplus(v[i]);
+    }
+    if (o.limit) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = fminf(fmaxf(v[i], o.lo), o.hi);
+    }
 }
 
-// Sums R values each over the lanes of a group (lane offsets OFF, OFF / 2, ..., 1): while a lane holds several
-// values it keeps one half and trades the other with its partner.  The lane ends up with the full sum of one value,
-// whose index is added to `which`.
-template <int R, int OFF>
-__device__ __forceinline__ float fold_lanes(const float (&v)[R], int lane, int& which) {
-    if constexpr (R == 1) {
-        float t = v[0];
+// Sums R values over the lanes at offsets OFF, OFF / 2, ..., MIN.  While a lane holds several values it keeps one half
+// and trades the other with its partner, so that R values cost about R shuffles.  The lane keeps the sums number
+// which .. which + (values left) - 1, in v[0 ..].
+template <int R, int OFF, int MIN>
+__device__ __forceinline__ void fold_between(float* v, int lane, int& which) {
+    if constexpr (OFF >= MIN) {
+        if constexpr (R > 1) {
+            constexpr int HALF = R / 2;
+            const bool up = (lane & OFF) != 0;
 #pragma unroll
-        for (int o = OFF; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        return t;
-    } else {
-        constexpr int HALF = R / 2;
-        const bool up = (lane & OFF) != 0;
-        float w[HALF];
-#pragma unroll
-        for (int j = 0; j < HALF; ++j) {
-            const float mine = up ? v[j + HALF] : v[j];
-            const float other = up ? v[j] : v[j + HALF];
-            w[j] = mine + __shfl_xor_sync(0xffffffffu, other, OFF);
+            for (int j = 0; j < HALF; ++j) {
+                const float mine = up ? v[j + HALF] : v[j];
+                const float other = up ? v[j] : v[j + HALF];
+                v[j] = mine + __shfl_xor_sync(0xffffffffu, other, OFF);
+            }
+            if (up) which += HALF;
+            fold_between<HALF, OFF / 2, MIN>(v, lane, which);
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], OFF);
+            fold_between<1, OFF / 2, MIN>(v, lane, which);
         }
-        if (up) which += HALF;
-        return fold_lanes<HALF, OFF / 2>(w, lane, which);
     }
 }
 
@@ -65,17 +71,45 @@ inline int selective_lanes(int dstate) {
 
 inline bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// Whether the token rows of x, dt, z (and a dense output) can be read in vectors of four channels, and B and C in
-// vectors of four entries.
+// Whether the token rows of x, dt, z (and of dense tensors of the same shape) are whole vectors of V channels, and
+// those of B and C whole vectors of V entries.
+inline bool rows_of(const SelectiveArgs& a, int V, const void* out1, const void* out2, size_t size) {
+    return a.channels / a.ngroups % V == 0 && a.x_batch % V == 0 && a.x_token % V == 0 && a.dt_batch % V == 0 &&
+           a.dt_token % V == 0 && (a.z == nullptr || (a.z_batch % V == 0 && a.z_token % V == 0)) &&
+           aligned_to(a.x, V * size) && aligned_to(a.dt, V * size) && aligned_to(a.z, V * size) &&
+           aligned_to(out1, V * size) && aligned_to(out2, V * size);
+}
+inline bool states_of(const SelectiveArgs& a, int V, size_t size) {
+    return a.dstate % V == 0 && a.B_batch % V == 0 && a.B_token % V == 0 && a.C_batch % V == 0 && a.C_token % V == 0 &&
+           aligned_to(a.B, V * size) && aligned_to(a.C, V * size);
+}
 inline bool rows_of_four(const SelectiveArgs& a, const void* out1, const void* out2, size_t size) {
-    return a.channels / a.ngroups % 4 == 0 && a.x_batch % 4 == 0 && a.x_token % 4 == 0 && a.dt_batch % 4 == 0 &&
-           a.dt_token % 4 == 0 && (a.z == nullptr || (a.z_batch % 4 == 0 && a.z_token % 4 == 0)) &&
-           aligned_to(a.x, 4 * size) && aligned_to(a.dt, 4 * size) && aligned_to(a.z, 4 * size) &&
-           aligned_to(out1, 4 * size) && aligned_to(out2, 4 * size);
+    return rows_of(a, 4, out1, out2, size);
 }
-inline bool states_of_four(const SelectiveArgs& a, size_t size) {
-    return a.dstate % 4 == 0 && a.B_batch % 4 == 0 && a.B_token % 4 == 0 && a.C_batch % 4 == 0 && a.C_token % 4 == 0 &&
-           aligned_to(a.B, 4 * size) && aligned_to(a.C, 4 * size);
+inline bool states_of_four(const SelectiveArgs& a, size_t size) { return states_of(a, 4, size); }
+
+// Sixteen bytes from global to shared memory without a register between; zeros where `live` is false.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool live) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+    const int bytes = live ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// How the forward pass runs: with wide lanes (four channels of eight entries) or narrow ones (two of four), the lanes
+// that share a channel, threads of a block and its channels.
+struct SelectiveShape {
+    bool wide;
+    int lp, threads, cc;
+};
+SelectiveShape selective_shape(const SelectiveArgs& a, bool wide);
+int launch_selective_hop(const SelectiveArgs& a, int nchunks, float* hops, const float* dtsum, cudaStream_t s);
+int selective_forward_bf16(const SelectiveArgs& a, const SelectivePlan& p, void* y, float* final_state, float* ws, cudaStream_t s);
+int selective_forward_f16(const SelectiveArgs& a, const SelectivePlan& p, void* y, float* final_state, float* ws, cudaStream_t s);
+int selective_forward_f32(const SelectiveArgs& a, const SelectivePlan& p, void* y, float* final_state, float* ws, cudaStream_t s);
 
 }  // namespace ssd
