@@ -455,7 +455,7 @@ SSD_API int ssd_step_ex(const void* x, const float* dt, const float* A, const vo
  *  * Outputs may not overlap inputs, except the states updated in place.
  *  * Workspaces come stream-ordered from the library's pool, as in
  *    ssd_forward.  Deterministic: no atomics, sums in a fixed order.
- *  * Limits: batch <= 65535, seqlen <= 4194240, channels and width <= 2^20
+ *  * Limits: batch <= 65535, seqlen <= 2097120, channels and width <= 2^20
  *    (SSD_ERR_UNSUPPORTED beyond).
  */
 

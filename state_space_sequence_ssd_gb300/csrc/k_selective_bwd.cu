@@ -12,48 +12,54 @@
 // states are recomputed in runs of kRun tokens from a checkpoint at each run's start, since only the decay, not its
 // inverse, is stable.  No atomics: sums over channels and blocks are written as rows of partial sums and added in a
 // fixed order.
+//
+// A lane holds four state entries of four neighbouring channels and LP lanes share a channel: shared memory returns 128
+// bytes a clock to the registers, broadcast or not, and with one channel a lane the operands of an entry (32 bytes over
+// the passes) took 32 clocks where the arithmetic takes 20.  The sums over channels, dB and dC, are formed over a lane's
+// four first, so that the exchange between lanes carries a quarter.  The packed pairs are two channels.
 #include "selective.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kBlock = 64;  // tokens of a block
-constexpr int kRun = 8;     // tokens whose states are held in registers
+constexpr int kBlock = 32;  // tokens of a block
+constexpr int kRun = 8;     // tokens between checkpoints
+constexpr int kHeld = 4;    // tokens whose states and decays are in registers
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int LP>
 struct Blk {
-    static constexpr int CW = 32 / LP, CC = kWarps * CW, N4 = 4 * LP, CV = CC / 4;
-    static constexpr int XI = (kBlock * CV + kThreads - 1) / kThreads;
-    // shared memory, in floats
-    static constexpr int OFF_B = 4 * kBlock * CC;                 // (dt, dt x, g, -) per token and channel, then B
-    static constexpr int OFF_C = OFF_B + kBlock * N4;
-    static constexpr int OFF_SB = OFF_C + kBlock * N4;            // sum_n lam B, sum_n A a h lam, y per token and channel
-    static constexpr int OFF_CK = OFF_SB + 3 * kBlock * CC;       // checkpoints, four floats per thread and run
-    static constexpr int OFF_RED = OFF_CK + 4 * kThreads * (kBlock / kRun);
-    static constexpr int FLOATS = OFF_RED + kWarps * kRun * 2 * N4;
+    static constexpr int CW = 32 / LP, NP = 4 * LP;  // lanes' groups of four channels in a warp; entries, padded
+    static constexpr int CONV = LP;                  // tokens that the block's threads convert at once
+    static constexpr int CONVS = (kBlock + CONV - 1) / CONV;
+    static constexpr int channels(int threads) { return 4 * threads / LP; }
+    // shared memory in floats: dt, dt x (later sum lam B), g (later sum A a h lam), y per token and channel; B, C; the
+    // warps' parts of dB and dC of a run; checkpoints, sixteen floats per thread and run
+    static constexpr int floats(int threads) {
+        return 4 * kBlock * channels(threads) + 2 * kBlock * NP + threads / 32 * kRun * 2 * NP + 16 * threads * (kBlock / kRun);
+    }
+    static constexpr int floats_terms(int threads) { return 3 * kBlock * channels(threads) + 2 * kBlock * NP; }
 };
 
 template <typename T>
-struct Row {  // where a block's tokens and channels are
+struct Rows {  // where a block's tokens and channels are
     const T *x, *dt, *z, *B, *C, *dy;
-    int b, grp, c0, nc, tb, te, len;  // c0: first channel; nc: channels of this block; tokens tb .. te - 1
+    int b, grp, tile, tiles, c0, nc, tb, te, last;  // c0: first channel, of nc; tokens tb .. te - 1, live ones before last
 };
 
-template <typename T, int LP>
-__device__ __forceinline__ Row<T> row_of(const SelectiveArgs& a, const void* dy) {
-    using K = Blk<LP>;
-    Row<T> r;
-    const int per = a.channels / a.ngroups, tiles = (per + K::CC - 1) / K::CC;
-    r.grp = blockIdx.x / tiles;
-    const int cb = (blockIdx.x % tiles) * K::CC;
-    r.c0 = r.grp * per + cb;
-    r.nc = min(K::CC, per - cb);
+template <typename T>
+__device__ __forceinline__ Rows<T> rows_at(const SelectiveArgs& a, const void* dy, int cc) {
+    Rows<T> r;
+    const int per = a.channels / a.ngroups;
+    r.tiles = (per + cc - 1) / cc;
+    r.grp = blockIdx.x / r.tiles;
+    r.tile = blockIdx.x % r.tiles;
+    r.c0 = r.grp * per + r.tile * cc;
+    r.nc = min(cc, per - r.tile * cc);
     r.b = blockIdx.z;
     r.tb = blockIdx.y * kBlock;
     r.te = min(r.tb + kBlock, a.seqlen);
-    r.len = row_length(a.lengths, r.b, a.seqlen);
+    r.last = min(r.te, row_length(a.lengths, r.b, a.seqlen));
     r.x = static_cast<const T*>(a.x) + r.b * a.x_batch + r.c0;
     r.dt = static_cast<const T*>(a.dt) + r.b * a.dt_batch + r.c0;
     r.z = a.z == nullptr ? nullptr : static_cast<const T*>(a.z) + r.b * a.z_batch + r.c0;
@@ -63,122 +69,185 @@ __device__ __forceinline__ Row<T> row_of(const SelectiveArgs& a, const void* dy)
     return r;
 }
 
-// The block's tokens into shared memory: (dt, dt x, g, -) per token and channel, B and C as float32; zero past the
-// length.  Returns this thread's sums of dt over its tokens, per channel of its vector.
+// Four tokens' vectors of x, dt, dy and z of a thread (tokens t0 + i CONV, channels 4 v0 ..), zeros where they are not
+// live, and their dt with its bias and dLoss/d(ungated y).
+template <typename T, int M>
+struct Loaded {
+    Vec<T, 4> x[M], d[M], dy[M], z[M];
+};
+template <typename T, int M, int CONV>
+__device__ __forceinline__ Loaded<T, M> load_rows(const SelectiveArgs& a, const Rows<T>& r, int t0, int v0, bool vec) {
+    Loaded<T, M> l;
+    const int vc = r.nc - 4 * v0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const int t = t0 + i * CONV, valid = t < r.last ? vc : 0;
+        l.x[i] = load_vec<T, 4>(r.x + t * a.x_token + 4 * v0, valid, vec);
+        l.d[i] = load_vec<T, 4>(r.dt + t * a.dt_token + 4 * v0, valid, vec);
+        l.dy[i] = load_vec<T, 4>(r.dy + (int64_t)t * a.channels + 4 * v0, valid, vec);
+        l.z[i] = r.z != nullptr ? load_vec<T, 4>(r.z + t * a.z_token + 4 * v0, valid, vec) : Vec<T, 4>::zero();
+    }
+    return l;
+}
+
+// The block's tokens into shared memory: dt, dt x and g per token and channel, B and C as float32; zero past the length.
 template <typename T, int LP>
-__device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Row<T>& r, float* sm, bool vec, bool vecb,
-                                            float (&dsum)[4]) {
+__device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T>& r, float* s_d, float* s_x, float* s_g,
+                                            float* s_B, float* s_C, bool vec, bool vecb, float (&dsum)[4]) {
     using K = Blk<LP>;
-    const int tid = threadIdx.x, v0 = tid % K::CV;
-    float4* s_q = reinterpret_cast<float4*>(sm);
+    constexpr int M = K::CONVS < 4 ? K::CONVS : 4;  // vectors side by side
+    const int tid = threadIdx.x, threads = blockDim.x, cc = K::channels(threads);
+    const int v0 = tid % (cc / 4), w0 = tid / (cc / 4);
     float bias[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         bias[e] = (a.dto.bias != nullptr && 4 * v0 + e < r.nc) ? a.dto.bias[r.c0 + 4 * v0 + e] : 0.f;
         dsum[e] = 0.f;
     }
-#pragma unroll 2
-    for (int i = 0; i < K::XI; ++i) {
-        const int idx = tid + i * kThreads, t = r.tb + idx / K::CV;
-        if (idx >= kBlock * K::CV) break;
-        const bool live = t < r.len && t < r.te;
-        const int valid = live ? max(0, r.nc - 4 * v0) : 0;
-        const Vec<T, 4> x = load_vec<T, 4>(r.x + t * a.x_token + 4 * v0, valid, vec);
-        const Vec<T, 4> d = load_vec<T, 4>(r.dt + t * a.dt_token + 4 * v0, valid, vec);
-        const Vec<T, 4> dy = load_vec<T, 4>(r.dy + (int64_t)t * a.channels + 4 * v0, valid, vec);
-        Vec<T, 4> z;
-        if (r.z != nullptr) z = load_vec<T, 4>(r.z + t * a.z_token + 4 * v0, valid, vec);
-        float dt[4], g[4];
+#pragma unroll 1
+    for (int i0 = 0; i0 < K::CONVS; i0 += M) {
+        const int t0 = w0 + i0 * K::CONV;
+        const Loaded<T, M> l = load_rows<T, M, K::CONV>(a, r, r.tb + t0, v0, vec);
+        float dt[4 * M], g[4 * M];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            dt[e] = d.get(e) + bias[e];
-            g[e] = dy.get(e);
-        }
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dt[4 * i + e] = l.d[i].get(e) + bias[e];
+                g[4 * i + e] = l.dy[i].get(e);
+            }
         effective(dt, a.dto);
         if (r.z != nullptr) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float zv = z.get(e);
-                g[e] *= zv * sigmoid(zv);
-            }
+            for (int i = 0; i < M; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float zv = l.z[i].get(e);
+                    g[4 * i + e] *= zv * sigmoid(zv);
+                }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            dt[e] = live ? dt[e] : 0.f;
-            s_q[(idx / K::CV) * K::CC + 4 * v0 + e] = make_float4(dt[e], dt[e] * x.get(e), g[e], 0.f);
-            dsum[e] += dt[e];
+        for (int i = 0; i < M; ++i) {
+            const int t = t0 + i * K::CONV, at = t * cc + 4 * v0;
+            const bool live = r.tb + t < r.last;
+            float dx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dt[4 * i + e] = live ? dt[4 * i + e] : 0.f;
+                dx[e] = dt[4 * i + e] * l.x[i].get(e);
+                dsum[e] += dt[4 * i + e];
+            }
+            if (K::CONV * K::CONVS == kBlock || t < kBlock) {
+                *reinterpret_cast<float4*>(s_d + at) = make_float4(dt[4 * i], dt[4 * i + 1], dt[4 * i + 2], dt[4 * i + 3]);
+                *reinterpret_cast<float4*>(s_x + at) = make_float4(dx[0], dx[1], dx[2], dx[3]);
+                *reinterpret_cast<float4*>(s_g + at) = make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
+            }
         }
     }
-    float4 *s_B = reinterpret_cast<float4*>(sm + K::OFF_B), *s_C = reinterpret_cast<float4*>(sm + K::OFF_C);
-    for (int idx = tid; idx < kBlock * LP; idx += kThreads) {
-        const int t = r.tb + idx / LP, n = 4 * (idx % LP);
-        const int valid = (t < r.len && t < r.te) ? max(0, a.dstate - n) : 0;
-        const Vec<T, 4> B = load_vec<T, 4>(r.B + t * a.B_token + n, valid, vecb);
-        const Vec<T, 4> C = load_vec<T, 4>(r.C + t * a.C_token + n, valid, vecb);
-        s_B[idx] = make_float4(B.get(0), B.get(1), B.get(2), B.get(3));
-        s_C[idx] = make_float4(C.get(0), C.get(1), C.get(2), C.get(3));
+#pragma unroll 2
+    for (int i = tid; i < kBlock * LP; i += threads) {
+        const int t = r.tb + i / LP, e = 4 * (i % LP), valid = t < r.last ? a.dstate - e : 0;
+        const Vec<T, 4> B = load_vec<T, 4>(r.B + t * a.B_token + e, valid, vecb);
+        const Vec<T, 4> C = load_vec<T, 4>(r.C + t * a.C_token + e, valid, vecb);
+        *reinterpret_cast<float4*>(s_B + 4 * i) = make_float4(B.get(0), B.get(1), B.get(2), B.get(3));
+        *reinterpret_cast<float4*>(s_C + 4 * i) = make_float4(C.get(0), C.get(1), C.get(2), C.get(3));
     }
 }
 
-__device__ __forceinline__ void read4(const float* p, int valid, f32x2& lo, f32x2& hi, float scale = 1.f) {
-    const Vec<float, 4> v = load_vec<float, 4, true>(p, valid, false);
-    lo = pk(v.get(0) * scale, v.get(1) * scale);
-    hi = pk(v.get(2) * scale, v.get(3) * scale);
+// A lane's four entries of four channels, as pairs of channels, from and to (channels, dstate) float32.
+using Entries = f32x2[4][2];
+__device__ __forceinline__ void read_entries(const float* p, int64_t c, int channels, int N, int e, float scale, Entries& o) {
+    const bool four = N % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    Vec<float, 4> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = load_vec<float, 4, true>(p + (c + i) * N + e, i < channels ? N - e : 0, four);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[i][0] = pk(v[0].get(i) * scale, v[1].get(i) * scale);
+        o[i][1] = pk(v[2].get(i) * scale, v[3].get(i) * scale);
+    }
 }
-__device__ __forceinline__ void write4(float* p, int valid, f32x2 lo, f32x2 hi) {
-    float v[4];
-    unpk(lo, v[0], v[1]);
-    unpk(hi, v[2], v[3]);
-    store_vec<float, 4>(p, Vec<float, 4>::of(v), valid, false);
+__device__ __forceinline__ void write_entries(float* p, int64_t c, int channels, int N, int e, const Entries& v) {
+    const bool four = N % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    float o[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        unpk(v[i][0], o[0][i], o[1][i]);
+        unpk(v[i][1], o[2][i], o[3][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        store_vec<float, 4>(p + (c + i) * N + e, Vec<float, 4>::of(o[i]), i < channels ? N - e : 0, four);
+}
+__device__ __forceinline__ void pairs_of(const float* p, f32x2 (&o)[2]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    o[0] = pk(v.x, v.y);
+    o[1] = pk(v.z, v.w);
+}
+__device__ __forceinline__ void twice_of(const float* p, f32x2 (&o)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    o[0] = pk(v.x, v.x);
+    o[1] = pk(v.y, v.y);
+    o[2] = pk(v.z, v.z);
+    o[3] = pk(v.w, v.w);
 }
 
 // Every block's own end state (from zero) into hops[k + 1], its own gradient at its start into mus[k - 1] (block 0's
 // into `nu0`), and its sum of dt.
 template <typename T, int LP>
-__global__ void __launch_bounds__(kThreads) selective_terms_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
-                                                                   float* __restrict__ hops, float* __restrict__ mus,
-                                                                   float* __restrict__ nu0, float* __restrict__ dtsum,
-                                                                   bool vec, bool vecb) {
+__global__ void __launch_bounds__(128, 3) selective_terms_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
+                                                                 float* __restrict__ hops, float* __restrict__ mus,
+                                                                 float* __restrict__ nu0, float* __restrict__ dtsum,
+                                                                 bool vec, bool vecb) {
     using K = Blk<LP>;
     extern __shared__ __align__(16) float sm[];
-    const Row<T> r = row_of<T, LP>(a, dy);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.dstate, k = blockIdx.y;
-    const int cl = warp * K::CW + lane / LP, q = lane % LP;
-    const bool mine = cl < r.nc;
-    const int nvalid = mine ? max(0, min(4, N - 4 * q)) : 0;
-    const int64_t at = (mine ? (int64_t)(r.c0 + cl) : 0) * N + 4 * q, n = (int64_t)a.channels * N;
+    const int tid = threadIdx.x, threads = blockDim.x, cc = K::channels(threads), N = a.dstate, k = blockIdx.y;
+    const Rows<T> r = rows_at<T>(a, dy, cc);
+    const int qd = tid / LP, q = tid % LP, mine = r.nc - 4 * qd;
+    const int64_t c = r.c0 + 4 * qd, n = (int64_t)a.channels * N;
+    float *s_d = sm, *s_x = s_d + kBlock * cc, *s_g = s_x + kBlock * cc, *s_B = s_g + kBlock * cc, *s_C = s_B + kBlock * K::NP;
     float dsum[4];
-    stage_block<T, LP>(a, r, sm, vec, vecb, dsum);
-    f32x2 A01, A23, h01 = 0ull, h23 = 0ull, v01 = 0ull, v23 = 0ull, p01 = pk(1.f, 1.f), p23 = p01;
-    read4(a.A + at, nvalid, A01, A23, kLog2e);
+    stage_block<T, LP>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, dsum);
+    Entries A, h, v, p;
+    read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            h[e][j] = v[e][j] = 0ull;
+            p[e][j] = pk(1.f, 1.f);
+        }
     __syncthreads();
-    const float4 *s_q = reinterpret_cast<const float4*>(sm) + cl, *s_B = reinterpret_cast<const float4*>(sm + K::OFF_B) + q,
-                 *s_C = reinterpret_cast<const float4*>(sm + K::OFF_C) + q;
-    const int steps = min(r.te, r.len) - r.tb;
-#pragma unroll 4
+    const int steps = r.last - r.tb;
+#pragma unroll 2
     for (int t = 0; t < steps; ++t) {
-        const float4 d = s_q[t * K::CC], B = s_B[t * LP], C = s_C[t * LP];
-        const f32x2 dd = pk(d.x, d.x), dx = pk(d.y, d.y), g = pk(d.z, d.z);
-        const f32x2 a01 = exp2_2(mul2(dd, A01)), a23 = exp2_2(mul2(dd, A23));
-        h01 = fma2(a01, h01, mul2(dx, pk(B.x, B.y)));
-        h23 = fma2(a23, h23, mul2(dx, pk(B.z, B.w)));
-        p01 = mul2(p01, a01);
-        p23 = mul2(p23, a23);
-        v01 = fma2(p01, mul2(g, pk(C.x, C.y)), v01);
-        v23 = fma2(p23, mul2(g, pk(C.z, C.w)), v23);
+        f32x2 d[2], x[2], g[2], B[4], C[4];
+        pairs_of(s_d + t * cc + 4 * qd, d);
+        pairs_of(s_x + t * cc + 4 * qd, x);
+        pairs_of(s_g + t * cc + 4 * qd, g);
+        twice_of(s_B + t * K::NP + 4 * q, B);
+        twice_of(s_C + t * K::NP + 4 * q, C);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x2 w = exp2_2(mul2(d[j], A[e][j]));
+                h[e][j] = fma2(w, h[e][j], mul2(x[j], B[e]));
+                p[e][j] = mul2(p[e][j], w);
+                v[e][j] = fma2(p[e][j], mul2(g[j], C[e]), v[e][j]);
+            }
     }
     const int64_t row = ((int64_t)r.b * nblocks + k) * n;
-    if (k + 1 < nblocks) write4(hops + row + n + at, nvalid, h01, h23);
-    if (k > 0) write4(mus + row - n + at, nvalid, v01, v23);
-    else write4(nu0 + r.b * n + at, nvalid, v01, v23);
+    if (k + 1 < nblocks) write_entries(hops + row + n, c, mine, N, 4 * q, h);
+    write_entries(k > 0 ? mus + row - n : nu0 + r.b * n, c, mine, N, 4 * q, v);
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sm[(tid / K::CV) * K::CC + 4 * (tid % K::CV) + e] = dsum[e];
+    const int v0 = tid % (cc / 4), w0 = tid / (cc / 4);
+    *reinterpret_cast<float4*>(sm + w0 * cc + 4 * v0) = make_float4(dsum[0], dsum[1], dsum[2], dsum[3]);
     __syncthreads();
-    for (int c = tid; c < r.nc; c += kThreads) {
+    for (int i = tid; i < r.nc; i += threads) {
         float s = 0.f;
-        for (int i = 0; i < kThreads / K::CV; ++i) s += sm[i * K::CC + c];
-        dtsum[((int64_t)r.b * nblocks + k) * a.channels + r.c0 + c] = s;
+        for (int w = 0; w < K::CONV; ++w) s += sm[w * cc + i];
+        dtsum[((int64_t)r.b * nblocks + k) * a.channels + r.c0 + i] = s;
     }
 }
 
@@ -194,218 +263,281 @@ __global__ void __launch_bounds__(256) selective_hops_kernel(const float* __rest
     if (i >= n) return;
     const float A2 = A[i] * kLog2e;
     const float* dp = dtsum + (int64_t)b * nblocks * channels + i / dstate;
-    if (blockIdx.z == 0) {
-        float* hp = hops + b * n * nblocks + i;
-        float h = init != nullptr ? init[b * n + i] : 0.f;
-        hp[0] = h;
-#pragma unroll 4
-        for (int k = 0; k + 1 < nblocks; ++k) {
-            h = fmaf(exp2_fast(A2 * dp[(int64_t)k * channels]), h, hp[(k + 1) * n]);
-            hp[(k + 1) * n] = h;
-        }
-    } else {
-        float* mp = mus + b * n * nblocks + i;
-        float m = dfinal != nullptr ? dfinal[b * n + i] : 0.f;
-        mp[(nblocks - 1) * n] = m;
-#pragma unroll 4
-        for (int k = nblocks - 1; k > 0; --k) {
-            m = fmaf(exp2_fast(A2 * dp[(int64_t)k * channels]), m, mp[(k - 1) * n]);
-            mp[(k - 1) * n] = m;
-        }
-        if (dinit != nullptr) dinit[b * n + i] = fmaf(exp2_fast(A2 * dp[0]), m, nu0[b * n + i]);
+    const bool back = blockIdx.z != 0;
+    float* at = (back ? mus : hops) + b * n * nblocks + (back ? (nblocks - 1) * n : 0) + i;
+    const int64_t step = back ? -n : n, dstep = back ? -channels : channels;
+    if (back) dp += (int64_t)(nblocks - 1) * channels;
+    const float* start = back ? dfinal : init;
+    float s = start != nullptr ? start[b * n + i] : 0.f;
+    // the terms of the next blocks are loaded ahead: only the sum waits for the block before
+    constexpr int AHEAD = 8;
+    *at = s;
+    for (int k = 0; k + 1 < nblocks; k += AHEAD) {
+        float term[AHEAD], sum[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (k + u + 1 < nblocks) {
+                term[u] = at[(u + 1) * step];
+                sum[u] = __ldg(dp + u * dstep);
+            }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (k + u + 1 < nblocks) {
+                s = fmaf(exp2_fast(A2 * sum[u]), s, term[u]);
+                at[(u + 1) * step] = s;
+            }
+        at += AHEAD * step;
+        dp += AHEAD * dstep;
     }
+    if (back && dinit != nullptr)
+        dinit[b * n + i] = fmaf(exp2_fast(A2 * dtsum[(int64_t)b * nblocks * channels + i / dstate]), s, nu0[b * n + i]);
 }
 
 template <typename T, int LP>
-__global__ void __launch_bounds__(kThreads) selective_block_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
-                                                                   float* __restrict__ hops, const float* __restrict__ mus,
-                                                                   T* __restrict__ dx, T* __restrict__ ddt,
-                                                                   T* __restrict__ dz, float* __restrict__ dbc,
-                                                                   float* __restrict__ chan, bool vec, bool vecb) {
+__global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
+                                                                 float* __restrict__ hops, const float* __restrict__ mus,
+                                                                 T* __restrict__ dx, T* __restrict__ ddt,
+                                                                 T* __restrict__ dz, float* __restrict__ dbc,
+                                                                 float* __restrict__ chan, bool vec, bool vecb) {
     using K = Blk<LP>;
+    constexpr int NP = K::NP;
     extern __shared__ __align__(16) float sm[];
-    const Row<T> r = row_of<T, LP>(a, dy);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.dstate, k = blockIdx.y;
-    const int cl = warp * K::CW + lane / LP, q = lane % LP;
-    const bool mine = cl < r.nc;
-    const int nvalid = mine ? max(0, min(4, N - 4 * q)) : 0;
-    const int64_t at = (mine ? (int64_t)(r.c0 + cl) : 0) * N + 4 * q, n = (int64_t)a.channels * N;
-    const int64_t row = ((int64_t)r.b * nblocks + k) * n;
-    float unused[4];
-    stage_block<T, LP>(a, r, sm, vec, vecb, unused);
-    f32x2 A01, A23, h01, h23, m01, m23, dA01 = 0ull, dA23 = 0ull;
-    read4(a.A + at, nvalid, A01, A23, kLog2e);
-    read4(hops + row + at, nvalid, h01, h23);
-    read4(mus + row + at, nvalid, m01, m23);
-    __syncthreads();
-    const float4 *s_q = reinterpret_cast<const float4*>(sm) + cl, *s_B = reinterpret_cast<const float4*>(sm + K::OFF_B) + q,
-                 *s_C = reinterpret_cast<const float4*>(sm + K::OFF_C) + q;
-    float *s_sb = sm + K::OFF_SB, *s_sa = s_sb + kBlock * K::CC, *s_y = s_sa + kBlock * K::CC;
-    ulonglong2* ck = reinterpret_cast<ulonglong2*>(sm + K::OFF_CK) + tid;
-    float* s_red = sm + K::OFF_RED;
-    const int steps = max(0, min(r.te, r.len) - r.tb);
-    const int runs = (steps + kRun - 1) / kRun;  // the tokens past the length are zeros: they change nothing
-    // forward: a checkpoint per run
-    for (int j = 0; j < runs; ++j) {
-        ck[j * kThreads] = make_ulonglong2(h01, h23);
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const float4 d = s_q[(j * kRun + i) * K::CC], B = s_B[(j * kRun + i) * LP];
-            const f32x2 dd = pk(d.x, d.x), dtx = pk(d.y, d.y);
-            h01 = fma2(exp2_2(mul2(dd, A01)), h01, mul2(dtx, pk(B.x, B.y)));
-            h23 = fma2(exp2_2(mul2(dd, A23)), h23, mul2(dtx, pk(B.z, B.w)));
-        }
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = threads / 32;
+    const int cc = K::channels(threads), N = a.dstate, k = blockIdx.y;
+    const Rows<T> r = rows_at<T>(a, dy, cc);
+    const int qd = tid / LP, q = tid % LP, mine = r.nc - 4 * qd;
+    const int64_t c = r.c0 + 4 * qd, n = (int64_t)a.channels * N, row = ((int64_t)r.b * nblocks + k) * n;
+    float *s_d = sm, *s_x = s_d + kBlock * cc, *s_g = s_x + kBlock * cc, *s_y = s_g + kBlock * cc, *s_B = s_y + kBlock * cc,
+          *s_C = s_B + kBlock * NP, *s_red = s_C + kBlock * NP;
+    ulonglong2* ck = reinterpret_cast<ulonglong2*>(s_red + warps * kRun * 2 * NP) + tid;
+    {
+        float unused[4];
+        stage_block<T, LP>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, unused);
     }
-    // backward, run by run
-    for (int j = runs - 1; j >= 0; --j) {
-        f32x2 H01[kRun + 1], H23[kRun + 1], a01[kRun], a23[kRun];
-        const ulonglong2 c0 = ck[j * kThreads];
-        H01[0] = c0.x;
-        H23[0] = c0.y;
-        float ys[kRun], sb[kRun], sa[kRun];
+    Entries A, h, m, dA;
+    read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
+    read_entries(hops + row, c, mine, N, 4 * q, 1.f, h);
+    read_entries(mus + row, c, mine, N, 4 * q, 1.f, m);
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const int t = j * kRun + i;
-            const float4 d = s_q[t * K::CC], B = s_B[t * LP], C = s_C[t * LP];
-            const f32x2 dd = pk(d.x, d.x), dtx = pk(d.y, d.y);
-            a01[i] = exp2_2(mul2(dd, A01));
-            a23[i] = exp2_2(mul2(dd, A23));
-            H01[i + 1] = fma2(a01[i], H01[i], mul2(dtx, pk(B.x, B.y)));
-            H23[i + 1] = fma2(a23[i], H23[i], mul2(dtx, pk(B.z, B.w)));
-            ys[i] = sum2(fma2(pk(C.z, C.w), H23[i + 1], mul2(pk(C.x, C.y), H01[i + 1])));
+    for (int e = 0; e < 4; ++e) dA[e][0] = dA[e][1] = 0ull;
+    __syncthreads();
+    const int steps = max(0, r.last - r.tb), runs = (steps + kRun - 1) / kRun;  // tokens past the length change nothing
+
+    auto advance = [&](int t) {  // the states over token t
+        f32x2 d[2], x[2], B[4];
+        pairs_of(s_d + t * cc + 4 * qd, d);
+        pairs_of(s_x + t * cc + 4 * qd, x);
+        twice_of(s_B + t * NP + 4 * q, B);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) h[e][j] = fma2(exp2_2(mul2(d[j], A[e][j])), h[e][j], mul2(x[j], B[e]));
+    };
+    // a channel's sums over its lanes, to the token's row: each lane ends with one (or several) of its four channels
+    auto join = [&](f32x2 lo, f32x2 hi, float* to) {
+        float v[4];
+        unpk(lo, v[0], v[1]);
+        unpk(hi, v[2], v[3]);
+        int which = 0;
+        fold_between<4, LP / 2, 1>(v, lane, which);
+        if (LP <= 4 || (q & (LP / 4 > 0 ? LP / 4 - 1 : 0)) == 0) {
+#pragma unroll
+            for (int e = 0; e < (LP >= 4 ? 1 : 4 / LP); ++e) to[4 * qd + which + e] = v[e];
+        }
+    };
+    // tokens t0 .. t0 + 3 from the states before them: forward with y and dC, then backward with the rest
+    auto half = [&](int t0) {
+        f32x2 w[kHeld][4][2], wh[kHeld][4][2];  // the decays, and the decayed states
+        float dC[kHeld][4];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int t = t0 + i;
+            f32x2 d[2], x[2], g[2], B[4], C[4], y[2];
+            pairs_of(s_d + t * cc + 4 * qd, d);
+            pairs_of(s_x + t * cc + 4 * qd, x);
+            pairs_of(s_g + t * cc + 4 * qd, g);
+            twice_of(s_B + t * NP + 4 * q, B);
+            twice_of(s_C + t * NP + 4 * q, C);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    w[i][e][j] = exp2_2(mul2(d[j], A[e][j]));
+                    wh[i][e][j] = mul2(w[i][e][j], h[e][j]);
+                    h[e][j] = fma2(x[j], B[e], wh[i][e][j]);
+                    y[j] = e == 0 ? mul2(C[0], h[0][j]) : fma2(C[e], h[e][j], y[j]);
+                }
+                dC[i][e] = sum2(fma2(h[e][1], g[1], mul2(h[e][0], g[0])));
+            }
+            join(y[0], y[1], s_y + t * cc);
         }
 #pragma unroll
-        for (int i = kRun - 1; i >= 0; --i) {
-            const int t = j * kRun + i;
-            const float4 d = s_q[t * K::CC], B = s_B[t * LP], C = s_C[t * LP];
-            const f32x2 dd = pk(d.x, d.x), dtx = pk(d.y, d.y), g = pk(d.z, d.z);
-            m01 = fma2(g, pk(C.x, C.y), m01);  // lam
-            m23 = fma2(g, pk(C.z, C.w), m23);
-            sb[i] = sum2(fma2(m23, pk(B.z, B.w), mul2(m01, pk(B.x, B.y))));
+        for (int i = kHeld - 1; i >= 0; --i) {
+            const int t = t0 + i;
+            f32x2 d[2], x[2], g[2], B[4], C[4], sb[2], sa[2];
+            pairs_of(s_d + t * cc + 4 * qd, d);
+            pairs_of(s_x + t * cc + 4 * qd, x);
+            pairs_of(s_g + t * cc + 4 * qd, g);
+            twice_of(s_B + t * NP + 4 * q, B);
+            twice_of(s_C + t * NP + 4 * q, C);
             float v[8];
-            unpk(mul2(m01, dtx), v[0], v[1]);
-            unpk(mul2(m23, dtx), v[2], v[3]);
-            unpk(mul2(H01[i + 1], g), v[4], v[5]);
-            unpk(mul2(H23[i + 1], g), v[6], v[7]);
-            m01 = mul2(m01, a01[i]);
-            m23 = mul2(m23, a23[i]);
-            const f32x2 held01 = mul2(m01, H01[i]), held23 = mul2(m23, H23[i]);
-            dA01 = fma2(held01, dd, dA01);
-            dA23 = fma2(held23, dd, dA23);
-            sa[i] = sum2(fma2(held23, A23, mul2(held01, A01)));
-            // over the warp's channels: dB's four entries, then dC's
-            int which = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f32x2 lam[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    lam[j] = fma2(g[j], C[e], m[e][j]);
+                    sb[j] = e == 0 ? mul2(lam[j], B[0]) : fma2(lam[j], B[e], sb[j]);
+                    m[e][j] = mul2(lam[j], w[i][e][j]);
+                    const f32x2 held = mul2(lam[j], wh[i][e][j]);
+                    dA[e][j] = fma2(held, d[j], dA[e][j]);
+                    sa[j] = e == 0 ? mul2(held, A[0][j]) : fma2(held, A[e][j], sa[j]);
+                }
+                v[e] = sum2(fma2(lam[1], x[1], mul2(lam[0], x[0])));
+                v[4 + e] = dC[i][e];
+            }
+            // every lane of these channels has read the token's dt x and g: they are lanes of one warp
+            join(sb[0], sb[1], s_x + t * cc);
+            join(sa[0], sa[1], s_g + t * cc);
+            int which = 0;  // over the warp's channels: dB's four entries, then dC's
             fold_between<8, 16, LP>(v, lane, which);
             constexpr int LEFT = K::CW >= 8 ? 1 : 8 / K::CW;
-            if ((lane / LP) % (K::CW >= 8 ? K::CW / 8 : 1) == 0) {
+            if (K::CW <= 8 || (lane / LP) % (K::CW / 8 > 0 ? K::CW / 8 : 1) == 0) {
 #pragma unroll
-                for (int e = 0; e < LEFT; ++e) {
-                    const int w = which + e;
-                    s_red[((warp * kRun + i) * 2 + w / 4) * K::N4 + 4 * q + w % 4] = v[e];
-                }
+                for (int e = 0; e < LEFT; ++e)
+                    s_red[((warp * kRun + t % kRun) * 2 + (which + e) / 4) * NP + 4 * q + (which + e) % 4] = v[e];
             }
         }
-        // over the channel's lanes
-        {
-            int w = 0;
-            fold_between<kRun, LP / 2, 1>(ys, lane, w);
-            int w2 = 0;
-            fold_between<kRun, LP / 2, 1>(sb, lane, w2);
-            w2 = 0;
-            fold_between<kRun, LP / 2, 1>(sa, lane, w2);
-            constexpr int LEFT = LP >= kRun ? 1 : kRun / LP;
-            if (q % (LP >= kRun ? LP / kRun : 1) == 0) {
+    };
+
+    // forward: a checkpoint before every run
+    for (int j = 0; j < runs; ++j) {
 #pragma unroll
-                for (int e = 0; e < LEFT; ++e) {
-                    const int at2 = (j * kRun + w + e) * K::CC + cl;
-                    s_y[at2] = ys[e];
-                    s_sb[at2] = sb[e];
-                    s_sa[at2] = sa[e];
-                }
+        for (int e = 0; e < 4; ++e) ck[(4 * j + e) * threads] = make_ulonglong2(h[e][0], h[e][1]);
+        if (j + 1 < runs) {
+#pragma unroll 2
+            for (int i = 0; i < kRun; ++i) advance(j * kRun + i);
+        }
+    }
+    auto restore = [&](int j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const ulonglong2 v = ck[(4 * j + e) * threads];
+            h[e][0] = v.x;
+            h[e][1] = v.y;
+        }
+    };
+    // backward, run by run, its second half first
+    const int64_t place = ((int64_t)r.tile * a.batch + r.b) * a.seqlen;  // dbc: (tiles, batch, seqlen, ngroups, 2, dstate)
+    for (int j = runs - 1; j >= 0; --j) {
+#pragma unroll 1
+        for (int s = 1; s >= 0; --s) {
+            restore(j);
+            if (s == 1) {
+#pragma unroll 2
+                for (int i = 0; i < kHeld; ++i) advance(j * kRun + i);
             }
+            half(j * kRun + s * kHeld);
         }
         __syncthreads();
-        for (int i = tid; i < kRun * 2 * N; i += kThreads) {
+        for (int i = tid; i < kRun * 2 * N; i += threads) {
             const int tt = i / (2 * N), which = (i / N) % 2, e = i % N, t = r.tb + j * kRun + tt;
-            if (t >= r.te) continue;
             float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += s_red[((w * kRun + tt) * 2 + which) * K::N4 + e];
-            // dbc: (channel blocks of a group, batch, seqlen, ngroups, 2, dstate)
-            const int per = a.channels / a.ngroups, tiles = (per + K::CC - 1) / K::CC;
-            const int64_t tile = blockIdx.x % tiles;
-            dbc[((((tile * a.batch + r.b) * a.seqlen + t) * a.ngroups + r.grp) * 2 + which) * N + e] = s;
+            for (int w = 0; w < warps; ++w) s += s_red[((w * kRun + tt) * 2 + which) * NP + e];
+            if (t < r.te) dbc[(((place + t) * a.ngroups + r.grp) * 2 + which) * N + e] = s;
         }
         __syncthreads();
     }
     // tokens past the last run have no gradient in B and C
-    for (int i = tid; i < (r.te - r.tb - runs * kRun) * 2 * N; i += kThreads) {
-        const int per = a.channels / a.ngroups, tiles = (per + K::CC - 1) / K::CC;
-        const int64_t tile = blockIdx.x % tiles;
+    for (int i = tid; i < (r.te - r.tb - runs * kRun) * 2 * N; i += threads) {
         const int t = r.tb + runs * kRun + i / (2 * N);
-        dbc[(((tile * a.batch + r.b) * a.seqlen + t) * a.ngroups + r.grp) * 2 * N + i % (2 * N)] = 0.f;
+        dbc[((place + t) * a.ngroups + r.grp) * 2 * N + i % (2 * N)] = 0.f;
     }
-    write4(hops + row + at, nvalid, dA01, dA23);  // this block's part of dA, in place of its start state
+    write_entries(hops + row, c, mine, N, 4 * q, dA);  // this block's part of dA, in place of its start state
     __syncthreads();
+
     // per token and channel
-    const int v0 = tid % K::CV, valid = r.nc - 4 * v0;
-    float dD[4] = {0.f, 0.f, 0.f, 0.f}, dbias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (valid > 0) {
-        for (int i = 0; i < K::XI; ++i) {
-            const int idx = tid + i * kThreads, t = r.tb + idx / K::CV;
-            if (idx >= kBlock * K::CV || t >= r.te) break;
-            const bool live = t < r.len;
-            float ox[4], od[4], oz[4];
-            const int got = live ? valid : 0;
-            const Vec<T, 4> x = load_vec<T, 4>(r.x + t * a.x_token + 4 * v0, got, vec);
-            const Vec<T, 4> d = load_vec<T, 4>(r.dt + t * a.dt_token + 4 * v0, got, vec);
-            const Vec<T, 4> gy = load_vec<T, 4>(r.dy + (int64_t)t * a.channels + 4 * v0, got, vec);
-            Vec<T, 4> z;
-            if (r.z != nullptr) z = load_vec<T, 4>(r.z + t * a.z_token + 4 * v0, got, vec);
+    const int v0 = tid % (cc / 4), w0 = tid / (cc / 4), vc = r.nc - 4 * v0;
+    constexpr int M = K::CONVS < 2 ? K::CONVS : 2;
+    float dD[4] = {0.f, 0.f, 0.f, 0.f}, dbias[4] = {0.f, 0.f, 0.f, 0.f}, bias[4], Dc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        bias[e] = a.dto.bias != nullptr && e < vc ? a.dto.bias[r.c0 + 4 * v0 + e] : 0.f;
+        Dc[e] = a.D != nullptr && e < vc ? a.D[r.c0 + 4 * v0 + e] : 0.f;
+    }
+    const bool gated = r.z != nullptr;
+#pragma unroll 1
+    for (int i0 = 0; i0 < K::CONVS; i0 += M) {
+        const int t0 = w0 + i0 * K::CONV;
+        const Loaded<T, M> l = load_rows<T, M, K::CONV>(a, r, r.tb + t0, v0, vec);
+        float raw[4 * M], slope[4 * M], g[4 * M], fz[4 * M];
+#pragma unroll
+        for (int i = 0; i < M; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float fx = 0.f, fd = 0.f, fz = 0.f;
-                if (live && e < valid) {
-                    const int c = r.c0 + 4 * v0 + e, s = (idx / K::CV) * K::CC + 4 * v0 + e;
-                    const float4 w = reinterpret_cast<const float4*>(sm)[s];  // dt, dt x, g
-                    const float xv = x.get(e), Dc = a.D != nullptr ? a.D[c] : 0.f;
-                    fx = fmaf(w.x, s_sb[s], Dc * w.z);
-                    fd = fmaf(xv, s_sb[s], kLn2 * s_sa[s]);
-                    const float raw = d.get(e) + (a.dto.bias != nullptr ? a.dto.bias[c] : 0.f);
-                    if (a.dto.limit) {
-                        const float soft = a.dto.softplus ? softplus(raw) : raw;
-                        if (!(soft >= a.dto.lo && soft <= a.dto.hi)) fd = 0.f;
-                    }
-                    if (a.dto.softplus) fd *= sigmoid(raw);
-                    dD[e] = fmaf(w.z, xv, dD[e]);
-                    dbias[e] += fd;
-                    if (r.z != nullptr) {
-                        const float zv = z.get(e), sg = sigmoid(zv);
-                        fz = gy.get(e) * fmaf(Dc, xv, s_y[s]) * sg * fmaf(zv, 1.f - sg, 1.f);
-                    }
-                }
-                ox[e] = fx;
-                od[e] = fd;
-                oz[e] = fz;
+                raw[4 * i + e] = l.d[i].get(e) + bias[e];
+                slope[4 * i + e] = 1.f;
+                g[4 * i + e] = l.dy[i].get(e);
+                fz[4 * i + e] = 0.f;
             }
-            const int64_t o = ((int64_t)r.b * a.seqlen + t) * a.channels + r.c0 + 4 * v0;
+        if (a.dto.softplus) {
+#pragma unroll
+            for (int i = 0; i < 4 * M; ++i) slope[i] = sigmoid(raw[i]);
+        }
+        if (a.dto.limit) {
+#pragma unroll
+            for (int i = 0; i < 4 * M; ++i) {
+                const float s = a.dto.softplus ? softplus(raw[i]) : raw[i];
+                slope[i] = (s >= a.dto.lo && s <= a.dto.hi) ? slope[i] : 0.f;
+            }
+        }
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float zv = l.z[i].get(e), sg = sigmoid(zv);
+                    const int t = t0 + i * K::CONV < kBlock ? t0 + i * K::CONV : 0;
+                    fz[4 * i + e] = g[4 * i + e] * fmaf(Dc[e], l.x[i].get(e), s_y[t * cc + 4 * v0 + e]) * sg * fmaf(zv, 1.f - sg, 1.f);
+                    g[4 * i + e] *= zv * sg;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int t = t0 + i * K::CONV;
+            if (K::CONV * K::CONVS != kBlock && t >= kBlock) break;
+            const bool live = r.tb + t < r.last;
+            const float4 d4 = *reinterpret_cast<const float4*>(s_d + t * cc + 4 * v0);
+            const float4 b4 = *reinterpret_cast<const float4*>(s_x + t * cc + 4 * v0);
+            const float4 a4 = *reinterpret_cast<const float4*>(s_g + t * cc + 4 * v0);
+            const float dt[4] = {d4.x, d4.y, d4.z, d4.w}, sb[4] = {b4.x, b4.y, b4.z, b4.w}, sa[4] = {a4.x, a4.y, a4.z, a4.w};
+            float ox[4], od[4], oz[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float xv = l.x[i].get(e);
+                ox[e] = live ? fmaf(dt[e], sb[e], Dc[e] * g[4 * i + e]) : 0.f;
+                od[e] = live ? fmaf(xv, sb[e], kLn2 * sa[e]) * slope[4 * i + e] : 0.f;
+                oz[e] = live ? fz[4 * i + e] : 0.f;
+                dD[e] += live ? g[4 * i + e] * xv : 0.f;
+                dbias[e] += od[e];
+            }
+            const int64_t o = ((int64_t)r.b * a.seqlen + r.tb + t) * a.channels + r.c0 + 4 * v0;
+            const int valid = r.tb + t < r.te ? vc : 0;
             store_vec<T, 4>(dx + o, Vec<T, 4>::of(ox), valid, vec);
             store_vec<T, 4>(ddt + o, Vec<T, 4>::of(od), valid, vec);
-            if (dz != nullptr) store_vec<T, 4>(dz + o, Vec<T, 4>::of(oz), valid, vec);
+            if (gated) store_vec<T, 4>(dz + o, Vec<T, 4>::of(oz), valid, vec);
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        sm[(tid / K::CV) * 2 * K::CC + 4 * v0 + e] = dD[e];
-        sm[(tid / K::CV) * 2 * K::CC + K::CC + 4 * v0 + e] = dbias[e];
-    }
+    float* sums = sm + w0 * 2 * cc + 4 * v0;
+    *reinterpret_cast<float4*>(sums) = make_float4(dD[0], dD[1], dD[2], dD[3]);
+    *reinterpret_cast<float4*>(sums + cc) = make_float4(dbias[0], dbias[1], dbias[2], dbias[3]);
     __syncthreads();
-    for (int i = tid; i < 2 * K::CC; i += kThreads) {
-        if (i % K::CC >= r.nc) continue;
+    for (int i = tid; i < 2 * cc; i += threads) {
+        if (i % cc >= r.nc) continue;
         float s = 0.f;
-        for (int j = 0; j < kThreads / K::CV; ++j) s += sm[j * 2 * K::CC + i];
-        chan[(((int64_t)r.b * nblocks + k) * 2 + i / K::CC) * a.channels + r.c0 + i % K::CC] = s;
+        for (int w = 0; w < K::CONV; ++w) s += sm[w * 2 * cc + i];
+        chan[(((int64_t)r.b * nblocks + k) * 2 + i / cc) * a.channels + r.c0 + i % cc] = s;
     }
 }
 
@@ -455,9 +587,18 @@ struct Parts {
     size_t total() const { return 2 * hops + nu0 + dtsum + chan + dbc; }
 };
 
+// Threads of a block: four warps (two where two lanes share a channel: shared memory), fewer where a group has fewer
+// channels than they cover.
+int block_threads(const SelectiveArgs& a) {
+    const int lp = selective_lanes(a.dstate), per = a.channels / a.ngroups;
+    int threads = lp == 2 ? 64 : 128;
+    while (threads > 32 && 4 * threads / 2 / lp >= per) threads /= 2;
+    return threads;
+}
+
 Parts parts_of(const SelectiveArgs& a) {
     Parts p;
-    const int cc = kWarps * 32 / selective_lanes(a.dstate);
+    const int cc = 4 * block_threads(a) / selective_lanes(a.dstate);
     p.nblocks = ceil_div(a.seqlen, kBlock);
     p.tiles = ceil_div(a.channels / a.ngroups, cc);
     const size_t n = (size_t)a.channels * a.dstate, rows = (size_t)a.batch * p.nblocks;
@@ -479,14 +620,15 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
     const bool vec = rows_of_four(a, g.dx, g.ddt, sizeof(T)) && aligned_to(g.dy, 4 * sizeof(T)) &&
                      aligned_to(g.dz, 4 * sizeof(T)) && a.channels % 4 == 0;
     const bool vecb = states_of_four(a, sizeof(T));
-    const int smem = K::FLOATS * 4;
+    const int threads = block_threads(a), smem = K::floats(threads) * 4, smem_terms = K::floats_terms(threads) * 4;
+    const int most = LP == 2 ? 64 : 128;
     const dim3 grid(a.ngroups * p.tiles, p.nblocks, a.batch);
     const int64_t n = (int64_t)a.channels * a.dstate;
-    int r = ensure_smem_limit(reinterpret_cast<const void*>(selective_terms_kernel<T, LP>), smem);
-    if (r == SSD_OK) r = ensure_smem_limit(reinterpret_cast<const void*>(selective_block_kernel<T, LP>), smem);
+    int r = ensure_smem_limit(reinterpret_cast<const void*>(selective_terms_kernel<T, LP>), K::floats_terms(most) * 4);
+    if (r == SSD_OK) r = ensure_smem_limit(reinterpret_cast<const void*>(selective_block_kernel<T, LP>), K::floats(most) * 4);
     if (r != SSD_OK) return r;
     launch_begin(kKindSelectiveBwd, s);
-    selective_terms_kernel<T, LP><<<grid, kThreads, smem, s>>>(a, dy, p.nblocks, hops, mus, nu0, dtsum, vec, vecb);
+    selective_terms_kernel<T, LP><<<grid, threads, smem_terms, s>>>(a, dy, p.nblocks, hops, mus, nu0, dtsum, vec, vecb);
     r = launch_end(kKindSelectiveBwd, s);
     if (r != SSD_OK) return r;
     launch_begin(kKindSelectiveBwd, s);
@@ -495,7 +637,7 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
     r = launch_end(kKindSelectiveBwd, s);
     if (r != SSD_OK) return r;
     launch_begin(kKindSelectiveBwd, s);
-    selective_block_kernel<T, LP><<<grid, kThreads, smem, s>>>(a, dy, p.nblocks, hops, mus, static_cast<T*>(g.dx),
+    selective_block_kernel<T, LP><<<grid, threads, smem, s>>>(a, dy, p.nblocks, hops, mus, static_cast<T*>(g.dx),
                                                                static_cast<T*>(g.ddt), static_cast<T*>(g.dz), dbc, chan, vec,
                                                                vecb);
     r = launch_end(kKindSelectiveBwd, s);
