@@ -2,7 +2,9 @@
 
 Each csrc/*.cu is compiled to an object in parallel with
 ``nvcc -gencode arch=compute_103a,code=sm_103a`` and linked (static cudart)
-into one shared library with a plain C ABI (include/ssd.h).
+into one shared library with a plain C ABI (include/ssd.h).  Beside it,
+csrc/layer_binding.cpp becomes ssd_layer_binding.so, the Python module that
+marshals the layer operators' calls (host code against torch's headers).
 
     python -m state_space_sequence_ssd_gb300.build [--force] [--verbose-ptxas]
 """
@@ -14,12 +16,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libssd_gb300.so")
+BINDING = os.path.join(BUILD, "ssd_layer_binding.so")
+BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,10 +50,46 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def _binding_stale() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(p) > t for p in (BINDING_SRC, os.path.join(ROOT, "include", "ssd.h")))
+
+
+def _compile_binding() -> str:
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+                os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")]
+    obj = os.path.join(BUILD, "layer_binding.o")
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                        *(f"-I{p}" for p in includes), "-c", BINDING_SRC, "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    tmp = BINDING + f".tmp{os.getpid()}"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-l:libssd_gb300.so", "-Wl,-rpath,$ORIGIN", f"-L{libs}",
+                        "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    if not (force or verbose_ptxas or _stale()):
-        return LIB
+    stale, binding_stale = force or verbose_ptxas or _stale(), force or _binding_stale()
     os.makedirs(BUILD, exist_ok=True)
+    if not stale:
+        if binding_stale:
+            _link_binding(_compile_binding())
+        return LIB
     nvcc = _nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
                     "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -63,8 +104,10 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         return obj, r.stderr
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(os.cpu_count() or 8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)  # host code, beside the kernels
         results = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     if verbose_ptxas:
         for _, log in results:
             if log.strip():
@@ -75,6 +118,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 

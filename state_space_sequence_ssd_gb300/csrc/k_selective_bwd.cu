@@ -31,7 +31,7 @@ template <int LP>
 struct Blk {
     static constexpr int CW = 32 / LP, NP = 4 * LP;  // lanes' groups of four channels in a warp; entries, padded
     static constexpr int CONV = LP;                  // tokens that the block's threads convert at once
-    static constexpr int CONVS = (kBlock + CONV - 1) / CONV;
+    static constexpr int CONVS = kBlock / CONV;
     static constexpr int channels(int threads) { return 4 * threads / LP; }
     // shared memory in floats: dt, dt x (later sum lam B), g (later sum A a h lam), y per token and channel; B, C; the
     // warps' parts of dB and dC of a run; checkpoints, sixteen floats per thread and run
@@ -95,62 +95,77 @@ template <typename T, int LP>
 __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T>& r, float* s_d, float* s_x, float* s_g,
                                             float* s_B, float* s_C, bool vec, bool vecb, float (&dsum)[4]) {
     using K = Blk<LP>;
-    constexpr int M = K::CONVS < 4 ? K::CONVS : 4;  // vectors side by side
+    constexpr int M = K::CONVS < 8 ? K::CONVS : 8;
     const int tid = threadIdx.x, threads = blockDim.x, cc = K::channels(threads);
     const int v0 = tid % (cc / 4), w0 = tid / (cc / 4);
     float bias[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        bias[e] = (a.dto.bias != nullptr && 4 * v0 + e < r.nc) ? a.dto.bias[r.c0 + 4 * v0 + e] : 0.f;
-        dsum[e] = 0.f;
-    }
+    for (int e = 0; e < 4; ++e) dsum[e] = 0.f;
 #pragma unroll 1
     for (int i0 = 0; i0 < K::CONVS; i0 += M) {
         const int t0 = w0 + i0 * K::CONV;
         const Loaded<T, M> l = load_rows<T, M, K::CONV>(a, r, r.tb + t0, v0, vec);
-        float dt[4 * M], g[4 * M];
+        if (i0 == 0) {
 #pragma unroll
-        for (int i = 0; i < M; ++i)
+            for (int e = 0; e < 4; ++e)
+                bias[e] = (a.dto.bias != nullptr && 4 * v0 + e < r.nc) ? __ldg(a.dto.bias + r.c0 + 4 * v0 + e) : 0.f;
+            constexpr int R = 4;  // vectors of B and of C in flight
+            for (int j0 = tid; j0 < kBlock * LP; j0 += R * threads) {
+                Vec<T, 4> B[R], C[R];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dt[4 * i + e] = l.d[i].get(e) + bias[e];
-                g[4 * i + e] = l.dy[i].get(e);
+                for (int u = 0; u < R; ++u) {
+                    const int j = j0 + u * threads, t = r.tb + j / LP, e = 4 * (j % LP);
+                    const int valid = j < kBlock * LP && t < r.last ? a.dstate - e : 0;
+                    B[u] = load_vec<T, 4>(r.B + t * a.B_token + e, valid, vecb);
+                    C[u] = load_vec<T, 4>(r.C + t * a.C_token + e, valid, vecb);
+                }
+#pragma unroll
+                for (int u = 0; u < R; ++u) {
+                    const int j = j0 + u * threads;
+                    if (j < kBlock * LP) {
+                        *reinterpret_cast<float4*>(s_B + 4 * j) = make_float4(B[u].get(0), B[u].get(1), B[u].get(2), B[u].get(3));
+                        *reinterpret_cast<float4*>(s_C + 4 * j) = make_float4(C[u].get(0), C[u].get(1), C[u].get(2), C[u].get(3));
+                    }
+                }
             }
-        effective(dt, a.dto);
-        if (r.z != nullptr) {
+        }
+        constexpr int S = M < 4 ? M : 4;  // vectors converted side by side
 #pragma unroll
-            for (int i = 0; i < M; ++i)
+        for (int s = 0; s < M; s += S) {
+            float dt[4 * S], g[4 * S];
+#pragma unroll
+            for (int i = 0; i < S; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float zv = l.z[i].get(e);
-                    g[4 * i + e] *= zv * sigmoid(zv);
+                    dt[4 * i + e] = l.d[s + i].get(e) + bias[e];
+                    g[4 * i + e] = l.dy[s + i].get(e);
                 }
-        }
+            effective(dt, a.dto);
+            if (r.z != nullptr) {
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-            const int t = t0 + i * K::CONV, at = t * cc + 4 * v0;
-            const bool live = r.tb + t < r.last;
-            float dx[4];
+                for (int i = 0; i < S; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dt[4 * i + e] = live ? dt[4 * i + e] : 0.f;
-                dx[e] = dt[4 * i + e] * l.x[i].get(e);
-                dsum[e] += dt[4 * i + e];
+                    for (int e = 0; e < 4; ++e) {
+                        const float zv = l.z[s + i].get(e);
+                        g[4 * i + e] *= zv * sigmoid(zv);
+                    }
             }
-            if (K::CONV * K::CONVS == kBlock || t < kBlock) {
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                const int t = t0 + (s + i) * K::CONV, at = t * cc + 4 * v0;
+                const bool live = r.tb + t < r.last;
+                float dx[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dt[4 * i + e] = live ? dt[4 * i + e] : 0.f;
+                    dx[e] = dt[4 * i + e] * l.x[s + i].get(e);
+                    dsum[e] += dt[4 * i + e];
+                }
                 *reinterpret_cast<float4*>(s_d + at) = make_float4(dt[4 * i], dt[4 * i + 1], dt[4 * i + 2], dt[4 * i + 3]);
                 *reinterpret_cast<float4*>(s_x + at) = make_float4(dx[0], dx[1], dx[2], dx[3]);
                 *reinterpret_cast<float4*>(s_g + at) = make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
             }
         }
-    }
-#pragma unroll 2
-    for (int i = tid; i < kBlock * LP; i += threads) {
-        const int t = r.tb + i / LP, e = 4 * (i % LP), valid = t < r.last ? a.dstate - e : 0;
-        const Vec<T, 4> B = load_vec<T, 4>(r.B + t * a.B_token + e, valid, vecb);
-        const Vec<T, 4> C = load_vec<T, 4>(r.C + t * a.C_token + e, valid, vecb);
-        *reinterpret_cast<float4*>(s_B + 4 * i) = make_float4(B.get(0), B.get(1), B.get(2), B.get(3));
-        *reinterpret_cast<float4*>(s_C + 4 * i) = make_float4(C.get(0), C.get(1), C.get(2), C.get(3));
     }
 }
 
@@ -440,11 +455,16 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
             half(j * kRun + s * kHeld);
         }
         __syncthreads();
-        for (int i = tid; i < kRun * 2 * N; i += threads) {
-            const int tt = i / (2 * N), which = (i / N) % 2, e = i % N, t = r.tb + j * kRun + tt;
-            float s = 0.f;
-            for (int w = 0; w < warps; ++w) s += s_red[((w * kRun + tt) * 2 + which) * NP + e];
-            if (t < r.te) dbc[(((place + t) * a.ngroups + r.grp) * 2 + which) * N + e] = s;
+        for (int i = tid; i < kRun * 2 * LP; i += threads) {  // four entries of a token's dB or dC, over the warps
+            const int tt = i / (2 * LP), which = i / LP % 2, e = i % LP * 4, t = r.tb + j * kRun + tt;
+            float4 s = *reinterpret_cast<const float4*>(s_red + 4 * i);
+            for (int w = 1; w < warps; ++w) {
+                const float4 u = *reinterpret_cast<const float4*>(s_red + w * kRun * 2 * NP + 4 * i);
+                s = make_float4(s.x + u.x, s.y + u.y, s.z + u.z, s.w + u.w);
+            }
+            const float o[4] = {s.x, s.y, s.z, s.w};
+            store_vec<float, 4>(dbc + (((place + t) * a.ngroups + r.grp) * 2 + which) * N + e, Vec<float, 4>::of(o),
+                                t < r.te ? N - e : 0, N % 4 == 0);
         }
         __syncthreads();
     }
@@ -602,10 +622,11 @@ Parts parts_of(const SelectiveArgs& a) {
     p.nblocks = ceil_div(a.seqlen, kBlock);
     p.tiles = ceil_div(a.channels / a.ngroups, cc);
     const size_t n = (size_t)a.channels * a.dstate, rows = (size_t)a.batch * p.nblocks;
-    p.hops = rows * n;
-    p.nu0 = a.batch * n;
-    p.dtsum = rows * a.channels;
-    p.chan = 2 * rows * a.channels;
+    auto whole = [](size_t floats) { return (floats + 3) & ~(size_t)3; };  // every part starts on 16 bytes
+    p.hops = whole(rows * n);
+    p.nu0 = whole(a.batch * n);
+    p.dtsum = whole(rows * a.channels);
+    p.chan = whole(2 * rows * a.channels);
     p.dbc = (size_t)p.tiles * a.batch * a.seqlen * a.ngroups * 2 * a.dstate;
     return p;
 }

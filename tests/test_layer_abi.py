@@ -155,14 +155,16 @@ def test_binding_refuses_what_is_not_on_the_gpu():
 def test_binding_reads_strides():
     from state_space_sequence_ssd_gb300 import layer
     t = torch.zeros((3, 5, 64))
-    assert list(layer._strides(t[..., 8:24], "t", 1)) == [320, 64]
-    assert list(layer._strides(t[:1, :, :8], "t", 1)) == [0, 64]
-    assert list(layer._strides(t.unflatten(-1, (4, 16)), "t", 2)) == [320, 64]
+    assert layer._native.row_strides(t[..., 8:24], 1) == [320, 64]
+    assert layer._native.row_strides(t[:1, :, :8], 1) == [0, 64]
+    assert layer._native.row_strides(t.unflatten(-1, (4, 16)), 2) == [320, 64]
     with pytest.raises(ValueError, match="dense"):
-        layer._strides(t.transpose(1, 2), "t", 1)
-    assert layer._flat_rows(t[..., :8], "t", 8)[1:] == (64, 15)
-    assert layer._flat_rows(t[:1, :1, :8], "t", 8)[1:] == (8, 1)
+        layer._native.row_strides(t.transpose(1, 2), 1)
+    assert layer._native.flat_rows(t[..., :8]) == (64, 15)
+    assert layer._native.flat_rows(t[:1, :1, :8]) == (8, 1)
     with pytest.raises(ValueError, match="evenly"):
-        layer._flat_rows(t[:, :4], "t", 64)
-    with pytest.raises(ValueError, match="add up"):
-        layer._split([3, 4], 8)
+        layer._native.flat_rows(t[:, :4])
+    with pytest.raises(ValueError, match="required"):
+        layer._native.flat_rows(None)
+    with pytest.raises(TypeError):
+        layer._native.flat_rows(t, t)
