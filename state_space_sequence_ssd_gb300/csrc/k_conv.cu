@@ -19,7 +19,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 // The taps and biases of V channels as pairs.  Tap 3 is the current token's: a narrower kernel's taps end there and its
 // first ones are unused (never multiplied: zero times an infinite input would be NaN).
@@ -155,25 +155,22 @@ __device__ __forceinline__ GradPiece grad_piece(const Pieces& dy, int c) {
     return {dy.p[2], dy.n[2], c - dy.n[1], dy.f32[2] != 0};
 }
 
-constexpr int kBwdRun = 32;  // tokens a warp of the backward kernel walks
-
-// A warp: 32 V channels of kBwdRun consecutive tokens, their dx and their part of dweight and dbias.  dx[t] needs
+// A warp: 32 V channels of RUN consecutive tokens, their dx and their part of dweight and dbias.  dx[t] needs
 // dLoss/dpre up to W-1 tokens on, so the walk goes that far past the run (those tokens' pre again).  Tokens are taken
-// four at a time: their x and dy are loaded together, one group ahead of their use.  The block's eight warps' sums of
-// one channel are joined in shared memory in warp order and written as one row of `partial`,
-// (rows, width + 1, channels).
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * kWarps, 2) conv_backward_kernel(ConvArgs a, Pieces dy, const T* __restrict__ dfinal,
-                                                                    T* __restrict__ dx, int64_t dx_batch, int64_t dx_token,
-                                                                    T* __restrict__ dinit, float* __restrict__ partial,
-                                                                    bool vec, bool vec_dx) {
-    constexpr int P = (V + 1) / 2, S = 4;
+// four at a time: their x and dy are loaded together, one group ahead of their use; groups whose tokens all count and
+// all leave, most of them, are computed without looking at each.  The block's warps' sums of one channel are joined in
+// shared memory in warp order and written as one row of `partial`, (rows, width + 1, channels).
+template <typename T, int V, int W, int RUN>
+__global__ void __launch_bounds__(32 * kWarps, V == 4 ? 3 : 4) conv_backward_kernel(
+    ConvArgs a, Pieces dy, const T* __restrict__ dfinal, T* __restrict__ dx, int64_t dx_batch, int64_t dx_token,
+    T* __restrict__ dinit, float* __restrict__ partial) {
+    constexpr int S = 4, P = (V + 1) / 2;
     __shared__ float sums[kWarps][W + 1][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.z, c = (blockIdx.x * 32 + lane) * V;
     const int valid = max(0, min(V, a.channels - c));
     const int len = row_length(a.lengths, b, a.seqlen);
-    const int t0 = (blockIdx.y * kWarps + warp) * kBwdRun;
+    const int t0 = (blockIdx.y * kWarps + warp) * RUN;
     f32x2 dw[W][P], db[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
@@ -186,63 +183,88 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv_backward_kernel(ConvArgs 
         load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
         // the run itself; the first one also gives the initial state's tokens, which have no output of their own
         const int first = (t0 == 0 && dinit != nullptr) ? -(W - 1) : t0;
-        const int last = min(t0 + kBwdRun, a.seqlen);
+        const int last = min(t0 + RUN, a.seqlen), lim = min(len, last + W - 1);
         const GradPiece gr = grad_piece(dy, c);
-        const int64_t g0 = (int64_t)b * a.seqlen * gr.wide + gr.at;
-        const T* gp = static_cast<const T*>(gr.p) + g0;
-        const float* gf = static_cast<const float*>(gr.p) + g0;
-        const T* xp = static_cast<const T*>(a.x) + b * a.x_batch + c;
+        const int64_t gstep = (int64_t)gr.wide * (gr.f32 ? 4 : sizeof(T)), xstep = a.x_token;
+        const char* gp = static_cast<const char*>(gr.p) + (((int64_t)b * a.seqlen + t0) * gr.wide + gr.at) * (gr.f32 ? 4 : sizeof(T));
+        const T* xp = static_cast<const T*>(a.x) + b * a.x_batch + t0 * xstep + c;
+        T* op = dx + b * dx_batch + (int64_t)(t0 - (W - 1)) * dx_token + c;  // of the token that leaves
         f32x2 x[S + 3][P], g[S + 3][P];  // inputs and dLoss/dpre of this group's tokens, after the three before them
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, vec) : Vec<T, V>::zero();
+            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, true) : Vec<T, V>::zero();
 #pragma unroll
-            for (int j = 0; j < P; ++j) { x[k][j] = v.pair(j); g[k][j] = 0ull; }
+            for (int j = 0; j < P; ++j) {
+                x[k][j] = v.pair(j);
+                g[k][j] = 0ull;
+            }
         }
-        Vec<T, V> nx[S], ng[S];
-        Vec<float, V> nf[S];
+        Vec<T, V> nx[S];
+        Vec<float, V> ng[S];  // dy as it lies in memory, in the first words where it is of 16 bits
         auto fetch = [&](int t) {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                const int got = t + i < min(len, last + W - 1) ? valid : 0;
-                nx[i] = load_vec<T, V>(xp + (int64_t)(t + i) * a.x_token, got, vec);
-                if (gr.f32) nf[i] = load_vec<float, V>(gf + (int64_t)(t + i) * gr.wide, got, vec);
-                else ng[i] = load_vec<T, V>(gp + (int64_t)(t + i) * gr.wide, got, vec);
+                const int got = t + i < lim ? valid : 0;
+                nx[i] = load_vec<T, V>(xp, got, true);
+                xp += xstep;
+                if (sizeof(T) == 4 || gr.f32) {
+                    ng[i] = load_vec<float, V>(reinterpret_cast<const float*>(gp), got, true);
+                } else {
+                    const Vec<T, V> v = load_vec<T, V>(reinterpret_cast<const T*>(gp), got, true);
+#pragma unroll
+                    for (int u = 0; u < Vec<T, V>::WORDS; ++u) ng[i].w[u] = v.w[u];
+                }
+                gp += gstep;
             }
         };
-        fetch(t0);
-        for (int t = t0; t < last + W - 1; t += S) {
-            f32x2 gy[S][P];
+        // one group of tokens from t on; WHOLE: t + S <= min(len, last) and t - (W-1) >= first, no final state's gradient
+        auto group = [&](int t, auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            float pre[S][2 * P], gv[S][2 * P];
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                Vec<T, V> gt;
+#pragma unroll
+                for (int u = 0; u < Vec<T, V>::WORDS; ++u) gt.w[u] = ng[i].w[u];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    x[3 + i][j] = nx[i].pair(j);
+                    unpk(sizeof(T) == 4 || gr.f32 ? ng[i].pair(j) : gt.pair(j), gv[i][2 * j], gv[i][2 * j + 1]);
+                }
+            }
+            if (t + S < last + W - 1) fetch(t + S);
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                f32x2 p[P];
+                taps_times<W, P>(w, bias, x + i, p);
+#pragma unroll
+                for (int j = 0; j < P; ++j) unpk(p[j], pre[i][2 * j], pre[i][2 * j + 1]);
+            }
+            if (a.silu) {
+#pragma unroll
+                for (int i = 0; i < S; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2 * P; ++e) {  // times s (1 + pre (1 - s))
+                        const float s = sigmoid(pre[i][e]);
+                        gv[i][e] *= fmaf(s * pre[i][e], 1.f - s, s);
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < S; ++i)
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    x[3 + i][j] = nx[i].pair(j);
-                    gy[i][j] = gr.f32 ? nf[i].pair(j) : ng[i].pair(j);
+                    f32x2 q = pk(gv[i][2 * j], gv[i][2 * j + 1]);
+                    if (!WHOLE && t + i >= len) q = 0ull;
+                    g[3 + i][j] = q;
+                    if (!WHOLE && t + i >= last) q = 0ull;
+                    db[j] = add2(db[j], q);
+#pragma unroll
+                    for (int k = 0; k < W; ++k) dw[k][j] = fma2(q, x[4 - W + k + i][j], dw[k][j]);
                 }
-            if (t + S < last + W - 1) fetch(t + S);
+            // the tokens W-1 before now have all their gradients and leave
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                // token t + i enters; token t + i - (W-1) then has all its gradients and leaves
-                f32x2 pre[P];
-                taps_times<W, P>(w, bias, x + i, pre);
-                const bool live = t + i < len;
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    f32x2 q = gy[i][j];
-                    if (a.silu) {  // times s (1 + pre (1 - s))
-                        const f32x2 s = sigmoid2(pre[j]), one = pk(1.f, 1.f);
-                        q = mul2(mul2(q, s), fma2(pre[j], fma2(s, pk(-1.f, -1.f), one), one));
-                    }
-                    g[3 + i][j] = live ? q : 0ull;
-                    if (t + i < last) {
-                        db[j] = add2(db[j], g[3 + i][j]);
-#pragma unroll
-                        for (int k = 0; k < W; ++k) dw[k][j] = fma2(g[3 + i][j], x[4 - W + k + i][j], dw[k][j]);
-                    }
-                }
                 const int o = t + i - (W - 1);
-                if (o < first || o >= last) continue;
                 f32x2 d[P];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
@@ -250,22 +272,35 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv_backward_kernel(ConvArgs 
 #pragma unroll
                     for (int k = 1; k < W; ++k) d[j] = fma2(w[3 - k][j], g[4 - W + k + i][j], d[j]);
                 }
-                const int r = o + W - 1 - len;  // the final state's row that holds token o
-                if (dfinal != nullptr && r >= 0 && r < W - 1) {
-                    const Vec<T, V> f = load_vec<T, V>(dfinal + ((int64_t)b * (W - 1) + r) * a.channels + c, valid, vec);
+                if (WHOLE) {
+                    store_vec<T, V>(op, Vec<T, V>::of_pairs(d), valid, true);
+                } else if (o >= first && o < last) {
+                    const int r = o + W - 1 - len;  // the final state's row that holds token o
+                    if (dfinal != nullptr && r >= 0 && r < W - 1) {
+                        const Vec<T, V> f = load_vec<T, V>(dfinal + ((int64_t)b * (W - 1) + r) * a.channels + c, valid, true);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) d[j] = add2(d[j], f.pair(j));
+                        for (int j = 0; j < P; ++j) d[j] = add2(d[j], f.pair(j));
+                    }
+                    store_vec<T, V>(o >= 0 ? op : dinit + ((int64_t)b * (W - 1) + o + W - 1) * a.channels + c,
+                                    o < len ? Vec<T, V>::of_pairs(d) : Vec<T, V>::zero(), valid, true);
                 }
-                const Vec<T, V> out = o < len ? Vec<T, V>::of_pairs(d) : Vec<T, V>::zero();
-                if (o >= 0)
-                    store_vec<T, V>(dx + b * dx_batch + o * dx_token + c, out, valid, vec_dx);
-                else
-                    store_vec<T, V>(dinit + ((int64_t)b * (W - 1) + o + W - 1) * a.channels + c, out, valid, vec);
+                op += dx_token;
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k)
 #pragma unroll
-                for (int j = 0; j < P; ++j) { x[k][j] = x[S + k][j]; g[k][j] = g[S + k][j]; }
+                for (int j = 0; j < P; ++j) {
+                    x[k][j] = x[S + k][j];
+                    g[k][j] = g[S + k][j];
+                }
+        };
+        // tokens that leave before `calm` are no part of a final state
+        const int calm = min(last, dfinal != nullptr ? len - (W - 1) : len);
+        fetch(t0);
+#pragma unroll 1
+        for (int t = t0; t < last + W - 1; t += S) {
+            if (t > t0 && t + S <= min(len, last) && t + S - (W - 1) <= calm) group(t, std::true_type());
+            else group(t, std::false_type());
         }
     }
 #pragma unroll
@@ -275,7 +310,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv_backward_kernel(ConvArgs 
             float lo, hi;
             unpk(k < W ? dw[k < W ? k : 0][j] : db[j], lo, hi);
             sums[warp][k][lane * V + 2 * j] = lo;
-            if (2 * j + 1 < V) sums[warp][k][lane * V + 2 * j + 1] = hi;
+            if (V > 1) sums[warp][k][lane * V + 2 * j + (V > 1)] = hi;
         }
     __syncthreads();
     const int64_t row = (int64_t)b * gridDim.y + blockIdx.y;
@@ -397,21 +432,32 @@ int forward_of(const ConvArgs& a, const Pieces& y, void* final_state, cudaStream
     return launch_end(kKindConv, s);
 }
 
+// Tokens that a warp of the backward kernel walks: long runs read the taps and the halo rarely and leave few rows of sums
+// (at 2 x 4096 x 4352, runs of 16, 32 and 64 tokens: 110, 83 and 71 us), short ones fill the SMs where tokens are few.
+constexpr int kLongRun = 64, kShortRun = 16;
+int backward_run(const ConvArgs& a) {
+    return (int64_t)a.batch * ceil_div(a.channels, 64) * ceil_div(a.seqlen, kWarps * kLongRun) >= 304 ? kLongRun : kShortRun;
+}
+
 template <typename T, int W>
 int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* dx, int64_t dx_batch, int64_t dx_token,
                 float* dweight, float* dbias, void* dinit, float* partial, cudaStream_t s) {
-    constexpr int V = 4;
     const T* df = static_cast<const T*>(dfinal);
     T *o = static_cast<T*>(dx), *di = static_cast<T*>(dinit);
-    const int rows = ceil_div(a.seqlen, kWarps * kBwdRun);
+    const int run = backward_run(a), rows = ceil_div(a.seqlen, kWarps * run);
+    const bool fours = whole_vectors(a, dy, dfinal, dinit, 4, sizeof(T)) && dx_batch % 4 == 0 && dx_token % 4 == 0 &&
+                       on(dx, 4 * sizeof(T));
     launch_begin(kKindConvBwd, s);
-    if (whole_vectors(a, dy, dfinal, dinit, V, sizeof(T))) {
-        const bool vec_dx = dx_batch % V == 0 && dx_token % V == 0 && on(dx, V * sizeof(T));
-        conv_backward_kernel<T, V, W><<<dim3(ceil_div(a.channels, 32 * V), rows, a.batch), 32 * kWarps, 0, s>>>(
-            a, dy, df, o, dx_batch, dx_token, di, partial, true, vec_dx);
+    auto go = [&](auto kernel, int channels) {
+        kernel<<<dim3(ceil_div(a.channels, channels), rows, a.batch), 32 * kWarps, 0, s>>>(a, dy, df, o, dx_batch, dx_token, di,
+                                                                                          partial);
+    };
+    if (fours) {
+        if (run == kLongRun) go(conv_backward_kernel<T, 4, W, kLongRun>, 128);
+        else go(conv_backward_kernel<T, 4, W, kShortRun>, 128);
     } else {
-        conv_backward_kernel<T, 1, W><<<dim3(ceil_div(a.channels, 32), rows, a.batch), 32 * kWarps, 0, s>>>(
-            a, dy, df, o, dx_batch, dx_token, di, partial, true, true);
+        if (run == kLongRun) go(conv_backward_kernel<T, 1, W, kLongRun>, 32);
+        else go(conv_backward_kernel<T, 1, W, kShortRun>, 32);
     }
     const int r = launch_end(kKindConvBwd, s);
     if (r != SSD_OK || (dweight == nullptr && dbias == nullptr)) return r;
@@ -459,7 +505,7 @@ int launch_conv_forward(const ConvArgs& a, const Pieces& y, void* final_state, c
     return by_type_and_width(a, [&](auto type, auto W) { return forward_of<decltype(type), W()>(a, y, final_state, s); });
 }
 
-int conv_backward_rows(const ConvArgs& a) { return a.batch * ceil_div(a.seqlen, kWarps * kBwdRun); }
+int conv_backward_rows(const ConvArgs& a) { return a.batch * ceil_div(a.seqlen, kWarps * backward_run(a)); }
 
 int launch_conv_backward(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* dx, int64_t dx_batch,
                          int64_t dx_token, float* dweight, float* dbias, void* dinit, float* partial, cudaStream_t s) {
