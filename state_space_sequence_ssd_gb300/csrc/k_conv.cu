@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* __restric
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;  // (tap or bias, channel)
     const int n = (W + 1) * channels;
+    grid_dep_wait();
     float s = 0.f;
     if (i < n) {
 #pragma unroll 8
@@ -462,8 +463,8 @@ int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* d
     const int r = launch_end(kKindConvBwd, s);
     if (r != SSD_OK || (dweight == nullptr && dbias == nullptr)) return r;
     launch_begin(kKindConvBwd, s);
-    conv_reduce_kernel<<<ceil_div((a.width + 1) * a.channels, 32), 256, 0, s>>>(partial, rows * a.batch, a.channels, a.width,
-                                                                               dweight, dbias);
+    launch_dependent(conv_reduce_kernel, dim3(ceil_div((a.width + 1) * a.channels, 32)), dim3(256), 0, s, partial, rows * a.batch,
+                     a.channels, a.width, dweight, dbias);
     return launch_end(kKindConvBwd, s);
 }
 

@@ -46,90 +46,114 @@ __device__ __forceinline__ float2 row_sums(float2 v, int lanes, float2* buf) {
 }
 __device__ __forceinline__ float row_sum(float v, int lanes, float2* buf) { return row_sums(make_float2(v, 0.f), lanes, buf).x; }
 
-// V columns of a float32 row from column c on (a null row: `otherwise`).  `vec`: 16-byte aligned groups of four.
+// V columns of a float32 row from column c on, as pairs (a null row: `otherwise`).  `vec`: 16-byte aligned groups of four.
 template <int V>
-__device__ __forceinline__ void load_columns(const float* p, int c, int width, bool vec, float otherwise, float (&o)[V]) {
+__device__ __forceinline__ void load_columns(const float* p, int c, int width, bool vec, float otherwise,
+                                             f32x2 (&o)[(V + 1) / 2]) {
     if (p == nullptr) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = otherwise;
+        for (int e = 0; e < (V + 1) / 2; ++e) o[e] = pk(otherwise, otherwise);
     } else if (V >= 4 && vec) {
 #pragma unroll
         for (int e = 0; e + 3 < V; e += 4) {
             const float4 q = c < width ? __ldg(reinterpret_cast<const float4*>(p + c + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            o[e] = q.x; o[e + 1] = q.y; o[e + 2] = q.z; o[e + 3] = q.w;
+            o[e / 2] = pk(q.x, q.y);
+            o[(e / 2 + 1) % ((V + 1) / 2)] = pk(q.z, q.w);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = c + e < width ? __ldg(p + c + e) : 0.f;
+        for (int e = 0; e < V; e += 2)
+            o[e / 2] = pk(c + e < width ? __ldg(p + c + e) : 0.f, e + 1 < V && c + e + 1 < width ? __ldg(p + c + e + 1) : 0.f);
     }
 }
 
-// NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  With NV = 0 the row
-// does not fit the registers and is read again (from L2) for each sum.
+// NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  A block takes its rows and
+// ends: at 8192 x 2048 bf16 that takes 19.7 us with two vectors a thread, where a resident grid whose blocks walk the
+// rows with the next one's loads in flight took 20.2 to 25, and one warp a row 23.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restrict__ x, int64_t x_row,
                                                                 const float* __restrict__ weight,
                                                                 const float* __restrict__ bias, float eps, int64_t rows,
                                                                 int width, int lanes, T* __restrict__ y,
                                                                 float* __restrict__ mean, float* __restrict__ rstd, bool vecw) {
+    constexpr int P = (V + 1) / 2;
     __shared__ float2 buf[2][kThreads / 32];
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t row = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
     const bool live = row < rows;
     const T* xr = x + (live ? row : 0) * x_row;
     const float inv = 1.f / (float)width;
-    Vec<T, V> r[NV > 0 ? NV : 1];
-    float s = 0.f;
-    if constexpr (NV > 0) {
+    Vec<T, V> r[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + lanes * i) * V;
-            r[i] = load_vec<T, V>(xr + c, live ? width - c : 0, true);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < V; ++e) s += r[i].get(e);
-    } else if (live) {
-        for (int c = lane; c < width; c += lanes) s += to_f32<T>(xr[c]);
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + lanes * i) * V;
+        r[i] = load_vec<T, V>(xr + c, live ? width - c : 0, true);
     }
-    const float m = row_sum(s, lanes, buf[0]) * inv;
-    float q = 0.f;
-    if constexpr (NV > 0) {
+    f32x2 s2 = 0ull, q2 = 0ull;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = r[i].get(e) - m;
-                if (V > 1 ? (lane + lanes * i) * V < width : lane + lanes * i < width) q = fmaf(d, d, q);
+        for (int e = 0; e < P; ++e) s2 = add2(s2, r[i].pair(e));
+    const float m = row_sum(sum2(s2), lanes, buf[0]) * inv;
+    const f32x2 m2 = pk(-m, V > 1 ? -m : 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((lane + lanes * i) * V < width) {
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const f32x2 d = add2(r[i].pair(e), m2);
+                q2 = fma2(d, d, q2);
             }
-    } else if (live) {
-        for (int c = lane; c < width; c += lanes) { const float d = to_f32<T>(xr[c]) - m; q = fmaf(d, d, q); }
-    }
-    const float rs = rsqrtf(fmaf(row_sum(q, lanes, buf[1]), inv, eps));
+        }
+    const float rs = rsqrtf(fmaf(row_sum(sum2(q2), lanes, buf[1]), inv, eps));
     if (!live) return;
     if (lane == 0) {
         if (mean != nullptr) mean[row] = m;
         if (rstd != nullptr) rstd[row] = rs;
     }
     T* yr = y + row * width;
-    if constexpr (NV > 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + lanes * i) * V;
-            if (c >= width) break;
-            float o[V], w[V], b[V];
-            load_columns<V>(weight, c, width, vecw, 1.f, w);
-            load_columns<V>(bias, c, width, vecw, 0.f, b);
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + lanes * i) * V;
+        if (c >= width) break;
+        f32x2 o[P], w[P], b[P];
+        load_columns<V>(weight, c, width, vecw, 1.f, w);
+        load_columns<V>(bias, c, width, vecw, 0.f, b);
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = fmaf((r[i].get(e) - m) * rs, w[e], b[e]);
-            store_vec<T, V>(yr + c, Vec<T, V>::of(o), width - c, true);
-        }
-    } else {
-        for (int c = lane; c < width; c += lanes)
-            yr[c] = from_f32<T>(fmaf((to_f32<T>(xr[c]) - m) * rs, weight != nullptr ? weight[c] : 1.f,
-                                     bias != nullptr ? bias[c] : 0.f));
+        for (int e = 0; e < P; ++e) o[e] = fma2(mul2(add2(r[i].pair(e), m2), pk(rs, rs)), w[e], b[e]);
+        store_vec<T, V>(yr + c, Vec<T, V>::of_pairs(o), width - c, true);
     }
+}
+
+// Rows that do not fit the registers, a block each: read again (from L2) for each sum and the output.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) norm_forward_wide_kernel(const T* __restrict__ x, int64_t x_row,
+                                                                     const float* __restrict__ weight,
+                                                                     const float* __restrict__ bias, float eps, int width,
+                                                                     T* __restrict__ y, float* __restrict__ mean,
+                                                                     float* __restrict__ rstd) {
+    __shared__ float2 buf[2][kThreads / 32];
+    const int64_t row = blockIdx.x;
+    const T* xr = x + row * x_row;
+    const float inv = 1.f / (float)width;
+    float s = 0.f, q = 0.f;
+#pragma unroll 8
+    for (int c = threadIdx.x; c < width; c += kThreads) s += to_f32<T>(xr[c]);
+    const float m = row_sum(s, kThreads, buf[0]) * inv;
+#pragma unroll 8
+    for (int c = threadIdx.x; c < width; c += kThreads) {
+        const float d = to_f32<T>(xr[c]) - m;
+        q = fmaf(d, d, q);
+    }
+    const float rs = rsqrtf(fmaf(row_sum(q, kThreads, buf[1]), inv, eps));
+    if (threadIdx.x == 0) {
+        if (mean != nullptr) mean[row] = m;
+        if (rstd != nullptr) rstd[row] = rs;
+    }
+#pragma unroll 8
+    for (int c = threadIdx.x; c < width; c += kThreads)
+        y[row * width + c] = from_f32<T>(fmaf((to_f32<T>(xr[c]) - m) * rs, weight != nullptr ? weight[c] : 1.f,
+                                              bias != nullptr ? bias[c] : 0.f));
 }
 
 // A block of `lanes` threads a row, kThreads / lanes rows at a time.  The thread's columns of dweight and dbias stay
@@ -145,12 +169,13 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __rest
     __shared__ float2 buf[2][kThreads / 32];
     const int lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes, per = kThreads / lanes;
     const float inv = 1.f / (float)width;
-    float w[NV][V], dw[NV][V], db[NV][V];
+    constexpr int P = (V + 1) / 2;
+    f32x2 w[NV][P], dw[NV][P], db[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         load_columns<V>(weight, (lane + lanes * i) * V, width, vecw, 1.f, w[i]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.f;
+        for (int e = 0; e < P; ++e) dw[i][e] = db[i][e] = 0ull;
     }
     Vec<T, V> nx[NV], ng[NV];
     float nm, nrs;
@@ -172,35 +197,39 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __rest
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += step, row += step, turn ^= 1) {
         Vec<T, V> cx[NV], cg[NV];
-        const float m = nm, rs = nrs;
-        float2 s = make_float2(0.f, 0.f);
+        const float rs = nrs;
+        const f32x2 rs2 = pk(rs, rs), shift = pk(-nm * rs, -nm * rs);  // xhat = x rstd - mean rstd
+        f32x2 s1 = 0ull, s2 = 0ull;
 #pragma unroll
         for (int i = 0; i < NV; ++i) { cx[i] = nx[i]; cg[i] = ng[i]; }
         if (r0 + step < rows) fetch(row + step);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float gy = cg[i].get(e), xh = (cx[i].get(e) - m) * rs;  // gy is zero past the row's end
-                db[i][e] += gy;
-                dw[i][e] = fmaf(gy, xh, dw[i][e]);
-                s.x = fmaf(gy, w[i][e], s.x);
-                s.y = fmaf(gy * w[i][e], xh, s.y);
+            for (int e = 0; e < P; ++e) {
+                const f32x2 gy = cg[i].pair(e), xh = fma2(cx[i].pair(e), rs2, shift);  // gy is zero past the row's end
+                const f32x2 g = mul2(gy, w[i][e]);
+                db[i][e] = add2(db[i][e], gy);
+                dw[i][e] = fma2(gy, xh, dw[i][e]);
+                s1 = add2(s1, g);
+                s2 = fma2(g, xh, s2);
             }
+        float2 s = make_float2(sum2(s1), sum2(s2));
         s = row_sums(s, lanes, buf[turn]);
         if (row >= rows) continue;
-        s.x *= inv;
-        s.y *= inv;
+        const float k1 = -s.x * inv * rs, k2 = -s.y * inv * rs;
         T* o = dx + row * width;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + lanes * i) * V;
             if (c >= width) break;
-            float out[V];
+            f32x2 out[P];
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                out[e] = rs * fmaf(-(cx[i].get(e) - m) * rs, s.y, fmaf(cg[i].get(e), w[i][e], -s.x));
-            store_vec<T, V>(o + c, Vec<T, V>::of(out), width - c, true);
+            for (int e = 0; e < P; ++e) {
+                const f32x2 xh = fma2(cx[i].pair(e), rs2, shift), g = mul2(cg[i].pair(e), w[i][e]);
+                out[e] = fma2(g, rs2, fma2(xh, pk(k2, k2), pk(k1, k1)));
+            }
+            store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), width - c, true);
         }
     }
     if (partial == nullptr) return;
@@ -211,7 +240,11 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __rest
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const int c = (lane + lanes * i) * V + e;
-            if (c < width) { to[c] = dw[i][e]; to[width + c] = db[i][e]; }
+            float a, b;
+            unpk(dw[i][e / 2], a, b);
+            if (c < width) to[c] = e & 1 ? b : a;
+            unpk(db[i][e / 2], a, b);
+            if (c < width) to[width + c] = e & 1 ? b : a;
         }
     if (per == 1) return;
     __syncthreads();
@@ -267,6 +300,7 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restric
     __shared__ float part[8][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
+    grid_dep_wait();
     float s = 0.f;
     if (i < 2 * width) {
 #pragma unroll 16
@@ -301,21 +335,23 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
                void* y, float* mean, float* rstd, cudaStream_t s) {
     constexpr int M = V == 1 ? 4 : 1;
     const int vecs = ceil_div(width, V);
-    const int lanes = row_lanes(rows, vecs, 8 * M, 1);
+    const int lanes = row_lanes(rows, vecs, 2 * M, 1);
     const int nv = ceil_div(vecs, lanes);
     const int64_t blocks = ceil_div64(rows, kThreads / lanes);
-    if (blocks > 2147483647) return SSD_ERR_UNSUPPORTED;
     const bool vecw = on(weight, 16) && on(bias, 16);
+    const T* xt = static_cast<const T*>(x);
+    T* yt = static_cast<T*>(y);
+    if (blocks > 2147483647) return SSD_ERR_UNSUPPORTED;
     launch_begin(kKindNorm, s);
     auto go = [&](auto kernel) {
-        kernel<<<(unsigned)blocks, kThreads, 0, s>>>(static_cast<const T*>(x), x_row, weight, bias, eps, rows, width, lanes,
-                                                     static_cast<T*>(y), mean, rstd, vecw);
+        kernel<<<(unsigned)blocks, kThreads, 0, s>>>(xt, x_row, weight, bias, eps, rows, width, lanes, yt, mean, rstd, vecw);
     };
     if (nv <= 1 * M) go(norm_forward_kernel<T, V, 1 * M>);
     else if (nv <= 2 * M) go(norm_forward_kernel<T, V, 2 * M>);
     else if (nv <= 4 * M) go(norm_forward_kernel<T, V, 4 * M>);
     else if (nv <= 8 * M) go(norm_forward_kernel<T, V, 8 * M>);
-    else go(norm_forward_kernel<T, 1, 0>);
+    else
+        norm_forward_wide_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(xt, x_row, weight, bias, eps, width, yt, mean, rstd);
     return launch_end(kKindNorm, s);
 }
 
@@ -389,7 +425,7 @@ int launch_layer_norm_backward(int dtype, const void* x, int64_t x_row, const fl
         r = backward_type<float>(x, x_row, weight, mean, rstd, dy, dy_row, rows, width, dx, partial, parts, s);
     if (r != SSD_OK || partial == nullptr) return r;
     launch_begin(kKindNormBwd, s);
-    norm_reduce_kernel<<<ceil_div(2 * width, 32), 256, 0, s>>>(partial, parts, width, dweight, dbias);
+    launch_dependent(norm_reduce_kernel, dim3(ceil_div(2 * width, 32)), dim3(256), 0, s, partial, parts, width, dweight, dbias);
     return launch_end(kKindNormBwd, s);
 }
 

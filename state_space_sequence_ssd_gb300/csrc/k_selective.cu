@@ -15,13 +15,26 @@ __global__ void __launch_bounds__(256) selective_hop_kernel(const float* __restr
     if (i >= n) return;
     const float A2 = A[i] * kLog2e;
     float h = init != nullptr ? init[b * n + i] : 0.f;
+    grid_dep_wait();  // the chunks' own states and sums
     float* hp = hops + b * n * nchunks + i;
     const float* dp = dtsum + (int64_t)b * nchunks * channels + i / dstate;
     hp[0] = h;
-#pragma unroll 4
-    for (int k = 0; k + 1 < nchunks; ++k) {
-        h = fmaf(exp2_fast(A2 * dp[(int64_t)k * channels]), h, hp[(k + 1) * n]);
-        hp[(k + 1) * n] = h;
+    // the states and sums of the next chunks are loaded ahead: only the sum waits for the chunk before
+    constexpr int AHEAD = 8;
+    for (int k = 0; k + 1 < nchunks; k += AHEAD) {
+        float own[AHEAD], sum[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (k + u + 1 < nchunks) {
+                own[u] = hp[(k + u + 1) * n];
+                sum[u] = dp[(int64_t)(k + u) * channels];
+            }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (k + u + 1 < nchunks) {
+                h = fmaf(exp2_fast(A2 * sum[u]), h, own[u]);
+                hp[(k + u + 1) * n] = h;
+            }
     }
 }
 
@@ -29,8 +42,8 @@ __global__ void __launch_bounds__(256) selective_hop_kernel(const float* __restr
 
 int launch_selective_hop(const SelectiveArgs& a, int nchunks, float* hops, const float* dtsum, cudaStream_t s) {
     launch_begin(kKindSelective, s);
-    selective_hop_kernel<<<dim3((unsigned)ceil_div64((int64_t)a.channels * a.dstate, 256), a.batch), 256, 0, s>>>(
-        a.A, a.init, a.channels, a.dstate, nchunks, hops, dtsum);
+    launch_dependent(selective_hop_kernel, dim3((unsigned)ceil_div64((int64_t)a.channels * a.dstate, 256), a.batch), dim3(256), 0,
+                     s, a.A, a.init, a.channels, a.dstate, nchunks, hops, dtsum);
     return launch_end(kKindSelective, s);
 }
 

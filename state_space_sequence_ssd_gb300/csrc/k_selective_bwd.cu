@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(256) selective_hops_kernel(const float* __rest
     if (back) dp += (int64_t)(nblocks - 1) * channels;
     const float* start = back ? dfinal : init;
     float s = start != nullptr ? start[b * n + i] : 0.f;
+    grid_dep_wait();  // the blocks' own terms
     // the terms of the next blocks are loaded ahead: only the sum waits for the block before
     constexpr int AHEAD = 8;
     *at = s;
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     }
     Entries A, h, m, dA;
     read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
+    grid_dep_wait();  // the hops
     read_entries(hops + row, c, mine, N, 4 * q, 1.f, h);
     read_entries(mus + row, c, mine, N, 4 * q, 1.f, m);
 #pragma unroll
@@ -567,6 +569,7 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
     __shared__ float part[8][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    grid_dep_wait();
     float s = 0.f;
     if (i < n) {
 #pragma unroll 8
@@ -586,6 +589,7 @@ __global__ void __launch_bounds__(256) join_bc_kernel(const float* __restrict__ 
                                                       float* __restrict__ dB, float* __restrict__ dC) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, n = rows * 2 * dstate;
     if (i >= n) return;
+    grid_dep_wait();
     float s = 0.f;
 #pragma unroll 8
     for (int t = 0; t < tiles; ++t) s += dbc[t * n + i];
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(256) join_bc_kernel(const float* __restrict__ 
 
 int column_sums(const float* in, int64_t stride, int rows, int64_t n, float* out, cudaStream_t s) {
     launch_begin(kKindSelectiveBwd, s);
-    column_sums_kernel<<<(unsigned)ceil_div64(n, 32), 256, 0, s>>>(in, stride, rows, n, out);
+    launch_dependent(column_sums_kernel, dim3((unsigned)ceil_div64(n, 32)), dim3(256), 0, s, in, stride, rows, n, out);
     return launch_end(kKindSelectiveBwd, s);
 }
 
@@ -653,14 +657,13 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
     r = launch_end(kKindSelectiveBwd, s);
     if (r != SSD_OK) return r;
     launch_begin(kKindSelectiveBwd, s);
-    selective_hops_kernel<<<dim3((unsigned)ceil_div64(n, 256), a.batch, 2), 256, 0, s>>>(
-        a.A, a.init, g.dfinal, a.channels, a.dstate, p.nblocks, hops, mus, nu0, dtsum, g.dinit);
+    launch_dependent(selective_hops_kernel, dim3((unsigned)ceil_div64(n, 256), a.batch, 2), dim3(256), 0, s, a.A, a.init, g.dfinal,
+                     a.channels, a.dstate, p.nblocks, hops, mus, nu0, dtsum, g.dinit);
     r = launch_end(kKindSelectiveBwd, s);
     if (r != SSD_OK) return r;
     launch_begin(kKindSelectiveBwd, s);
-    selective_block_kernel<T, LP><<<grid, threads, smem, s>>>(a, dy, p.nblocks, hops, mus, static_cast<T*>(g.dx),
-                                                               static_cast<T*>(g.ddt), static_cast<T*>(g.dz), dbc, chan, vec,
-                                                               vecb);
+    launch_dependent(selective_block_kernel<T, LP>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus,
+                     static_cast<T*>(g.dx), static_cast<T*>(g.ddt), static_cast<T*>(g.dz), dbc, chan, vec, vecb);
     r = launch_end(kKindSelectiveBwd, s);
     const int rows = a.batch * p.nblocks;
     if (r == SSD_OK) r = column_sums(hops, n, rows, n, g.dA, s);
@@ -670,7 +673,8 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
     if (r != SSD_OK) return r;
     const int64_t tokens = (int64_t)a.batch * a.seqlen * a.ngroups;
     launch_begin(kKindSelectiveBwd, s);
-    join_bc_kernel<<<(unsigned)ceil_div64(tokens * 2 * a.dstate, 256), 256, 0, s>>>(dbc, p.tiles, tokens, a.dstate, g.dB, g.dC);
+    launch_dependent(join_bc_kernel, dim3((unsigned)ceil_div64(tokens * 2 * a.dstate, 256)), dim3(256), 0, s, dbc, p.tiles, tokens,
+                     a.dstate, g.dB, g.dC);
     return launch_end(kKindSelectiveBwd, s);
 }
 

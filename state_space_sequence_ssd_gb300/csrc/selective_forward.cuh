@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
     };
     read(a.A, kLog2e, A);
     const float* from = nullptr;
+    if (!STATE_ONLY) grid_dep_wait();  // the hop, where this run follows it
     if (!STATE_ONLY && nchunks > 1) from = hops + ((int64_t)b * nchunks + part) * n;
     else if (!STATE_ONLY && a.init != nullptr) from = a.init + b * n;
     read(from, 1.f, h);
@@ -364,25 +365,27 @@ int forward_shape(const SelectiveArgs& a, const SelectiveShape& f, int chunks, T
     const int smem = K::bytes(f.cc);
     float* hops = ws;
     float* dtsum = ws == nullptr ? nullptr : ws + (int64_t)a.batch * nchunks * a.channels * a.dstate;
-    auto go = [&](auto kernel, int parts) {
+    auto go = [&](auto kernel, int parts, bool follows) {
         int r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), K::bytes(K::channels(128)));
         if (r != SSD_OK) return r;
         launch_begin(kKindSelective, s);
-        kernel<<<dim3(tiles, parts, a.batch), f.threads, smem, s>>>(a, chunk, nchunks, y, final_state, hops, dtsum);
+        const dim3 grid(tiles, parts, a.batch);
+        if (follows) launch_dependent(kernel, grid, dim3(f.threads), smem, s, a, chunk, nchunks, y, final_state, hops, dtsum);
+        else kernel<<<grid, f.threads, smem, s>>>(a, chunk, nchunks, y, final_state, hops, dtsum);
         return launch_end(kKindSelective, s);
     };
     const bool vec = rows_of(a, K::E, y, nullptr, sizeof(T)) && f.cc % K::E == 0 && states_of(a, K::E, sizeof(T)) &&
                      K::NP % K::E == 0;
     int r = SSD_OK;
     if (nchunks > 1) {
-        r = vec ? go(selective_kernel<T, CH, ST, LP, true, true>, nchunks - 1)
-                : go(selective_kernel<T, CH, ST, LP, true, false>, nchunks - 1);
+        r = vec ? go(selective_kernel<T, CH, ST, LP, true, true>, nchunks - 1, false)
+                : go(selective_kernel<T, CH, ST, LP, true, false>, nchunks - 1, false);
         if (r != SSD_OK) return r;
         r = launch_selective_hop(a, nchunks, hops, dtsum, s);
         if (r != SSD_OK) return r;
     }
-    return vec ? go(selective_kernel<T, CH, ST, LP, false, true>, nchunks)
-               : go(selective_kernel<T, CH, ST, LP, false, false>, nchunks);
+    return vec ? go(selective_kernel<T, CH, ST, LP, false, true>, nchunks, nchunks > 1)
+               : go(selective_kernel<T, CH, ST, LP, false, false>, nchunks, nchunks > 1);
 }
 
 template <typename T>
