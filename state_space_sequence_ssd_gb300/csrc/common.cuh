@@ -115,15 +115,7 @@ enum KernelKind {
     kKindStep = 5,
     kKindBwdChunk = 6,
     kKindBwdReduce = 7,
-    kKindConv = 8,
-    kKindConvBwd = 9,
-    kKindConvStep = 10,
-    kKindSelective = 11,
-    kKindSelectiveBwd = 12,
-    kKindSelectiveStep = 13,
-    kKindNorm = 14,
-    kKindNormBwd = 15,
-    kNumKinds = 16
+    kNumKinds = 8
 };
 
 // Sets a kernel's dynamic shared-memory limit once per (kernel, device).

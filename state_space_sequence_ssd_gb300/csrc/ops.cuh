@@ -223,6 +223,19 @@ __device__ __forceinline__ int row_slot(const int* slots, int b, int nslots, int
 
 // ------------------------------------------------------------------ launchers (arguments are checked by ops_api.cu)
 
+// Kernel kinds of the layer operators, after those of the scan.
+enum LayerKind {
+    kKindConv = kNumKinds,
+    kKindConvBwd,
+    kKindConvStep,
+    kKindSelective,
+    kKindSelectiveBwd,
+    kKindSelectiveStep,
+    kKindNorm,
+    kKindNormBwd,
+    kAllKinds
+};
+
 // Up to three dense row-major output (or gradient) pieces side by side: piece i holds n[i] channels.
 struct Pieces {
     void* p[3] = {nullptr, nullptr, nullptr};

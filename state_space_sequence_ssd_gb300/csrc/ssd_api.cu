@@ -13,7 +13,7 @@
 #include <queue>
 #include <vector>
 
-#include "common.cuh"
+#include "ops.cuh"
 
 namespace ssd {
 
@@ -29,8 +29,8 @@ std::mutex g_prof_mu;
 unsigned g_prof_mask = 0;  // bit k: launches of kernel kind k record an event pair
 std::vector<EventPair> g_prof_open;   // recorded, not yet read
 std::vector<cudaEvent_t> g_prof_free; // reusable events
-double g_prof_ms[kNumKinds];
-int g_prof_count[kNumKinds];
+double g_prof_ms[kAllKinds];
+int g_prof_count[kAllKinds];
 long long g_launches = 0;
 EventPair g_pending = {-1, nullptr, nullptr};
 
@@ -45,7 +45,7 @@ cudaEvent_t take_event() {
     return e;
 }
 
-const char* const kKindNames[kNumKinds] = {"chunk_cumsum", "chunk_state", "state_passing", "chunk_scan",
+const char* const kKindNames[kAllKinds] = {"chunk_cumsum", "chunk_state", "state_passing", "chunk_scan",
                                            "bc_to_f16", "step", "bwd_chunk", "bwd_reduce",
                                            "conv", "conv_bwd", "conv_step", "selective", "selective_bwd",
                                            "selective_step", "layer_norm", "layer_norm_bwd"};
@@ -795,7 +795,7 @@ int ssd_profile_reset(void) {
         g_prof_free.push_back(p.stop);
     }
     g_prof_open.clear();
-    for (int k = 0; k < kNumKinds; ++k) {
+    for (int k = 0; k < kAllKinds; ++k) {
         g_prof_ms[k] = 0.0;
         g_prof_count[k] = 0;
     }
@@ -815,7 +815,7 @@ int ssd_profile_read(float* total_ms, int* launches, int max_kinds, int* n_kinds
         g_prof_free.push_back(p.stop);
     }
     g_prof_open.clear();
-    const int n = max_kinds < kNumKinds ? max_kinds : kNumKinds;
+    const int n = max_kinds < kAllKinds ? max_kinds : kAllKinds;
     for (int k = 0; k < n; ++k) {
         if (total_ms) total_ms[k] = (float)g_prof_ms[k];
         if (launches) launches[k] = g_prof_count[k];
@@ -825,7 +825,7 @@ int ssd_profile_read(float* total_ms, int* launches, int max_kinds, int* n_kinds
 }
 
 const char* ssd_kernel_name(int kind) {
-    return (kind >= 0 && kind < kNumKinds) ? kKindNames[kind] : "unknown";
+    return (kind >= 0 && kind < kAllKinds) ? kKindNames[kind] : "unknown";
 }
 
 long long ssd_launch_count(void) {
