@@ -362,68 +362,82 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
             for (int e = 0; e < (LP >= 4 ? 1 : 4 / LP); ++e) to[4 * qd + which + e] = v[e];
         }
     };
+    // a token's dt, dt x, g, B and C; loaded a token ahead, so that no load waits behind a store it might meet
+    struct Operands {
+        float4 d, x, g, B, C;
+    };
+    auto operands = [&](int t) {
+        auto at = [](const float* p) { return *reinterpret_cast<const float4*>(p); };
+        return Operands{at(s_d + t * cc + 4 * qd), at(s_x + t * cc + 4 * qd), at(s_g + t * cc + 4 * qd), at(s_B + t * NP + 4 * q),
+                        at(s_C + t * NP + 4 * q)};
+    };
+    // four values over the warp's channels, to entries 4 q .. of a token's row of dB (which = 0) or dC (1)
+    auto join_channels = [&](float (&v)[4], int t, int half) {
+        int which = 0;
+        fold_between<4, 16, LP>(v, lane, which);
+        constexpr int LEFT = K::CW >= 4 ? 1 : 4 / K::CW;
+        float* to = s_red + ((warp * kRun + t % kRun) * 2 + half) * NP + 4 * q + which;
+        if (K::CW <= 4 || ((lane / LP) & (K::CW / 4 > 0 ? K::CW / 4 - 1 : 0)) == 0) {
+#pragma unroll
+            for (int e = 0; e < LEFT; ++e) to[e] = v[e];
+        }
+    };
     // tokens t0 .. t0 + 3 from the states before them: forward with y and dC, then backward with the rest
     auto half = [&](int t0) {
         f32x2 w[kHeld][4][2], wh[kHeld][4][2];  // the decays, and the decayed states
-        float dC[kHeld][4];
+        Operands o = operands(t0);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             const int t = t0 + i;
-            f32x2 d[2], x[2], g[2], B[4], C[4], y[2];
-            pairs_of(s_d + t * cc + 4 * qd, d);
-            pairs_of(s_x + t * cc + 4 * qd, x);
-            pairs_of(s_g + t * cc + 4 * qd, g);
-            twice_of(s_B + t * NP + 4 * q, B);
-            twice_of(s_C + t * NP + 4 * q, C);
+            const Operands next = operands(i + 1 < kHeld ? t + 1 : t);
+            const f32x2 d[2] = {pk(o.d.x, o.d.y), pk(o.d.z, o.d.w)}, x[2] = {pk(o.x.x, o.x.y), pk(o.x.z, o.x.w)},
+                        g[2] = {pk(o.g.x, o.g.y), pk(o.g.z, o.g.w)};
+            const float B[4] = {o.B.x, o.B.y, o.B.z, o.B.w}, C[4] = {o.C.x, o.C.y, o.C.z, o.C.w};
+            f32x2 y[2];
+            float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     w[i][e][j] = exp2_2(mul2(d[j], A[e][j]));
                     wh[i][e][j] = mul2(w[i][e][j], h[e][j]);
-                    h[e][j] = fma2(x[j], B[e], wh[i][e][j]);
-                    y[j] = e == 0 ? mul2(C[0], h[0][j]) : fma2(C[e], h[e][j], y[j]);
+                    h[e][j] = fma2(x[j], pk(B[e], B[e]), wh[i][e][j]);
+                    y[j] = e == 0 ? mul2(pk(C[0], C[0]), h[0][j]) : fma2(pk(C[e], C[e]), h[e][j], y[j]);
                 }
-                dC[i][e] = sum2(fma2(h[e][1], g[1], mul2(h[e][0], g[0])));
+                v[e] = sum2(fma2(h[e][1], g[1], mul2(h[e][0], g[0])));
             }
             join(y[0], y[1], s_y + t * cc);
+            join_channels(v, t, 1);
+            o = next;
         }
 #pragma unroll
         for (int i = kHeld - 1; i >= 0; --i) {
             const int t = t0 + i;
-            f32x2 d[2], x[2], g[2], B[4], C[4], sb[2], sa[2];
-            pairs_of(s_d + t * cc + 4 * qd, d);
-            pairs_of(s_x + t * cc + 4 * qd, x);
-            pairs_of(s_g + t * cc + 4 * qd, g);
-            twice_of(s_B + t * NP + 4 * q, B);
-            twice_of(s_C + t * NP + 4 * q, C);
-            float v[8];
+            const Operands next = operands(i > 0 ? t - 1 : t);
+            const f32x2 d[2] = {pk(o.d.x, o.d.y), pk(o.d.z, o.d.w)}, x[2] = {pk(o.x.x, o.x.y), pk(o.x.z, o.x.w)},
+                        g[2] = {pk(o.g.x, o.g.y), pk(o.g.z, o.g.w)};
+            const float B[4] = {o.B.x, o.B.y, o.B.z, o.B.w}, C[4] = {o.C.x, o.C.y, o.C.z, o.C.w};
+            f32x2 sb[2], sa[2];
+            float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 f32x2 lam[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    lam[j] = fma2(g[j], C[e], m[e][j]);
-                    sb[j] = e == 0 ? mul2(lam[j], B[0]) : fma2(lam[j], B[e], sb[j]);
+                    lam[j] = fma2(g[j], pk(C[e], C[e]), m[e][j]);
+                    sb[j] = e == 0 ? mul2(lam[j], pk(B[0], B[0])) : fma2(lam[j], pk(B[e], B[e]), sb[j]);
                     m[e][j] = mul2(lam[j], w[i][e][j]);
                     const f32x2 held = mul2(lam[j], wh[i][e][j]);
                     dA[e][j] = fma2(held, d[j], dA[e][j]);
                     sa[j] = e == 0 ? mul2(held, A[0][j]) : fma2(held, A[e][j], sa[j]);
                 }
                 v[e] = sum2(fma2(lam[1], x[1], mul2(lam[0], x[0])));
-                v[4 + e] = dC[i][e];
             }
-            // every lane of these channels has read the token's dt x and g: they are lanes of one warp
+            // in place of dt x and g: every lane of these channels, lanes of one warp, has read the token's
             join(sb[0], sb[1], s_x + t * cc);
             join(sa[0], sa[1], s_g + t * cc);
-            int which = 0;  // over the warp's channels: dB's four entries, then dC's
-            fold_between<8, 16, LP>(v, lane, which);
-            constexpr int LEFT = K::CW >= 8 ? 1 : 8 / K::CW;
-            if (K::CW <= 8 || (lane / LP) % (K::CW / 8 > 0 ? K::CW / 8 : 1) == 0) {
-#pragma unroll
-                for (int e = 0; e < LEFT; ++e)
-                    s_red[((warp * kRun + t % kRun) * 2 + (which + e) / 4) * NP + 4 * q + (which + e) % 4] = v[e];
-            }
+            join_channels(v, t, 0);
+            o = next;
         }
     };
 
