@@ -11,15 +11,15 @@
 //
 // Every kernel is bound by HBM: the inputs are read once, the outputs written once, and a handful of
 // multiply-adds with one exponential and one quotient per element hide under that.  So a thread holds V
-// neighbouring channels (16 bytes in the forward pass) and walks consecutive tokens with the last W-1 inputs
-// in registers, a warp covers 32 V channels of a row, and a token's halo is read again only at the start of
-// a thread's run of tokens, from L2.  Sums are float32; y, dx and the states are rounded once.
+// neighbouring channels and walks consecutive tokens with the last W-1 inputs in registers, a warp covers 32 V
+// channels of a row, and a token's halo is read again only at the start of a thread's run of tokens, from L2.  Sums are float32; y, dx and the states are rounded once.
 #include "ops.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kStep = 8;  // tokens of the forward kernel whose loads are in flight together
 
 // The taps and biases of V channels as pairs.  Tap 3 is the current token's: a narrower kernel's taps end there and its
 // first ones are unused (never multiplied: zero times an infinite input would be NaN).
@@ -80,66 +80,76 @@ __device__ __forceinline__ Vec<T, V> input_at(const ConvArgs& a, int b, int t, i
                           valid, vec);
 }
 
-// A warp: 32 V channels of RUN consecutive tokens, STEP of them loaded at a time so that a warp keeps that many loads
-// in flight.
+// A warp: 32 V channels of RUN consecutive tokens, STEP of them loaded at a time, one step ahead of their use.  Runs whose
+// tokens all count, most of them, are computed without looking at each.  Two channels a thread leave registers for 32 warps
+// an SM: at 2 x 4096 x 4352 of bfloat16 30.4 us (4.7 TB/s; a plain copy of as many bytes takes 22.6), where four channels
+// with half the warps take 33.3, steps of half as many tokens 33, runs of 16 tokens 34 and of 64 36.
 template <typename T, int V, int W, int RUN>
-__global__ void __launch_bounds__(32 * kWarps) conv_forward_kernel(ConvArgs a, Pieces y, T* __restrict__ final_state,
-                                                                   bool vec) {
-    constexpr int P = (V + 1) / 2, STEP = RUN < 8 ? RUN : 8;
+__global__ void __launch_bounds__(32 * kWarps, 8) conv_forward_kernel(ConvArgs a, Pieces y, T* __restrict__ final_state) {
+    constexpr int P = (V + 1) / 2, STEP = RUN < kStep ? RUN : kStep;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.z, c = (blockIdx.x * 32 + lane) * V;
     const int valid = min(V, a.channels - c);
     if (valid <= 0) return;
     const int len = row_length(a.lengths, b, a.seqlen);
-    const int64_t row0 = (int64_t)b * a.seqlen;
     if (final_state != nullptr && blockIdx.y == 0 && warp < W - 1) {
-        const Vec<T, V> v = input_at<T, V>(a, b, len - (W - 1) + warp, len, c, valid, vec);
-        store_vec<T, V>(final_state + ((int64_t)b * (W - 1) + warp) * a.channels + c, v, valid, vec);
+        const Vec<T, V> v = input_at<T, V>(a, b, len - (W - 1) + warp, len, c, valid, true);
+        store_vec<T, V>(final_state + ((int64_t)b * (W - 1) + warp) * a.channels + c, v, valid, true);
     }
     const int t0 = (blockIdx.y * kWarps + warp) * RUN;
     if (t0 >= a.seqlen) return;
-    Vec<T, V> in[STEP];
-    f32x2 x[STEP + 3][P];  // the inputs of this step's tokens, after the three before them
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, vec) : Vec<T, V>::zero();
-#pragma unroll
-        for (int i = 0; i < P; ++i) x[k][i] = v.pair(i);
-    }
-    f32x2 w[4][P], bias[P];
-    load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
     const int64_t xt = a.x_token;
     const T* xp = static_cast<const T*>(a.x) + b * a.x_batch + t0 * xt + c;
-    int piece = c < y.n[0] ? 0 : c - y.n[0] < y.n[1] ? 1 : 2;
-    const int wide = piece == 0 ? y.n[0] : piece == 1 ? y.n[1] : y.n[2];
-    T* yp = piece_at<T>(y, row0 + t0, c);
-#pragma unroll 1
-    for (int s = 0; s < RUN; s += STEP) {
+    const int wide = c < y.n[0] ? y.n[0] : c - y.n[0] < y.n[1] ? y.n[1] : y.n[2];
+    T* yp = piece_at<T>(y, (int64_t)b * a.seqlen + t0, c);
+    auto run = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        Vec<T, V> next[STEP];
+        auto fetch = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < STEP; ++i) in[i] = load_vec<T, V>(xp + i * xt, t0 + s + i < len ? valid : 0, vec);
-        xp += STEP * xt;
-#pragma unroll
-        for (int i = 0; i < STEP; ++i)
-#pragma unroll
-            for (int j = 0; j < P; ++j) x[3 + i][j] = in[i].pair(j);
-#pragma unroll
-        for (int i = 0; i < STEP; ++i) {
-            const int t = t0 + s + i;
-            if (t >= a.seqlen) return;
-            f32x2 pre[P];
-            taps_times<W, P>(w, bias, x + i, pre);
-            if (a.silu) {
-#pragma unroll
-                for (int j = 0; j < P; ++j) pre[j] = mul2(pre[j], sigmoid2(pre[j]));
+            for (int i = 0; i < STEP; ++i) {
+                next[i] = load_vec<T, V>(xp, WHOLE || t + i < len ? valid : 0, true);
+                xp += xt;
             }
-            store_vec<T, V>(yp, t < len ? Vec<T, V>::of_pairs(pre) : Vec<T, V>::zero(), valid, vec);
-            yp += wide;
+        };
+        fetch(t0);
+        f32x2 x[STEP + 3][P];  // the inputs of this step's tokens, after the three before them
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, true) : Vec<T, V>::zero();
+#pragma unroll
+            for (int i = 0; i < P; ++i) x[k][i] = v.pair(i);
         }
+        f32x2 w[4][P], bias[P];
+        load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
+#pragma unroll 1
+        for (int s = 0; s < RUN; s += STEP) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
+            for (int i = 0; i < STEP; ++i)
 #pragma unroll
-            for (int j = 0; j < P; ++j) x[k][j] = x[STEP + k][j];
-    }
+                for (int j = 0; j < P; ++j) x[3 + i][j] = next[i].pair(j);
+            if (s + STEP < RUN) fetch(t0 + s + STEP);
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+                const int t = t0 + s + i;
+                f32x2 pre[P];
+                taps_times<W, P>(w, bias, x + i, pre);
+                if (a.silu) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) pre[j] = mul2(pre[j], sigmoid2(pre[j]));
+                }
+                store_vec<T, V>(yp, WHOLE || t < len ? Vec<T, V>::of_pairs(pre) : Vec<T, V>::zero(),
+                                WHOLE || t < a.seqlen ? valid : 0, true);
+                yp += wide;
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) x[k][j] = x[STEP + k][j];
+        }
+    };
+    if (t0 + RUN <= len) run(std::true_type());
+    else run(std::false_type());
 }
 
 // The gradient's piece that holds channel c: its base, its width, the channel's place in it.
@@ -159,16 +169,19 @@ __device__ __forceinline__ GradPiece grad_piece(const Pieces& dy, int c) {
 // dLoss/dpre up to W-1 tokens on, so the walk goes that far past the run (those tokens' pre again).  Tokens are taken
 // four at a time: their x and dy are loaded together, one group ahead of their use; groups whose tokens all count and
 // all leave, most of them, are computed without looking at each.  The block's warps' sums of one channel are joined in
-// shared memory in warp order and written as one row of `partial`, (rows, width + 1, channels).
+// shared memory in warp order and written as one row of `partial`, (rows, width + 1, channels).  Bound by issue slots
+// (13 multiply-adds, an exponential, a quotient and the conversions per element; 61% of the slots are used), not by HBM:
+// at 2 x 4096 x 4352 of bfloat16 66 us, with the reduction, where 20 warps an SM hold two channels a thread; four
+// channels and 12 warps 71, 16 warps 75, 24 warps 71, groups of two tokens 87 and of eight 82.
 template <typename T, int V, int W, int RUN>
-__global__ void __launch_bounds__(32 * kWarps, V == 4 ? 3 : 4) conv_backward_kernel(
+__global__ void __launch_bounds__(32 * kWarps, V == 2 ? 5 : 4) conv_backward_kernel(
     ConvArgs a, Pieces dy, const T* __restrict__ dfinal, T* __restrict__ dx, int64_t dx_batch, int64_t dx_token,
     T* __restrict__ dinit, float* __restrict__ partial) {
     constexpr int S = 4, P = (V + 1) / 2;
     __shared__ float sums[kWarps][W + 1][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.z, c = (blockIdx.x * 32 + lane) * V;
-    const int valid = max(0, min(V, a.channels - c));
+    constexpr int valid = V;  // channels are whole vectors
     const int len = row_length(a.lengths, b, a.seqlen);
     const int t0 = (blockIdx.y * kWarps + warp) * RUN;
     f32x2 dw[W][P], db[P];
@@ -178,7 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps, V == 4 ? 3 : 4) conv_backward_ker
 #pragma unroll
         for (int k = 0; k < W; ++k) dw[k][j] = 0ull;
     }
-    if (valid > 0 && t0 < a.seqlen) {
+    if (c < a.channels && t0 < a.seqlen) {
         f32x2 w[4][P], bias[P];
         load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
         // the run itself; the first one also gives the initial state's tokens, which have no output of their own
@@ -202,20 +215,25 @@ __global__ void __launch_bounds__(32 * kWarps, V == 4 ? 3 : 4) conv_backward_ker
         Vec<T, V> nx[S];
         Vec<float, V> ng[S];  // dy as it lies in memory, in the first words where it is of 16 bits
         auto fetch = [&](int t) {
+            auto load = [&](auto whole, auto wide) {
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                const int got = t + i < lim ? valid : 0;
-                nx[i] = load_vec<T, V>(xp, got, true);
-                xp += xstep;
-                if (sizeof(T) == 4 || gr.f32) {
-                    ng[i] = load_vec<float, V>(reinterpret_cast<const float*>(gp), got, true);
-                } else {
-                    const Vec<T, V> v = load_vec<T, V>(reinterpret_cast<const T*>(gp), got, true);
+                for (int i = 0; i < S; ++i) {
+                    const int got = decltype(whole)::value || t + i < lim ? valid : 0;
+                    nx[i] = load_vec<T, V>(xp, got, true);
+                    xp += xstep;
+                    if constexpr (decltype(wide)::value) {
+                        ng[i] = load_vec<float, V>(reinterpret_cast<const float*>(gp), got, true);
+                    } else {
+                        const Vec<T, V> v = load_vec<T, V>(reinterpret_cast<const T*>(gp), got, true);
 #pragma unroll
-                    for (int u = 0; u < Vec<T, V>::WORDS; ++u) ng[i].w[u] = v.w[u];
+                        for (int u = 0; u < Vec<T, V>::WORDS; ++u) ng[i].w[u] = v.w[u];
+                    }
+                    gp += gstep;
                 }
-                gp += gstep;
-            }
+            };
+            const bool all = t + S <= lim;
+            if (sizeof(T) == 4 || gr.f32) all ? load(std::true_type(), std::true_type()) : load(std::false_type(), std::true_type());
+            else all ? load(std::true_type(), std::false_type()) : load(std::false_type(), std::false_type());
         };
         // one group of tokens from t on; WHOLE: t + S <= min(len, last) and t - (W-1) >= first, no final state's gradient
         auto group = [&](int t, auto whole) {
@@ -229,7 +247,9 @@ __global__ void __launch_bounds__(32 * kWarps, V == 4 ? 3 : 4) conv_backward_ker
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     x[3 + i][j] = nx[i].pair(j);
-                    unpk(sizeof(T) == 4 || gr.f32 ? ng[i].pair(j) : gt.pair(j), gv[i][2 * j], gv[i][2 * j + 1]);
+                    f32x2 q = ng[i].pair(j);
+                    if (sizeof(T) != 4 && !gr.f32) q = gt.pair(j);
+                    unpk(q, gv[i][2 * j], gv[i][2 * j + 1]);
                 }
             }
             if (t + S < last + W - 1) fetch(t + S);
@@ -420,15 +440,15 @@ void run_forward(const ConvArgs& a, const Pieces& y, void* final_state, cudaStre
     // long runs read the taps and the halo of W-1 tokens rarely; short ones fill the SMs on short prompts
     auto blocks = [&](int run) { return dim3(tiles, ceil_div(a.seqlen, kWarps * run), a.batch); };
     if ((int64_t)tiles * a.batch * ceil_div(a.seqlen, kWarps * 32) >= 304)
-        conv_forward_kernel<T, V, W, 32><<<blocks(32), 32 * kWarps, 0, s>>>(a, y, f, true);
+        conv_forward_kernel<T, V, W, 32><<<blocks(32), 32 * kWarps, 0, s>>>(a, y, f);
     else
-        conv_forward_kernel<T, V, W, 4><<<blocks(4), 32 * kWarps, 0, s>>>(a, y, f, true);
+        conv_forward_kernel<T, V, W, 4><<<blocks(4), 32 * kWarps, 0, s>>>(a, y, f);
 }
 
 template <typename T, int W>
 int forward_of(const ConvArgs& a, const Pieces& y, void* final_state, cudaStream_t s) {
     launch_begin(kKindConv, s);
-    if (whole_vectors(a, y, final_state, nullptr, 4, sizeof(T))) run_forward<T, 4, W>(a, y, final_state, s);
+    if (whole_vectors(a, y, final_state, nullptr, 2, sizeof(T))) run_forward<T, 2, W>(a, y, final_state, s);
     else run_forward<T, 1, W>(a, y, final_state, s);
     return launch_end(kKindConv, s);
 }
@@ -446,16 +466,16 @@ int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* d
     const T* df = static_cast<const T*>(dfinal);
     T *o = static_cast<T*>(dx), *di = static_cast<T*>(dinit);
     const int run = backward_run(a), rows = ceil_div(a.seqlen, kWarps * run);
-    const bool fours = whole_vectors(a, dy, dfinal, dinit, 4, sizeof(T)) && dx_batch % 4 == 0 && dx_token % 4 == 0 &&
-                       on(dx, 4 * sizeof(T));
+    const bool pairs = whole_vectors(a, dy, dfinal, dinit, 2, sizeof(T)) && dx_batch % 2 == 0 && dx_token % 2 == 0 &&
+                       on(dx, 2 * sizeof(T));
     launch_begin(kKindConvBwd, s);
     auto go = [&](auto kernel, int channels) {
         kernel<<<dim3(ceil_div(a.channels, channels), rows, a.batch), 32 * kWarps, 0, s>>>(a, dy, df, o, dx_batch, dx_token, di,
                                                                                           partial);
     };
-    if (fours) {
-        if (run == kLongRun) go(conv_backward_kernel<T, 4, W, kLongRun>, 128);
-        else go(conv_backward_kernel<T, 4, W, kShortRun>, 128);
+    if (pairs) {
+        if (run == kLongRun) go(conv_backward_kernel<T, 2, W, kLongRun>, 64);
+        else go(conv_backward_kernel<T, 2, W, kShortRun>, 64);
     } else {
         if (run == kLongRun) go(conv_backward_kernel<T, 1, W, kLongRun>, 32);
         else go(conv_backward_kernel<T, 1, W, kShortRun>, 32);
