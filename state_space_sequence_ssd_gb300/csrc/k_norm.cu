@@ -67,61 +67,85 @@ __device__ __forceinline__ void load_columns(const float* p, int c, int width, b
     }
 }
 
-// NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  A block takes its rows and
-// ends: at 8192 x 2048 bf16 that takes 19.7 us with two vectors a thread, where a resident grid whose blocks walk the
-// rows with the next one's loads in flight took 20.2 to 25, and one warp a row 23.
-template <typename T, int V, int NV>
+// R neighbouring rows of NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  A block
+// takes its rows and ends.  Two rows a thread share the reductions' barriers and the reads of weight and bias, four times
+// a row's bytes: at 8192 x 2048 of bfloat16 17.5 us (3.8 TB/s; a plain copy of as many bytes takes 11.8) where one row
+// takes 19.3, a resident grid whose blocks walk the rows with the next one's loads in flight 20 to 25, one warp a row 23.
+template <typename T, int V, int NV, int R>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restrict__ x, int64_t x_row,
                                                                 const float* __restrict__ weight,
                                                                 const float* __restrict__ bias, float eps, int64_t rows,
                                                                 int width, int lanes, T* __restrict__ y,
                                                                 float* __restrict__ mean, float* __restrict__ rstd, bool vecw) {
+    static_assert(R == 1 || R == 2, "one or two rows");
     constexpr int P = (V + 1) / 2;
     __shared__ float2 buf[2][kThreads / 32];
     const int lane = threadIdx.x & (lanes - 1);
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
-    const bool live = row < rows;
-    const T* xr = x + (live ? row : 0) * x_row;
+    const int64_t row = ((int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes) * R;
     const float inv = 1.f / (float)width;
-    Vec<T, V> r[NV];
+    Vec<T, V> r[R][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + lanes * i) * V;
-        r[i] = load_vec<T, V>(xr + c, live ? width - c : 0, true);
-    }
-    f32x2 s2 = 0ull, q2 = 0ull;
+    for (int k = 0; k < R; ++k) {
+        const bool live = row + k < rows;
+        const T* xr = x + (live ? row + k : 0) * x_row;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < P; ++e) s2 = add2(s2, r[i].pair(e));
-    const float m = row_sum(sum2(s2), lanes, buf[0]) * inv;
-    const f32x2 m2 = pk(-m, V > 1 ? -m : 0.f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if ((lane + lanes * i) * V < width) {
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-                const f32x2 d = add2(r[i].pair(e), m2);
-                q2 = fma2(d, d, q2);
-            }
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + lanes * i) * V;
+            r[k][i] = load_vec<T, V>(xr + c, live ? width - c : 0, true);
         }
-    const float rs = rsqrtf(fmaf(row_sum(sum2(q2), lanes, buf[1]), inv, eps));
-    if (!live) return;
-    if (lane == 0) {
-        if (mean != nullptr) mean[row] = m;
-        if (rstd != nullptr) rstd[row] = rs;
     }
-    T* yr = y + row * width;
+    float m[2] = {0.f, 0.f}, rs[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        f32x2 s = 0ull;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < P; ++e) s = add2(s, r[k][i].pair(e));
+        m[k] = sum2(s) * inv;
+    }
+    const float2 mm = row_sums(make_float2(m[0], m[1]), lanes, buf[0]);
+    m[0] = mm.x;
+    m[1] = mm.y;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const f32x2 m2 = pk(-m[k], V > 1 ? -m[k] : 0.f);
+        f32x2 q = 0ull;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((lane + lanes * i) * V < width) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const f32x2 d = add2(r[k][i].pair(e), m2);
+                    q = fma2(d, d, q);
+                }
+            }
+        rs[k] = sum2(q) * inv;
+    }
+    const float2 qq = row_sums(make_float2(rs[0], rs[1]), lanes, buf[1]);
+    rs[0] = rsqrtf(qq.x + eps);
+    rs[1] = rsqrtf(qq.y + eps);
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+        if (lane == 0 && row + k < rows) {
+            if (mean != nullptr) mean[row + k] = m[k];
+            if (rstd != nullptr) rstd[row + k] = rs[k];
+        }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + lanes * i) * V;
         if (c >= width) break;
-        f32x2 o[P], w[P], b[P];
+        f32x2 w[P], b[P];
         load_columns<V>(weight, c, width, vecw, 1.f, w);
         load_columns<V>(bias, c, width, vecw, 0.f, b);
 #pragma unroll
-        for (int e = 0; e < P; ++e) o[e] = fma2(mul2(add2(r[i].pair(e), m2), pk(rs, rs)), w[e], b[e]);
-        store_vec<T, V>(yr + c, Vec<T, V>::of_pairs(o), width - c, true);
+        for (int k = 0; k < R; ++k) {
+            f32x2 o[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+                o[e] = fma2(mul2(add2(r[k][i].pair(e), pk(-m[k], -m[k])), pk(rs[k], rs[k])), w[e], b[e]);
+            store_vec<T, V>(y + (row + k) * width + c, Vec<T, V>::of_pairs(o), row + k < rows ? width - c : 0, true);
+        }
     }
 }
 
@@ -157,7 +181,10 @@ __global__ void __launch_bounds__(kThreads) norm_forward_wide_kernel(const T* __
 }
 
 // A block of `lanes` threads a row, kThreads / lanes rows at a time.  The thread's columns of dweight and dbias stay
-// in registers while the block walks its rows, and the next rows' loads are in flight while a row is summed.
+// in registers while the block walks its rows, and the next rows' loads are in flight while a row is summed.  With the
+// reduction 26.7 us at 8192 x 2048 of bfloat16 (a plain sum of two such tensors takes 15.7): 53% of the issue slots at 16
+// warps an SM, which the sums' registers allow.  Smaller parts of a row a thread (8 columns instead of 16) and more
+// blocks took 39 us and more, loads three rows ahead through shared memory as long as these one row ahead.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __restrict__ x, int64_t x_row,
                                                                  const float* __restrict__ weight,
@@ -294,24 +321,26 @@ __global__ void __launch_bounds__(kThreads) norm_backward_wide_kernel(const T* _
     }
 }
 
-// dweight and dbias from the blocks' rows of `partial`: eight strided sums, then those eight.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restrict__ partial, int parts, int width,
+// dweight and dbias from the blocks' rows of `partial`: kJoin strided sums, then those.  The rows lie in L2 and what counts
+// is how many of them are on their way at once.
+constexpr int kJoin = 32;
+__global__ void __launch_bounds__(32 * kJoin) norm_reduce_kernel(const float* __restrict__ partial, int parts, int width,
                                                           float* __restrict__ dweight, float* __restrict__ dbias) {
-    __shared__ float part[8][33];
+    __shared__ float part[kJoin][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
     grid_dep_wait();
     float s = 0.f;
     if (i < 2 * width) {
-#pragma unroll 16
-        for (int r = warp; r < parts; r += 8) s += partial[(int64_t)r * 2 * width + i];
+#pragma unroll 8
+        for (int r = warp; r < parts; r += kJoin) s += partial[(int64_t)r * 2 * width + i];
     }
     part[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || i >= 2 * width) return;
     s = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += part[q][lane];
+    for (int q = 0; q < kJoin; ++q) s += part[q][lane];
     if (i < width) {
         if (dweight != nullptr) dweight[i] = s;
     } else if (dbias != nullptr) {
@@ -337,7 +366,10 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
     const int vecs = ceil_div(width, V);
     const int lanes = row_lanes(rows, vecs, 2 * M, 1);
     const int nv = ceil_div(vecs, lanes);
-    const int64_t blocks = ceil_div64(rows, kThreads / lanes);
+    // Two rows a thread where the SMs have 1024 threads' work all the same: with one and with two rows 3.7 and 3.4 us at
+    // 608 x 2048 of bfloat16, 9.0 and 6.2 at 608 x 8192, 11.8 and 10.6 at 4864 x 2048; but 5.2 and 5.6 at 304 x 8192.
+    const bool two = rows * lanes >= 152 * 1024 && nv <= 4 * M;
+    const int64_t blocks = ceil_div64(rows, kThreads / lanes * (two ? 2 : 1));
     const bool vecw = on(weight, 16) && on(bias, 16);
     const T* xt = static_cast<const T*>(x);
     T* yt = static_cast<T*>(y);
@@ -346,10 +378,10 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)blocks, kThreads, 0, s>>>(xt, x_row, weight, bias, eps, rows, width, lanes, yt, mean, rstd, vecw);
     };
-    if (nv <= 1 * M) go(norm_forward_kernel<T, V, 1 * M>);
-    else if (nv <= 2 * M) go(norm_forward_kernel<T, V, 2 * M>);
-    else if (nv <= 4 * M) go(norm_forward_kernel<T, V, 4 * M>);
-    else if (nv <= 8 * M) go(norm_forward_kernel<T, V, 8 * M>);
+    if (nv <= 1 * M) two ? go(norm_forward_kernel<T, V, 1 * M, 2>) : go(norm_forward_kernel<T, V, 1 * M, 1>);
+    else if (nv <= 2 * M) two ? go(norm_forward_kernel<T, V, 2 * M, 2>) : go(norm_forward_kernel<T, V, 2 * M, 1>);
+    else if (nv <= 4 * M) two ? go(norm_forward_kernel<T, V, 4 * M, 2>) : go(norm_forward_kernel<T, V, 4 * M, 1>);
+    else if (nv <= 8 * M) go(norm_forward_kernel<T, V, 8 * M, 1>);
     else
         norm_forward_wide_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(xt, x_row, weight, bias, eps, width, yt, mean, rstd);
     return launch_end(kKindNorm, s);
@@ -407,8 +439,7 @@ int launch_layer_norm_forward(int dtype, const void* x, int64_t x_row, const flo
 }
 
 // Blocks of the backward kernel: two per SM, or one per eight rows where there are few.
-int layer_norm_parts(int64_t rows, int width, int sms) {
-    (void)width;
+int layer_norm_parts(int64_t rows, int sms) {
     const int64_t want = ceil_div64(rows, 8);
     return (int)(want < 2 * sms ? want : 2 * sms);
 }
@@ -425,7 +456,7 @@ int launch_layer_norm_backward(int dtype, const void* x, int64_t x_row, const fl
         r = backward_type<float>(x, x_row, weight, mean, rstd, dy, dy_row, rows, width, dx, partial, parts, s);
     if (r != SSD_OK || partial == nullptr) return r;
     launch_begin(kKindNormBwd, s);
-    launch_dependent(norm_reduce_kernel, dim3(ceil_div(2 * width, 32)), dim3(256), 0, s, partial, parts, width, dweight, dbias);
+    launch_dependent(norm_reduce_kernel, dim3(ceil_div(2 * width, 32)), dim3(32 * kJoin), 0, s, partial, parts, width, dweight, dbias);
     return launch_end(kKindNormBwd, s);
 }
 

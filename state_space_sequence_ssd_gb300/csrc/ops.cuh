@@ -294,8 +294,8 @@ int launch_selective_step(const SelectiveArgs& a, float* state, const int* slots
 
 int launch_layer_norm_forward(int dtype, const void* x, int64_t x_row, const float* weight, const float* bias, float eps,
                               int64_t rows, int width, void* y, float* mean, float* rstd, cudaStream_t s);
-// partial: layer_norm_parts(rows, width, sms) x 2 x width float32
-int layer_norm_parts(int64_t rows, int width, int sms);
+// partial: layer_norm_parts(rows, sms) x 2 x width float32
+int layer_norm_parts(int64_t rows, int sms);
 int launch_layer_norm_backward(int dtype, const void* x, int64_t x_row, const float* weight, const float* mean,
                                const float* rstd, const void* dy, int64_t dy_row, int64_t rows, int width, void* dx,
                                float* dweight, float* dbias, float* partial, int parts, cudaStream_t s);

@@ -231,7 +231,7 @@ int ssd_layer_norm_backward(int dtype, const void* x, long long x_row_stride, co
     if (!on(x, size) || !on(dy, size) || !on(dx, size) || !on(weight, 4) || !on(mean, 4) || !on(rstd, 4) ||
         !on(dweight, 4) || !on(dbias, 4))
         return SSD_ERR_INVALID_ARG;
-    const int parts = layer_norm_parts(rows, width, multiprocessors());
+    const int parts = layer_norm_parts(rows, multiprocessors());
     void* ws = nullptr;
     if ((dweight != nullptr || dbias != nullptr) &&
         take_workspace(&ws, (size_t)parts * 2 * width * sizeof(float), stream) != SSD_OK)
