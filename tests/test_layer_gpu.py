@@ -416,3 +416,56 @@ def test_another_stream(ssd):
     ny2, _, _ = ssd.ssd_layer_norm_forward(s["x"], stream=other)
     torch.cuda.current_stream().wait_stream(other)
     assert torch.equal(y, want) and torch.equal(final, wfinal) and torch.equal(cy, cy2) and torch.equal(ny, ny2)
+
+
+# ------------------------------------------------------------------------------------------------ long strides
+
+def test_offsets_past_32_bits(ssd):
+    """Slices of rows so wide that the last tokens lie more than 2^31 elements on: the results are those of dense copies."""
+    d, T, L, ch, N = Draw(4), torch.bfloat16, 2200, 40, 8
+    wide = torch.empty(1, L, 1 << 20, device="cuda", dtype=T)
+    assert wide.stride(1) * (L - 1) > 2 ** 31
+    wide[..., :4 * ch + 2 * N] = d.normal(1, L, 4 * ch + 2 * N, dtype=T)
+    x, dt, z, dx = (wide[..., i * ch:(i + 1) * ch] for i in range(4))
+    B, C = (wide[..., 4 * ch + i * N:4 * ch + (i + 1) * N].unflatten(-1, (1, N)) for i in range(2))
+    dense = lambda *ts: [t.contiguous() for t in ts]
+    w, bias, A, dy = d.normal(ch, 4), d.normal(ch), -d.normal(ch, N).abs(), d.normal(1, L, ch, dtype=T)
+
+    def same(a, b):
+        a, b = ([v for v in (o.values() if isinstance(o, dict) else o) if v is not None] for o in (a, b))
+        assert len(a) == len(b) and all(torch.equal(p, q) for p, q in zip(a, b))
+
+    same(ssd.ssd_conv_forward(x, w, bias), ssd.ssd_conv_forward(*dense(x), w, bias))
+    want = ssd.ssd_conv_backward(*dense(x), w, bias, dy)
+    same(ssd.ssd_conv_backward(x, w, bias, dy, dx=dx), want)
+    assert torch.equal(dx, want["dx"])
+    opts = dict(dt_bias=bias, dt_softplus=True)
+    same(ssd.ssd_selective_forward(x, dt, A, B, C, bias, z=z, **opts),
+         ssd.ssd_selective_forward(*dense(x, dt), A, *dense(B, C), bias, z=z.contiguous(), **opts))
+    same(ssd.ssd_selective_backward(x, dt, A, B, C, bias, dy, z=z, **opts),
+         ssd.ssd_selective_backward(*dense(x, dt), A, *dense(B, C), bias, dy, z=z.contiguous(), **opts))
+    want = ssd.ssd_layer_norm_forward(*dense(x[0]), w[:, 0].contiguous(), bias)
+    same(ssd.ssd_layer_norm_forward(x[0], w[:, 0].contiguous(), bias), want)
+    same(ssd.ssd_layer_norm_backward(x[0], w[:, 0].contiguous(), *want[1:], dy[0]),
+         ssd.ssd_layer_norm_backward(*dense(x[0]), w[:, 0].contiguous(), *want[1:], dy[0]))
+
+
+@pytest.mark.parametrize("op", ["conv", "selective"])
+def test_slots_past_32_bits(ssd, op):
+    """A pool whose last slots lie more than 2^31 elements on."""
+    d, ch = Draw(6), 512
+    rest = (4, ch) if op == "selective" else (3, ch)
+    n = 2 ** 31 // (rest[0] * ch) + 3
+    pool = torch.empty(n, *((ch, 4) if op == "selective" else rest), device="cuda", dtype=torch.float32)
+    slots = torch.tensor([n - 1, 1, n - 2], dtype=torch.int32, device="cuda")
+    small = d.normal(3, *pool.shape[1:])
+    pool[slots.long()] = small
+    x = d.normal(3, ch)
+    if op == "conv":
+        run = lambda state, at: ssd.ssd_conv_step(x, w, None, state, at)
+        w = d.normal(ch, 4)
+    else:
+        run = lambda state, at: ssd.ssd_selective_step(x, x.abs(), A, B, B, None, state, at)
+        A, B = -d.normal(ch, 4).abs(), d.normal(3, 1, 4)
+    y = run(pool, slots)
+    assert torch.equal(y, run(small, None)) and torch.equal(pool[slots.long()], small)
