@@ -163,19 +163,24 @@ SelectivePlan selective_plan(const SelectiveArgs& a, int sms) {
     // the last need): wide lanes 640, 740 and 900 (380, 460 and 570), narrow ones, which do a quarter of that work, 250,
     // 290 and 350 (180, 210 and 250) -- so narrow lanes where the SMs would otherwise stay idle.  A split costs two
     // launches and the hop besides, about 5 us and 60 ns a chunk.
+    // Where rows have their own lengths half of the blocks are taken to have work (the others end at once): with lengths
+    // spread evenly from nothing to the row 166 us at 8 x 2048 x 2048 x 16 of bfloat16 and 108 at 16 x 512 x 2048 x 16,
+    // 192 and 115 with the split for whole rows; with whole rows 285 and 160, 304 and 159; with at least half rows 263 and
+    // 144, 252 and 139.
     SelectivePlan best = {true, 1};
     double best_t = -1.0;
     for (int wide = a.dstate <= 16 ? 0 : 1; wide <= 1; ++wide) {
         const SelectiveShape f = selective_shape(a, wide != 0);
         const int64_t blocks = (int64_t)a.batch * a.ngroups * ceil_div(a.channels / a.ngroups, f.cc);
+        const int share = a.lengths != nullptr ? 2 : 1;
         const int64_t slots = (int64_t)sms * (3 * 128 / f.threads);
         auto run = [&](int64_t n, double one, double two, double three) {
             const double rest = (double)((n % slots + sms - 1) / sms) * f.threads / 128;  // warps on a quarter in the last wave
             return (double)(n / slots) * three + (rest <= 0 ? 0.0 : rest <= 1 ? one : rest <= 2 ? two : three);
         };
         for (int k = 1; k <= 512 && (k == 1 || a.seqlen / k >= 32); ++k) {
-            double t = wide ? run(blocks * k, 640.0, 740.0, 900.0) : run(blocks * k, 250.0, 290.0, 350.0);
-            if (k > 1) t += wide ? run(blocks * (k - 1), 380.0, 460.0, 570.0) : run(blocks * (k - 1), 180.0, 210.0, 250.0);
+            double t = wide ? run(ceil_div64(blocks * k, share), 640.0, 740.0, 900.0) : run(ceil_div64(blocks * k, share), 250.0, 290.0, 350.0);
+            if (k > 1) t += wide ? run(ceil_div64(blocks * (k - 1), share), 380.0, 460.0, 570.0) : run(ceil_div64(blocks * (k - 1), share), 180.0, 210.0, 250.0);
             t *= (double)a.seqlen / k;
             if (k > 1) t += 10000.0 + 120.0 * k;
             if (best_t < 0.0 || t < best_t) {

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
         }
         copies_commit();
     };
-    if (tb < last || !STATE_ONLY) fetch(tb, 0);
+    if (tb < last) fetch(tb, 0);
 
     // this lane's channels CH qd .. and entries ST q ..
     const int qd = tid / LP, q = tid % LP;
@@ -210,11 +210,11 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
     T* yp = y + ((int64_t)b * a.seqlen + tb + w0) * a.channels + g0 + 4 * v0;
 
     int buf = 0;
-    for (int t0 = tb; t0 < te; t0 += TS, buf ^= 1) {
-        if (STATE_ONLY && t0 >= last) break;
+    int t0 = tb;
+    for (; t0 < last; t0 += TS, buf ^= 1) {
         copies_wait<0>();
         __syncthreads();  // the tile's copies have landed; the last tile's sums and inputs are read
-        if (t0 + TS < te) fetch(t0 + TS, buf ^ 1);
+        if (t0 + TS < last) fetch(t0 + TS, buf ^ 1);
         const T* in = raw + buf * buffer;
         if (w0 < TS) {
             // all of the thread's vectors side by side: each value's dt is a chain of a dozen dependent instructions
@@ -325,6 +325,12 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
                 }
             }
             yp += (int64_t)TS * a.channels;
+        }
+    }
+    if (!STATE_ONLY) {  // the tiles past the row's length
+        for (int t = t0 + w0; t < te; t += K::CONV) {
+            store_vec<T, 4>(yp, Vec<T, 4>::zero(), vc, VEC);
+            yp += (int64_t)K::CONV * a.channels;
         }
     }
     float* to = nullptr;
