@@ -63,11 +63,14 @@ namespace {
 // A lane holds four state entries of one channel for R rows, and LP lanes share the channel.  Bound by HBM: the state
 // is read and written once.  The rows' states are loaded together and A once for them; each of the first R lanes
 // forms one row's dt and gate for the others, and ends with that row's output.  An idle row (slot -1) writes zeros
-// and leaves every slot alone.
-template <typename T, int LP, int R>
-__global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, float* __restrict__ state,
+// and leaves every slot alone.  VEC: states, A, B and C are whole vectors of four entries, known when it is compiled.
+// 256 rows of 4096 x 16 take 29.4 us, 4.6 TB/s; half of that is instructions (65% of the issue slots are used), and more
+// bytes in flight do not help: eight rows copied to shared memory ahead 31, two rows or one 33 and 41, a fifth block an SM 36.
+template <typename T, int LP, int R, bool VEC>
+__global__ void __launch_bounds__(256, 4) selective_step_kernel(SelectiveArgs a, float* __restrict__ state,
                                                              const int* __restrict__ slots, int nslots, T* __restrict__ y,
-                                                             int* err, bool vecs, bool vecb) {
+                                                             int* err, bool some, bool someb) {
+    const bool vecs = VEC || some, vecb = VEC || someb;  // states and A; B and C
     const int b0 = blockIdx.y * R, N = a.dstate, q = threadIdx.x % LP;
     const int64_t c = (int64_t)blockIdx.x * (256 / LP) + threadIdx.x / LP;
     const bool mine = c < a.channels;
@@ -134,11 +137,13 @@ int step_lanes(const SelectiveArgs& a, float* state, const int* slots, int nslot
     const bool vecs = a.dstate % 4 == 0 && aligned_to(state, 16) && aligned_to(a.A, 16), vecb = states_of_four(a, sizeof(T));
     const int tiles = ceil_div(a.channels, 256 / LP);
     launch_begin(kKindSelectiveStep, s);
+    auto go = [&](auto kernel, int rows) {
+        kernel<<<dim3(tiles, ceil_div(a.batch, rows)), 256, 0, s>>>(a, state, slots, nslots, y, err, vecs, vecb);
+    };
     // several rows a thread where the batch fills the SMs all the same
-    if (a.batch / R * tiles >= 152 * 4)
-        selective_step_kernel<T, LP, R><<<dim3(tiles, ceil_div(a.batch, R)), 256, 0, s>>>(a, state, slots, nslots, y, err, vecs, vecb);
-    else
-        selective_step_kernel<T, LP, 1><<<dim3(tiles, a.batch), 256, 0, s>>>(a, state, slots, nslots, y, err, vecs, vecb);
+    const bool many = a.batch / R * tiles >= 152 * 4;
+    if (vecs && vecb) many ? go(selective_step_kernel<T, LP, R, true>, R) : go(selective_step_kernel<T, LP, 1, true>, 1);
+    else many ? go(selective_step_kernel<T, LP, R, false>, R) : go(selective_step_kernel<T, LP, 1, false>, 1);
     return launch_end(kKindSelectiveStep, s);
 }
 
