@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(256) selective_hops_kernel(const float* __rest
 
 template <typename T, int LP>
 __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
-                                                                 float* __restrict__ hops, const float* __restrict__ mus,
+                                                                 const float* start, const float* end, float* dA_parts,
                                                                  T* __restrict__ dx, T* __restrict__ ddt,
                                                                  T* __restrict__ dz, float* __restrict__ dbc,
                                                                  float* __restrict__ chan, bool vec, bool vecb) {
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     Entries A, h, m, dA;
     read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
     grid_dep_wait();  // the hops
-    read_entries(hops + row, c, mine, N, 4 * q, 1.f, h);
-    read_entries(mus + row, c, mine, N, 4 * q, 1.f, m);
+    read_entries(start + row, c, start != nullptr ? mine : 0, N, 4 * q, 1.f, h);
+    read_entries(end + row, c, end != nullptr ? mine : 0, N, 4 * q, 1.f, m);
 #pragma unroll
     for (int e = 0; e < 4; ++e) dA[e][0] = dA[e][1] = 0ull;
     __syncthreads();
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
         const int t = r.tb + runs * kRun + i / (2 * N);
         dbc[((place + t) * a.ngroups + r.grp) * 2 * N + i % (2 * N)] = 0.f;
     }
-    write_entries(hops + row, c, mine, N, 4 * q, dA);  // this block's part of dA, in place of its start state
+    write_entries(dA_parts + row, c, mine, N, 4 * q, dA);  // in place of the start state, where that came from a hop
     __syncthreads();
 
     // per token and channel
@@ -577,17 +577,41 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     }
 }
 
-// out[i] = sum over rows of in[row * stride + i], i < n, in a fixed order: eight strided sums, then those eight.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ in, int64_t stride, int rows, int64_t n,
-                                                          float* __restrict__ out) {
+// What the blocks' parts are added to, in one launch: thread blocks of three kinds after one another.  dA and then dD and
+// ddt_bias are sums over rows, eight strided ones and then those eight; dB and dC sums over the tiles of channels.
+struct Sums {
+    const float *dA_parts, *chan, *dbc;
+    float *dA, *dD, *dbias, *dB, *dC;
+    int64_t n, tokens;  // channels x entries; tokens x groups
+    int rows, channels, tiles, dstate;
+    int a_blocks, d_blocks;
+};
+__global__ void __launch_bounds__(256) selective_sums_kernel(Sums u) {
     __shared__ float part[8][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    int block = blockIdx.x;
     grid_dep_wait();
+    if (block >= u.a_blocks + u.d_blocks) {
+        const int64_t i = (int64_t)(block - u.a_blocks - u.d_blocks) * 256 + threadIdx.x, n = u.tokens * 2 * u.dstate;
+        if (i >= n) return;
+        float s = 0.f;
+#pragma unroll 8
+        for (int t = 0; t < u.tiles; ++t) s += u.dbc[t * n + i];
+        const int64_t row = i / (2 * u.dstate);
+        const int e = (int)(i % (2 * u.dstate));
+        if (e < u.dstate) u.dB[row * u.dstate + e] = s;
+        else u.dC[row * u.dstate + e - u.dstate] = s;
+        return;
+    }
+    const bool channels = block >= u.a_blocks;
+    if (channels) block -= u.a_blocks;
+    const float* in = channels ? u.chan : u.dA_parts;
+    const int64_t n = channels ? 2 * u.channels : u.n;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)block * 32 + lane;
     float s = 0.f;
     if (i < n) {
 #pragma unroll 8
-        for (int r = warp; r < rows; r += 8) s += in[r * stride + i];
+        for (int r = warp; r < u.rows; r += 8) s += in[r * n + i];
     }
     part[warp][lane] = s;
     __syncthreads();
@@ -595,28 +619,9 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
     s = 0.f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) s += part[q][lane];
-    out[i] = s;
-}
-
-// dB and dC from the channel blocks' parts, (tiles, tokens and groups, 2, dstate), added in order
-__global__ void __launch_bounds__(256) join_bc_kernel(const float* __restrict__ dbc, int tiles, int64_t rows, int dstate,
-                                                      float* __restrict__ dB, float* __restrict__ dC) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, n = rows * 2 * dstate;
-    if (i >= n) return;
-    grid_dep_wait();
-    float s = 0.f;
-#pragma unroll 8
-    for (int t = 0; t < tiles; ++t) s += dbc[t * n + i];
-    const int64_t row = i / (2 * dstate);
-    const int e = (int)(i % (2 * dstate));
-    if (e < dstate) dB[row * dstate + e] = s;
-    else dC[row * dstate + e - dstate] = s;
-}
-
-int column_sums(const float* in, int64_t stride, int rows, int64_t n, float* out, cudaStream_t s) {
-    launch_begin(kKindSelectiveBwd, s);
-    launch_dependent(column_sums_kernel, dim3((unsigned)ceil_div64(n, 32)), dim3(256), 0, s, in, stride, rows, n, out);
-    return launch_end(kKindSelectiveBwd, s);
+    if (!channels) u.dA[i] = s;
+    else if (i < u.channels && u.dD != nullptr) u.dD[i] = s;
+    else if (i >= u.channels && u.dbias != nullptr) u.dbias[i - u.channels] = s;
 }
 
 struct Parts {
@@ -666,29 +671,34 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
     int r = ensure_smem_limit(reinterpret_cast<const void*>(selective_terms_kernel<T, LP>), K::floats_terms(most) * 4);
     if (r == SSD_OK) r = ensure_smem_limit(reinterpret_cast<const void*>(selective_block_kernel<T, LP>), K::floats(most) * 4);
     if (r != SSD_OK) return r;
-    launch_begin(kKindSelectiveBwd, s);
-    selective_terms_kernel<T, LP><<<grid, threads, smem_terms, s>>>(a, dy, p.nblocks, hops, mus, nu0, dtsum, vec, vecb);
-    r = launch_end(kKindSelectiveBwd, s);
+    T *dx = static_cast<T*>(g.dx), *ddt = static_cast<T*>(g.ddt), *dz = static_cast<T*>(g.dz);
+    if (p.nblocks == 1 && g.dinit == nullptr) {  // the block starts and ends with the row
+        launch_begin(kKindSelectiveBwd, s);
+        selective_block_kernel<T, LP><<<grid, threads, smem, s>>>(a, dy, 1, a.init, g.dfinal, hops, dx, ddt, dz, dbc, chan, vec, vecb);
+        r = launch_end(kKindSelectiveBwd, s);
+    } else {
+        launch_begin(kKindSelectiveBwd, s);
+        selective_terms_kernel<T, LP><<<grid, threads, smem_terms, s>>>(a, dy, p.nblocks, hops, mus, nu0, dtsum, vec, vecb);
+        r = launch_end(kKindSelectiveBwd, s);
+        if (r != SSD_OK) return r;
+        launch_begin(kKindSelectiveBwd, s);
+        launch_dependent(selective_hops_kernel, dim3((unsigned)ceil_div64(n, 256), a.batch, 2), dim3(256), 0, s, a.A, a.init,
+                         g.dfinal, a.channels, a.dstate, p.nblocks, hops, mus, nu0, dtsum, g.dinit);
+        r = launch_end(kKindSelectiveBwd, s);
+        if (r != SSD_OK) return r;
+        launch_begin(kKindSelectiveBwd, s);
+        launch_dependent(selective_block_kernel<T, LP>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus, hops, dx, ddt,
+                         dz, dbc, chan, vec, vecb);
+        r = launch_end(kKindSelectiveBwd, s);
+    }
     if (r != SSD_OK) return r;
+    Sums u = {hops, chan, dbc, g.dA, g.dD, g.ddt_bias, g.dB, g.dC, n, (int64_t)a.batch * a.seqlen * a.ngroups,
+              a.batch * p.nblocks, a.channels, p.tiles, a.dstate, (int)ceil_div64(n, 32), 0};
+    if (g.dD != nullptr || g.ddt_bias != nullptr) u.d_blocks = ceil_div(2 * a.channels, 32);
+    const int64_t blocks = u.a_blocks + u.d_blocks + ceil_div64(u.tokens * 2 * a.dstate, 256);
+    if (blocks > 2147483647) return SSD_ERR_UNSUPPORTED;
     launch_begin(kKindSelectiveBwd, s);
-    launch_dependent(selective_hops_kernel, dim3((unsigned)ceil_div64(n, 256), a.batch, 2), dim3(256), 0, s, a.A, a.init, g.dfinal,
-                     a.channels, a.dstate, p.nblocks, hops, mus, nu0, dtsum, g.dinit);
-    r = launch_end(kKindSelectiveBwd, s);
-    if (r != SSD_OK) return r;
-    launch_begin(kKindSelectiveBwd, s);
-    launch_dependent(selective_block_kernel<T, LP>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus,
-                     static_cast<T*>(g.dx), static_cast<T*>(g.ddt), static_cast<T*>(g.dz), dbc, chan, vec, vecb);
-    r = launch_end(kKindSelectiveBwd, s);
-    const int rows = a.batch * p.nblocks;
-    if (r == SSD_OK) r = column_sums(hops, n, rows, n, g.dA, s);
-    if (r == SSD_OK && g.dD != nullptr) r = column_sums(chan, 2 * a.channels, rows, a.channels, g.dD, s);
-    if (r == SSD_OK && g.ddt_bias != nullptr)
-        r = column_sums(chan + a.channels, 2 * a.channels, rows, a.channels, g.ddt_bias, s);
-    if (r != SSD_OK) return r;
-    const int64_t tokens = (int64_t)a.batch * a.seqlen * a.ngroups;
-    launch_begin(kKindSelectiveBwd, s);
-    launch_dependent(join_bc_kernel, dim3((unsigned)ceil_div64(tokens * 2 * a.dstate, 256)), dim3(256), 0, s, dbc, p.tiles, tokens,
-                     a.dstate, g.dB, g.dC);
+    launch_dependent(selective_sums_kernel, dim3((unsigned)blocks), dim3(256), 0, s, u);
     return launch_end(kKindSelectiveBwd, s);
 }
 
