@@ -6,7 +6,7 @@
 //   dB[t][n] = sum_c lam dt x              dC[t][n] = sum_c g h[t]           (over the channels of a group)
 //   dA[n] = sum_t dt a h[t-1] lam          dD = sum_t g x          dz[t] = dy y0 d(z sigmoid z)/dz,  y0 ungated
 //
-// The sequence is cut into blocks of kBlock tokens.  One kernel forms every block's own end state and its own
+// The sequence is cut into blocks of 32 or 16 tokens.  One kernel forms every block's own end state and its own
 // gradient at its start, from zero; a hop carries both across the blocks (forward and backward in time); the main
 // kernel then works on every block by itself, from its true start state and end gradient.  Inside a block the
 // states are recomputed in runs of kRun tokens from a checkpoint at each run's start, since only the decay, not its
@@ -22,23 +22,23 @@
 namespace ssd {
 namespace {
 
-constexpr int kBlock = 32;  // tokens of a block
 constexpr int kRun = 8;     // tokens between checkpoints
 constexpr int kHeld = 4;    // tokens whose states and decays are in registers
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int LP>
+template <int LP, int BLOCK>  // BLOCK: tokens of a block
 struct Blk {
     static constexpr int CW = 32 / LP, NP = 4 * LP;  // lanes' groups of four channels in a warp; entries, padded
     static constexpr int CONV = LP;                  // tokens that the block's threads convert at once
-    static constexpr int CONVS = kBlock / CONV;
+    static constexpr int CONVS = BLOCK / CONV;
+    static_assert(CONVS > 0, "tokens for every thread");
     static constexpr int channels(int threads) { return 4 * threads / LP; }
     // shared memory in floats: dt, dt x (later sum lam B), g (later sum A a h lam), y per token and channel; B, C; the
     // warps' parts of dB and dC of a run; checkpoints, sixteen floats per thread and run
     static constexpr int floats(int threads) {
-        return 4 * kBlock * channels(threads) + 2 * kBlock * NP + threads / 32 * kRun * 2 * NP + 16 * threads * (kBlock / kRun);
+        return 4 * BLOCK * channels(threads) + 2 * BLOCK * NP + threads / 32 * kRun * 2 * NP + 16 * threads * (BLOCK / kRun);
     }
-    static constexpr int floats_terms(int threads) { return 3 * kBlock * channels(threads) + 2 * kBlock * NP; }
+    static constexpr int floats_terms(int threads) { return 3 * BLOCK * channels(threads) + 2 * BLOCK * NP; }
 };
 
 template <typename T>
@@ -47,7 +47,7 @@ struct Rows {  // where a block's tokens and channels are
     int b, grp, tile, tiles, c0, nc, tb, te, last;  // c0: first channel, of nc; tokens tb .. te - 1, live ones before last
 };
 
-template <typename T>
+template <typename T, int BLOCK>
 __device__ __forceinline__ Rows<T> rows_at(const SelectiveArgs& a, const void* dy, int cc) {
     Rows<T> r;
     const int per = a.channels / a.ngroups;
@@ -57,8 +57,8 @@ __device__ __forceinline__ Rows<T> rows_at(const SelectiveArgs& a, const void* d
     r.c0 = r.grp * per + r.tile * cc;
     r.nc = min(cc, per - r.tile * cc);
     r.b = blockIdx.z;
-    r.tb = blockIdx.y * kBlock;
-    r.te = min(r.tb + kBlock, a.seqlen);
+    r.tb = blockIdx.y * BLOCK;
+    r.te = min(r.tb + BLOCK, a.seqlen);
     r.last = min(r.te, row_length(a.lengths, r.b, a.seqlen));
     r.x = static_cast<const T*>(a.x) + r.b * a.x_batch + r.c0;
     r.dt = static_cast<const T*>(a.dt) + r.b * a.dt_batch + r.c0;
@@ -91,10 +91,10 @@ __device__ __forceinline__ Loaded<T, M> load_rows(const SelectiveArgs& a, const 
 }
 
 // The block's tokens into shared memory: dt, dt x and g per token and channel, B and C as float32; zero past the length.
-template <typename T, int LP>
+template <typename T, int LP, int BLOCK>
 __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T>& r, float* s_d, float* s_x, float* s_g,
                                             float* s_B, float* s_C, bool vec, bool vecb, float (&dsum)[4]) {
-    using K = Blk<LP>;
+    using K = Blk<LP, BLOCK>;
     constexpr int M = K::CONVS < 8 ? K::CONVS : 8;
     const int tid = threadIdx.x, threads = blockDim.x, cc = K::channels(threads);
     const int v0 = tid % (cc / 4), w0 = tid / (cc / 4);
@@ -110,19 +110,19 @@ __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T
             for (int e = 0; e < 4; ++e)
                 bias[e] = (a.dto.bias != nullptr && 4 * v0 + e < r.nc) ? __ldg(a.dto.bias + r.c0 + 4 * v0 + e) : 0.f;
             constexpr int R = 4;  // vectors of B and of C in flight
-            for (int j0 = tid; j0 < kBlock * LP; j0 += R * threads) {
+            for (int j0 = tid; j0 < BLOCK * LP; j0 += R * threads) {
                 Vec<T, 4> B[R], C[R];
 #pragma unroll
                 for (int u = 0; u < R; ++u) {
                     const int j = j0 + u * threads, t = r.tb + j / LP, e = 4 * (j % LP);
-                    const int valid = j < kBlock * LP && t < r.last ? a.dstate - e : 0;
+                    const int valid = j < BLOCK * LP && t < r.last ? a.dstate - e : 0;
                     B[u] = load_vec<T, 4>(r.B + t * a.B_token + e, valid, vecb);
                     C[u] = load_vec<T, 4>(r.C + t * a.C_token + e, valid, vecb);
                 }
 #pragma unroll
                 for (int u = 0; u < R; ++u) {
                     const int j = j0 + u * threads;
-                    if (j < kBlock * LP) {
+                    if (j < BLOCK * LP) {
                         *reinterpret_cast<float4*>(s_B + 4 * j) = make_float4(B[u].get(0), B[u].get(1), B[u].get(2), B[u].get(3));
                         *reinterpret_cast<float4*>(s_C + 4 * j) = make_float4(C[u].get(0), C[u].get(1), C[u].get(2), C[u].get(3));
                     }
@@ -209,20 +209,20 @@ __device__ __forceinline__ void twice_of(const float* p, f32x2 (&o)[4]) {
 
 // Every block's own end state (from zero) into hops[k + 1], its own gradient at its start into mus[k - 1] (block 0's
 // into `nu0`), and its sum of dt.
-template <typename T, int LP>
+template <typename T, int LP, int BLOCK>
 __global__ void __launch_bounds__(128, 3) selective_terms_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
                                                                  float* __restrict__ hops, float* __restrict__ mus,
                                                                  float* __restrict__ nu0, float* __restrict__ dtsum,
                                                                  bool vec, bool vecb) {
-    using K = Blk<LP>;
+    using K = Blk<LP, BLOCK>;
     extern __shared__ __align__(16) float sm[];
     const int tid = threadIdx.x, threads = blockDim.x, cc = K::channels(threads), N = a.dstate, k = blockIdx.y;
-    const Rows<T> r = rows_at<T>(a, dy, cc);
+    const Rows<T> r = rows_at<T, BLOCK>(a, dy, cc);
     const int qd = tid / LP, q = tid % LP, mine = r.nc - 4 * qd;
     const int64_t c = r.c0 + 4 * qd, n = (int64_t)a.channels * N;
-    float *s_d = sm, *s_x = s_d + kBlock * cc, *s_g = s_x + kBlock * cc, *s_B = s_g + kBlock * cc, *s_C = s_B + kBlock * K::NP;
+    float *s_d = sm, *s_x = s_d + BLOCK * cc, *s_g = s_x + BLOCK * cc, *s_B = s_g + BLOCK * cc, *s_C = s_B + BLOCK * K::NP;
     float dsum[4];
-    stage_block<T, LP>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, dsum);
+    stage_block<T, LP, BLOCK>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, dsum);
     Entries A, h, v, p;
     read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
 #pragma unroll
@@ -309,26 +309,26 @@ __global__ void __launch_bounds__(256) selective_hops_kernel(const float* __rest
         dinit[b * n + i] = fmaf(exp2_fast(A2 * dtsum[(int64_t)b * nblocks * channels + i / dstate]), s, nu0[b * n + i]);
 }
 
-template <typename T, int LP>
+template <typename T, int LP, int BLOCK>
 __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
                                                                  const float* start, const float* end, float* dA_parts,
                                                                  T* __restrict__ dx, T* __restrict__ ddt,
                                                                  T* __restrict__ dz, float* __restrict__ dbc,
                                                                  float* __restrict__ chan, bool vec, bool vecb) {
-    using K = Blk<LP>;
+    using K = Blk<LP, BLOCK>;
     constexpr int NP = K::NP;
     extern __shared__ __align__(16) float sm[];
     const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = threads / 32;
     const int cc = K::channels(threads), N = a.dstate, k = blockIdx.y;
-    const Rows<T> r = rows_at<T>(a, dy, cc);
+    const Rows<T> r = rows_at<T, BLOCK>(a, dy, cc);
     const int qd = tid / LP, q = tid % LP, mine = r.nc - 4 * qd;
     const int64_t c = r.c0 + 4 * qd, n = (int64_t)a.channels * N, row = ((int64_t)r.b * nblocks + k) * n;
-    float *s_d = sm, *s_x = s_d + kBlock * cc, *s_g = s_x + kBlock * cc, *s_y = s_g + kBlock * cc, *s_B = s_y + kBlock * cc,
-          *s_C = s_B + kBlock * NP, *s_red = s_C + kBlock * NP;
+    float *s_d = sm, *s_x = s_d + BLOCK * cc, *s_g = s_x + BLOCK * cc, *s_y = s_g + BLOCK * cc, *s_B = s_y + BLOCK * cc,
+          *s_C = s_B + BLOCK * NP, *s_red = s_C + BLOCK * NP;
     ulonglong2* ck = reinterpret_cast<ulonglong2*>(s_red + warps * kRun * 2 * NP) + tid;
     {
         float unused[4];
-        stage_block<T, LP>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, unused);
+        stage_block<T, LP, BLOCK>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, unused);
     }
     Entries A, h, m, dA;
     read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float zv = l.z[i].get(e), sg = sigmoid(zv);
-                    const int t = t0 + i * K::CONV < kBlock ? t0 + i * K::CONV : 0;
+                    const int t = t0 + i * K::CONV < BLOCK ? t0 + i * K::CONV : 0;
                     fz[4 * i + e] = g[4 * i + e] * fmaf(Dc[e], l.x[i].get(e), s_y[t * cc + 4 * v0 + e]) * sg * fmaf(zv, 1.f - sg, 1.f);
                     g[4 * i + e] *= zv * sg;
                 }
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             const int t = t0 + i * K::CONV;
-            if (K::CONV * K::CONVS != kBlock && t >= kBlock) break;
+            if (K::CONV * K::CONVS != BLOCK && t >= BLOCK) break;
             const bool live = r.tb + t < r.last;
             const float4 d4 = *reinterpret_cast<const float4*>(s_d + t * cc + 4 * v0);
             const float4 b4 = *reinterpret_cast<const float4*>(s_x + t * cc + 4 * v0);
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(256) selective_sums_kernel(Sums u) {
 }
 
 struct Parts {
-    int nblocks, tiles;
+    int tokens, nblocks, tiles;  // of a block; blocks of a row; blocks of a group's channels
     size_t hops, nu0, dtsum, chan, dbc;  // floats of each part
     size_t total() const { return 2 * hops + nu0 + dtsum + chan + dbc; }
 };
@@ -639,11 +639,16 @@ int block_threads(const SelectiveArgs& a) {
     return threads;
 }
 
+// Blocks of 32 tokens, or of 16 where those of 32 would leave an SM quarter without a warp: half a block's time for twice
+// the hops, sums and checkpoints.  With 32 and with 16 tokens at 16 entries of bfloat16: 34 and 21 us at 2 x 128 x 512, 35
+// and 28 at 512 x 1024, 47 and 50 at 4 x 64 x 4096, 139 and 150 at 2 x 1024 x 2048.  Rows that fit 32 tokens need no hop.
 Parts parts_of(const SelectiveArgs& a) {
     Parts p;
-    const int cc = 4 * block_threads(a) / selective_lanes(a.dstate);
-    p.nblocks = ceil_div(a.seqlen, kBlock);
-    p.tiles = ceil_div(a.channels / a.ngroups, cc);
+    const int threads = block_threads(a), lp = selective_lanes(a.dstate);
+    p.tiles = ceil_div(a.channels / a.ngroups, 4 * threads / lp);
+    const int64_t warps = (int64_t)a.batch * a.ngroups * p.tiles * ceil_div(a.seqlen, 32) * (threads / 32);
+    p.tokens = lp <= 16 && warps <= 152 * 4 && (a.seqlen <= 16 || a.seqlen > 32) ? 16 : 32;
+    p.nblocks = ceil_div(a.seqlen, p.tokens);
     const size_t n = (size_t)a.channels * a.dstate, rows = (size_t)a.batch * p.nblocks;
     auto whole = [](size_t floats) { return (floats + 3) & ~(size_t)3; };  // every part starts on 16 bytes
     p.hops = whole(rows * n);
@@ -654,10 +659,9 @@ Parts parts_of(const SelectiveArgs& a) {
     return p;
 }
 
-template <typename T, int LP>
-int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, cudaStream_t s) {
-    using K = Blk<LP>;
-    const Parts p = parts_of(a);
+template <typename T, int LP, int BLOCK>
+int backward_blocks(const SelectiveArgs& a, const Parts& p, const SelectiveGrads& g, float* ws, cudaStream_t s) {
+    using K = Blk<LP, BLOCK>;
     float *hops = ws, *mus = hops + p.hops, *nu0 = mus + p.hops, *dtsum = nu0 + p.nu0, *chan = dtsum + p.dtsum,
           *dbc = chan + p.chan;
     const T* dy = static_cast<const T*>(g.dy);
@@ -668,17 +672,17 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
     const int most = LP == 2 ? 64 : 128;
     const dim3 grid(a.ngroups * p.tiles, p.nblocks, a.batch);
     const int64_t n = (int64_t)a.channels * a.dstate;
-    int r = ensure_smem_limit(reinterpret_cast<const void*>(selective_terms_kernel<T, LP>), K::floats_terms(most) * 4);
-    if (r == SSD_OK) r = ensure_smem_limit(reinterpret_cast<const void*>(selective_block_kernel<T, LP>), K::floats(most) * 4);
+    int r = ensure_smem_limit(reinterpret_cast<const void*>(selective_terms_kernel<T, LP, BLOCK>), K::floats_terms(most) * 4);
+    if (r == SSD_OK) r = ensure_smem_limit(reinterpret_cast<const void*>(selective_block_kernel<T, LP, BLOCK>), K::floats(most) * 4);
     if (r != SSD_OK) return r;
     T *dx = static_cast<T*>(g.dx), *ddt = static_cast<T*>(g.ddt), *dz = static_cast<T*>(g.dz);
     if (p.nblocks == 1 && g.dinit == nullptr) {  // the block starts and ends with the row
         launch_begin(kKindSelectiveBwd, s);
-        selective_block_kernel<T, LP><<<grid, threads, smem, s>>>(a, dy, 1, a.init, g.dfinal, hops, dx, ddt, dz, dbc, chan, vec, vecb);
+        selective_block_kernel<T, LP, BLOCK><<<grid, threads, smem, s>>>(a, dy, 1, a.init, g.dfinal, hops, dx, ddt, dz, dbc, chan, vec, vecb);
         r = launch_end(kKindSelectiveBwd, s);
     } else {
         launch_begin(kKindSelectiveBwd, s);
-        selective_terms_kernel<T, LP><<<grid, threads, smem_terms, s>>>(a, dy, p.nblocks, hops, mus, nu0, dtsum, vec, vecb);
+        selective_terms_kernel<T, LP, BLOCK><<<grid, threads, smem_terms, s>>>(a, dy, p.nblocks, hops, mus, nu0, dtsum, vec, vecb);
         r = launch_end(kKindSelectiveBwd, s);
         if (r != SSD_OK) return r;
         launch_begin(kKindSelectiveBwd, s);
@@ -687,7 +691,7 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
         r = launch_end(kKindSelectiveBwd, s);
         if (r != SSD_OK) return r;
         launch_begin(kKindSelectiveBwd, s);
-        launch_dependent(selective_block_kernel<T, LP>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus, hops, dx, ddt,
+        launch_dependent(selective_block_kernel<T, LP, BLOCK>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus, hops, dx, ddt,
                          dz, dbc, chan, vec, vecb);
         r = launch_end(kKindSelectiveBwd, s);
     }
@@ -700,6 +704,14 @@ int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, c
     launch_begin(kKindSelectiveBwd, s);
     launch_dependent(selective_sums_kernel, dim3((unsigned)blocks), dim3(256), 0, s, u);
     return launch_end(kKindSelectiveBwd, s);
+}
+
+template <typename T, int LP>
+int backward_lanes(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, cudaStream_t s) {
+    const Parts p = parts_of(a);
+    if constexpr (LP <= 16)
+        if (p.tokens == 16) return backward_blocks<T, LP, 16>(a, p, g, ws, s);
+    return backward_blocks<T, LP, 32>(a, p, g, ws, s);
 }
 
 template <typename T>

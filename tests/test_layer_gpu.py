@@ -180,7 +180,9 @@ SEL = [("bf16", 2, 40, 32, 1, 16, True, True, True, True, None, None, 0),
        ("bf16", 1, 16, 260, 4, 17, True, True, True, False, None, None, 0),
        ("f16", 2, 77, 534, 2, 13, True, True, True, True, [77, 30], None, 1), ("bf16", 3, 45, 7, 1, 3, True, True, True, False, None, None, 1),
        ("bf16", 1, 66, 129, 3, 9, True, False, True, True, None, None, 3), ("f16", 2, 50, 535, 1, 20, True, True, False, True, [50, 49], None, 1),
-       ("bf16", 2, 40, 31, 1, 27, True, False, True, True, None, None, 2), ("f32", 2, 90, 135, 1, 19, True, True, True, True, None, None, 1)]
+       ("bf16", 2, 40, 31, 1, 27, True, False, True, True, None, None, 2), ("f32", 2, 90, 135, 1, 19, True, True, True, True, None, None, 1),
+       ("bf16", 4, 130, 1200, 1, 16, True, True, True, True, None, None, 0), ("f16", 4, 130, 1201, 1, 13, True, False, True, True, [130, 0, 95, 64], None, 1),
+       ("f32", 1, 24, 40, 1, 16, True, True, True, True, None, None, 0), ("f32", 2, 16, 12, 1, 40, True, True, True, True, [16, 0], None, 0)]
 
 
 def selective_case(c, seed=7):
