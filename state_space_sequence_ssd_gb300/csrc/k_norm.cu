@@ -67,86 +67,175 @@ __device__ __forceinline__ void load_columns(const float* p, int c, int width, b
     }
 }
 
-// R neighbouring rows of NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  A block
-// takes its rows and ends.  Two rows a thread share the reductions' barriers and the reads of weight and bias, four times
-// a row's bytes: at 8192 x 2048 of bfloat16 17.5 us (3.8 TB/s; a plain copy of as many bytes takes 11.8) where one row
-// takes 19.3, a resident grid whose blocks walk the rows with the next one's loads in flight 20 to 25, one warp a row 23.
-template <typename T, int V, int NV, int R>
+// NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  A block takes its rows and ends.
+template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restrict__ x, int64_t x_row,
                                                                 const float* __restrict__ weight,
                                                                 const float* __restrict__ bias, float eps, int64_t rows,
                                                                 int width, int lanes, T* __restrict__ y,
                                                                 float* __restrict__ mean, float* __restrict__ rstd, bool vecw) {
-    static_assert(R == 1 || R == 2, "one or two rows");
     constexpr int P = (V + 1) / 2;
     __shared__ float2 buf[2][kThreads / 32];
     const int lane = threadIdx.x & (lanes - 1);
-    const int64_t row = ((int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes) * R;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+    const bool live = row < rows;
+    const T* xr = x + (live ? row : 0) * x_row;
     const float inv = 1.f / (float)width;
-    Vec<T, V> r[R][NV];
+    Vec<T, V> r[NV];
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const bool live = row + k < rows;
-        const T* xr = x + (live ? row + k : 0) * x_row;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + lanes * i) * V;
-            r[k][i] = load_vec<T, V>(xr + c, live ? width - c : 0, true);
-        }
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + lanes * i) * V;
+        r[i] = load_vec<T, V>(xr + c, live ? width - c : 0, true);
     }
-    float m[2] = {0.f, 0.f}, rs[2] = {0.f, 0.f};
+    f32x2 s2 = 0ull, q2 = 0ull;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        f32x2 s = 0ull;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int e = 0; e < P; ++e) s2 = add2(s2, r[i].pair(e));
+    const float m = row_sum(sum2(s2), lanes, buf[0]) * inv;
+    const f32x2 m2 = pk(-m, V > 1 ? -m : 0.f);
 #pragma unroll
-            for (int e = 0; e < P; ++e) s = add2(s, r[k][i].pair(e));
-        m[k] = sum2(s) * inv;
-    }
-    const float2 mm = row_sums(make_float2(m[0], m[1]), lanes, buf[0]);
-    m[0] = mm.x;
-    m[1] = mm.y;
+    for (int i = 0; i < NV; ++i)
+        if ((lane + lanes * i) * V < width) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const f32x2 m2 = pk(-m[k], V > 1 ? -m[k] : 0.f);
-        f32x2 q = 0ull;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if ((lane + lanes * i) * V < width) {
-#pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    const f32x2 d = add2(r[k][i].pair(e), m2);
-                    q = fma2(d, d, q);
-                }
+            for (int e = 0; e < P; ++e) {
+                const f32x2 d = add2(r[i].pair(e), m2);
+                q2 = fma2(d, d, q2);
             }
-        rs[k] = sum2(q) * inv;
-    }
-    const float2 qq = row_sums(make_float2(rs[0], rs[1]), lanes, buf[1]);
-    rs[0] = rsqrtf(qq.x + eps);
-    rs[1] = rsqrtf(qq.y + eps);
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-        if (lane == 0 && row + k < rows) {
-            if (mean != nullptr) mean[row + k] = m[k];
-            if (rstd != nullptr) rstd[row + k] = rs[k];
         }
+    const float rs = rsqrtf(fmaf(row_sum(sum2(q2), lanes, buf[1]), inv, eps));
+    if (!live) return;
+    if (lane == 0) {
+        if (mean != nullptr) mean[row] = m;
+        if (rstd != nullptr) rstd[row] = rs;
+    }
+    T* yr = y + row * width;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + lanes * i) * V;
         if (c >= width) break;
-        f32x2 w[P], b[P];
+        f32x2 o[P], w[P], b[P];
         load_columns<V>(weight, c, width, vecw, 1.f, w);
         load_columns<V>(bias, c, width, vecw, 0.f, b);
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            f32x2 o[P];
+        for (int e = 0; e < P; ++e) o[e] = fma2(mul2(add2(r[i].pair(e), m2), pk(rs, rs)), w[e], b[e]);
+        store_vec<T, V>(yr + c, Vec<T, V>::of_pairs(o), width - c, true);
+    }
+}
+
+// The same for many rows, with vectors of 16 bytes: a resident grid whose blocks walk the rows, two neighbouring ones a
+// thread, so that they share the reductions' barriers and the weight and bias that it holds.  A thread's pieces of the
+// next rows are copied to shared memory that it alone reads, so that they need neither registers nor barriers while they
+// are on their way.  At 8192 x 2048 of bfloat16 15.1 us (4.4 TB/s; a plain copy of as many bytes takes 11.9); with the
+// copies of one, three or four pairs of rows ahead 15.5, 15.9 and 16.2, without holding the weight 17.2, and the kernel
+// above takes 19.3.
+constexpr int kAhead = 2;  // pairs of rows
+constexpr int resident(int nv) { return nv <= 2 ? 3 : 2; }  // blocks of an SM
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(kThreads, resident(NV)) norm_ring_kernel(const T* __restrict__ x, int64_t x_row,
+                                                                const float* __restrict__ weight,
+                                                                const float* __restrict__ bias, float eps, int64_t rows,
+                                                                int width, int lanes, T* __restrict__ y,
+                                                                float* __restrict__ mean, float* __restrict__ rstd, bool vecw) {
+    constexpr int P = (V + 1) / 2, R = 2;
+    constexpr bool HOLD = NV <= 2;  // weight and bias stay in registers
+    __shared__ float2 buf[2][kThreads / 32];
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & (lanes - 1), per = kThreads / lanes;
+    const float inv = 1.f / (float)width;
+    uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * per * R;
+    int64_t row = ((int64_t)blockIdx.x * per + threadIdx.x / lanes) * R;
+    auto fetch = [&](int64_t r0, int turn) {
 #pragma unroll
-            for (int e = 0; e < P; ++e)
-                o[e] = fma2(mul2(add2(r[k][i].pair(e), pk(-m[k], -m[k])), pk(rs[k], rs[k])), w[e], b[e]);
-            store_vec<T, V>(y + (row + k) * width + c, Vec<T, V>::of_pairs(o), row + k < rows ? width - c : 0, true);
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + lanes * i) * V;
+                const bool in = r0 + k < rows && c < width;
+                copy16(ring + ((turn * R + k) * NV + i) * kThreads, in ? x + (r0 + k) * x_row + c : x, in);
+            }
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(row + k * step, k);
+    f32x2 w[NV][P], b[NV][P];
+    if (HOLD) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            load_columns<V>(weight, (lane + lanes * i) * V, width, vecw, 1.f, w[i]);
+            load_columns<V>(bias, (lane + lanes * i) * V, width, vecw, 0.f, b[i]);
         }
     }
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * per * R; r0 < rows; r0 += step, row += step) {
+        Vec<T, V> r[R][NV];
+        copies_wait<kAhead - 1>();
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const uint4 u = ring[((turn * R + k) * NV + i) * kThreads];
+                r[k][i].w[0] = u.x; r[k][i].w[1] = u.y; r[k][i].w[2] = u.z; r[k][i].w[3] = u.w;
+            }
+        float m[2], rs[2];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            f32x2 s = 0ull;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < P; ++e) s = add2(s, r[k][i].pair(e));
+            m[k] = sum2(s) * inv;
+        }
+        fetch(row + kAhead * step, turn);
+        if (++turn == kAhead) turn = 0;
+        const float2 mm = row_sums(make_float2(m[0], m[1]), lanes, buf[0]);
+        m[0] = mm.x;
+        m[1] = mm.y;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const f32x2 m2 = pk(-m[k], -m[k]);
+            f32x2 q = 0ull;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if ((lane + lanes * i) * V < width) {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) {
+                        const f32x2 d = add2(r[k][i].pair(e), m2);
+                        q = fma2(d, d, q);
+                    }
+                }
+            rs[k] = sum2(q) * inv;
+        }
+        const float2 qq = row_sums(make_float2(rs[0], rs[1]), lanes, buf[1]);
+        rs[0] = rsqrtf(qq.x + eps);
+        rs[1] = rsqrtf(qq.y + eps);
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            if (lane == 0 && row + k < rows) {
+                if (mean != nullptr) mean[row + k] = m[k];
+                if (rstd != nullptr) rstd[row + k] = rs[k];
+            }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + lanes * i) * V;
+            if (c >= width) break;
+            if (!HOLD) {
+                load_columns<V>(weight, c, width, vecw, 1.f, w[i]);
+                load_columns<V>(bias, c, width, vecw, 0.f, b[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                f32x2 o[P];
+#pragma unroll
+                for (int e = 0; e < P; ++e)
+                    o[e] = fma2(mul2(add2(r[k][i].pair(e), pk(-m[k], -m[k])), pk(rs[k], rs[k])), w[i][e], b[i][e]);
+                store_vec<T, V>(y + (row + k) * width + c, Vec<T, V>::of_pairs(o), row + k < rows ? width - c : 0, true);
+            }
+        }
+    }
+    copies_wait<0>();
 }
 
 // Rows that do not fit the registers, a block each: read again (from L2) for each sum and the output.
@@ -366,10 +455,7 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
     const int vecs = ceil_div(width, V);
     const int lanes = row_lanes(rows, vecs, 2 * M, 1);
     const int nv = ceil_div(vecs, lanes);
-    // Two rows a thread where the SMs have 1024 threads' work all the same: with one and with two rows 3.7 and 3.4 us at
-    // 608 x 2048 of bfloat16, 9.0 and 6.2 at 608 x 8192, 11.8 and 10.6 at 4864 x 2048; but 5.2 and 5.6 at 304 x 8192.
-    const bool two = rows * lanes >= 152 * 1024 && nv <= 4 * M;
-    const int64_t blocks = ceil_div64(rows, kThreads / lanes * (two ? 2 : 1));
+    const int64_t blocks = ceil_div64(rows, kThreads / lanes);
     const bool vecw = on(weight, 16) && on(bias, 16);
     const T* xt = static_cast<const T*>(x);
     T* yt = static_cast<T*>(y);
@@ -378,10 +464,28 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)blocks, kThreads, 0, s>>>(xt, x_row, weight, bias, eps, rows, width, lanes, yt, mean, rstd, vecw);
     };
-    if (nv <= 1 * M) two ? go(norm_forward_kernel<T, V, 1 * M, 2>) : go(norm_forward_kernel<T, V, 1 * M, 1>);
-    else if (nv <= 2 * M) two ? go(norm_forward_kernel<T, V, 2 * M, 2>) : go(norm_forward_kernel<T, V, 2 * M, 1>);
-    else if (nv <= 4 * M) two ? go(norm_forward_kernel<T, V, 4 * M, 2>) : go(norm_forward_kernel<T, V, 4 * M, 1>);
-    else if (nv <= 8 * M) go(norm_forward_kernel<T, V, 8 * M, 1>);
+    if constexpr (sizeof(T) * V == 16) {
+        // A resident grid pays from about 24 thousand values an SM: with one row a thread's group and with the walk 4.4 and
+        // 4.8 us at 1216 x 2048 of bfloat16, 7.2 and 5.8 at 1824 x 2048, 5.1 and 6.2 at 304 x 8192, 9.0 and 7.0 at
+        // 608 x 8192, 5.6 and 6.4 at 1216 x 2048 of float32, 9.1 and 8.8 at 2432 x 2048.
+        if (rows * width >= 152 * 24576 && nv <= 4) {
+            int r = SSD_OK;
+            auto walk = [&](auto kernel, int held) {
+                const int smem = kAhead * 2 * held * kThreads * 16;
+                r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+                const int64_t pairs = ceil_div64(rows, kThreads / lanes * 2), most = 152 * resident(held);
+                if (r == SSD_OK)
+                    kernel<<<(unsigned)(pairs < most ? pairs : most), kThreads, smem, s>>>(xt, x_row, weight, bias, eps, rows, width, lanes, yt, mean, rstd, vecw);
+            };
+            nv == 1 ? walk(norm_ring_kernel<T, V, 1>, 1) : nv == 2 ? walk(norm_ring_kernel<T, V, 2>, 2) : walk(norm_ring_kernel<T, V, 4>, 4);
+            const int e = launch_end(kKindNorm, s);
+            return r != SSD_OK ? r : e;
+        }
+    }
+    if (nv <= 1 * M) go(norm_forward_kernel<T, V, 1 * M>);
+    else if (nv <= 2 * M) go(norm_forward_kernel<T, V, 2 * M>);
+    else if (nv <= 4 * M) go(norm_forward_kernel<T, V, 4 * M>);
+    else if (nv <= 8 * M) go(norm_forward_kernel<T, V, 8 * M>);
     else
         norm_forward_wide_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(xt, x_row, weight, bias, eps, width, yt, mean, rstd);
     return launch_end(kKindNorm, s);

@@ -204,6 +204,18 @@ __device__ __forceinline__ Vec<T, V> Vec<T, V>::of_pairs(const f32x2 (&v)[(V + 1
     return of(g);
 }
 
+// Sixteen bytes from global to shared memory without a register between; zeros where `live` is false.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool live) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+    const int bytes = live ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // A row's length, held to [0, seqlen] (no lengths: the whole row).
 __device__ __forceinline__ int row_length(const int* lengths, int b, int seqlen) {
     return lengths == nullptr ? seqlen : min(max(lengths[b], 0), seqlen);

@@ -88,18 +88,6 @@ inline bool rows_of_four(const SelectiveArgs& a, const void* out1, const void* o
 }
 inline bool states_of_four(const SelectiveArgs& a, size_t size) { return states_of(a, 4, size); }
 
-// Sixteen bytes from global to shared memory without a register between; zeros where `live` is false.
-__device__ __forceinline__ void copy16(void* to, const void* from, bool live) {
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
-    const int bytes = live ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
-
 // How the forward pass runs: with wide lanes (four channels of eight entries) or narrow ones (two of four), the lanes
 // that share a channel, threads of a block and its channels.
 struct SelectiveShape {

@@ -348,7 +348,8 @@ def test_idle_and_wrong_slots(ssd, op):
 
 NORM = [("bf16", 5, 64, 0), ("f16", 3, 1, 0), ("f32", 300, 7, 0), ("bf16", 1, 2048, 0), ("f32", 2, 31, 1), ("f16", 33, 1000, 8),
         ("bf16", 9, 2049, 0), ("f32", 17, 1024, 4), ("bf16", 4, 16384, 0), ("f16", 2, 20000, 0), ("f32", 3, 9001, 2),
-        ("bf16", 700, 512, 0), ("f32", 1000, 24, 0), ("bf16", 5001, 1000, 0), ("f16", 20001, 49, 0), ("f32", 9999, 260, 4)]
+        ("bf16", 700, 512, 0), ("f32", 1000, 24, 0), ("bf16", 5001, 1000, 0), ("f16", 20001, 49, 0), ("f32", 9999, 260, 4),
+        ("f32", 4001, 1028, 4), ("bf16", 60001, 64, 0), ("f16", 500, 8000, 8)]
 
 
 def norm_case(c, seed=13):
