@@ -126,9 +126,9 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restr
 // The same for many rows, with vectors of 16 bytes: a resident grid whose blocks walk the rows, two neighbouring ones a
 // thread, so that they share the reductions' barriers and the weight and bias that it holds.  A thread's pieces of the
 // next rows are copied to shared memory that it alone reads, so that they need neither registers nor barriers while they
-// are on their way.  At 8192 x 2048 of bfloat16 15.1 us (4.4 TB/s; a plain copy of as many bytes takes 11.9); with the
-// copies of one, three or four pairs of rows ahead 15.5, 15.9 and 16.2, without holding the weight 17.2, and the kernel
-// above takes 19.3.
+// are on their way.  At 8192 x 2048 of bfloat16 14.3 us (4.7 TB/s; a plain copy of as many bytes takes 11.9), where the
+// kernel above takes 19.3, and at 30400 x 2048 46 (5.4 TB/s) where that takes 63.  Copies of one, three and four pairs of
+// rows ahead took 3 to 7% longer than two, reading the weight again for each row 14%.
 constexpr int kAhead = 2;  // pairs of rows
 constexpr int resident(int nv) { return nv <= 2 ? 3 : 2; }  // blocks of an SM
 template <typename T, int V, int NV>
