@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(32 * kWarps, V == 2 ? 5 : 4) conv_backward_ker
 
 // dweight (channels, W) and dbias from the rows of `partial`, summed in a fixed order: eight strided sums of
 // rows, then those eight.
-__global__ void __launch_bounds__(256) conv_reduce_kernel(const float* __restrict__ partial, int rows, int channels, int W,
+// (`partial` is written while this kernel may already run, so it is neither const for the kernel nor read as such.)
+__global__ void __launch_bounds__(256) conv_reduce_kernel(const float* partial, int rows, int channels, int W,
                                                           float* __restrict__ dweight, float* __restrict__ dbias) {
     __shared__ float part[8][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -411,9 +411,10 @@ __global__ void __launch_bounds__(kThreads) norm_backward_wide_kernel(const T* _
 }
 
 // dweight and dbias from the blocks' rows of `partial`: kJoin strided sums, then those.  The rows lie in L2 and what counts
-// is how many of them are on their way at once.
+// is how many of them are on their way at once.  (`partial` is written while this kernel may already run, so it is neither
+// const for the kernel nor read as such.)
 constexpr int kJoin = 32;
-__global__ void __launch_bounds__(32 * kJoin) norm_reduce_kernel(const float* __restrict__ partial, int parts, int width,
+__global__ void __launch_bounds__(32 * kJoin) norm_reduce_kernel(const float* partial, int parts, int width,
                                                           float* __restrict__ dweight, float* __restrict__ dbias) {
     __shared__ float part[kJoin][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -6,10 +6,11 @@ namespace ssd {
 namespace {
 
 // The states that every chunk starts from: hops[0] = init, hops[k + 1] = exp(A dtsum[k]) hops[k] + (chunk k's own end
-// state, which hops[k + 1] holds on entry).
+// state, which hops[k + 1] holds on entry).  hops and dtsum are written by a launch that may still run when this one
+// starts: plain loads behind the wait, from pointers that promise nothing.
 __global__ void __launch_bounds__(256) selective_hop_kernel(const float* __restrict__ A, const float* __restrict__ init,
-                                                            int channels, int dstate, int nchunks, float* __restrict__ hops,
-                                                            const float* __restrict__ dtsum) {
+                                                            int channels, int dstate, int nchunks, float* hops,
+                                                            const float* dtsum) {
     const int64_t n = (int64_t)channels * dstate, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int b = blockIdx.y;
     if (i >= n) return;

@@ -268,12 +268,12 @@ __global__ void __launch_bounds__(128, 3) selective_terms_kernel(SelectiveArgs a
 }
 
 // hops[k]: the state that block k starts from; mus[k]: the gradient that reaches the state after block k from later
-// tokens; dinit.
+// tokens; dinit.  The four workspaces are written by a launch that may still run when this one starts: plain loads behind
+// the wait, from pointers that promise nothing.
 __global__ void __launch_bounds__(256) selective_hops_kernel(const float* __restrict__ A, const float* __restrict__ init,
                                                              const float* __restrict__ dfinal, int channels, int dstate,
-                                                             int nblocks, float* __restrict__ hops, float* __restrict__ mus,
-                                                             const float* __restrict__ nu0, const float* __restrict__ dtsum,
-                                                             float* __restrict__ dinit) {
+                                                             int nblocks, float* hops, float* mus, const float* nu0,
+                                                             const float* dtsum, float* __restrict__ dinit) {
     const int64_t n = (int64_t)channels * dstate, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int b = blockIdx.y;
     if (i >= n) return;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256) selective_hops_kernel(const float* __rest
         for (int u = 0; u < AHEAD; ++u)
             if (k + u + 1 < nblocks) {
                 term[u] = at[(u + 1) * step];
-                sum[u] = __ldg(dp + u * dstep);
+                sum[u] = dp[u * dstep];
             }
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)

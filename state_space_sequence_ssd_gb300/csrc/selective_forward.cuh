@@ -69,7 +69,7 @@ __device__ __forceinline__ void read_entries(const float* p, f32x2 (&o)[PAIRS]) 
 // VEC: every row of x, dt, z, y, B and C is whole 16-byte pieces, copied without a register between.
 template <typename T, int CH, int ST, int LP, bool STATE_ONLY, bool VEC>
 __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int chunk, int nchunks, T* __restrict__ y,
-                                                           float* __restrict__ final_state, float* __restrict__ hops,
+                                                           float* __restrict__ final_state, float* hops,
                                                            float* __restrict__ dtsum) {
     using K = Tile<T, CH, ST, LP>;
     constexpr int TS = K::TS, NP = K::NP, E = K::E, PAIRS = ST / 2;
