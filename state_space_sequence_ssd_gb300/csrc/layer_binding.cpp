@@ -23,6 +23,14 @@ using at::Tensor;
 // A Python exception that is already set.
 struct Raised {};
 
+// A reference that is given up at the end of the scope.
+struct Held {
+    PyObject* o = nullptr;
+    Held() = default;
+    Held(const Held&) = delete;
+    ~Held() { Py_XDECREF(o); }
+};
+
 [[noreturn]] void refuse(PyObject* kind, const std::string& text) {
     PyErr_SetString(kind, text.c_str());
     throw Raised();
@@ -238,6 +246,7 @@ PyObject* conv_backward(PyObject* const* a) {
     const Lead l = lead(x, "x", 3);
     const int64_t b = x.size(0), L = x.size(1), ch = x.size(2);
     const Taps w = taps(a[1], a[2], ch, l);
+    Held seq;  // until the call is made: it may be all that holds the pieces (of an iterator that makes them)
     const void *dy[3] = {nullptr, nullptr, nullptr};
     int n[3] = {0, 0, 0}, f32[3] = {0, 0, 0};
     auto piece = [&](PyObject* o, int i) {
@@ -251,17 +260,11 @@ PyObject* conv_backward(PyObject* const* a) {
     if (THPVariable_Check(a[3])) {
         piece(a[3], 0);
     } else {
-        PyObject* seq = PySequence_Fast(a[3], "dy must be a tensor or a sequence of one to three");
-        if (seq == nullptr) throw Raised();
-        const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
-        try {
-            if (count < 1 || count > 3) refuse(PyExc_ValueError, "dy must be a tensor or a sequence of one to three");
-            for (Py_ssize_t i = 0; i < count; ++i) piece(PySequence_Fast_GET_ITEM(seq, i), (int)i);
-        } catch (...) {
-            Py_DECREF(seq);
-            throw;
-        }
-        Py_DECREF(seq);
+        seq.o = PySequence_Fast(a[3], "dy must be a tensor or a sequence of one to three");
+        if (seq.o == nullptr) throw Raised();
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq.o);
+        if (count < 1 || count > 3) refuse(PyExc_ValueError, "dy must be a tensor or a sequence of one to three");
+        for (Py_ssize_t i = 0; i < count; ++i) piece(PySequence_Fast_GET_ITEM(seq.o, i), (int)i);
     }
     if ((int64_t)n[0] + n[1] + n[2] != ch) refuse(PyExc_ValueError, "the pieces of dy must add up to x's " + std::to_string(ch) + " channels");
     void* init = dense(a[4], "init_state", l.type, {b, w.width - 1, ch}, l);

@@ -71,8 +71,9 @@ def ssd_conv_backward(x, weight, bias, dy, init_state=None, lengths=None, silu=T
     final state.  ``dx`` may be given: a tensor like x whose last dimension is dense (a slice of a projection's
     gradient)."""
     if stream is not None:
+        dy = [dy] if isinstance(dy, torch.Tensor) else list(dy)  # an iterator's pieces are taken once
         return _on(stream, _native.conv_backward, (x, weight, bias, dy, init_state, lengths, silu, dfinal, dx, want_dinit),
-                   (x, weight, bias, *([dy] if isinstance(dy, torch.Tensor) else dy), init_state, lengths, dfinal, dx))
+                   (x, weight, bias, *dy, init_state, lengths, dfinal, dx))
     return _native.conv_backward(x, weight, bias, dy, init_state, lengths, silu, dfinal, dx, want_dinit)
 
 
