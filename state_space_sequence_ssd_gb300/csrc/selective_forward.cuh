@@ -67,7 +67,10 @@ __device__ __forceinline__ void read_entries(const float* p, f32x2 (&o)[PAIRS]) 
 }
 
 // VEC: every row of x, dt, z, y, B and C is whole 16-byte pieces, copied without a register between.
-template <typename T, int CH, int ST, int LP, bool STATE_ONLY, bool VEC>
+// PAD: the lanes hold more entries than there are.  Those have A = B = C = 0 and stay zero, until dt x is infinite: zero
+// times that is NaN, and so would be y.  A tile with such a value, told by the barrier that it has anyway, goes through a
+// loop that sets them to zero again at each token.  (A first run's entries past the last are not stored, so it needs none.)
+template <typename T, int CH, int ST, int LP, bool STATE_ONLY, bool VEC, bool PAD>
 __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int chunk, int nchunks, T* __restrict__ y,
                                                            float* __restrict__ final_state, float* hops,
                                                            float* __restrict__ dtsum) {
@@ -216,6 +219,7 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
         __syncthreads();  // the tile's copies have landed; the last tile's sums and inputs are read
         if (t0 + TS < last) fetch(t0 + TS, buf ^ 1);
         const T* in = raw + buf * buffer;
+        float undefined = 0.f;  // PAD: not zero once a dt x is not finite
         if (w0 < TS) {
             // all of the thread's vectors side by side: each value's dt is a chain of a dozen dependent instructions
             float d[4 * CONVS];
@@ -239,6 +243,7 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
                     d[4 * i + e] = live ? d[4 * i + e] : 0.f;
                     dx[e] = d[4 * i + e] * xv[i].get(e);
                     if (STATE_ONLY) dsum[e] += d[4 * i + e];
+                    if (PAD) undefined = fmaf(0.f, dx[e], undefined);
                 }
                 *reinterpret_cast<float4*>(s_d + at) = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
                 *reinterpret_cast<float4*>(s_x + at) = make_float4(dx[0], dx[1], dx[2], dx[3]);
@@ -248,15 +253,16 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
             const Vec<T, 4> v = load_vec<T, 4, true>(in + 3 * TS * CC + 4 * i, 4, true);
             reinterpret_cast<float4*>(s_B)[i] = make_float4(v.get(0), v.get(1), v.get(2), v.get(3));
         }
-        __syncthreads();
+        bool clear = false;
+        if (PAD) clear = __syncthreads_or(undefined != 0.f) != 0;
+        else __syncthreads();
         const int steps = last - t0 < TS ? last - t0 : TS;  // none for a tile past the length
         float d[CH], x[CH];
         f32x2 B[PAIRS];
         read_channels(s_d + CH * qd, d);
         read_channels(s_x + CH * qd, x);
         read_entries(s_B + ST * q, B);
-#pragma unroll 2
-        for (int t = 0; t < steps; ++t) {
+        auto token = [&](int t, auto clearing) {
             // the next token's operands, before this one's sums are stored over dt
             const int up = t + 1 < TS ? t + 1 : 0;
             float dn[CH], xn[CH];
@@ -270,6 +276,14 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
                 const f32x2 dd = pk(d[c], d[c]), xx = pk(x[c], x[c]);
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) h[c][i] = fma2(exp2_2(mul2(dd, A[c][i])), h[c][i], mul2(xx, B[i]));
+                if constexpr (decltype(clearing)::value) {
+#pragma unroll
+                    for (int i = 0; i < PAIRS; ++i) {
+                        float lo, hi;
+                        unpk(h[c][i], lo, hi);
+                        h[c][i] = pk(ST * q + 2 * i < N ? lo : 0.f, ST * q + 2 * i + 1 < N ? hi : 0.f);
+                    }
+                }
             }
             if (!STATE_ONLY) {
                 float v[CH];
@@ -292,6 +306,13 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
             for (int c = 0; c < CH; ++c) { d[c] = dn[c]; x[c] = xn[c]; }
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) B[i] = Bn[i];
+        };
+        if (PAD && clear) {
+#pragma unroll 1
+            for (int t = 0; t < steps; ++t) token(t, std::integral_constant<bool, PAD>());
+        } else {
+#pragma unroll 2
+            for (int t = 0; t < steps; ++t) token(t, std::false_type());
         }
         if (!STATE_ONLY) {
             __syncthreads();
@@ -380,18 +401,24 @@ int forward_shape(const SelectiveArgs& a, const SelectiveShape& f, int chunks, T
         else kernel<<<grid, f.threads, smem, s>>>(a, chunk, nchunks, y, final_state, hops, dtsum);
         return launch_end(kKindSelective, s);
     };
-    const bool vec = rows_of(a, K::E, y, nullptr, sizeof(T)) && f.cc % K::E == 0 && states_of(a, K::E, sizeof(T)) &&
-                     K::NP % K::E == 0;
+    constexpr bool WHOLE = K::NP % K::E == 0;  // the padded entries are whole copies
+    const bool vec = WHOLE && rows_of(a, K::E, y, nullptr, sizeof(T)) && f.cc % K::E == 0 && states_of(a, K::E, sizeof(T));
     int r = SSD_OK;
     if (nchunks > 1) {
-        r = vec ? go(selective_kernel<T, CH, ST, LP, true, true>, nchunks - 1, false)
-                : go(selective_kernel<T, CH, ST, LP, true, false>, nchunks - 1, false);
+        if constexpr (WHOLE)
+            if (vec) r = go(selective_kernel<T, CH, ST, LP, true, true, false>, nchunks - 1, false);
+        if (!vec) r = go(selective_kernel<T, CH, ST, LP, true, false, false>, nchunks - 1, false);
         if (r != SSD_OK) return r;
         r = launch_selective_hop(a, nchunks, hops, dtsum, s);
         if (r != SSD_OK) return r;
     }
-    return vec ? go(selective_kernel<T, CH, ST, LP, false, true>, nchunks, nchunks > 1)
-               : go(selective_kernel<T, CH, ST, LP, false, false>, nchunks, nchunks > 1);
+    const bool pad = a.dstate < K::NP;
+    if constexpr (WHOLE) {
+        if (vec) return pad ? go(selective_kernel<T, CH, ST, LP, false, true, true>, nchunks, nchunks > 1)
+                            : go(selective_kernel<T, CH, ST, LP, false, true, false>, nchunks, nchunks > 1);
+    }
+    return pad ? go(selective_kernel<T, CH, ST, LP, false, false, true>, nchunks, nchunks > 1)
+               : go(selective_kernel<T, CH, ST, LP, false, false, false>, nchunks, nchunks > 1);
 }
 
 template <typename T>

@@ -1,0 +1,75 @@
+"""Live infinities and NaN through the selective scan: what the 64-bit definition makes of them, entry for entry, where dstate
+leaves entries, channels and tokens of the kernels' tiles without a use.
+
+Every term is positive (or of one sign per channel), so that the definition's infinities do not meet and their signs are
+certain; where it still is NaN the kernels' result has to be NaN or infinite, where it is finite their result has to be close to
+it (the tolerances are those of test_layer_gpu.py)."""
+import numpy as np
+import pytest
+import torch
+
+from test_layer_gpu import TYPES, ROUND, Draw, np64, plain_selective, selective_args, spoil, ssd, step_roundings  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+#        type, batch, tokens, channels, groups, dstate, gate, lengths
+CASES = [("f32", 2, 40, 8, 1, 3, True, None), ("bf16", 2, 40, 24, 1, 13, True, [40, 37]), ("f16", 2, 50, 12, 2, 1, False, [47, 50]),
+         ("f32", 1, 33, 9, 1, 5, True, None), ("bf16", 1, 45, 16, 1, 24, True, [41]), ("f16", 2, 40, 8, 1, 33, False, None),
+         ("f32", 2, 60, 8, 2, 100, True, [60, 59]), ("bf16", 2, 40, 32, 1, 16, True, [40, 33]), ("f32", 1, 200, 8, 1, 3, False, None),
+         ("bf16", 3, 70, 16, 1, 20, True, [70, 0, 33])]
+
+
+def case(c, what, seed=17):
+    """Inputs of one sign with `what` put into them: (inputs, options, the generator)."""
+    kind, b, L, ch, G, N, gate, lengths = c
+    d, T = Draw(seed), TYPES[kind]
+    some = lambda *shape, dtype=T: (d.normal(*shape).abs() + 0.1).to(dtype)  # noqa: E731
+    s = dict(x=some(b, L, ch), A=-torch.exp(d.normal(ch, N, scale=0.3)), dt=d.normal(b, L, ch, dtype=T, scale=0.3), B=some(b, L, G, N),
+             C=some(b, L, G, N), D=some(ch, dtype=torch.float32), z=some(b, L, ch) if gate else None,
+             bias=d.normal(ch, scale=0.2) - 4, init=some(b, ch, N, dtype=torch.float32),
+             lengths=None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    if what == "x":  # two channels, each of one sign
+        s["x"][0, L // 2, 1], s["x"][0, L // 3, ch - 1] = INF, -INF
+        s["init"][0, ch - 1] *= -1
+        s["x"][0, :, ch - 1] *= torch.where(s["x"][0, :, ch - 1] > 0, -1, 1)
+    elif what == "x nan":
+        s["x"][0, L // 2, 0] = NAN
+    elif what == "dt":
+        s["dt"][0, L // 2, 1] = INF
+    elif what == "last x":  # the row's last token: no later one carries it
+        n = L if lengths is None else lengths[0]
+        s["x"][0, n - 1, 1] = INF
+    for k in ("x", "dt", "z", "B", "C"):
+        spoil(s[k], s["lengths"], NAN)
+    return s, dict(dt_bias=s["bias"], dt_softplus=True, z=s["z"]), d
+
+
+def agree(name, got, want, mag, roundings):
+    rel, least = ROUND[got.dtype]
+    g = got.double().cpu().numpy()
+    assert g.shape == want.shape, name
+    finite = np.isfinite(want)
+    tol = rel * np.abs(want[finite]) + least + roundings * 2.0 ** -22 * (1 + rel) * mag[finite]
+    bad = ~(np.abs(g[finite] - want[finite]) <= tol)
+    assert not bad.any(), f"{name}: {bad.sum()} of {bad.size} finite ones off, {np.count_nonzero(~np.isfinite(g[finite]))} not finite"
+    inf = np.isinf(want)
+    assert np.array_equal(g[inf], want[inf]), f"{name}: an infinity became {g[inf][g[inf] != want[inf]][:4]}"
+    assert not np.isfinite(g[np.isnan(want)]).any(), f"{name}: a NaN became a number"
+
+
+def plain(s, opts, **kw):
+    with np.errstate(invalid="ignore", over="ignore"):
+        return plain_selective(s, {"dt_limit": None, **opts}, **kw), plain_selective(s, {"dt_limit": None, **opts}, mag=True, **kw)
+
+
+@pytest.mark.parametrize("what", ["x", "x nan", "dt", "last x"])
+@pytest.mark.parametrize("c", CASES)
+def test_forward(ssd, c, what):  # noqa: F811
+    s, opts, _ = case(c, what)
+    y, final = ssd.ssd_selective_forward(*selective_args(s), s["init"], s["lengths"], **opts)
+    (ref, rfinal), (mag, mfinal) = plain(s, opts)
+    assert what == "x nan" or np.isinf(ref).any()
+    k = step_roundings(s) + s["x"].shape[1] + s["A"].shape[1]
+    agree("y", y, ref, mag, k + 8)
+    agree("final", final, rfinal, mfinal, k)
