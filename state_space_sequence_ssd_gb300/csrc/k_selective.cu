@@ -113,8 +113,18 @@ __global__ void __launch_bounds__(256, 4) selective_step_kernel(SelectiveArgs a,
         const f32x2 dd = pk(d, d), dxx = pk(dx, dx);
         const f32x2 h01 = fma2(exp2_2(mul2(dd, A01)), h[r].pair(0), mul2(dxx, Bv[r].pair(0)));
         const f32x2 h23 = fma2(exp2_2(mul2(dd, A23)), h[r].pair(1), mul2(dxx, Bv[r].pair(1)));
-        acc[r] = sum2(fma2(Cv[r].pair(1), h23, mul2(Cv[r].pair(0), h01)));
         const f32x2 o[2] = {h01, h23};
+        // entries past dstate, whose zeros are NaN once dt x is infinite, are left out of the sum
+        if constexpr (VEC) {
+            acc[r] = nvalid > 0 ? sum2(fma2(Cv[r].pair(1), h23, mul2(Cv[r].pair(0), h01))) : 0.f;
+        } else {
+            float p[4], sum = 0.f;
+            unpk(mul2(Cv[r].pair(0), h01), p[0], p[1]);
+            unpk(mul2(Cv[r].pair(1), h23), p[2], p[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += e < nvalid ? p[e] : 0.f;
+            acc[r] = sum;
+        }
         if (slot[r] >= 0)
             store_vec<float, 4>(state + ((int64_t)slot[r] * a.channels + c) * N + 4 * q, Vec<float, 4>::of_pairs(o), nvalid, vecs);
     }

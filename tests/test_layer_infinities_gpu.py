@@ -73,3 +73,21 @@ def test_forward(ssd, c, what):  # noqa: F811
     k = step_roundings(s) + s["x"].shape[1] + s["A"].shape[1]
     agree("y", y, ref, mag, k + 8)
     agree("final", final, rfinal, mfinal, k)
+
+
+@pytest.mark.parametrize("what", ["x", "x nan", "dt"])
+@pytest.mark.parametrize("c", CASES)
+def test_step(ssd, c, what):  # noqa: F811
+    """The token that holds the infinity and the one after it, from the state before them."""
+    s, opts, _ = case(c[:-1] + (None,), what)
+    b, L, ch, G, N = *s["x"].shape, *s["B"].shape[2:]
+    state = s["init"].clone()
+    for t in (L // 3, L // 2, L // 2 + 1):
+        one = {n: v[:, t] if n in ("x", "dt", "B", "C", "z") and v is not None else v for n, v in s.items()}
+        row = {n: v[:, t:t + 1] if n in ("x", "dt", "B", "C", "z") and v is not None else v for n, v in s.items()}
+        row["init"] = state.clone()
+        (ref, rfinal), (mag, mfinal) = plain(row, {**opts, "z": row["z"]})
+        y = ssd.ssd_selective_step(*selective_args(one), state, **{**opts, "z": one["z"]})
+        k = step_roundings(s) + 1 + N
+        agree("y", y, ref[:, 0], mag[:, 0], k + 8)
+        agree("state", state, rfinal, mfinal, k)
