@@ -100,4 +100,22 @@ int selective_forward_bf16(const SelectiveArgs& a, const SelectivePlan& p, void*
 int selective_forward_f16(const SelectiveArgs& a, const SelectivePlan& p, void* y, float* final_state, float* ws, cudaStream_t s);
 int selective_forward_f32(const SelectiveArgs& a, const SelectivePlan& p, void* y, float* final_state, float* ws, cudaStream_t s);
 
+
+// How the gradient runs: the tokens of a block, blocks of a row, blocks of a group's channels, and the floats of each part
+// of its workspace.
+struct SelectiveParts {
+    int tokens, nblocks, tiles;  // of a block; blocks of a row; blocks of a group's channels
+    size_t hops, nu0, dtsum, chan, dbc;  // floats of each part
+    size_t total() const { return 2 * hops + nu0 + dtsum + chan + dbc; }
+};
+SelectiveParts selective_parts(const SelectiveArgs& a);
+int selective_block_threads(const SelectiveArgs& a);
+int launch_selective_hops(const SelectiveArgs& a, const SelectiveGrads& g, const SelectiveParts& p, float* hops, float* mus,
+                          const float* nu0, const float* dtsum, cudaStream_t s);
+int launch_selective_sums(const SelectiveArgs& a, const SelectiveGrads& g, const SelectiveParts& p, const float* dA_parts,
+                          const float* chan, const float* dbc, cudaStream_t s);
+int selective_backward_bf16(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, cudaStream_t s);
+int selective_backward_f16(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, cudaStream_t s);
+int selective_backward_f32(const SelectiveArgs& a, const SelectiveGrads& g, float* ws, cudaStream_t s);
+
 }  // namespace ssd

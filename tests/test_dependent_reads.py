@@ -13,7 +13,7 @@ KERNELS = {"conv_reduce_kernel": ("k_conv.cu", ["partial"], True),
            "selective_hop_kernel": ("k_selective.cu", ["hops", "dtsum"], True),
            "selective_kernel": ("selective_forward.cuh", ["hops"], False),
            "selective_hops_kernel": ("k_selective_bwd.cu", ["hops", "mus", "nu0", "dtsum"], True),
-           "selective_block_kernel": ("k_selective_bwd.cu", ["start", "end"], False),
+           "selective_block_kernel": ("selective_backward.cuh", ["start", "end"], False),
            "selective_sums_kernel": ("k_selective_bwd.cu", [], True)}
 
 
@@ -43,6 +43,6 @@ def test_what_the_launch_before_writes_is_read_plainly(name):
 
 def test_every_dependent_kernel_of_the_layer_operators_is_listed():
     seen = set()
-    for file in ("k_conv.cu", "k_norm.cu", "k_selective.cu", "k_selective_bwd.cu", "selective_forward.cuh"):
+    for file in ("k_conv.cu", "k_norm.cu", "k_selective.cu", "k_selective_bwd.cu", "selective_backward.cuh", "selective_forward.cuh"):
         seen |= set(re.findall(r"launch_dependent\((\w+)", open(os.path.join(CSRC, file)).read()))
     assert seen - {"kernel"} == set(KERNELS) - {"selective_kernel"}  # that one is launched under a generic name
