@@ -32,7 +32,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int LP, int BLOCK>  // BLOCK: tokens of a block
 struct Blk {
-    static constexpr int CW = 32 / LP, NP = 4 * LP;  // lanes' groups of four channels in a warp; entries, padded
+    static constexpr int NP = 4 * LP;                // entries, padded
     static constexpr int CONV = LP;                  // tokens that the block's threads convert at once
     static constexpr int CONVS = BLOCK / CONV;
     static_assert(CONVS > 0, "tokens for every thread");
@@ -95,14 +95,15 @@ __device__ __forceinline__ Loaded<T, M> load_rows(const SelectiveArgs& a, const 
 }
 
 // The block's tokens into shared memory: dt, dt x and g per token and channel, B and C as float32; zero past the length.
+// Returns zero, or NaN where this thread's part of dt x, g, B or C is not all finite.
 template <typename T, int LP, int BLOCK>
-__device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T>& r, float* s_d, float* s_x, float* s_g,
-                                            float* s_B, float* s_C, bool vec, bool vecb, float (&dsum)[4]) {
+__device__ __forceinline__ float stage_block(const SelectiveArgs& a, const Rows<T>& r, float* s_d, float* s_x, float* s_g,
+                                             float* s_B, float* s_C, bool vec, bool vecb, float (&dsum)[4]) {
     using K = Blk<LP, BLOCK>;
     constexpr int M = K::CONVS < 8 ? K::CONVS : 8;
     const int tid = threadIdx.x, threads = blockDim.x, cc = K::channels(threads);
     const int v0 = tid % (cc / 4), w0 = tid / (cc / 4);
-    float bias[4];
+    float bias[4], undefined = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) dsum[e] = 0.f;
 #pragma unroll 1
@@ -129,6 +130,8 @@ __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T
                     if (j < BLOCK * LP) {
                         *reinterpret_cast<float4*>(s_B + 4 * j) = make_float4(B[u].get(0), B[u].get(1), B[u].get(2), B[u].get(3));
                         *reinterpret_cast<float4*>(s_C + 4 * j) = make_float4(C[u].get(0), C[u].get(1), C[u].get(2), C[u].get(3));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) undefined = fmaf(0.f, C[u].get(e), fmaf(0.f, B[u].get(e), undefined));
                     }
                 }
             }
@@ -164,6 +167,7 @@ __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T
                     dt[4 * i + e] = live ? dt[4 * i + e] : 0.f;
                     dx[e] = dt[4 * i + e] * l.x[s + i].get(e);
                     dsum[e] += dt[4 * i + e];
+                    undefined = fmaf(0.f, g[4 * i + e], fmaf(0.f, dx[e], undefined));
                 }
                 *reinterpret_cast<float4*>(s_d + at) = make_float4(dt[4 * i], dt[4 * i + 1], dt[4 * i + 2], dt[4 * i + 3]);
                 *reinterpret_cast<float4*>(s_x + at) = make_float4(dx[0], dx[1], dx[2], dx[3]);
@@ -171,6 +175,7 @@ __device__ __forceinline__ void stage_block(const SelectiveArgs& a, const Rows<T
             }
         }
     }
+    return undefined;
 }
 
 // A lane's four entries of four channels, as pairs of channels, from and to (channels, dstate) float32.
@@ -270,7 +275,122 @@ __global__ void __launch_bounds__(128, 3) selective_terms_kernel(SelectiveArgs a
     }
 }
 
-template <typename T, int LP, int BLOCK>
+// A channel's sums over its lanes, to the token's row: each lane ends with one (or several) of its four channels.
+template <int LP>
+__device__ __forceinline__ void join_lanes(f32x2 lo, f32x2 hi, int lane, float* to) {
+    float v[4];
+    unpk(lo, v[0], v[1]);
+    unpk(hi, v[2], v[3]);
+    int which = 0;
+    fold_between<4, LP / 2, 1>(v, lane, which);
+    if (LP <= 4 || (lane & (LP / 4 > 0 ? LP / 4 - 1 : 0)) == 0) {
+#pragma unroll
+        for (int e = 0; e < (LP >= 4 ? 1 : 4 / LP); ++e) to[which + e] = v[e];
+    }
+}
+// Four values over the warp's channels, to a lane's entries of a token's row of dB or dC.
+template <int LP>
+__device__ __forceinline__ void join_warp(float (&v)[4], int lane, float* to) {
+    constexpr int CW = 32 / LP, LEFT = CW >= 4 ? 1 : 4 / CW;
+    int which = 0;
+    fold_between<4, 16, LP>(v, lane, which);
+    if (CW <= 4 || ((lane / LP) & (CW / 4 > 0 ? CW / 4 - 1 : 0)) == 0) {
+#pragma unroll
+        for (int e = 0; e < LEFT; ++e) to[which + e] = v[e];
+    }
+}
+// A token's dt, dt x, g, B and C for a lane's channels and entries; loaded a token ahead, so that no load waits behind a
+// store it might meet.
+struct Operands {
+    float4 d, x, g, B, C;
+};
+template <int LP>
+struct Lane {
+    float *s_d, *s_x, *s_g, *s_B, *s_C;
+    int cc, qd, q;
+    static constexpr int NP = 4 * LP;
+    __device__ __forceinline__ Operands operands(int t) const {
+        auto at = [](const float* p) { return *reinterpret_cast<const float4*>(p); };
+        return Operands{at(s_d + t * cc + 4 * qd), at(s_x + t * cc + 4 * qd), at(s_g + t * cc + 4 * qd), at(s_B + t * NP + 4 * q),
+                        at(s_C + t * NP + 4 * q)};
+    }
+    __device__ __forceinline__ void advance(int t, const Entries& A, Entries& h) const {  // the states over token t
+        f32x2 d[2], x[2], B[4];
+        pairs_of(s_d + t * cc + 4 * qd, d);
+        pairs_of(s_x + t * cc + 4 * qd, x);
+        twice_of(s_B + t * NP + 4 * q, B);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) h[e][j] = fma2(exp2_2(mul2(d[j], A[e][j])), h[e][j], mul2(x[j], B[e]));
+    }
+};
+
+// The tokens of one run, last to first, each by itself from the run's checkpoint; y, red: this lane's places in the rows of
+// y and of the warp's parts of dB and dC.  Entries past dstate, channels past the group's last and tokens past the length are
+// zeros that add nothing -- unless they meet an infinity, zero times which is NaN: one of the token's other factors, or one in a
+// state that an earlier token left.  So a run that is not whole, and the runs of a block that holds an infinity or a NaN, come
+// here, where such zeros are left out of the sums; the same roundings otherwise.  A call of its own (its arrays in local
+// memory), so that it takes no registers from the runs that need none of this.
+template <int LP>
+__device__ __noinline__ void alone(const Lane<LP> at, const ulonglong2* ck, int first, int end, int entries, int channels,
+                                   float* y_row, float* red, const Entries& A, Entries& m, Entries& dA) {
+    const int lane = threadIdx.x & 31, threads = blockDim.x;
+    auto entry = [&](int e, f32x2 u, f32x2 v, f32x2 s) { return e < entries ? fma2(u, v, s) : s; };
+    auto over_channels = [&](const f32x2 (&u)[2], const f32x2 (&v)[2]) {
+        float s[2], p[2];
+        unpk(mul2(u[0], v[0]), s[0], s[1]);
+        s[0] = channels > 0 ? s[0] : 0.f;
+        s[1] = channels > 1 ? s[1] : 0.f;
+        unpk(fma2(u[1], v[1], pk(s[0], s[1])), p[0], p[1]);
+        return (channels > 2 ? p[0] : s[0]) + (channels > 3 ? p[1] : s[1]);
+    };
+#pragma unroll 1
+    for (int t = end - 1; t >= first; --t) {
+        Entries h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const ulonglong2 v = ck[e * threads];
+            h[e][0] = v.x;
+            h[e][1] = v.y;
+        }
+#pragma unroll 1
+        for (int i = first; i < t; ++i) at.advance(i, A, h);
+        const Operands o = at.operands(t);
+        const f32x2 d[2] = {pk(o.d.x, o.d.y), pk(o.d.z, o.d.w)}, x[2] = {pk(o.x.x, o.x.y), pk(o.x.z, o.x.w)},
+                    g[2] = {pk(o.g.x, o.g.y), pk(o.g.z, o.g.w)};
+        const float B[4] = {o.B.x, o.B.y, o.B.z, o.B.w}, C[4] = {o.C.x, o.C.y, o.C.z, o.C.w};
+        f32x2 y[2] = {0ull, 0ull}, sb[2] = {0ull, 0ull}, sa[2] = {0ull, 0ull};
+        float vB[4], vC[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f32x2 lam[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x2 w = exp2_2(mul2(d[j], A[e][j])), wh = mul2(w, h[e][j]);
+                h[e][j] = fma2(x[j], pk(B[e], B[e]), wh);
+                y[j] = entry(e, pk(C[e], C[e]), h[e][j], y[j]);
+                lam[j] = fma2(g[j], pk(C[e], C[e]), m[e][j]);
+                sb[j] = entry(e, lam[j], pk(B[e], B[e]), sb[j]);
+                m[e][j] = mul2(lam[j], w);
+                const f32x2 held = mul2(lam[j], wh);
+                dA[e][j] = fma2(held, d[j], dA[e][j]);
+                sa[j] = entry(e, held, A[e][j], sa[j]);
+            }
+            vC[e] = over_channels(h[e], g);
+            vB[e] = over_channels(lam, x);
+        }
+        float* row = red + t % kRun * 2 * Lane<LP>::NP;
+        join_lanes<LP>(y[0], y[1], lane, y_row + t * at.cc);
+        join_warp<LP>(vC, lane, row + Lane<LP>::NP);
+        join_lanes<LP>(sb[0], sb[1], lane, at.s_x + t * at.cc + 4 * at.qd);
+        join_lanes<LP>(sa[0], sa[1], lane, at.s_g + t * at.cc + 4 * at.qd);
+        join_warp<LP>(vB, lane, row);
+    }
+}
+
+// PAD: the lanes hold more entries than there are, or the blocks more channels, or the runs more tokens (`alone`).
+template <typename T, int LP, int BLOCK, bool PAD>
 __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a, const T* __restrict__ dy, int nblocks,
                                                                  const float* start, const float* end, float* dA_parts,
                                                                  T* __restrict__ dx, T* __restrict__ ddt,
@@ -287,10 +407,8 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     float *s_d = sm, *s_x = s_d + BLOCK * cc, *s_g = s_x + BLOCK * cc, *s_y = s_g + BLOCK * cc, *s_B = s_y + BLOCK * cc,
           *s_C = s_B + BLOCK * NP, *s_red = s_C + BLOCK * NP;
     ulonglong2* ck = reinterpret_cast<ulonglong2*>(s_red + warps * kRun * 2 * NP) + tid;
-    {
-        float unused[4];
-        stage_block<T, LP, BLOCK>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, unused);
-    }
+    float unused[4];
+    const float undefined = stage_block<T, LP, BLOCK>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, unused);
     Entries A, h, m, dA;
     read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
     grid_dep_wait();  // the hops
@@ -298,50 +416,17 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     read_entries(end + row, c, end != nullptr ? mine : 0, N, 4 * q, 1.f, m);
 #pragma unroll
     for (int e = 0; e < 4; ++e) dA[e][0] = dA[e][1] = 0ull;
-    __syncthreads();
+    bool finite = true;
+    if (PAD) finite = __syncthreads_or(undefined != 0.f) == 0;
+    else __syncthreads();
     const int steps = max(0, r.last - r.tb), runs = (steps + kRun - 1) / kRun;  // tokens past the length change nothing
 
-    auto advance = [&](int t) {  // the states over token t
-        f32x2 d[2], x[2], B[4];
-        pairs_of(s_d + t * cc + 4 * qd, d);
-        pairs_of(s_x + t * cc + 4 * qd, x);
-        twice_of(s_B + t * NP + 4 * q, B);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) h[e][j] = fma2(exp2_2(mul2(d[j], A[e][j])), h[e][j], mul2(x[j], B[e]));
-    };
-    // a channel's sums over its lanes, to the token's row: each lane ends with one (or several) of its four channels
-    auto join = [&](f32x2 lo, f32x2 hi, float* to) {
-        float v[4];
-        unpk(lo, v[0], v[1]);
-        unpk(hi, v[2], v[3]);
-        int which = 0;
-        fold_between<4, LP / 2, 1>(v, lane, which);
-        if (LP <= 4 || (q & (LP / 4 > 0 ? LP / 4 - 1 : 0)) == 0) {
-#pragma unroll
-            for (int e = 0; e < (LP >= 4 ? 1 : 4 / LP); ++e) to[4 * qd + which + e] = v[e];
-        }
-    };
-    // a token's dt, dt x, g, B and C; loaded a token ahead, so that no load waits behind a store it might meet
-    struct Operands {
-        float4 d, x, g, B, C;
-    };
-    auto operands = [&](int t) {
-        auto at = [](const float* p) { return *reinterpret_cast<const float4*>(p); };
-        return Operands{at(s_d + t * cc + 4 * qd), at(s_x + t * cc + 4 * qd), at(s_g + t * cc + 4 * qd), at(s_B + t * NP + 4 * q),
-                        at(s_C + t * NP + 4 * q)};
-    };
-    // four values over the warp's channels, to entries 4 q .. of a token's row of dB (which = 0) or dC (1)
+    const Lane<LP> at = {s_d, s_x, s_g, s_B, s_C, cc, qd, q};
+    auto advance = [&](int t) { at.advance(t, A, h); };
+    auto operands = [&](int t) { return at.operands(t); };
+    auto join = [&](f32x2 lo, f32x2 hi, float* to) { join_lanes<LP>(lo, hi, lane, to + 4 * qd); };
     auto join_channels = [&](float (&v)[4], int t, int half) {
-        int which = 0;
-        fold_between<4, 16, LP>(v, lane, which);
-        constexpr int LEFT = K::CW >= 4 ? 1 : 4 / K::CW;
-        float* to = s_red + ((warp * kRun + t % kRun) * 2 + half) * NP + 4 * q + which;
-        if (K::CW <= 4 || ((lane / LP) & (K::CW / 4 > 0 ? K::CW / 4 - 1 : 0)) == 0) {
-#pragma unroll
-            for (int e = 0; e < LEFT; ++e) to[e] = v[e];
-        }
+        join_warp<LP>(v, lane, s_red + ((warp * kRun + t % kRun) * 2 + half) * NP + 4 * q);
     };
     // tokens t0 .. t0 + 3 from the states before them: forward with y and dC, then backward with the rest
     auto half = [&](int t0) {
@@ -421,15 +506,30 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     };
     // backward, run by run, its second half first
     const int64_t place = ((int64_t)r.tile * a.batch + r.b) * a.seqlen;  // dbc: (tiles, batch, seqlen, ngroups, 2, dstate)
+    const int whole = finite ? steps / kRun : 0;
     for (int j = runs - 1; j >= 0; --j) {
+        if (PAD && j >= whole) {
+            Entries A2, m2, dA2;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) { A2[e][i] = A[e][i]; m2[e][i] = m[e][i]; dA2[e][i] = dA[e][i]; }
+            alone<LP>(at, ck + 4 * j * threads, j * kRun, min(steps, (j + 1) * kRun), N - 4 * q, mine, s_y + 4 * qd,
+                      s_red + warp * kRun * 2 * NP + 4 * q, A2, m2, dA2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) { m[e][i] = m2[e][i]; dA[e][i] = dA2[e][i]; }
+        } else {
 #pragma unroll 1
-        for (int s = 1; s >= 0; --s) {
-            restore(j);
-            if (s == 1) {
+            for (int s = 1; s >= 0; --s) {
+                restore(j);
+                if (s == 1) {
 #pragma unroll 2
-                for (int i = 0; i < kHeld; ++i) advance(j * kRun + i);
+                    for (int i = 0; i < kHeld; ++i) advance(j * kRun + i);
+                }
+                half(j * kRun + s * kHeld);
             }
-            half(j * kRun + s * kHeld);
         }
         __syncthreads();
         for (int i = tid; i < kRun * 2 * LP; i += threads) {  // four entries of a token's dB or dC, over the warps
@@ -440,8 +540,9 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
                 s = make_float4(s.x + u.x, s.y + u.y, s.z + u.z, s.w + u.w);
             }
             const float o[4] = {s.x, s.y, s.z, s.w};
-            store_vec<float, 4>(dbc + (((place + t) * a.ngroups + r.grp) * 2 + which) * N + e, Vec<float, 4>::of(o),
-                                t < r.te ? N - e : 0, N % 4 == 0);
+            store_vec<float, 4>(dbc + (((place + t) * a.ngroups + r.grp) * 2 + which) * N + e,
+                                !PAD || t < r.last ? Vec<float, 4>::of(o) : Vec<float, 4>::zero(), t < r.te ? N - e : 0,
+                                N % 4 == 0);
         }
         __syncthreads();
     }
@@ -551,12 +652,14 @@ int backward_blocks(const SelectiveArgs& a, const SelectiveParts& p, const Selec
     const int most = LP == 2 ? 64 : 128;
     const dim3 grid(a.ngroups * p.tiles, p.nblocks, a.batch);
     int r = ensure_smem_limit(reinterpret_cast<const void*>(selective_terms_kernel<T, LP, BLOCK>), K::floats_terms(most) * 4);
-    if (r == SSD_OK) r = ensure_smem_limit(reinterpret_cast<const void*>(selective_block_kernel<T, LP, BLOCK>), K::floats(most) * 4);
+    const bool pad = a.dstate < K::NP || a.channels / a.ngroups % K::channels(threads) != 0 || a.seqlen % kRun != 0 || a.lengths != nullptr;
+    const auto block = pad ? selective_block_kernel<T, LP, BLOCK, true> : selective_block_kernel<T, LP, BLOCK, false>;
+    if (r == SSD_OK) r = ensure_smem_limit(reinterpret_cast<const void*>(block), K::floats(most) * 4);
     if (r != SSD_OK) return r;
     T *dx = static_cast<T*>(g.dx), *ddt = static_cast<T*>(g.ddt), *dz = static_cast<T*>(g.dz);
     if (p.nblocks == 1 && g.dinit == nullptr) {  // the block starts and ends with the row
         launch_begin(kKindSelectiveBwd, s);
-        selective_block_kernel<T, LP, BLOCK><<<grid, threads, smem, s>>>(a, dy, 1, a.init, g.dfinal, hops, dx, ddt, dz, dbc, chan, vec, vecb);
+        block<<<grid, threads, smem, s>>>(a, dy, 1, a.init, g.dfinal, hops, dx, ddt, dz, dbc, chan, vec, vecb);
         r = launch_end(kKindSelectiveBwd, s);
     } else {
         launch_begin(kKindSelectiveBwd, s);
@@ -566,8 +669,12 @@ int backward_blocks(const SelectiveArgs& a, const SelectiveParts& p, const Selec
         r = launch_selective_hops(a, g, p, hops, mus, nu0, dtsum, s);
         if (r != SSD_OK) return r;
         launch_begin(kKindSelectiveBwd, s);
-        launch_dependent(selective_block_kernel<T, LP, BLOCK>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus, hops, dx, ddt,
-                         dz, dbc, chan, vec, vecb);
+        if (pad)
+            launch_dependent(selective_block_kernel<T, LP, BLOCK, true>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus, hops,
+                             dx, ddt, dz, dbc, chan, vec, vecb);
+        else
+            launch_dependent(selective_block_kernel<T, LP, BLOCK, false>, grid, dim3(threads), smem, s, a, dy, p.nblocks, hops, mus,
+                             hops, dx, ddt, dz, dbc, chan, vec, vecb);
         r = launch_end(kKindSelectiveBwd, s);
     }
     if (r != SSD_OK) return r;

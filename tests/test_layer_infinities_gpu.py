@@ -30,16 +30,18 @@ def case(c, what, seed=17):
              bias=d.normal(ch, scale=0.2) - 4, init=some(b, ch, N, dtype=torch.float32),
              lengths=None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda"))
     if what == "x":  # two channels, each of one sign
-        s["x"][0, L // 2, 1], s["x"][0, L // 3, ch - 1] = INF, -INF
-        s["init"][0, ch - 1] *= -1
-        s["x"][0, :, ch - 1] *= torch.where(s["x"][0, :, ch - 1] > 0, -1, 1)
+        if ch > 1:
+            s["x"][0, L // 3, ch - 1] = -INF
+            s["init"][0, ch - 1] *= -1
+            s["x"][0, :, ch - 1] *= torch.where(s["x"][0, :, ch - 1] > 0, -1, 1)
+        s["x"][0, L // 2, min(1, ch - 1)] = INF
     elif what == "x nan":
         s["x"][0, L // 2, 0] = NAN
     elif what == "dt":
-        s["dt"][0, L // 2, 1] = INF
+        s["dt"][0, L // 2, min(1, ch - 1)] = INF
     elif what == "last x":  # the row's last token: no later one carries it
         n = L if lengths is None else lengths[0]
-        s["x"][0, n - 1, 1] = INF
+        s["x"][0, n - 1, min(1, ch - 1)] = INF
     for k in ("x", "dt", "z", "B", "C"):
         spoil(s[k], s["lengths"], NAN)
     return s, dict(dt_bias=s["bias"], dt_softplus=True, z=s["z"]), d
@@ -59,8 +61,27 @@ def agree(name, got, want, mag, roundings):
 
 
 def plain(s, opts, **kw):
-    with np.errstate(invalid="ignore", over="ignore"):
-        return plain_selective(s, {"dt_limit": None, **opts}, **kw), plain_selective(s, {"dt_limit": None, **opts}, mag=True, **kw)
+    """Every row by itself and at its own length: a token past it is not there at all.  (The definition with its magnitudes.)"""
+    b, L = s["x"].shape[:2]
+    n = [L] * b if s["lengths"] is None else s["lengths"].tolist()
+    out = []
+    for mag in (False, True):
+        rows = []
+        for i in range(b):
+            cut = {k: v if v is None or k in ("A", "D", "bias", "lengths") else v[i:i + 1] if k == "init" else v[i:i + 1, :n[i]]
+                   for k, v in s.items()}
+            cut["lengths"] = None
+            given = {k: v[i:i + 1] if k == "dfinal" else v[i:i + 1, :n[i]] for k, v in kw.items()}
+            with np.errstate(invalid="ignore", over="ignore"):
+                rows.append(plain_selective(cut, {"dt_limit": None, **opts, "z": cut["z"]}, mag=mag, **given))
+        longer = lambda v, i: np.pad(v, [(0, 0), (0, L - n[i])] + [(0, 0)] * (v.ndim - 2))  # noqa: E731
+        if kw:
+            summed = ("dA", "dD", "ddt_bias")
+            out.append({k: sum(r[k] for r in rows) if k in summed else
+                        np.concatenate([r[k] if k == "dinit" else longer(r[k], i) for i, r in enumerate(rows)]) for k in rows[0]})
+        else:
+            out.append((np.concatenate([longer(r[0], i) for i, r in enumerate(rows)]), np.concatenate([r[1] for r in rows])))
+    return out
 
 
 @pytest.mark.parametrize("what", ["x", "x nan", "dt", "last x"])
@@ -91,3 +112,24 @@ def test_step(ssd, c, what):  # noqa: F811
         k = step_roundings(s) + 1 + N
         agree("y", y, ref[:, 0], mag[:, 0], k + 8)
         agree("state", state, rfinal, mfinal, k)
+
+
+@pytest.mark.parametrize("what", ["x", "x nan", "dt", "last x", "dy", "B", "C"])
+@pytest.mark.parametrize("c", CASES + [("f32", 1, 37, 1, 1, 4, True, None), ("bf16", 1, 44, 2, 2, 16, False, [39])])
+def test_backward(ssd, c, what):  # noqa: F811
+    """The last two cases have one channel a group, so that the sums over channels have one infinite term."""
+    s, opts, d = case(c, what)
+    b, L, ch, G, N = *s["x"].shape, *s["B"].shape[2:]
+    n = L if c[-1] is None else c[-1][0]
+    dy, df = (d.normal(b, L, ch).abs() + 0.1).to(s["x"].dtype), d.normal(b, ch, N).abs() + 0.1
+    if what == "dy":
+        dy[0, n - 2, ch - 1] = INF
+    elif what in ("B", "C"):
+        s[what][0, n - 2, G - 1, N - 1] = INF
+    spoil(dy, s["lengths"], NAN)
+    out = ssd.ssd_selective_backward(*selective_args(s), dy, s["init"], s["lengths"], dfinal=df, want_dinit=True, **opts)
+    ref, mag = plain(s, opts, dy=np64(dy), dfinal=np64(df))
+    k = 2 * step_roundings(s) + 2 * L + N + 16
+    for name in out:
+        if out[name] is not None:
+            agree(name, out[name], ref[name], mag[name], k + (ch / 4 if name in ("dB", "dC") else 0 if out[name].dim() > 2 else b * L / 4))
