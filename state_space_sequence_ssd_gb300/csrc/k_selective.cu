@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) selective_hop_kernel(const float* __restr
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
             if (k + u + 1 < nchunks) {
-                h = fmaf(exp2_fast(A2 * sum[u]), h, own[u]);
+                h = carried(A2 * sum[u], h, own[u]);
                 hp[(k + u + 1) * n] = h;
             }
     }

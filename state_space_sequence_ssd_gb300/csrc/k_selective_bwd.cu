@@ -38,14 +38,14 @@ __global__ void __launch_bounds__(256) selective_hops_kernel(const float* __rest
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
             if (k + u + 1 < nblocks) {
-                s = fmaf(exp2_fast(A2 * sum[u]), s, term[u]);
+                s = carried(A2 * sum[u], s, term[u]);
                 at[(u + 1) * step] = s;
             }
         at += AHEAD * step;
         dp += AHEAD * dstep;
     }
     if (back && dinit != nullptr)
-        dinit[b * n + i] = fmaf(exp2_fast(A2 * dtsum[(int64_t)b * nblocks * channels + i / dstate]), s, nu0[b * n + i]);
+        dinit[b * n + i] = carried(A2 * dtsum[(int64_t)b * nblocks * channels + i / dstate], s, nu0[b * n + i]);
 }
 
 // What the blocks' parts are added to, in one launch: thread blocks of three kinds after one another.  dA and then dD and

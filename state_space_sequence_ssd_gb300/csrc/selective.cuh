@@ -38,6 +38,12 @@ __device__ __forceinline__ void effective(float (&v)[M], const DtOpts& o) {
     }
 }
 
+// What arrives of s over tokens whose decays multiply to 2^v, and `own` that these tokens add.  The product may round to zero
+// where none of its decays is: an infinite s stays infinite then, as it does token by token, and is no zero times infinity.
+__device__ __forceinline__ float carried(float v, float s, float own) {
+    return fabsf(s) == __int_as_float(0x7f800000) && v > -__int_as_float(0x7f800000) ? s + own : fmaf(exp2_fast(v), s, own);
+}
+
 // Sums R values over the lanes at offsets OFF, OFF / 2, ..., MIN.  While a lane holds several values it keeps one half
 // and trades the other with its partner, so that R values cost about R shuffles.  The lane keeps the sums number
 // which .. which + (values left) - 1, in v[0 ..].

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(128, 3) selective_terms_kernel(SelectiveArgs a
     const int64_t c = r.c0 + 4 * qd, n = (int64_t)a.channels * N;
     float *s_d = sm, *s_x = s_d + BLOCK * cc, *s_g = s_x + BLOCK * cc, *s_B = s_g + BLOCK * cc, *s_C = s_B + BLOCK * K::NP;
     float dsum[4];
-    stage_block<T, LP, BLOCK>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, dsum);
+    const float undefined = stage_block<T, LP, BLOCK>(a, r, s_d, s_x, s_g, s_B, s_C, vec, vecb, dsum);
     Entries A, h, v, p;
     read_entries(a.A, c, mine, N, 4 * q, kLog2e, A);
 #pragma unroll
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(128, 3) selective_terms_kernel(SelectiveArgs a
             h[e][j] = v[e][j] = 0ull;
             p[e][j] = pk(1.f, 1.f);
         }
-    __syncthreads();
+    const bool finite = __syncthreads_or(undefined != 0.f) == 0;
     const int steps = r.last - r.tb;
 #pragma unroll 2
     for (int t = 0; t < steps; ++t) {
@@ -260,6 +260,22 @@ __global__ void __launch_bounds__(128, 3) selective_terms_kernel(SelectiveArgs a
                 p[e][j] = mul2(p[e][j], w);
                 v[e][j] = fma2(p[e][j], mul2(g[j], C[e]), v[e][j]);
             }
+    }
+    if (!finite) {
+        // the products of decays may have rounded to zero, which an infinite g would make NaN: the gradient token by token
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e][0] = v[e][1] = 0ull;
+#pragma unroll 1
+        for (int t = steps - 1; t >= 0; --t) {
+            f32x2 d[2], g[2], C[4];
+            pairs_of(s_d + t * cc + 4 * qd, d);
+            pairs_of(s_g + t * cc + 4 * qd, g);
+            twice_of(s_C + t * K::NP + 4 * q, C);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) v[e][j] = mul2(exp2_2(mul2(d[j], A[e][j])), fma2(g[j], C[e], v[e][j]));
+        }
     }
     const int64_t row = ((int64_t)r.b * nblocks + k) * n;
     if (k + 1 < nblocks) write_entries(hops + row + n, c, mine, N, 4 * q, h);

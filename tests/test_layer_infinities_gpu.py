@@ -133,3 +133,43 @@ def test_backward(ssd, c, what):  # noqa: F811
     for name in out:
         if out[name] is not None:
             agree(name, out[name], ref[name], mag[name], k + (ch / 4 if name in ("dB", "dC") else 0 if out[name].dim() > 2 else b * L / 4))
+
+
+def strong(c, what):
+    """Decays of about e^-7 a token: none is zero, but over a chunk or a block of the kernels their product is, in float32."""
+    s, opts, d = case(c, what)
+    s["A"] = s["A"] - 9
+    s["bias"] += 4
+    opts["dt_bias"] = s["bias"]
+    return s, opts, d
+
+
+STRONG = [("f32", 1, 200, 8, 1, 16, False, None), ("bf16", 2, 300, 12, 1, 5, True, [300, 150]), ("f16", 1, 130, 8, 2, 20, False, None)]
+
+
+@pytest.mark.parametrize("what", ["x", "dt", "none"])
+@pytest.mark.parametrize("c", STRONG)
+def test_forward_carries_an_infinite_state_over_strong_decays(ssd, c, what):  # noqa: F811
+    s, opts, _ = strong(c, what)
+    y, final = ssd.ssd_selective_forward(*selective_args(s), s["init"], s["lengths"], **opts)
+    (ref, rfinal), (mag, mfinal) = plain(s, opts)
+    k = step_roundings(s) + s["x"].shape[1] + s["A"].shape[1]
+    agree("y", y, ref, mag, k + 8)
+    agree("final", final, rfinal, mfinal, k)
+
+
+@pytest.mark.parametrize("what", ["x", "dy", "none"])
+@pytest.mark.parametrize("c", STRONG)
+def test_backward_carries_an_infinite_gradient_over_strong_decays(ssd, c, what):  # noqa: F811
+    s, opts, d = strong(c, what)
+    b, L, ch, N = *s["x"].shape, s["A"].shape[1]
+    dy, df = (d.normal(b, L, ch).abs() + 0.1).to(s["x"].dtype), d.normal(b, ch, N).abs() + 0.1
+    if what == "dy":
+        dy[0, L - 2, ch - 1] = INF
+    spoil(dy, s["lengths"], NAN)
+    out = ssd.ssd_selective_backward(*selective_args(s), dy, s["init"], s["lengths"], dfinal=df, want_dinit=True, **opts)
+    ref, mag = plain(s, opts, dy=np64(dy), dfinal=np64(df))
+    k = 2 * step_roundings(s) + 2 * L + N + 16
+    for name in out:
+        if out[name] is not None:
+            agree(name, out[name], ref[name], mag[name], k + (ch / 4 if name in ("dB", "dC") else 0 if out[name].dim() > 2 else b * L / 4))
