@@ -515,7 +515,8 @@ typedef struct ssd_selective_strides {
  *     y[b,t,c] = sum_n C[b,t,g,n] * h[c,n] + D[c] * x[b,t,c]
  * with ssd_input_options around it: dt_bias (channels), dt_softplus, dt_limit
  * act on dt, and y <- y * z * sigmoid(z) with z shaped like x; D_per_channel is
- * not read (D is one weight per channel here).
+ * not read (D is one weight per channel here).  A NaN dt stays NaN under dt_limit
+ * (ssd_forward_ex and ssd_step_ex make it dt_min).
  *   x, dt, z     (batch, seqlen, channels); B, C (batch, seqlen, ngroups, dstate)
  *   A            (channels, dstate) f32; D (channels) f32 or NULL
  *   init_state, final_state (batch, channels, dstate) f32 or NULL

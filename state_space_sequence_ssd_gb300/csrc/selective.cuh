@@ -24,6 +24,14 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(p, e, fmaxf(v, 0.f));
 }
 
+// v held to [lo, hi]; a NaN stays one (fminf and fmaxf would make it lo).
+__device__ __forceinline__ float held_to(float v, float lo, float hi) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(lo));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(hi));
+    return r;
+}
+
 // The effective dt of M values of raw dt with their bias added: softplus, limits.  The options are looked at once for
 // all of them: a branch within each value's chain of dependent instructions would run the chains one after another.
 template <int M>
@@ -34,7 +42,7 @@ __device__ __forceinline__ void effective(float (&v)[M], const DtOpts& o) {
     }
     if (o.limit) {
 #pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = fminf(fmaxf(v[i], o.lo), o.hi);
+        for (int i = 0; i < M; ++i) v[i] = held_to(v[i], o.lo, o.hi);
     }
 }
 

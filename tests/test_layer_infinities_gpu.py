@@ -173,3 +173,29 @@ def test_backward_carries_an_infinite_gradient_over_strong_decays(ssd, c, what):
     for name in out:
         if out[name] is not None:
             agree(name, out[name], ref[name], mag[name], k + (ch / 4 if name in ("dB", "dC") else 0 if out[name].dim() > 2 else b * L / 4))
+
+
+@pytest.mark.parametrize("c", [("f32", 2, 40, 8, 1, 3, True, None), ("bf16", 2, 40, 32, 1, 16, True, [40, 33])])
+def test_a_nan_dt_is_not_hidden_by_its_limits(ssd, c):  # noqa: F811
+    """The channel is NaN from there on, in a prompt, a step and the gradient; the others are as they would be."""
+    s, opts, d = case(c, "")
+    opts["dt_limit"] = (0.01, 0.03)
+    t, ch, N = 20, s["x"].shape[2], s["A"].shape[1]
+    s["dt"][0, t, 2] = NAN
+    y, final = ssd.ssd_selective_forward(*selective_args(s), s["init"], s["lengths"], **opts)
+    (ref, rfinal), (mag, mfinal) = plain(s, opts)
+    assert np.isnan(ref[0, t:, 2]).all() and np.isnan(rfinal[0, 2]).all() and np.isfinite(ref[:, :, :2]).all()
+    k = step_roundings(s) + s["x"].shape[1] + N
+    agree("y", y, ref, mag, k + 8)
+    agree("final", final, rfinal, mfinal, k)
+    one = {n: v[:, t] if n in ("x", "dt", "B", "C", "z") and v is not None else v for n, v in s.items()}
+    step = ssd.ssd_selective_step(*selective_args(one), s["init"].clone(), **{**opts, "z": one["z"]})
+    assert bool(torch.isnan(step[0, 2])) and int(torch.isnan(step).sum()) == 1
+    dy = (d.normal(*s["x"].shape).abs() + 0.1).to(s["x"].dtype)
+    spoil(dy, s["lengths"], NAN)
+    out = ssd.ssd_selective_backward(*selective_args(s), dy, s["init"], s["lengths"], **opts)
+    ref, mag = plain(s, opts, dy=np64(dy))
+    assert np.isnan(ref["dx"][0, t, 2]) and np.isfinite(ref["dx"][1]).all()
+    k = 2 * k + s["x"].shape[1] + 16
+    for name in ("dx", "ddt", "dz", "dA", "dB", "dC", "dD"):
+        agree(name, out[name], ref[name], mag[name], k + (ch / 4 if name in ("dB", "dC") else 0 if out[name].dim() > 2 else 20))
