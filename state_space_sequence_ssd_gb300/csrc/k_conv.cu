@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(32 * kWarps, V == 2 ? 5 : 4) conv_backward_ker
                     f32x2 q = pk(gv[i][2 * j], gv[i][2 * j + 1]);
                     if (!WHOLE && t + i >= len) q = 0ull;
                     g[3 + i][j] = q;
-                    if (!WHOLE && t + i >= last) q = 0ull;
+                    // the next run's tokens and those past the length add nothing, not zero times an infinite input
+                    if (!WHOLE && t + i >= min(last, len)) continue;
                     db[j] = add2(db[j], q);
 #pragma unroll
                     for (int k = 0; k < W; ++k) dw[k][j] = fma2(q, x[4 - W + k + i][j], dw[k][j]);
