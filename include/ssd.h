@@ -586,7 +586,9 @@ SSD_API int ssd_layer_norm_backward(int dtype, const void* x, long long x_row_st
  * SSD_ERR_RANGE if a value converted to a float16 tensor-core operand was
  * outside float16's finite range since the last read; otherwise SSD_ERR_SLOT
  * if a single-token call (ssd_conv_step, ssd_selective_step) met a slot index
- * past its pool since the last read; or SSD_ERR_CUDA if the read itself failed.
+ * past its pool since that was last reported; or SSD_ERR_CUDA if the read itself
+ * failed.  A slot flag beside one of the other two waits for the next read: read
+ * until SSD_OK.
  */
 SSD_API int ssd_get_device_error(void);
 

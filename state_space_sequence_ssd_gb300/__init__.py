@@ -421,5 +421,6 @@ def ssd_forward_plan(batch, seqlen, nheads, headdim, ngroups, dstate, chunk_size
 
 def ssd_get_device_error():
     """SSD_OK (0), SSD_ERR_TIMEOUT (5) if a bounded device wait gave up since the last read, SSD_ERR_RANGE (7) if a
-    float16 operand left its range, or SSD_ERR_SLOT (8) if a single-token call met a slot past its pool."""
+    float16 operand left its range, or SSD_ERR_SLOT (8) if a single-token call met a slot past its pool.  A slot flag
+    beside one of the other two is reported by the next read."""
     return _ffi.lib().ssd_get_device_error()

@@ -761,14 +761,16 @@ int ssd_step_multi(const void* x, const float* dt, const float* A, const void* B
 
 int ssd_get_device_error(void) {
     int v[3] = {0, 0, 0};
-    const int zero[3] = {0, 0, 0};
+    const int zero[2] = {0, 0};
     if (cudaMemcpyFromSymbol(v, g_ssd_device_error, sizeof(v)) != cudaSuccess) return SSD_ERR_CUDA;
-    if ((v[0] != 0 || v[1] != 0 || v[2] != 0) &&
-        cudaMemcpyToSymbol(g_ssd_device_error, zero, sizeof(zero)) != cudaSuccess)
-        return SSD_ERR_CUDA;
-    if (v[0] != 0) return SSD_ERR_TIMEOUT;
-    if (v[1] != 0) return SSD_ERR_RANGE;
-    return v[2] != 0 ? SSD_ERR_SLOT : SSD_OK;
+    // the scan's words together: what a stage reads after a wait that gave up may raise the range flag too
+    if (v[0] != 0 || v[1] != 0) {
+        if (cudaMemcpyToSymbol(g_ssd_device_error, zero, sizeof(zero)) != cudaSuccess) return SSD_ERR_CUDA;
+        return v[0] != 0 ? SSD_ERR_TIMEOUT : SSD_ERR_RANGE;
+    }
+    if (v[2] == 0) return SSD_OK;
+    if (cudaMemcpyToSymbol(g_ssd_device_error, zero, sizeof(int), 2 * sizeof(int)) != cudaSuccess) return SSD_ERR_CUDA;
+    return SSD_ERR_SLOT;
 }
 
 int ssd_debug_set_wait_limit_ns(unsigned long long ns) {
