@@ -503,7 +503,8 @@ SSD_API int ssd_conv_step(int dtype, const void* x, long long x_row_stride, cons
 
 /* Strides of the selective scan's inputs in elements, per row and per token (a
  * NULL pointer: all dense).  B and C are (ngroups, dstate) dense within a token;
- * ssd_selective_step reads the *_batch members only. */
+ * ssd_selective_step reads the *_batch members only, and those of z are read
+ * where there is a z. */
 typedef struct ssd_selective_strides {
     long long x_batch, x_token, dt_batch, dt_token, z_batch, z_token, B_batch, B_token, C_batch, C_token;
 } ssd_selective_strides;

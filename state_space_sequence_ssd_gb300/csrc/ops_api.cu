@@ -52,8 +52,8 @@ int read_conv(int dtype, const void* x, int64_t x_batch, int64_t x_token, const 
 }
 
 int read_selective(int dtype, const void* x, const void* dt, const float* A, const void* B, const void* C, const float* D,
-                   const float* init, const int* lengths, const ssd_selective_strides* st, int batch, int seqlen,
-                   int channels, int ngroups, int dstate, const ssd_input_options* o, SelectiveArgs* a) {
+                   const float* init, const int* lengths, const ssd_selective_strides* given, int batch, int seqlen,
+                   int channels, int ngroups, int dstate, const ssd_input_options* o, bool step, SelectiveArgs* a) {
     if (!x || !dt || !A || !B || !C || !known(dtype) || batch <= 0 || seqlen <= 0 || channels <= 0 || ngroups <= 0 ||
         dstate <= 0 || channels % ngroups != 0)
         return SSD_ERR_INVALID_ARG;
@@ -74,15 +74,17 @@ int read_selective(int dtype, const void* x, const void* dt, const float* A, con
         dto.hi = o->dt_max;
     }
     const int64_t row = channels, bc = (int64_t)ngroups * dstate;
-    ssd_selective_strides dense = {seqlen * row, row, seqlen * row, row, seqlen * row, row, seqlen * bc, bc, seqlen * bc, bc};
-    if (st == nullptr) st = &dense;
-    const long long all[] = {st->x_batch, st->x_token, st->dt_batch, st->dt_token, st->z_batch,
-                             st->z_token, st->B_batch, st->B_token, st->C_batch, st->C_token};
+    ssd_selective_strides s = {seqlen * row, row, seqlen * row, row, seqlen * row, row, seqlen * bc, bc, seqlen * bc, bc};
+    if (given != nullptr) s = *given;
+    if (step) s.x_token = s.dt_token = s.z_token = s.B_token = s.C_token = 0;  // not read
+    if (z == nullptr) s.z_batch = s.z_token = 0;
+    const long long all[] = {s.x_batch, s.x_token, s.dt_batch, s.dt_token, s.z_batch,
+                             s.z_token, s.B_batch, s.B_token, s.C_batch, s.C_token};
     for (long long v : all)
         if (v < 0) return SSD_ERR_INVALID_ARG;
     *a = SelectiveArgs{dtype, batch, seqlen, channels, ngroups, dstate, x, dt, B, C, z,
-                       st->x_batch, st->x_token, st->dt_batch, st->dt_token, st->B_batch, st->B_token,
-                       st->C_batch, st->C_token, st->z_batch, st->z_token, A, D, init, lengths, dto};
+                       s.x_batch, s.x_token, s.dt_batch, s.dt_token, s.B_batch, s.B_token,
+                       s.C_batch, s.C_token, s.z_batch, s.z_token, A, D, init, lengths, dto};
     return SSD_OK;
 }
 
@@ -159,7 +161,7 @@ int ssd_selective_forward(int dtype, const void* x, const void* dt, const float*
                           cudaStream_t stream) {
     SelectiveArgs a;
     int r = read_selective(dtype, x, dt, A, B, C, D, init_state, lengths, strides, batch, seqlen, channels, ngroups, dstate,
-                           options, &a);
+                           options, false, &a);
     if (r != SSD_OK) return r;
     if (!y || !on(y, size_of(dtype)) || !on(final_state, 4)) return SSD_ERR_INVALID_ARG;
     const SelectivePlan plan = selective_plan(a, multiprocessors());
@@ -178,7 +180,7 @@ int ssd_selective_backward(int dtype, const void* x, const void* dt, const float
                            float* dinit, cudaStream_t stream) {
     SelectiveArgs a;
     int r = read_selective(dtype, x, dt, A, B, C, D, init_state, lengths, strides, batch, seqlen, channels, ngroups, dstate,
-                           options, &a);
+                           options, false, &a);
     if (r != SSD_OK) return r;
     const uintptr_t size = size_of(dtype);
     if (!dy || !dx || !ddt || !dA || !dB || !dC || (a.z != nullptr) != (dz != nullptr)) return SSD_ERR_INVALID_ARG;
@@ -198,7 +200,7 @@ int ssd_selective_step(int dtype, const void* x, const void* dt, const float* A,
                        cudaStream_t stream) {
     SelectiveArgs a;
     const int r = read_selective(dtype, x, dt, A, B, C, D, nullptr, nullptr, strides, batch, 1, channels, ngroups, dstate,
-                                 options, &a);
+                                 options, true, &a);
     if (r != SSD_OK) return r;
     if (!y || !on(y, size_of(dtype)) || !state || !on(state, 4) || !on(slots, 4) || nslots <= 0 ||
         (slots == nullptr && nslots < batch))

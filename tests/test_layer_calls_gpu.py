@@ -38,3 +38,26 @@ def test_a_slot_flag_waits_behind_a_range_flag(ssd):  # noqa: F811
     ssd.ssd_forward(x, d.normal(1, 64, 4).abs(), -d.normal(4).abs(), wide, bc, None, None, 64)
     ssd.ssd_conv_step(d.normal(2, 8), d.normal(8, 4), None, d.normal(3, 3, 8), torch.tensor([3, 0], dtype=torch.int32, device="cuda"))
     assert [ssd.ssd_get_device_error() for _ in range(3)] == [7, 8, 0]
+
+
+def test_strides_that_a_call_does_not_read(ssd):  # noqa: F811
+    """A step's strides per token, and z's without a z, may hold anything."""
+    import ctypes
+    from state_space_sequence_ssd_gb300 import _ffi
+    d, b, L, ch, N = Draw(31), 3, 5, 24, 16
+    x, dt, B, C = d.normal(b, L, ch), d.normal(b, L, ch).abs(), d.normal(b, L, 1, N), d.normal(b, L, 1, N)
+    A, state = -d.normal(ch, N).abs(), d.normal(b, ch, N)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    lib, stream = _ffi.lib(), torch.cuda.current_stream().cuda_stream
+    want = ssd.ssd_selective_step(x[:, 0], dt[:, 0], A, B[:, 0], C[:, 0], None, state.clone())
+    junk = _ffi.SelectiveStrides(L * ch, -1, L * ch, -3, -5, 7, L * N, 1, L * N, -2 ** 40)
+    y = torch.empty(b, ch, device="cuda")
+    assert lib.ssd_selective_step(_ffi.SSD_F32, p(x), p(dt), p(A), p(B), p(C), None, p(state), None, b, ctypes.addressof(junk), b,
+                                  ch, 1, N, None, p(y), stream) == 0
+    assert torch.equal(y, want)
+    want, _ = ssd.ssd_selective_forward(x, dt, A, B, C)
+    st = _ffi.SelectiveStrides(L * ch, ch, L * ch, ch, -1, -1, L * N, N, L * N, N)
+    y = torch.empty(b, L, ch, device="cuda")
+    assert lib.ssd_selective_forward(_ffi.SSD_F32, p(x), p(dt), p(A), p(B), p(C), None, None, None, ctypes.addressof(st), b, L, ch, 1,
+                                     N, None, p(y), None, stream) == 0
+    assert torch.equal(y, want)
