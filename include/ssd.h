@@ -621,7 +621,8 @@ SSD_API int ssd_debug_stall(int kinds);
  * it needs.  ssd_profile_read() waits for those
  * events and returns, per kernel kind (see ssd_kernel_name), the summed
  * device time in milliseconds and the launch count since the last reset;
- * *n_kinds is the number of kinds written, at most max_kinds.
+ * *n_kinds is the number of kinds written, at most max_kinds; with max_kinds 0
+ * nothing is written and it is the number of kinds there are.
  * ssd_launch_count() counts every kernel the library has launched since load
  * (profiling enabled or not).
  */

@@ -822,7 +822,7 @@ int ssd_profile_read(float* total_ms, int* launches, int max_kinds, int* n_kinds
         if (total_ms) total_ms[k] = (float)g_prof_ms[k];
         if (launches) launches[k] = g_prof_count[k];
     }
-    if (n_kinds) *n_kinds = n > 0 ? n : 0;
+    if (n_kinds) *n_kinds = n > 0 ? n : kAllKinds;
     return status;
 }
 
