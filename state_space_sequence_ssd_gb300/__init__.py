@@ -20,26 +20,17 @@ strided rows and other element types.
 from __future__ import annotations
 
 from . import _ffi
+from .layer import (ssd_conv_backward, ssd_conv_forward, ssd_conv_step, ssd_layer_norm_backward, ssd_layer_norm_forward,
+                    ssd_selective_backward, ssd_selective_forward, ssd_selective_step)
 
 __all__ = ["ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan", "ssd_forward",
            "ssd_forward_noalloc", "ssd_forward_heads", "ssd_partition_heads", "ssd_forward_plan", "ssd_step",
            "ssd_step_multi", "ssd_forward_ex", "ssd_step_ex", "ssd_backward", "ssd_get_device_error", "SSDError", "library_path",
            "ssd_conv_forward", "ssd_conv_backward", "ssd_conv_step", "ssd_selective_forward", "ssd_selective_backward",
            "ssd_selective_step", "ssd_layer_norm_forward", "ssd_layer_norm_backward"]
-_LAYER = frozenset(n for n in __all__ if n.startswith(("ssd_conv_", "ssd_selective_", "ssd_layer_norm_")))
 
 SSDError = _ffi.SSDError
 library_path = _ffi.LIB_PATH
-
-
-def __getattr__(name):
-    """The layer operators, looked up when they are first used (their module imports torch)."""
-    if name in _LAYER:
-        from . import layer
-        for n in _LAYER:
-            globals()[n] = getattr(layer, n)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

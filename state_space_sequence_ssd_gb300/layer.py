@@ -16,31 +16,37 @@ from __future__ import annotations
 import importlib.util
 import os
 
-import torch
-
 from . import _ffi
 
 _BINDING = os.path.join(os.path.dirname(_ffi.LIB_PATH), "ssd_layer_binding.so")
 
 
-def _load():
-    if not os.path.exists(_BINDING):
-        raise RuntimeError(f"the layer operators' binding was not found at {_BINDING}; build it with "
-                           "`python -m state_space_sequence_ssd_gb300.build` (no fallback exists)")
-    _ffi.lib()
-    spec = importlib.util.spec_from_file_location("ssd_layer_binding", _BINDING)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.set_fail(_ffi.check)
-    return module
+class _Native:
+    """The functions of the binding, which is loaded when one is first asked for (it needs torch and the library)."""
+
+    def __getattr__(self, name):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        if not os.path.exists(_BINDING):
+            raise RuntimeError(f"the layer operators' binding was not found at {_BINDING}; build it with "
+                               "`python -m state_space_sequence_ssd_gb300.build` (no fallback exists)")
+        import torch  # noqa: F401  (its libraries are the binding's)
+        _ffi.lib()
+        spec = importlib.util.spec_from_file_location("ssd_layer_binding", _BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_fail(_ffi.check)
+        self.__dict__.update(vars(module))
+        return getattr(module, name)
 
 
-_native = _load()
+_native = _Native()
 
 
 def _on(stream, call, args, inputs):
     """Runs `call` with `stream` as the current one, so that its outputs belong to it, and tells the allocator that
     it uses the inputs."""
+    import torch
     with torch.cuda.stream(stream):
         out = call(*args)
     for t in inputs:
@@ -71,6 +77,7 @@ def ssd_conv_backward(x, weight, bias, dy, init_state=None, lengths=None, silu=T
     final state.  ``dx`` may be given: a tensor like x whose last dimension is dense (a slice of a projection's
     gradient)."""
     if stream is not None:
+        import torch
         dy = [dy] if isinstance(dy, torch.Tensor) else list(dy)  # an iterator's pieces are taken once
         return _on(stream, _native.conv_backward, (x, weight, bias, dy, init_state, lengths, silu, dfinal, dx, want_dinit),
                    (x, weight, bias, *dy, init_state, lengths, dfinal, dx))
