@@ -4,7 +4,9 @@ Each csrc/*.cu is compiled to an object in parallel with
 ``nvcc -gencode arch=compute_103a,code=sm_103a`` and linked (static cudart)
 into one shared library with a plain C ABI (include/ssd.h).  Beside it,
 csrc/layer_binding.cpp becomes ssd_layer_binding.so, the Python module that
-marshals the layer operators' calls (host code against torch's headers).
+marshals the layer operators' calls (host code against torch's headers).  The
+library needs no torch: it is built all the same where there is none, and before
+an error of the binding is raised.
 
     python -m state_space_sequence_ssd_gb300.build [--force] [--verbose-ptxas]
 """
@@ -13,10 +15,12 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -50,6 +54,23 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def _torch_dir() -> str | None:
+    """The folder of the torch that would be imported (without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None or spec.origin is None else os.path.dirname(spec.origin)
+
+
+def _binding_lacks() -> str | None:
+    """What is missing here to build the binding, if anything."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return "torch"
+    for header in (os.path.join(torch_dir, "include", "ATen", "ATen.h"), os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return header
+    return None if shutil.which("g++") else "g++"
+
+
 def _binding_stale() -> bool:
     if not os.path.exists(BINDING):
         return True
@@ -59,7 +80,7 @@ def _binding_stale() -> bool:
 
 def _compile_binding() -> str:
     import torch
-    torch_dir = os.path.dirname(torch.__file__)
+    torch_dir = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     includes = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
                 os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")]
@@ -73,9 +94,8 @@ def _compile_binding() -> str:
 
 
 def _link_binding(obj: str) -> None:
-    import torch
     tmp = BINDING + f".tmp{os.getpid()}"
-    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    libs = os.path.join(_torch_dir(), "lib")
     r = subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-l:libssd_gb300.so", "-Wl,-rpath,$ORIGIN", f"-L{libs}",
                         "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
     if r.returncode != 0:
@@ -84,8 +104,11 @@ def _link_binding(obj: str) -> None:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    stale, binding_stale = force or verbose_ptxas or _stale(), force or _binding_stale()
+    stale, lacks = force or verbose_ptxas or _stale(), _binding_lacks()
+    binding_stale = lacks is None and (force or _binding_stale())
     os.makedirs(BUILD, exist_ok=True)
+    if lacks is not None and not os.path.exists(BINDING):
+        warnings.warn(f"the layer operators' Python binding is not built: {lacks} is missing here")
     if not stale:
         if binding_stale:
             _link_binding(_compile_binding())
@@ -105,9 +128,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
 
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(os.cpu_count() or 8, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)  # host code, beside the kernels
+        binding = ex.submit(_compile_binding) if lacks is None else None  # host code, beside the kernels
         results = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
     if verbose_ptxas:
         for _, log in results:
             if log.strip():
@@ -118,7 +140,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if binding is not None:
+        _link_binding(binding.result())
     return LIB
 
 
