@@ -71,9 +71,19 @@ def _binding_lacks() -> str | None:
     return None if shutil.which("g++") else "g++"
 
 
+def _made_for() -> str:
+    """The torch and the Python that a binding belongs to."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{f.read()}"
+
+
 def _binding_stale() -> bool:
-    if not os.path.exists(BINDING):
+    stamp = BINDING + ".made_for"
+    if not os.path.exists(BINDING) or not os.path.exists(stamp):
         return True
+    with open(stamp) as f:
+        if f.read() != _made_for():
+            return True
     t = os.path.getmtime(BINDING)
     return any(os.path.getmtime(p) > t for p in (BINDING_SRC, os.path.join(ROOT, "include", "ssd.h")))
 
@@ -101,6 +111,8 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING + ".made_for", "w") as f:
+        f.write(_made_for())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:

@@ -1,4 +1,4 @@
-"""What build() does where torch or its headers are not what they were; no compiler is run (no GPU needed)."""
+"""What build() does where torch, its headers or its version are not what they were; no compiler is run (no GPU needed)."""
 import os
 import subprocess
 import sys
@@ -52,3 +52,18 @@ def test_the_library_is_there_when_the_binding_does_not_compile(made):
     with pytest.raises(RuntimeError, match="no such header"):
         B.build()
     assert os.path.exists(B.LIB) and not os.path.exists(B.BINDING)
+
+
+def test_another_torch_makes_the_binding_stale(made, monkeypatch, tmp_path):
+    B.build()
+    import torch
+    other = tmp_path / "torch"
+    os.makedirs(other / "include" / "ATen")
+    (other / "include" / "ATen" / "ATen.h").write_text("")
+    (other / "version.py").write_text("__version__ = '0.0.1'\n")
+    (other / "__init__.py").write_text("")
+    n = len(made)
+    monkeypatch.setattr(torch, "__file__", str(other / "__init__.py"))
+    monkeypatch.setattr(torch.__spec__, "origin", str(other / "__init__.py"))
+    B.build()
+    assert made[n:] == ["layer_binding.o", "ssd_layer_binding.so"]
