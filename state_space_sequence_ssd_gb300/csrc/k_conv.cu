@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStep = 8;  // tokens of the forward kernel whose loads are in flight together
+constexpr int kManyBlocks = 304;  // two an SM: from there on a warp walks a long run of tokens
 
 // The taps and biases of V channels as pairs.  Tap 3 is the current token's: a narrower kernel's taps end there and its
 // first ones are unused (never multiplied: zero times an infinite input would be NaN).
@@ -439,12 +440,15 @@ template <typename T, int V, int W>
 void run_forward(const ConvArgs& a, const Pieces& y, void* final_state, cudaStream_t s) {
     const int tiles = ceil_div(a.channels, 32 * V);
     T* f = static_cast<T*>(final_state);
-    // long runs read the taps and the halo of W-1 tokens rarely; short ones fill the SMs on short prompts
+    // Long runs read the taps and the halo of W-1 tokens rarely; short ones fill the SMs on short prompts, and there only: the
+    // grid of short runs holds kManyBlocks blocks of long ones at most.  (test_layer_sizes_gpu.py has the long runs.)
+    constexpr int LONG = 32, SHORT = 4;
+    static_assert(kManyBlocks * (LONG / SHORT) <= kMaxGrid, "short runs fit the grid");
     auto blocks = [&](int run) { return dim3(tiles, ceil_div(a.seqlen, kWarps * run), a.batch); };
-    if ((int64_t)tiles * a.batch * ceil_div(a.seqlen, kWarps * 32) >= 304)
-        conv_forward_kernel<T, V, W, 32><<<blocks(32), 32 * kWarps, 0, s>>>(a, y, f);
+    if ((int64_t)tiles * a.batch * ceil_div(a.seqlen, kWarps * LONG) >= kManyBlocks)
+        conv_forward_kernel<T, V, W, LONG><<<blocks(LONG), 32 * kWarps, 0, s>>>(a, y, f);
     else
-        conv_forward_kernel<T, V, W, 4><<<blocks(4), 32 * kWarps, 0, s>>>(a, y, f);
+        conv_forward_kernel<T, V, W, SHORT><<<blocks(SHORT), 32 * kWarps, 0, s>>>(a, y, f);
 }
 
 template <typename T, int W>
@@ -456,10 +460,12 @@ int forward_of(const ConvArgs& a, const Pieces& y, void* final_state, cudaStream
 }
 
 // Tokens that a warp of the backward kernel walks: long runs read the taps and the halo rarely and leave few rows of sums
-// (at 2 x 4096 x 4352, runs of 16, 32 and 64 tokens: 110, 83 and 71 us), short ones fill the SMs where tokens are few.
+// (at 2 x 4096 x 4352, an earlier form with runs of 16, 32 and 64 tokens: 110, 83 and 71 us), short ones fill the SMs where
+// tokens are few.  (test_layer_sizes_gpu.py has the long runs.)
 constexpr int kLongRun = 64, kShortRun = 16;
+static_assert(kManyBlocks * (kLongRun / kShortRun) <= kMaxGrid, "short runs fit the grid");
 int backward_run(const ConvArgs& a) {
-    return (int64_t)a.batch * ceil_div(a.channels, 64) * ceil_div(a.seqlen, kWarps * kLongRun) >= 304 ? kLongRun : kShortRun;
+    return (int64_t)a.batch * ceil_div(a.channels, 64) * ceil_div(a.seqlen, kWarps * kLongRun) >= kManyBlocks ? kLongRun : kShortRun;
 }
 
 template <typename T, int W>
@@ -493,7 +499,7 @@ int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* d
 template <typename T, int V, int W>
 void run_step(const ConvArgs& a, T* state, const int* slots, int nslots, const Pieces& y, int* err, cudaStream_t s) {
     const int tiles = ceil_div(a.channels, 128 * V);
-    // four rows a thread where the batch fills the SMs all the same
+    // four rows a thread where the batch fills the SMs all the same (test_layer_sizes_gpu.py has them)
     if (a.batch / 4 * tiles >= 152)
         conv_step_kernel<T, V, W, 4><<<dim3(tiles, ceil_div(a.batch, 4)), 128, 0, s>>>(a, state, slots, nslots, y, err, true);
     else

@@ -130,12 +130,15 @@ int selective_block_threads(const SelectiveArgs& a) {
 // Blocks of 32 tokens, or of 16 where those of 32 would leave an SM quarter without a warp: half a block's time for twice
 // the hops, sums and checkpoints.  With 32 and with 16 tokens at 16 entries of bfloat16: 34 and 21 us at 2 x 128 x 512, 35
 // and 28 at 512 x 1024, 47 and 50 at 4 x 64 x 4096, 139 and 150 at 2 x 1024 x 2048.  Rows that fit 32 tokens need no hop.
+// (test_layer_sizes_gpu.py has the blocks of 32 for every number of lanes.)
+constexpr int kFewWarps = 152 * 4;
+static_assert(kFewWarps * 2 <= kMaxGrid, "blocks of 16 tokens fit the grid");
 SelectiveParts selective_parts(const SelectiveArgs& a) {
     SelectiveParts p;
     const int threads = selective_block_threads(a), lp = selective_lanes(a.dstate);
     p.tiles = ceil_div(a.channels / a.ngroups, 4 * threads / lp);
     const int64_t warps = (int64_t)a.batch * a.ngroups * p.tiles * ceil_div(a.seqlen, 32) * (threads / 32);
-    p.tokens = lp <= 16 && warps <= 152 * 4 && (a.seqlen <= 16 || a.seqlen > 32) ? 16 : 32;
+    p.tokens = lp <= 16 && warps <= kFewWarps && (a.seqlen <= 16 || a.seqlen > 32) ? 16 : 32;
     p.nblocks = ceil_div(a.seqlen, p.tokens);
     const size_t n = (size_t)a.channels * a.dstate, rows = (size_t)a.batch * p.nblocks;
     auto whole = [](size_t floats) { return (floats + 3) & ~(size_t)3; };  // every part starts on 16 bytes

@@ -235,6 +235,9 @@ __device__ __forceinline__ int row_slot(const int* slots, int b, int nslots, int
 
 // ------------------------------------------------------------------ launchers (arguments are checked by ops_api.cu)
 
+// Blocks of a grid in y and in z.
+constexpr int kMaxGrid = 65535;
+
 // Kernel kinds of the layer operators, after those of the scan.
 enum LayerKind {
     kKindConv = kNumKinds,

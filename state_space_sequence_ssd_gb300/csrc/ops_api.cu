@@ -13,8 +13,9 @@ bool on(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p)
 uintptr_t size_of(int dtype) { return dtype == SSD_F32 ? 4 : 2; }
 bool known(int dtype) { return dtype == SSD_BF16 || dtype == SSD_F16 || dtype == SSD_F32; }
 
-// Limits of the grids (one block per at least 32 tokens in y, one per row in z) and of 32-bit channel counts.
-constexpr int kMaxBatch = 65535, kMaxTokens = 65535 * 32, kMaxChannels = 1 << 20;
+// Limits of the grids (one row of blocks in z per row; blocks of at least 32 tokens in y, or of 16 on rows that a rule holds
+// short: kMaxGrid in ops.cuh, asserted beside the rules) and of 32-bit channel counts.
+constexpr int kMaxBatch = kMaxGrid, kMaxTokens = kMaxGrid * 32, kMaxChannels = 1 << 20;
 
 // Whether `batch` rows of `tokens` tokens of `channels` elements at these strides do not overlap.
 bool apart(int64_t batch_stride, int64_t token_stride, int64_t batch, int64_t tokens, int64_t channels) {
