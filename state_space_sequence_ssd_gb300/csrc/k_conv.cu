@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStep = 8;  // tokens of the forward kernel whose loads are in flight together
-constexpr int kManyBlocks = 304;  // two an SM: from there on a warp walks a long run of tokens
+constexpr int kManyBlocks = 2 * kSms;  // two an SM: from there on a warp walks a long run of tokens
 
 // The taps and biases of V channels as pairs.  Tap 3 is the current token's: a narrower kernel's taps end there and its
 // first ones are unused (never multiplied: zero times an infinite input would be NaN).
@@ -72,13 +72,13 @@ __device__ __forceinline__ T* piece_at(const Pieces& y, int64_t row, int c) {
 
 // x at token t of row b (t < 0: the initial state's rows; past the length: zero)
 template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> input_at(const ConvArgs& a, int b, int t, int len, int c, int valid, bool vec) {
+__device__ __forceinline__ Vec<T, V> input_at(const ConvArgs& a, int b, int t, int len, int c, int valid) {
     const Vec<T, V> z = Vec<T, V>::zero();
     if (t >= len) return z;
-    if (t >= 0) return load_vec<T, V>(static_cast<const T*>(a.x) + b * a.x_batch + t * a.x_token + c, valid, vec);
+    if (t >= 0) return load_vec<T, V>(static_cast<const T*>(a.x) + b * a.x_batch + t * a.x_token + c, valid, true);
     if (a.init == nullptr || t < -(a.width - 1)) return z;
     return load_vec<T, V>(static_cast<const T*>(a.init) + ((int64_t)b * (a.width - 1) + t + a.width - 1) * a.channels + c,
-                          valid, vec);
+                          valid, true);
 }
 
 // A warp: 32 V channels of RUN consecutive tokens, STEP of them loaded at a time, one step ahead of their use.  Runs whose
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) conv_forward_kernel(ConvArgs a
     if (valid <= 0) return;
     const int len = row_length(a.lengths, b, a.seqlen);
     if (final_state != nullptr && blockIdx.y == 0 && warp < W - 1) {
-        const Vec<T, V> v = input_at<T, V>(a, b, len - (W - 1) + warp, len, c, valid, true);
+        const Vec<T, V> v = input_at<T, V>(a, b, len - (W - 1) + warp, len, c, valid);
         store_vec<T, V>(final_state + ((int64_t)b * (W - 1) + warp) * a.channels + c, v, valid, true);
     }
     const int t0 = (blockIdx.y * kWarps + warp) * RUN;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) conv_forward_kernel(ConvArgs a
         f32x2 x[STEP + 3][P];  // the inputs of this step's tokens, after the three before them
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, true) : Vec<T, V>::zero();
+            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid) : Vec<T, V>::zero();
 #pragma unroll
             for (int i = 0; i < P; ++i) x[k][i] = v.pair(i);
         }
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(32 * kWarps, V == 2 ? 5 : 4) conv_backward_ker
         f32x2 x[S + 3][P], g[S + 3][P];  // inputs and dLoss/dpre of this group's tokens, after the three before them
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid, true) : Vec<T, V>::zero();
+            const Vec<T, V> v = k >= 4 - W ? input_at<T, V>(a, b, t0 - 3 + k, len, c, valid) : Vec<T, V>::zero();
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 x[k][j] = v.pair(j);
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* partial, 
 // slot's W-1 inputs are written back moved on by one.  An idle row (slot -1) writes zeros and leaves every slot alone.
 template <typename T, int V, int W, int R>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, T* __restrict__ state, const int* __restrict__ slots,
-                                                        int nslots, Pieces y, int* err, bool vec) {
+                                                        int nslots, Pieces y, int* err) {
     constexpr int P = (V + 1) / 2;
     const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V, b0 = blockIdx.y * R;
     const int valid = min(V, a.channels - c);
@@ -392,9 +392,9 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, T* __restric
     for (int r = 0; r < R; ++r) {
         const int got = slot[r] >= 0 ? valid : 0;
         const T* st = state + (int64_t)slot[r] * (W - 1) * a.channels + c;
-        in[r][3] = load_vec<T, V>(static_cast<const T*>(a.x) + (b0 + r) * a.x_batch + c, got, vec);
+        in[r][3] = load_vec<T, V>(static_cast<const T*>(a.x) + (b0 + r) * a.x_batch + c, got, true);
 #pragma unroll
-        for (int k = 4 - W; k < 3; ++k) in[r][k] = load_vec<T, V, true>(st + (int64_t)(k - (4 - W)) * a.channels, got, vec);
+        for (int k = 4 - W; k < 3; ++k) in[r][k] = load_vec<T, V, true>(st + (int64_t)(k - (4 - W)) * a.channels, got, true);
     }
     f32x2 w[4][P], bias[P];
     load_taps<V>(a.weight, a.bias, W, c, valid, w, bias);
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, T* __restric
         if (slot[r] >= 0) {
             T* st = state + (int64_t)slot[r] * (W - 1) * a.channels + c;
 #pragma unroll
-            for (int k = 4 - W; k < 3; ++k) store_vec<T, V>(st + (int64_t)(k - (4 - W)) * a.channels, in[r][k + 1], valid, vec);
+            for (int k = 4 - W; k < 3; ++k) store_vec<T, V>(st + (int64_t)(k - (4 - W)) * a.channels, in[r][k + 1], valid, true);
             f32x2 x[4][P], pre[P];
 #pragma unroll
             for (int k = 4 - W; k < 4; ++k)
@@ -418,21 +418,19 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, T* __restric
             }
             out = Vec<T, V>::of_pairs(pre);
         }
-        store_vec<T, V>(piece_at<T>(y, b0 + r, c), out, valid, vec);
+        store_vec<T, V>(piece_at<T>(y, b0 + r, c), out, valid, true);
     }
 }
-
-bool on(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // Whether vectors of V elements of `size` bytes fit every row of the call: rows, strides and pieces are whole
 // vectors from aligned bases.
 bool whole_vectors(const ConvArgs& a, const Pieces& y, const void* s1, const void* s2, int V, int size) {
     const int bytes = V * size;
-    if (a.channels % V || a.x_batch % V || a.x_token % V || !on(a.x, bytes) || !on(a.init, bytes) || !on(s1, bytes) ||
-        !on(s2, bytes))
+    if (a.channels % V || a.x_batch % V || a.x_token % V || !aligned_to(a.x, bytes) || !aligned_to(a.init, bytes) || !aligned_to(s1, bytes) ||
+        !aligned_to(s2, bytes))
         return false;
     for (int i = 0; i < 3; ++i)
-        if (y.n[i] % V || !on(y.p[i], y.f32[i] ? 4 * V : bytes)) return false;
+        if (y.n[i] % V || !aligned_to(y.p[i], y.f32[i] ? 4 * V : bytes)) return false;
     return true;
 }
 
@@ -475,7 +473,7 @@ int backward_of(const ConvArgs& a, const Pieces& dy, const void* dfinal, void* d
     T *o = static_cast<T*>(dx), *di = static_cast<T*>(dinit);
     const int run = backward_run(a), rows = ceil_div(a.seqlen, kWarps * run);
     const bool pairs = whole_vectors(a, dy, dfinal, dinit, 2, sizeof(T)) && dx_batch % 2 == 0 && dx_token % 2 == 0 &&
-                       on(dx, 2 * sizeof(T));
+                       aligned_to(dx, 2 * sizeof(T));
     launch_begin(kKindConvBwd, s);
     auto go = [&](auto kernel, int channels) {
         kernel<<<dim3(ceil_div(a.channels, channels), rows, a.batch), 32 * kWarps, 0, s>>>(a, dy, df, o, dx_batch, dx_token, di,
@@ -500,10 +498,10 @@ template <typename T, int V, int W>
 void run_step(const ConvArgs& a, T* state, const int* slots, int nslots, const Pieces& y, int* err, cudaStream_t s) {
     const int tiles = ceil_div(a.channels, 128 * V);
     // four rows a thread where the batch fills the SMs all the same (test_layer_sizes_gpu.py has them)
-    if (a.batch / 4 * tiles >= 152)
-        conv_step_kernel<T, V, W, 4><<<dim3(tiles, ceil_div(a.batch, 4)), 128, 0, s>>>(a, state, slots, nslots, y, err, true);
+    if (a.batch / 4 * tiles >= kSms)
+        conv_step_kernel<T, V, W, 4><<<dim3(tiles, ceil_div(a.batch, 4)), 128, 0, s>>>(a, state, slots, nslots, y, err);
     else
-        conv_step_kernel<T, V, W, 1><<<dim3(tiles, a.batch), 128, 0, s>>>(a, state, slots, nslots, y, err, true);
+        conv_step_kernel<T, V, W, 1><<<dim3(tiles, a.batch), 128, 0, s>>>(a, state, slots, nslots, y, err);
 }
 
 template <typename T, int W>

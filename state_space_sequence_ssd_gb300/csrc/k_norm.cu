@@ -438,14 +438,12 @@ __global__ void __launch_bounds__(32 * kJoin) norm_reduce_kernel(const float* pa
     }
 }
 
-bool on(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-
 // Threads that share a row of `vecs` vectors, a power of two: enough that a thread holds at most `most` vectors, more
 // (down to one each) while the rows alone leave the SMs with less than about 1024 threads.
 int row_lanes(int64_t rows, int vecs, int most, int least) {
     int lanes = least;
     while (lanes < kThreads && (int64_t)lanes * most < vecs) lanes *= 2;
-    while (lanes < kThreads && lanes < vecs && rows * lanes < 152 * 1024) lanes *= 2;
+    while (lanes < kThreads && lanes < vecs && rows * lanes < kSms * 1024) lanes *= 2;
     return lanes;
 }
 
@@ -457,7 +455,7 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
     const int lanes = row_lanes(rows, vecs, 2 * M, 1);
     const int nv = ceil_div(vecs, lanes);
     const int64_t blocks = ceil_div64(rows, kThreads / lanes);
-    const bool vecw = on(weight, 16) && on(bias, 16);
+    const bool vecw = aligned_to(weight, 16) && aligned_to(bias, 16);
     const T* xt = static_cast<const T*>(x);
     T* yt = static_cast<T*>(y);
     if (blocks > 2147483647) return SSD_ERR_UNSUPPORTED;
@@ -469,12 +467,12 @@ int forward_of(const void* x, int64_t x_row, const float* weight, const float* b
         // A resident grid pays from about 24 thousand values an SM: with one row a thread's group and with the walk 4.4 and
         // 4.8 us at 1216 x 2048 of bfloat16, 7.2 and 5.8 at 1824 x 2048, 5.1 and 6.2 at 304 x 8192, 9.0 and 7.0 at
         // 608 x 8192, 5.6 and 6.4 at 1216 x 2048 of float32, 9.1 and 8.8 at 2432 x 2048.
-        if (rows * width >= 152 * 24576 && nv <= 4) {
+        if (rows * width >= kSms * 24576 && nv <= 4) {
             int r = SSD_OK;
             auto walk = [&](auto kernel, int held) {
                 const int smem = kAhead * 2 * held * kThreads * 16;
                 r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
-                const int64_t pairs = ceil_div64(rows, kThreads / lanes * 2), most = 152 * resident(held);
+                const int64_t pairs = ceil_div64(rows, kThreads / lanes * 2), most = kSms * resident(held);
                 if (r == SSD_OK)
                     kernel<<<(unsigned)(pairs < most ? pairs : most), kThreads, smem, s>>>(xt, x_row, weight, bias, eps, rows, width, lanes, yt, mean, rstd, vecw);
             };
@@ -502,7 +500,7 @@ int backward_of(const void* x, int64_t x_row, const float* weight, const float* 
     const int smem = lanes == kThreads || partial == nullptr ? 0 : kThreads / lanes * 2 * width * 4;
     const T *xt = static_cast<const T*>(x), *gt = static_cast<const T*>(dy);
     T* o = static_cast<T*>(dx);
-    const bool vecw = on(weight, 16);
+    const bool vecw = aligned_to(weight, 16);
     launch_begin(kKindNormBwd, s);
     auto go = [&](auto kernel) {
         kernel<<<parts, kThreads, smem, s>>>(xt, x_row, weight, mean, rstd, gt, dy_row, rows, width, lanes, o, partial, vecw);
@@ -520,7 +518,7 @@ template <typename T>
 int forward_type(const void* x, int64_t x_row, const float* weight, const float* bias, float eps, int64_t rows, int width,
                  void* y, float* mean, float* rstd, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    if (width % V == 0 && x_row % V == 0 && on(x, 16) && on(y, 16))
+    if (width % V == 0 && x_row % V == 0 && aligned_to(x, 16) && aligned_to(y, 16))
         return forward_of<T, V>(x, x_row, weight, bias, eps, rows, width, y, mean, rstd, s);
     return forward_of<T, 1>(x, x_row, weight, bias, eps, rows, width, y, mean, rstd, s);
 }
@@ -529,7 +527,7 @@ template <typename T>
 int backward_type(const void* x, int64_t x_row, const float* weight, const float* mean, const float* rstd, const void* dy,
                   int64_t dy_row, int64_t rows, int width, void* dx, float* partial, int parts, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    if (width % V == 0 && x_row % V == 0 && dy_row % V == 0 && on(x, 16) && on(dy, 16) && on(dx, 16))
+    if (width % V == 0 && x_row % V == 0 && dy_row % V == 0 && aligned_to(x, 16) && aligned_to(dy, 16) && aligned_to(dx, 16))
         return backward_of<T, V>(x, x_row, weight, mean, rstd, dy, dy_row, rows, width, dx, partial, parts, s);
     return backward_of<T, 1>(x, x_row, weight, mean, rstd, dy, dy_row, rows, width, dx, partial, parts, s);
 }

@@ -152,7 +152,7 @@ int step_lanes(const SelectiveArgs& a, float* state, const int* slots, int nslot
         kernel<<<dim3(tiles, ceil_div(a.batch, rows)), 256, 0, s>>>(a, state, slots, nslots, y, err, vecs, vecb);
     };
     // several rows a thread where the batch fills the SMs all the same (test_layer_sizes_gpu.py has them)
-    const bool many = a.batch / R * tiles >= 152 * 4;
+    const bool many = a.batch / R * tiles >= kSms * 4;
     if (vecs && vecb) many ? go(selective_step_kernel<T, LP, R, true>, R) : go(selective_step_kernel<T, LP, 1, true>, 1);
     else many ? go(selective_step_kernel<T, LP, R, false>, R) : go(selective_step_kernel<T, LP, 1, false>, 1);
     return launch_end(kKindSelectiveStep, s);

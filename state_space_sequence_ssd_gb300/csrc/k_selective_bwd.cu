@@ -131,7 +131,7 @@ int selective_block_threads(const SelectiveArgs& a) {
 // the hops, sums and checkpoints.  With 32 and with 16 tokens at 16 entries of bfloat16: 34 and 21 us at 2 x 128 x 512, 35
 // and 28 at 512 x 1024, 47 and 50 at 4 x 64 x 4096, 139 and 150 at 2 x 1024 x 2048.  Rows that fit 32 tokens need no hop.
 // (test_layer_sizes_gpu.py has the blocks of 32 for every number of lanes.)
-constexpr int kFewWarps = 152 * 4;
+constexpr int kFewWarps = kSms * 4;
 static_assert(kFewWarps * 2 <= kMaxGrid, "blocks of 16 tokens fit the grid");
 SelectiveParts selective_parts(const SelectiveArgs& a) {
     SelectiveParts p;

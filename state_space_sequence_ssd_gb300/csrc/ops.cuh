@@ -235,8 +235,10 @@ __device__ __forceinline__ int row_slot(const int* slots, int b, int nslots, int
 
 // ------------------------------------------------------------------ launchers (arguments are checked by ops_api.cu)
 
-// Blocks of a grid in y and in z.
-constexpr int kMaxGrid = 65535;
+// Blocks of a grid in y and in z; SMs that the launch rules mean to fill.
+constexpr int kMaxGrid = 65535, kSms = 152;
+
+inline bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // Kernel kinds of the layer operators, after those of the scan.
 enum LayerKind {

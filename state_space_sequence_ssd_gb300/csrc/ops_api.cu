@@ -9,7 +9,6 @@ using namespace ssd;
 
 namespace {
 
-bool on(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 uintptr_t size_of(int dtype) { return dtype == SSD_F32 ? 4 : 2; }
 bool known(int dtype) { return dtype == SSD_BF16 || dtype == SSD_F16 || dtype == SSD_F32; }
 
@@ -29,7 +28,7 @@ int read_pieces(void* const (&p)[3], const int (&n)[3], const int (&f32)[3], int
     int64_t sum = 0;
     for (int i = 0; i < 3; ++i) {
         if (n[i] < 0 || (n[i] > 0 && p[i] == nullptr)) return SSD_ERR_INVALID_ARG;
-        if (n[i] > 0 && !on(p[i], f32[i] ? 4 : size)) return SSD_ERR_INVALID_ARG;
+        if (n[i] > 0 && !aligned_to(p[i], f32[i] ? 4 : size)) return SSD_ERR_INVALID_ARG;
         if (i > 0 && n[i] > 0 && n[i - 1] == 0) return SSD_ERR_INVALID_ARG;
         sum += n[i];
         out->p[i] = n[i] > 0 ? p[i] : nullptr;
@@ -47,7 +46,8 @@ int read_conv(int dtype, const void* x, int64_t x_batch, int64_t x_token, const 
     if (width < 2 || width > 4 || batch > kMaxBatch || seqlen > kMaxTokens || channels > kMaxChannels)
         return SSD_ERR_UNSUPPORTED;
     const uintptr_t size = size_of(dtype);
-    if (!on(x, size) || !on(weight, 4) || !on(bias, 4) || !on(init, size) || !on(lengths, 4)) return SSD_ERR_INVALID_ARG;
+    if (!aligned_to(x, size) || !aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(init, size) ||
+        !aligned_to(lengths, 4)) return SSD_ERR_INVALID_ARG;
     *a = ConvArgs{dtype, batch, seqlen, channels, width, silu != 0, x, x_batch, x_token, weight, bias, init, lengths};
     return SSD_OK;
 }
@@ -61,12 +61,13 @@ int read_selective(int dtype, const void* x, const void* dt, const float* A, con
     if (dstate > 128 || batch > kMaxBatch || seqlen > kMaxTokens || channels > kMaxChannels) return SSD_ERR_UNSUPPORTED;
     const uintptr_t size = size_of(dtype);
     const void* z = o != nullptr ? o->z : nullptr;
-    if (!on(x, size) || !on(dt, size) || !on(B, size) || !on(C, size) || !on(z, size) || !on(A, 4) || !on(D, 4) ||
-        !on(init, 4) || !on(lengths, 4))
+    if (!aligned_to(x, size) || !aligned_to(dt, size) || !aligned_to(B, size) || !aligned_to(C, size) ||
+        !aligned_to(z, size) || !aligned_to(A, 4) || !aligned_to(D, 4) ||
+        !aligned_to(init, 4) || !aligned_to(lengths, 4))
         return SSD_ERR_INVALID_ARG;
     DtOpts dto;
     if (o != nullptr) {
-        if (!on(o->dt_bias, 4)) return SSD_ERR_INVALID_ARG;
+        if (!aligned_to(o->dt_bias, 4)) return SSD_ERR_INVALID_ARG;
         if (o->dt_limit && !(o->dt_min <= o->dt_max)) return SSD_ERR_INVALID_ARG;  // also rejects a NaN bound
         dto.bias = o->dt_bias;
         dto.softplus = o->dt_softplus != 0;
@@ -110,7 +111,7 @@ int ssd_conv_forward(int dtype, const void* x, long long x_batch_stride, long lo
     Pieces y;
     r = read_pieces({y0, y1, y2}, {n0, n1, n2}, {0, 0, 0}, channels, size_of(dtype), &y);
     if (r != SSD_OK) return r;
-    if (!on(final_state, size_of(dtype))) return SSD_ERR_INVALID_ARG;
+    if (!aligned_to(final_state, size_of(dtype))) return SSD_ERR_INVALID_ARG;
     return launch_conv_forward(a, y, final_state, stream);
 }
 
@@ -128,7 +129,8 @@ int ssd_conv_backward(int dtype, const void* x, long long x_batch_stride, long l
                     {f32_0, f32_1, f32_2}, channels, size_of(dtype), &dy);
     if (r != SSD_OK) return r;
     const uintptr_t size = size_of(dtype);
-    if (!dx || !on(dx, size) || !on(dfinal, size) || !on(dinit, size) || !on(dweight, 4) || !on(dbias, 4) ||
+    if (!dx || !aligned_to(dx, size) || !aligned_to(dfinal, size) || !aligned_to(dinit, size) ||
+        !aligned_to(dweight, 4) || !aligned_to(dbias, 4) ||
         !apart(dx_batch_stride, dx_token_stride, batch, seqlen, channels))
         return SSD_ERR_INVALID_ARG;
     void* ws = nullptr;
@@ -148,7 +150,8 @@ int ssd_conv_step(int dtype, const void* x, long long x_row_stride, const float*
     Pieces y;
     r = read_pieces({y0, y1, y2}, {n0, n1, n2}, {0, 0, 0}, channels, size_of(dtype), &y);
     if (r != SSD_OK) return r;
-    if (!state || !on(state, size_of(dtype)) || !on(slots, 4) || nslots <= 0 || (slots == nullptr && nslots < batch))
+    if (!state || !aligned_to(state, size_of(dtype)) || !aligned_to(slots, 4) || nslots <= 0 ||
+        (slots == nullptr && nslots < batch))
         return SSD_ERR_INVALID_ARG;
     int* err = error_words();
     if (err == nullptr) return SSD_ERR_CUDA;
@@ -164,7 +167,7 @@ int ssd_selective_forward(int dtype, const void* x, const void* dt, const float*
     int r = read_selective(dtype, x, dt, A, B, C, D, init_state, lengths, strides, batch, seqlen, channels, ngroups, dstate,
                            options, false, &a);
     if (r != SSD_OK) return r;
-    if (!y || !on(y, size_of(dtype)) || !on(final_state, 4)) return SSD_ERR_INVALID_ARG;
+    if (!y || !aligned_to(y, size_of(dtype)) || !aligned_to(final_state, 4)) return SSD_ERR_INVALID_ARG;
     const SelectivePlan plan = selective_plan(a, multiprocessors());
     const size_t bytes = selective_workspace(a, plan);
     void* ws = nullptr;
@@ -185,8 +188,9 @@ int ssd_selective_backward(int dtype, const void* x, const void* dt, const float
     if (r != SSD_OK) return r;
     const uintptr_t size = size_of(dtype);
     if (!dy || !dx || !ddt || !dA || !dB || !dC || (a.z != nullptr) != (dz != nullptr)) return SSD_ERR_INVALID_ARG;
-    if (!on(dy, size) || !on(dx, size) || !on(ddt, size) || !on(dz, size) || !on(dA, 4) || !on(dB, 4) || !on(dC, 4) ||
-        !on(dD, 4) || !on(ddt_bias, 4) || !on(dinit, 4) || !on(dfinal, 4))
+    if (!aligned_to(dy, size) || !aligned_to(dx, size) || !aligned_to(ddt, size) || !aligned_to(dz, size) ||
+        !aligned_to(dA, 4) || !aligned_to(dB, 4) || !aligned_to(dC, 4) ||
+        !aligned_to(dD, 4) || !aligned_to(ddt_bias, 4) || !aligned_to(dinit, 4) || !aligned_to(dfinal, 4))
         return SSD_ERR_INVALID_ARG;
     const SelectiveGrads g = {dy, dfinal, dx, ddt, dz, dA, dB, dC, dD, ddt_bias, dinit};
     void* ws = nullptr;
@@ -203,7 +207,8 @@ int ssd_selective_step(int dtype, const void* x, const void* dt, const float* A,
     const int r = read_selective(dtype, x, dt, A, B, C, D, nullptr, nullptr, strides, batch, 1, channels, ngroups, dstate,
                                  options, true, &a);
     if (r != SSD_OK) return r;
-    if (!y || !on(y, size_of(dtype)) || !state || !on(state, 4) || !on(slots, 4) || nslots <= 0 ||
+    if (!y || !aligned_to(y, size_of(dtype)) || !state || !aligned_to(state, 4) || !aligned_to(slots, 4) ||
+        nslots <= 0 ||
         (slots == nullptr && nslots < batch))
         return SSD_ERR_INVALID_ARG;
     int* err = error_words();
@@ -218,7 +223,8 @@ int ssd_layer_norm_forward(int dtype, const void* x, long long x_row_stride, con
         return SSD_ERR_INVALID_ARG;
     if (width > kMaxChannels) return SSD_ERR_UNSUPPORTED;
     const uintptr_t size = size_of(dtype);
-    if (!on(x, size) || !on(y, size) || !on(weight, 4) || !on(bias, 4) || !on(mean, 4) || !on(rstd, 4))
+    if (!aligned_to(x, size) || !aligned_to(y, size) || !aligned_to(weight, 4) || !aligned_to(bias, 4) ||
+        !aligned_to(mean, 4) || !aligned_to(rstd, 4))
         return SSD_ERR_INVALID_ARG;
     return launch_layer_norm_forward(dtype, x, x_row_stride, weight, bias, eps, rows, width, y, mean, rstd, stream);
 }
@@ -231,8 +237,9 @@ int ssd_layer_norm_backward(int dtype, const void* x, long long x_row_stride, co
         return SSD_ERR_INVALID_ARG;
     if (width > kMaxChannels) return SSD_ERR_UNSUPPORTED;
     const uintptr_t size = size_of(dtype);
-    if (!on(x, size) || !on(dy, size) || !on(dx, size) || !on(weight, 4) || !on(mean, 4) || !on(rstd, 4) ||
-        !on(dweight, 4) || !on(dbias, 4))
+    if (!aligned_to(x, size) || !aligned_to(dy, size) || !aligned_to(dx, size) || !aligned_to(weight, 4) ||
+        !aligned_to(mean, 4) || !aligned_to(rstd, 4) ||
+        !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
         return SSD_ERR_INVALID_ARG;
     const int parts = layer_norm_parts(rows, multiprocessors());
     void* ws = nullptr;

@@ -83,8 +83,6 @@ inline int selective_lanes(int dstate) {
     return lp;
 }
 
-inline bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-
 // Whether the token rows of x, dt, z (and of dense tensors of the same shape) are whole vectors of V channels, and
 // those of B and C whole vectors of V entries.
 inline bool rows_of(const SelectiveArgs& a, int V, const void* out1, const void* out2, size_t size) {

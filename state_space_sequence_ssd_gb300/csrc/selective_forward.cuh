@@ -107,13 +107,6 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
     const int64_t xs = K::COPY * a.x_token, ds = K::COPY * a.dt_token, zs = K::COPY * a.z_token;
     const T *xc = xg + (int64_t)(tb + row) * a.x_token + col, *dc = dg + (int64_t)(tb + row) * a.dt_token + col;
     const T* zc = gated ? zg + (int64_t)(tb + row) * a.z_token + col : zg;
-    constexpr int BC = (STATE_ONLY ? 1 : 2) * TS * NP / E;
-    auto bc_at = [&](int i, int t0, bool& live) {
-        const bool isC = i >= TS * NP / E;
-        const int j = isC ? i - TS * NP / E : i, t = t0 + j / (NP / E), e = j % (NP / E) * E;
-        live = t < last && e < N;
-        return isC ? Cg + (int64_t)t * a.C_token + e : Bg + (int64_t)t * a.B_token + e;
-    };
     auto fetch = [&](int t0, int buf) {
         T* to = raw + buf * buffer;
         if constexpr (VEC) {
@@ -160,9 +153,12 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
         }
         T* bc = to + 3 * TS * CC;
         if constexpr (VEC) {
-            for (int i = tid; i < BC; i += threads) {
-                bool live;
-                const T* from = bc_at(i, t0, live);
+            constexpr int ROW = NP / E, PART = TS * ROW;  // copies of a token's B, and of all of them
+            for (int i = tid; i < (STATE_ONLY ? 1 : 2) * PART; i += threads) {
+                const bool isC = i >= PART;
+                const int j = isC ? i - PART : i, t = t0 + j / ROW, e = j % ROW * E;
+                const bool live = t < last && e < N;
+                const T* from = isC ? Cg + (int64_t)t * a.C_token + e : Bg + (int64_t)t * a.B_token + e;
                 copy16(bc + i * E, live ? from : Bg, live);
             }
         } else {
