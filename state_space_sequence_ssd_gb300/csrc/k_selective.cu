@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(256, 4) selective_step_kernel(SelectiveArgs a,
     const Vec<float, 4> A4 = load_vec<float, 4>(a.A + (mine ? c * N + 4 * q : 0), nvalid, vecs);
     const f32x2 log2e = pk(kLog2e, kLog2e), A01 = mul2(A4.pair(0), log2e), A23 = mul2(A4.pair(1), log2e);
     float dv[1] = {dq + bias};
-    effective(dv, a.dto);
+    effective<false>(dv, a.dto);
     dq = dv[0];
     const float dxq = dq * xq;
     float acc[R];

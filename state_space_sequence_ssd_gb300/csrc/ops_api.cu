@@ -66,14 +66,18 @@ int read_selective(int dtype, const void* x, const void* dt, const float* A, con
         !aligned_to(init, 4) || !aligned_to(lengths, 4))
         return SSD_ERR_INVALID_ARG;
     DtOpts dto;
+    dto.lo = -INFINITY;  // no limits
+    dto.hi = INFINITY;
     if (o != nullptr) {
         if (!aligned_to(o->dt_bias, 4)) return SSD_ERR_INVALID_ARG;
         if (o->dt_limit && !(o->dt_min <= o->dt_max)) return SSD_ERR_INVALID_ARG;  // also rejects a NaN bound
         dto.bias = o->dt_bias;
         dto.softplus = o->dt_softplus != 0;
         dto.limit = o->dt_limit != 0;
-        dto.lo = o->dt_min;
-        dto.hi = o->dt_max;
+        if (dto.limit) {
+            dto.lo = o->dt_min;
+            dto.hi = o->dt_max;
+        }
     }
     const int64_t row = channels, bc = (int64_t)ngroups * dstate;
     ssd_selective_strides s = {seqlen * row, row, seqlen * row, row, seqlen * row, row, seqlen * bc, bc, seqlen * bc, bc};

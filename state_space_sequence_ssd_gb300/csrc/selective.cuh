@@ -34,13 +34,15 @@ __device__ __forceinline__ float held_to(float v, float lo, float hi) {
 
 // The effective dt of M values of raw dt with their bias added: softplus, limits.  The options are looked at once for
 // all of them: a branch within each value's chain of dependent instructions would run the chains one after another.
-template <int M>
+// Without limits lo and hi are infinities; a step takes them without a branch, which would stand between its loads and their
+// use (256 rows of 4096 x 16: 28.7 us, 31.2 with it), a prompt with one (2 x 4096 x 4096 x 16: 282 us, 285 without).
+template <bool BRANCH, int M>
 __device__ __forceinline__ void effective(float (&v)[M], const DtOpts& o) {
     if (o.softplus) {
 #pragma unroll
         for (int i = 0; i < M; ++i) v[i] = softplus(v[i]);
     }
-    if (o.limit) {
+    if (!BRANCH || o.limit) {
 #pragma unroll
         for (int i = 0; i < M; ++i) v[i] = held_to(v[i], o.lo, o.hi);
     }

@@ -147,7 +147,7 @@ __device__ __forceinline__ float stage_block(const SelectiveArgs& a, const Rows<
                     dt[4 * i + e] = l.d[s + i].get(e) + bias[e];
                     g[4 * i + e] = l.dy[s + i].get(e);
                 }
-            effective(dt, a.dto);
+            effective<true>(dt, a.dto);
             if (r.z != nullptr) {
 #pragma unroll
                 for (int i = 0; i < S; ++i)

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(128, 3) selective_kernel(SelectiveArgs a, int 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) d[4 * i + e] = dt.get(e) + bias[e];
             }
-            effective(d, a.dto);
+            effective<true>(d, a.dto);
 #pragma unroll
             for (int i = 0; i < CONVS; ++i) {
                 const int at = place + i * K::CONV * CC;
