@@ -441,8 +441,17 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     auto advance = [&](int t) { at.advance(t, A, h); };
     auto operands = [&](int t) { return at.operands(t); };
     auto join = [&](f32x2 lo, f32x2 hi, float* to) { join_lanes<LP>(lo, hi, lane, to + 4 * qd); };
+    // four values over the warp's channels, to entries 4 q .. of a token's row of dB (half = 0) or dC (1); join_warp written
+    // out, which keeps this kernel's registers as they are without `alone` (500 us at 2 x 4096 x 2048 x 16, 507 otherwise)
     auto join_channels = [&](float (&v)[4], int t, int half) {
-        join_warp<LP>(v, lane, s_red + ((warp * kRun + t % kRun) * 2 + half) * NP + 4 * q);
+        constexpr int CW = 32 / LP, LEFT = CW >= 4 ? 1 : 4 / CW;
+        int which = 0;
+        fold_between<4, 16, LP>(v, lane, which);
+        float* to = s_red + ((warp * kRun + t % kRun) * 2 + half) * NP + 4 * q + which;
+        if (CW <= 4 || ((lane / LP) & (CW / 4 > 0 ? CW / 4 - 1 : 0)) == 0) {
+#pragma unroll
+            for (int e = 0; e < LEFT; ++e) to[e] = v[e];
+        }
     };
     // tokens t0 .. t0 + 3 from the states before them: forward with y and dC, then backward with the rest
     auto half = [&](int t0) {
