@@ -59,10 +59,11 @@ struct Term<true> {
     }
 };
 
-// dec: log2 decay of step c for row (b, h) at dec[row * dec_row + c * dec_step]
+// dec: log2 decay of step c for row (b, h) at dec[row * dec_row + c * dec_step].  The span decays are written by the launch
+// before, which may still run when this one starts: plain loads behind the wait, from a pointer that promises nothing.
 template <bool H16>
 __global__ void __launch_bounds__(kThreads) state_passing_kernel(const float* S, const __half* S16,
-                                                                 const float* __restrict__ dec,
+                                                                 const float* dec,
                                                                  int64_t dec_step, int64_t dec_row,
                                                                  const float* __restrict__ init, Dims d,
                                                                  float* states, float* __restrict__ final_state,
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) state_passing_kernel(const float* S,
         if (k < nc) {
             const int c = rev ? nc - 1 - k : k;
             nv[k] = Term<H16>::load(S, S16, base + (int64_t)c * cstride);
-            nd[k] = __ldg(csl + (int64_t)c * dec_step);
+            nd[k] = csl[(int64_t)c * dec_step];
         }
     }
     for (int c0 = 0; c0 < nc; c0 += kUnroll) {
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) state_passing_kernel(const float* S,
             if (cn < nc) {
                 const int c = rev ? nc - 1 - cn : cn;
                 nv[k] = Term<H16>::load(S, S16, base + (int64_t)c * cstride);
-                nd[k] = __ldg(csl + (int64_t)c * dec_step);
+                nd[k] = csl[(int64_t)c * dec_step];
             }
         }
 #pragma unroll

@@ -8,7 +8,8 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "state_space_sequence_ssd_gb300", "csrc")
 # kernel -> its file, the parameters that the launch before it writes, and whether it reads nothing else after its wait
-KERNELS = {"conv_reduce_kernel": ("k_conv.cu", ["partial"], True),
+KERNELS = {"state_passing_kernel": ("k_state_passing.cu", ["S", "S16", "dec"], True),
+           "conv_reduce_kernel": ("k_conv.cu", ["partial"], True),
            "norm_reduce_kernel": ("k_norm.cu", ["partial"], True),
            "selective_hop_kernel": ("k_selective.cu", ["hops", "dtsum"], True),
            "selective_kernel": ("selective_forward.cuh", ["hops"], False),
@@ -41,8 +42,8 @@ def test_what_the_launch_before_writes_is_read_plainly(name):
         assert "__ldg" not in body[body.index("grid_dep_wait()"):]
 
 
-def test_every_dependent_kernel_of_the_layer_operators_is_listed():
+def test_every_dependent_kernel_is_listed():
     seen = set()
-    for file in ("k_conv.cu", "k_norm.cu", "k_selective.cu", "k_selective_bwd.cu", "selective_backward.cuh", "selective_forward.cuh"):
+    for file in ("k_state_passing.cu", "k_conv.cu", "k_norm.cu", "k_selective.cu", "k_selective_bwd.cu", "selective_backward.cuh", "selective_forward.cuh"):
         seen |= set(re.findall(r"launch_dependent\((\w+)", open(os.path.join(CSRC, file)).read()))
     assert seen - {"kernel"} == set(KERNELS) - {"selective_kernel"}  # that one is launched under a generic name
