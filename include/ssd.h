@@ -522,8 +522,10 @@ typedef struct ssd_selective_strides {
  *   A            (channels, dstate) f32; D (channels) f32 or NULL
  *   init_state, final_state (batch, channels, dstate) f32 or NULL
  *   y            (batch, seqlen, channels) dense
- * Value domain: A <= 0 and an effective dt >= 0, as for ssd_forward.  dstate is
- * 1 to 128 (SSD_ERR_UNSUPPORTED beyond).
+ * Value domain: A <= 0 and an effective dt >= 0, as for ssd_forward; a token's
+ * decay below 2^-126 is zero.  An infinity or a NaN in a live place reaches what
+ * the recurrence carries it to and nothing else.  dstate is 1 to 128
+ * (SSD_ERR_UNSUPPORTED beyond).
  */
 SSD_API int ssd_selective_forward(int dtype, const void* x, const void* dt, const float* A, const void* B,
                                   const void* C, const float* D, const float* init_state, const int* lengths,
@@ -541,6 +543,12 @@ SSD_API int ssd_selective_forward(int dtype, const void* x, const void* dt, cons
  *   dD        (channels) f32 or NULL; ddt_bias (channels) f32 or NULL
  *   dz        (batch, seqlen, channels), given exactly when options->z is
  *   dinit     (batch, channels, dstate) f32 or NULL
+ * Its workspace grows with dstate and its square: about channels * (dstate / 4 +
+ * dstate^2 / 256 + 0.4) bytes for a token of a row (dstate / 4 becomes dstate / 2
+ * where there are too few tokens and channels to fill the device): 0.09 GB at
+ * 2 x 4096 tokens of 2048 channels and 16 entries, 2.2 GB at 2 x 4096 x 8192 x 64,
+ * 17 GB at 8 x 8192 x 8192 x 64.  Where the device has not that much left the call
+ * returns SSD_ERR_NO_MEMORY; fewer rows or groups of channels a call need less.
  */
 SSD_API int ssd_selective_backward(int dtype, const void* x, const void* dt, const float* A, const void* B,
                                    const void* C, const float* D, const float* init_state, const int* lengths,

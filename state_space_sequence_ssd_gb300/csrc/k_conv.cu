@@ -83,7 +83,7 @@ __device__ __forceinline__ Vec<T, V> input_at(const ConvArgs& a, int b, int t, i
 
 // A warp: 32 V channels of RUN consecutive tokens, STEP of them loaded at a time, one step ahead of their use.  Runs whose
 // tokens all count, most of them, are computed without looking at each.  Two channels a thread leave registers for 32 warps
-// an SM: at 2 x 4096 x 4352 of bfloat16 30.4 us (4.7 TB/s; a plain copy of as many bytes takes 22.6), where four channels
+// an SM: at 2 x 4096 x 4352 of bfloat16 29.7 us (4.8 TB/s; a plain copy of as many bytes takes 22.6), where four channels
 // with half the warps take 33.3, steps of half as many tokens 33, runs of 16 tokens 34 and of 64 36.
 template <typename T, int V, int W, int RUN>
 __global__ void __launch_bounds__(32 * kWarps, 8) conv_forward_kernel(ConvArgs a, Pieces y, T* __restrict__ final_state) {
@@ -170,10 +170,11 @@ __device__ __forceinline__ GradPiece grad_piece(const Pieces& dy, int c) {
 // dLoss/dpre up to W-1 tokens on, so the walk goes that far past the run (those tokens' pre again).  Tokens are taken
 // four at a time: their x and dy are loaded together, one group ahead of their use; groups whose tokens all count and
 // all leave, most of them, are computed without looking at each.  The block's warps' sums of one channel are joined in
-// shared memory in warp order and written as one row of `partial`, (rows, width + 1, channels).  Bound by issue slots
-// (13 multiply-adds, an exponential, a quotient and the conversions per element; 61% of the slots are used), not by HBM:
-// at 2 x 4096 x 4352 of bfloat16 66 us, with the reduction, where 20 warps an SM hold two channels a thread; four
-// channels and 12 warps 71, 16 warps 75, 24 warps 71, groups of two tokens 87 and of eight 82.
+// shared memory in warp order and written as one row of `partial`, (rows, width + 1, channels).  Not bound by HBM (3.0 of
+// 6.8 TB/s) nor by issue slots (58% used) but by latency: 18 warps an SM, which the registers allow, wait for each other's
+// 13 multiply-adds, exponential and quotient per element and for loads.  At 2 x 4096 x 4352 of bfloat16 65 us, with the
+// reduction, where 20 warps an SM hold two channels a thread; four channels and 12 warps 71, 16 warps 75, 24 warps 71,
+// groups of two tokens 87 and of eight 82.
 template <typename T, int V, int W, int RUN>
 __global__ void __launch_bounds__(32 * kWarps, V == 2 ? 5 : 4) conv_backward_kernel(
     ConvArgs a, Pieces dy, const T* __restrict__ dfinal, T* __restrict__ dx, int64_t dx_batch, int64_t dx_token,

@@ -126,8 +126,9 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const T* __restr
 // The same for many rows, with vectors of 16 bytes: a resident grid whose blocks walk the rows, two neighbouring ones a
 // thread, so that they share the reductions' barriers and the weight and bias that it holds.  A thread's pieces of the
 // next rows are copied to shared memory that it alone reads, so that they need neither registers nor barriers while they
-// are on their way.  At 8192 x 2048 of bfloat16 14.3 us (4.7 TB/s; a plain copy of as many bytes takes 11.9), where the
-// kernel above takes 19.3, and at 30400 x 2048 46 (5.4 TB/s) where that takes 63.  Copies of one, three and four pairs of
+// are on their way.  At 8192 x 2048 of bfloat16 14.4 us where two sets of inputs take turns (part of them stays in L2), 16.7
+// where they come from HBM (4.0 TB/s; a plain copy of as many bytes 12.3); the kernel above takes 19.3 where this takes
+// 14.4, and at 30400 x 2048 63 where this takes 46 (5.4 TB/s).  Copies of one, three and four pairs of
 // rows ahead took 3 to 7% longer than two, reading the weight again for each row 14%.
 constexpr int kAhead = 2;  // pairs of rows
 constexpr int resident(int nv) { return nv <= 2 ? 3 : 2; }  // blocks of an SM
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(kThreads) norm_forward_wide_kernel(const T* __
 
 // A block of `lanes` threads a row, kThreads / lanes rows at a time.  The thread's columns of dweight and dbias stay
 // in registers while the block walks its rows, and the next rows' loads are in flight while a row is summed.  With the
-// reduction 26.7 us at 8192 x 2048 of bfloat16 (a plain sum of two such tensors takes 15.7): 53% of the issue slots at 16
-// warps an SM, which the sums' registers allow.  Smaller parts of a row a thread (8 columns instead of 16) and more
+// reduction 27.2 us at 8192 x 2048 of bfloat16 (a plain sum of two such tensors takes 15.7): bound by latency, with 52% of the
+// issue slots used at 15 warps an SM, which the sums' registers allow.  Smaller parts of a row a thread (8 columns instead of 16) and more
 // blocks took 39 us and more, loads three rows ahead through shared memory as long as these one row ahead.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __restrict__ x, int64_t x_row,

@@ -65,8 +65,7 @@ namespace {
 // is read and written once.  The rows' states are loaded together and A once for them; each of the first R lanes
 // forms one row's dt and gate for the others, and ends with that row's output.  An idle row (slot -1) writes zeros
 // and leaves every slot alone.  VEC: states, A, B and C are whole vectors of four entries, known when it is compiled.
-// 256 rows of 4096 x 16 take 29.4 us, 4.6 TB/s; half of that is instructions (65% of the issue slots are used), and more
-// bytes in flight do not help: eight rows copied to shared memory ahead 31, two rows or one 33 and 41, a fifth block an SM 36.
+// 256 rows of 4096 x 16 take 28.7 us, 5.0 TB/s, with 58% of the issue slots used; more bytes in flight do not help: eight rows copied to shared memory ahead 31, two rows or one 33 and 41, a fifth block an SM 36.
 template <typename T, int LP, int R, bool VEC>
 __global__ void __launch_bounds__(256, 4) selective_step_kernel(SelectiveArgs a, float* __restrict__ state,
                                                              const int* __restrict__ slots, int nslots, T* __restrict__ y,
@@ -178,7 +177,10 @@ SelectivePlan selective_plan(const SelectiveArgs& a, int sms) {
     // with one, two and three warps on it, measured at bf16 and 16 entries (and for the first run, which all chunks but
     // the last need): wide lanes 640, 740 and 900 (380, 460 and 570), narrow ones, which do a quarter of that work, 250,
     // 290 and 350 (180, 210 and 250) -- so narrow lanes where the SMs would otherwise stay idle.  A split costs two
-    // launches and the hop besides, about 5 us and 60 ns a chunk.
+    // launches and the hop besides, about 5 us and 60 ns a chunk.  What the estimate leaves out: a chunk's states in memory
+    // (4 x batch x channels x dstate x 4 bytes), other types and numbers of entries, and that one lane a channel (dstate of 8
+    // or less) fits two blocks on an SM, or one in float32, by its shared memory; it says 225 us where 282 are measured at
+    // 2 x 4096 x 4096 x 16.
     // Where rows have their own lengths half of the blocks are taken to have work (the others end at once): with lengths
     // spread evenly from nothing to the row 166 us at 8 x 2048 x 2048 x 16 of bfloat16 and 108 at 16 x 512 x 2048 x 16,
     // 192 and 115 with the split for whole rows; with whole rows 285 and 160, 304 and 159; with at least half rows 263 and

@@ -12,8 +12,8 @@
 // kernel then works on every block by itself, from its true start state and end gradient.  Inside a block the
 // states are recomputed in runs of kRun tokens from a checkpoint at each run's start, since only the decay, not its
 // inverse, is stable.  No atomics: sums over channels and blocks are written as rows of partial sums and added in a
-// fixed order, by one launch for all of them.  At 2 x 4096 x 2048 x 16 of bfloat16 495 us, about 128 of them for the
-// blocks' own terms: 255 registers a thread leave the main kernel two warps on an SM quarter and 46% of the issue slots.
+// fixed order, by one launch for all of them.  At 2 x 4096 x 2048 x 16 of bfloat16 500 us, about 130 of them for the
+// blocks' own terms: 240 registers a thread leave the main kernel two warps on an SM quarter and 48% of the issue slots.
 //
 // A lane holds four state entries of four neighbouring channels and LP lanes share a channel: shared memory returns 128
 // bytes a clock to the registers, broadcast or not, and with one channel a lane the operands of an entry (32 bytes over
