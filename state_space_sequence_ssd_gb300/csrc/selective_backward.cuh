@@ -345,11 +345,11 @@ struct Lane {
 // The tokens of one run, last to first, each by itself from the run's checkpoint; y, red: this lane's places in the rows of
 // y and of the warp's parts of dB and dC.  Entries past dstate, channels past the group's last and tokens past the length are
 // zeros that add nothing -- unless they meet an infinity, zero times which is NaN: one of the token's other factors, or one in a
-// state that an earlier token left.  So a run that is not whole, and the runs of a block that holds an infinity or a NaN, come
-// here, where such zeros are left out of the sums; the same roundings otherwise.  A call of its own (its arrays in local
-// memory), so that it takes no registers from the runs that need none of this.
+// state that an earlier token left.  So the runs of a block that holds an infinity or a NaN come here, where such zeros are left
+// out of the sums; the same roundings otherwise.  Few registers count here, not time: kernels that have this beside their
+// other runs take 5% longer (520 us against 497 at 2 x 4096 x 2000 x 16), so only shapes with padding do.
 template <int LP>
-__device__ __noinline__ void alone(const Lane<LP> at, const ulonglong2* ck, int first, int end, int entries, int channels,
+__device__ __forceinline__ void alone(const Lane<LP> at, const ulonglong2* ck, int first, int end, int entries, int channels,
                                    float* y_row, float* red, const Entries& A, Entries& m, Entries& dA) {
     const int lane = threadIdx.x & 31, threads = blockDim.x;
     auto entry = [&](int e, f32x2 u, f32x2 v, f32x2 s) { return e < entries ? fma2(u, v, s) : s; };
@@ -531,31 +531,24 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
     };
     // backward, run by run, its second half first
     const int64_t place = ((int64_t)r.tile * a.batch + r.b) * a.seqlen;  // dbc: (tiles, batch, seqlen, ngroups, 2, dstate)
-    const int whole = finite ? steps / kRun : 0;
-    for (int j = runs - 1; j >= 0; --j) {
-        if (PAD && j >= whole) {
-            Entries A2, m2, dA2;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) { A2[e][i] = A[e][i]; m2[e][i] = m[e][i]; dA2[e][i] = dA[e][i]; }
-            alone<LP>(at, ck + 4 * j * threads, j * kRun, min(steps, (j + 1) * kRun), N - 4 * q, mine, s_y + 4 * qd,
-                      s_red + warp * kRun * 2 * NP + 4 * q, A2, m2, dA2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) { m[e][i] = m2[e][i]; dA[e][i] = dA2[e][i]; }
-        } else {
+    // whether the states after the last run's tokens (none was infinite before if these are finite) and the gradient that comes
+    // to it are finite, so that its tokens past the length do add zeros
+    auto settled = [&](int j) {
+        restore(j);
 #pragma unroll 1
-            for (int s = 1; s >= 0; --s) {
-                restore(j);
-                if (s == 1) {
-#pragma unroll 2
-                    for (int i = 0; i < kHeld; ++i) advance(j * kRun + i);
-                }
-                half(j * kRun + s * kHeld);
+        for (int t = j * kRun; t < steps; ++t) advance(t);
+        float undefined = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float lo, hi;
+                unpk(fma2(h[e][i], 0ull, mul2(m[e][i], 0ull)), lo, hi);
+                undefined += lo + hi;
             }
-        }
+        return __syncthreads_or(undefined != 0.f) == 0;
+    };
+    auto store_run = [&](int j) {
         __syncthreads();
         for (int i = tid; i < kRun * 2 * LP; i += threads) {  // four entries of a token's dB or dC, over the warps
             const int tt = i / (2 * LP), which = i / LP % 2, e = i % LP * 4, t = r.tb + j * kRun + tt;
@@ -570,6 +563,27 @@ __global__ void __launch_bounds__(128, 2) selective_block_kernel(SelectiveArgs a
                                 N % 4 == 0);
         }
         __syncthreads();
+    };
+    int j = runs - 1;
+    if constexpr (PAD) {
+        const bool careful = !finite || (steps % kRun != 0 && !settled(j));
+        for (; careful && j >= 0; --j) {
+            alone<LP>(at, ck + 4 * j * threads, j * kRun, min(steps, (j + 1) * kRun), N - 4 * q, mine, s_y + 4 * qd,
+                      s_red + warp * kRun * 2 * NP + 4 * q, A, m, dA);
+            store_run(j);
+        }
+    }
+    for (; j >= 0; --j) {
+#pragma unroll 1
+        for (int s = 1; s >= 0; --s) {
+            restore(j);
+            if (s == 1) {
+#pragma unroll 2
+                for (int i = 0; i < kHeld; ++i) advance(j * kRun + i);
+            }
+            half(j * kRun + s * kHeld);
+        }
+        store_run(j);
     }
     // tokens past the last run have no gradient in B and C
     for (int i = tid; i < (r.te - r.tb - runs * kRun) * 2 * N; i += threads) {
