@@ -587,6 +587,55 @@ SSD_API int ssd_layer_norm_backward(int dtype, const void* x, long long x_row_st
                                     cudaStream_t stream);
 
 /*
+ * The gated linear recurrence: one state per channel, its decay and its input both gated by the token.
+ *     v = sigmoid(r[b,t,c]),  g = sigmoid(i[b,t,c]),  a = exp(A[c] * v)
+ *     h[c] <- a * h[c] + sqrt(1 - a^2) * g * x[b,t,c],   y[b,t,c] = h[c]
+ * so that a state of unit variance keeps it whatever the decay.  Strides in elements, per row and per token (a NULL pointer:
+ * all dense); ssd_gated_step reads the *_batch members only.
+ */
+typedef struct ssd_gated_strides {
+    long long x_batch, x_token, r_batch, r_token, i_batch, i_token;
+} ssd_gated_strides;
+
+/* Tokens between the states that ssd_gated_forward keeps for ssd_gated_backward. */
+#define SSD_GATED_SPAN 64
+
+/*
+ * ssd_gated_forward
+ *   x, r, i      (batch, seqlen, channels); r and i are the gates in front of their sigmoid
+ *   A            (channels) f32, below zero
+ *   init_state, final_state (batch, channels) f32 or NULL
+ *   y            (batch, seqlen, channels) dense
+ *   states       (batch, ceil(seqlen / SSD_GATED_SPAN), channels) f32 or NULL: the state in front of every
+ *                SSD_GATED_SPAN-th token (the final state past a row's length), for ssd_gated_backward
+ * Value domain: A < 0; a token's decay, gate or 1 - a^2 below 2^-126 is zero.  An infinity or a NaN in a live place reaches what the
+ * recurrence carries it to and nothing else.  One launch, no workspace.
+ */
+SSD_API int ssd_gated_forward(int dtype, const void* x, const void* r, const void* i, const float* A,
+                              const float* init_state, const int* lengths, const ssd_gated_strides* strides, int batch,
+                              int seqlen, int channels, void* y, float* final_state, float* states, cudaStream_t stream);
+
+/*
+ * ssd_gated_backward -- gradients through ssd_gated_forward from dy (dense, y's layout) and dfinal ((batch, channels)
+ * f32, or NULL).  states are those that the forward pass kept for the same inputs (init_state is not read then), or
+ * NULL: they are computed again from the inputs into a workspace.  Outputs, dense and fully written:
+ *   dx, dr, di   (batch, seqlen, channels): dr and di are those of the gates in front of their sigmoid
+ *   dA           (channels) f32; dinit (batch, channels) f32 or NULL
+ */
+SSD_API int ssd_gated_backward(int dtype, const void* x, const void* r, const void* i, const float* A,
+                               const float* init_state, const int* lengths, const ssd_gated_strides* strides, int batch,
+                               int seqlen, int channels, const float* states, const void* dy, const float* dfinal, void* dx,
+                               void* dr, void* di, float* dA, float* dinit, cudaStream_t stream);
+
+/*
+ * ssd_gated_step -- ssd_gated_forward for one token of every row: x, r, i, y (batch, channels), state (nslots,
+ * channels) f32 updated in place.
+ */
+SSD_API int ssd_gated_step(int dtype, const void* x, const void* r, const void* i, const float* A, float* state,
+                           const int* slots, int nslots, const ssd_gated_strides* strides, int batch, int channels, void* y,
+                           cudaStream_t stream);
+
+/*
  * ssd_get_device_error -- reads and clears the library's device error words
  * on the current device (synchronizes with the device).  Returns SSD_OK;
  * SSD_ERR_TIMEOUT if a kernel's bounded wait gave up since the last read
@@ -594,7 +643,7 @@ SSD_API int ssd_layer_norm_backward(int dtype, const void* x, long long x_row_st
  * of that call are incomplete while the device stays usable); otherwise
  * SSD_ERR_RANGE if a value converted to a float16 tensor-core operand was
  * outside float16's finite range since the last read; otherwise SSD_ERR_SLOT
- * if a single-token call (ssd_conv_step, ssd_selective_step) met a slot index
+ * if a single-token call (ssd_conv_step, ssd_selective_step, ssd_gated_step) met a slot index
  * past its pool since that was last reported; or SSD_ERR_CUDA if the read itself
  * failed.  A slot flag beside one of the other two waits for the next read: read
  * until SSD_OK.

@@ -20,14 +20,15 @@ strided rows and other element types.
 from __future__ import annotations
 
 from . import _ffi
-from .layer import (ssd_conv_backward, ssd_conv_forward, ssd_conv_step, ssd_layer_norm_backward, ssd_layer_norm_forward,
-                    ssd_selective_backward, ssd_selective_forward, ssd_selective_step)
+from .layer import (ssd_conv_backward, ssd_conv_forward, ssd_conv_step, ssd_gated_backward, ssd_gated_forward, ssd_gated_step,
+                    ssd_layer_norm_backward, ssd_layer_norm_forward, ssd_selective_backward, ssd_selective_forward, ssd_selective_step)
 
 __all__ = ["ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan", "ssd_forward",
            "ssd_forward_noalloc", "ssd_forward_heads", "ssd_partition_heads", "ssd_forward_plan", "ssd_step",
            "ssd_step_multi", "ssd_forward_ex", "ssd_step_ex", "ssd_backward", "ssd_get_device_error", "SSDError", "library_path",
            "ssd_conv_forward", "ssd_conv_backward", "ssd_conv_step", "ssd_selective_forward", "ssd_selective_backward",
-           "ssd_selective_step", "ssd_layer_norm_forward", "ssd_layer_norm_backward"]
+           "ssd_selective_step", "ssd_layer_norm_forward", "ssd_layer_norm_backward",
+           "ssd_gated_forward", "ssd_gated_backward", "ssd_gated_step"]
 
 SSDError = _ffi.SSDError
 library_path = _ffi.LIB_PATH

@@ -51,6 +51,9 @@ SIGNATURES = {
     "ssd_selective_step": (_i, [_i] + [_p] * 8 + [_i, _p] + [_i] * 4 + [_p] * 3),
     "ssd_layer_norm_forward": (_i, [_i, _p, _l, _p, _p, ctypes.c_float, _l, _i] + [_p] * 4),
     "ssd_layer_norm_backward": (_i, [_i, _p, _l, _p, _p, _p, _p, _l, _l, _i] + [_p] * 4),
+    "ssd_gated_forward": (_i, [_i] + [_p] * 7 + [_i] * 3 + [_p] * 4),
+    "ssd_gated_backward": (_i, [_i] + [_p] * 7 + [_i] * 3 + [_p] * 9),
+    "ssd_gated_step": (_i, [_i] + [_p] * 6 + [_i, _p] + [_i] * 2 + [_p] * 2),
     "ssd_get_device_error": (_i, []),
     "ssd_debug_set_wait_limit_ns": (_i, [ctypes.c_ulonglong]),
     "ssd_debug_stall": (_i, [_i]),
@@ -73,6 +76,11 @@ class InputOptions(ctypes.Structure):
 class SelectiveStrides(ctypes.Structure):
     """struct ssd_selective_strides."""
     _fields_ = [(f"{name}_{dim}", ctypes.c_longlong) for name in ("x", "dt", "z", "B", "C") for dim in ("batch", "token")]
+
+
+class GatedStrides(ctypes.Structure):
+    """struct ssd_gated_strides."""
+    _fields_ = [(f"{name}_{dim}", ctypes.c_longlong) for name in ("x", "r", "i") for dim in ("batch", "token")]
 
 
 _lock = threading.Lock()

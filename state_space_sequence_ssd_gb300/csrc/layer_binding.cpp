@@ -438,6 +438,83 @@ PyObject* selective_step(PyObject* const* a) {
     return wrap(y);
 }
 
+// What the gated recurrence's entries share, from x, r, i, A.
+struct Gated {
+    Lead l;
+    int64_t b, L, ch;
+    const void *x, *r, *i;
+    const float* A;
+    ssd_gated_strides st;
+};
+Gated gated(PyObject* ox, PyObject* orr, PyObject* oi, PyObject* oA, int ndim) {
+    const Tensor& x = tensor(ox, "x");
+    Gated s{lead(x, "x", ndim)};
+    const Tensor &r = tensor(orr, "r"), &i = tensor(oi, "i"), &A = tensor(oA, "A");
+    const bool tokens = ndim == 3;
+    s.b = x.size(0);
+    s.L = tokens ? x.size(1) : 1;
+    s.ch = x.size(ndim - 1);
+    check(r, "r", s.l.type, x.sizes(), s.l);
+    check(i, "i", s.l.type, x.sizes(), s.l);
+    need_dense_end(x, "x", 1);
+    need_dense_end(r, "r", 1);
+    need_dense_end(i, "i", 1);
+    auto token = [&](const Tensor& t) { return tokens ? stride(t, 1) : 0; };
+    s.st = {stride(x, 0), token(x), stride(r, 0), token(r), stride(i, 0), token(i)};
+    s.x = x.data_ptr();
+    s.r = r.data_ptr();
+    s.i = i.data_ptr();
+    s.A = dense<float>(A, "A", at::kFloat, {s.ch}, s.l);
+    return s;
+}
+float* floats(const Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; }
+int64_t gated_spans(int64_t L) { return (L + SSD_GATED_SPAN - 1) / SSD_GATED_SPAN; }
+
+// x, r, i, A, init_state, lengths, want_final, want_states
+PyObject* gated_forward(PyObject* const* a) {
+    const Gated s = gated(a[0], a[1], a[2], a[3], 3);
+    const float* init = dense<float>(a[4], "init_state", at::kFloat, {s.b, s.ch}, s.l);
+    const int* lengths = dense<int>(a[5], "lengths", at::kInt, {s.b}, s.l);
+    Tensor y = empty({s.b, s.L, s.ch}, s.l.type, s.l), final_state, states;
+    if (truth(a[6])) final_state = empty({s.b, s.ch}, at::kFloat, s.l);
+    if (truth(a[7])) states = empty({s.b, gated_spans(s.L), s.ch}, at::kFloat, s.l);
+    done("ssd_gated_forward", ssd_gated_forward(s.l.code, s.x, s.r, s.i, s.A, init, lengths, &s.st, size_int(s.b), size_int(s.L), size_int(s.ch),
+                                                y.data_ptr(), floats(final_state), floats(states), s.l.stream));
+    return tuple_of({wrap(y), wrap(final_state), wrap(states)});
+}
+
+// x, r, i, A, dy, init_state, lengths, states, dfinal, want_dinit
+PyObject* gated_backward(PyObject* const* a) {
+    const Gated s = gated(a[0], a[1], a[2], a[3], 3);
+    const Lead& l = s.l;
+    const void* dy = dense(tensor(a[4], "dy"), "dy", l.type, {s.b, s.L, s.ch}, l);
+    const float* init = dense<float>(a[5], "init_state", at::kFloat, {s.b, s.ch}, l);
+    const int* lengths = dense<int>(a[6], "lengths", at::kInt, {s.b}, l);
+    const float* states = dense<float>(a[7], "states", at::kFloat, {s.b, gated_spans(s.L), s.ch}, l);
+    const float* dfinal = dense<float>(a[8], "dfinal", at::kFloat, {s.b, s.ch}, l);
+    Tensor dx = empty({s.b, s.L, s.ch}, l.type, l), dr = empty({s.b, s.L, s.ch}, l.type, l), di = empty({s.b, s.L, s.ch}, l.type, l),
+           dA = empty({s.ch}, at::kFloat, l), dinit;
+    if (truth(a[9])) dinit = empty({s.b, s.ch}, at::kFloat, l);
+    done("ssd_gated_backward", ssd_gated_backward(l.code, s.x, s.r, s.i, s.A, init, lengths, &s.st, size_int(s.b), size_int(s.L), size_int(s.ch), states, dy,
+                                                  dfinal, dx.data_ptr(), dr.data_ptr(), di.data_ptr(), floats(dA), floats(dinit), l.stream));
+    return dict_of({{"dx", &dx}, {"dr", &dr}, {"di", &di}, {"dA", &dA}, {"dinit", &dinit}});
+}
+
+// x, r, i, A, state, slots
+PyObject* gated_step(PyObject* const* a) {
+    const Gated s = gated(a[0], a[1], a[2], a[3], 2);
+    const Tensor& state = tensor(a[4], "state");
+    if (state.dim() != 2) refuse(PyExc_ValueError, "state must be a (slots, " + std::to_string(s.ch) + ") tensor");
+    const int64_t n = state.size(0);
+    const int* slots = dense<int>(a[5], "slots", at::kInt, {s.b}, s.l);
+    if (slots == nullptr && n < s.b)
+        refuse(PyExc_ValueError, "state holds " + std::to_string(n) + " rows for a batch of " + std::to_string(s.b));
+    float* p = dense<float>(state, "state", at::kFloat, {n, s.ch}, s.l);
+    Tensor y = empty({s.b, s.ch}, s.l.type, s.l);
+    done("ssd_gated_step", ssd_gated_step(s.l.code, s.x, s.r, s.i, s.A, p, slots, size_int(n), &s.st, size_int(s.b), size_int(s.ch), y.data_ptr(), s.l.stream));
+    return wrap(y);
+}
+
 // Rows of the last dimension whose leading dimensions run through one stride.
 struct Flat {
     long long step, rows;
@@ -550,6 +627,9 @@ PyMethodDef g_methods[] = {
     method<selective_step, 12>("selective_step"),
     method<norm_forward, 4>("norm_forward"),
     method<norm_backward, 6>("norm_backward"),
+    method<gated_forward, 8>("gated_forward"),
+    method<gated_backward, 10>("gated_backward"),
+    method<gated_step, 6>("gated_step"),
     method<flat_rows, 1>("flat_rows"),
     method<row_strides, 2>("row_strides"),
     method<set_fail, 1>("set_fail"),

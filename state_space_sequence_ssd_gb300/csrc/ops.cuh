@@ -250,6 +250,9 @@ enum LayerKind {
     kKindSelectiveStep,
     kKindNorm,
     kKindNormBwd,
+    kKindGated,
+    kKindGatedBwd,
+    kKindGatedStep,
     kAllKinds
 };
 
@@ -316,6 +319,27 @@ int layer_norm_parts(int64_t rows, int sms);
 int launch_layer_norm_backward(int dtype, const void* x, int64_t x_row, const float* weight, const float* mean,
                                const float* rstd, const void* dy, int64_t dy_row, int64_t rows, int width, void* dx,
                                float* dweight, float* dbias, float* partial, int parts, cudaStream_t s);
+
+struct GatedArgs {
+    int dtype, batch, seqlen, channels;
+    const void *x, *r, *i;
+    int64_t x_batch, x_token, r_batch, r_token, i_batch, i_token;
+    const float* A;     // (channels)
+    const float* init;  // (batch, channels) or nullptr
+    const int* lengths;
+};
+struct GatedGrads {
+    const void* dy;       // dense
+    const float* dfinal;  // or nullptr
+    void *dx, *dr, *di;
+    float *dA, *dinit;  // dinit may be nullptr
+};
+// Floats of the states that the forward pass keeps for the gradient, and of the gradient's sums of parts.
+size_t gated_states_floats(const GatedArgs& g);
+size_t gated_sums_floats(const GatedArgs& g);
+int launch_gated_forward(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s);
+int launch_gated_backward(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s);
+int launch_gated_step(const GatedArgs& g, float* state, const int* slots, int nslots, void* y, int* err, cudaStream_t s);
 
 // Workspace, error words and device size, implemented in ssd_api.cu.
 int take_workspace(void** ptr, size_t bytes, cudaStream_t s);

@@ -94,6 +94,24 @@ int read_selective(int dtype, const void* x, const void* dt, const float* A, con
     return SSD_OK;
 }
 
+int read_gated(int dtype, const void* x, const void* r, const void* i, const float* A, const float* init, const int* lengths,
+               const ssd_gated_strides* given, int batch, int seqlen, int channels, bool step, GatedArgs* a) {
+    if (!x || !r || !i || !A || !known(dtype) || batch <= 0 || seqlen <= 0 || channels <= 0) return SSD_ERR_INVALID_ARG;
+    if (batch > kMaxBatch || seqlen > kMaxTokens || channels > kMaxChannels) return SSD_ERR_UNSUPPORTED;
+    const uintptr_t size = size_of(dtype);
+    if (!aligned_to(x, size) || !aligned_to(r, size) || !aligned_to(i, size) || !aligned_to(A, 4) || !aligned_to(init, 4) ||
+        !aligned_to(lengths, 4))
+        return SSD_ERR_INVALID_ARG;
+    const int64_t row = channels;
+    ssd_gated_strides s = {seqlen * row, row, seqlen * row, row, seqlen * row, row};
+    if (given != nullptr) s = *given;
+    if (step) s.x_token = s.r_token = s.i_token = 0;  // not read
+    for (long long v : {s.x_batch, s.x_token, s.r_batch, s.r_token, s.i_batch, s.i_token})
+        if (v < 0) return SSD_ERR_INVALID_ARG;
+    *a = GatedArgs{dtype, batch, seqlen, channels, x, r, i, s.x_batch, s.x_token, s.r_batch, s.r_token, s.i_batch, s.i_token, A, init, lengths};
+    return SSD_OK;
+}
+
 // Gives `ws` back to the pool in stream order; an error of the launches comes first.
 int give_back(void* ws, cudaStream_t s, int r) {
     if (ws != nullptr && cudaFreeAsync(ws, s) != cudaSuccess && r == SSD_OK) r = SSD_ERR_CUDA;
@@ -253,6 +271,50 @@ int ssd_layer_norm_backward(int dtype, const void* x, long long x_row_stride, co
     const int r = launch_layer_norm_backward(dtype, x, x_row_stride, weight, mean, rstd, dy, dy_row_stride, rows, width, dx,
                                              dweight, dbias, static_cast<float*>(ws), parts, stream);
     return give_back(ws, stream, r);
+}
+
+int ssd_gated_forward(int dtype, const void* x, const void* r, const void* i, const float* A, const float* init_state,
+                      const int* lengths, const ssd_gated_strides* strides, int batch, int seqlen, int channels, void* y,
+                      float* final_state, float* states, cudaStream_t stream) {
+    GatedArgs a;
+    const int e = read_gated(dtype, x, r, i, A, init_state, lengths, strides, batch, seqlen, channels, false, &a);
+    if (e != SSD_OK) return e;
+    if (!y || !aligned_to(y, size_of(dtype)) || !aligned_to(final_state, 4) || !aligned_to(states, 4)) return SSD_ERR_INVALID_ARG;
+    return launch_gated_forward(a, y, final_state, states, stream);
+}
+
+int ssd_gated_backward(int dtype, const void* x, const void* r, const void* i, const float* A, const float* init_state,
+                       const int* lengths, const ssd_gated_strides* strides, int batch, int seqlen, int channels,
+                       const float* states, const void* dy, const float* dfinal, void* dx, void* dr, void* di, float* dA,
+                       float* dinit, cudaStream_t stream) {
+    GatedArgs a;
+    int e = read_gated(dtype, x, r, i, A, init_state, lengths, strides, batch, seqlen, channels, false, &a);
+    if (e != SSD_OK) return e;
+    const uintptr_t size = size_of(dtype);
+    if (!dy || !dx || !dr || !di || !dA || !aligned_to(dy, size) || !aligned_to(dx, size) || !aligned_to(dr, size) ||
+        !aligned_to(di, size) || !aligned_to(dA, 4) || !aligned_to(dinit, 4) || !aligned_to(dfinal, 4) || !aligned_to(states, 4))
+        return SSD_ERR_INVALID_ARG;
+    const GatedGrads d = {dy, dfinal, dx, dr, di, dA, dinit};
+    const size_t sums = gated_sums_floats(a), own = states == nullptr ? gated_states_floats(a) : 0;
+    void* ws = nullptr;
+    if (take_workspace(&ws, (sums + own) * sizeof(float), stream) != SSD_OK) return SSD_ERR_NO_MEMORY;
+    float* f = static_cast<float*>(ws);
+    if (states == nullptr) e = launch_gated_forward(a, nullptr, nullptr, f + sums, stream);
+    if (e == SSD_OK) e = launch_gated_backward(a, d, states == nullptr ? f + sums : states, f, stream);
+    return give_back(ws, stream, e);
+}
+
+int ssd_gated_step(int dtype, const void* x, const void* r, const void* i, const float* A, float* state, const int* slots,
+                   int nslots, const ssd_gated_strides* strides, int batch, int channels, void* y, cudaStream_t stream) {
+    GatedArgs a;
+    const int e = read_gated(dtype, x, r, i, A, nullptr, nullptr, strides, batch, 1, channels, true, &a);
+    if (e != SSD_OK) return e;
+    if (!y || !aligned_to(y, size_of(dtype)) || !state || !aligned_to(state, 4) || !aligned_to(slots, 4) || nslots <= 0 ||
+        (slots == nullptr && nslots < batch))
+        return SSD_ERR_INVALID_ARG;
+    int* err = error_words();
+    if (err == nullptr) return SSD_ERR_CUDA;
+    return launch_gated_step(a, state, slots, nslots, y, err, stream);
 }
 
 }  // extern "C"

@@ -48,7 +48,8 @@ cudaEvent_t take_event() {
 const char* const kKindNames[kAllKinds] = {"chunk_cumsum", "chunk_state", "state_passing", "chunk_scan",
                                            "bc_to_f16", "step", "bwd_chunk", "bwd_reduce",
                                            "conv", "conv_bwd", "conv_step", "selective", "selective_bwd",
-                                           "selective_step", "layer_norm", "layer_norm_bwd"};
+                                           "selective_step", "layer_norm", "layer_norm_bwd",
+                                           "gated", "gated_bwd", "gated_step"};
 
 }  // namespace
 

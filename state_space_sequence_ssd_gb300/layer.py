@@ -152,3 +152,36 @@ def ssd_layer_norm_backward(x, weight, mean, rstd, dy, want_dbias=True, stream=N
         return _on(stream, _native.norm_backward, (x, weight, mean, rstd, dy, want_dbias),
                    (x, weight, mean, rstd, dy))
     return _native.norm_backward(x, weight, mean, rstd, dy, want_dbias)
+
+
+def ssd_gated_forward(x, r, i, A, init_state=None, lengths=None, want_final=True, want_states=False, stream=None):
+    """Gated linear recurrence h <- a h + sqrt(1 - a^2) sigmoid(i) x with a = exp(A sigmoid(r)) -> (y, final_state or
+    None, states or None).
+
+    x, r, i (batch, L, channels), A (channels,) f32 below zero, init_state (batch, channels) f32 or None; y is the state
+    after every token, in x's type.  states (batch, ceil(L / 64), channels) f32 are what ssd_gated_backward takes, the
+    state in front of every 64th token."""
+    if stream is not None:
+        return _on(stream, _native.gated_forward, (x, r, i, A, init_state, lengths, want_final, want_states),
+                   (x, r, i, A, init_state, lengths))
+    return _native.gated_forward(x, r, i, A, init_state, lengths, want_final, want_states)
+
+
+def ssd_gated_backward(x, r, i, A, dy, init_state=None, lengths=None, states=None, dfinal=None, want_dinit=False, stream=None):
+    """Gradients through ssd_gated_forward given dy (y's layout, dense) and dfinal ((batch, channels) f32 or None) ->
+    dict of dx, dr, di (batch, L, channels), dA (channels,) f32, dinit (batch, channels) f32 (None unless wanted).
+
+    states are those of the forward pass on the same inputs (init_state is not read then); None computes them again."""
+    if stream is not None:
+        return _on(stream, _native.gated_backward, (x, r, i, A, dy, init_state, lengths, states, dfinal, want_dinit),
+                   (x, r, i, A, dy, init_state, lengths, states, dfinal))
+    return _native.gated_backward(x, r, i, A, dy, init_state, lengths, states, dfinal, want_dinit)
+
+
+def ssd_gated_step(x, r, i, A, state, slots=None, stream=None):
+    """ssd_gated_forward for one token of every row -> y (batch, channels).
+
+    x, r, i (batch, channels); state (nslots, channels) f32 updated in place."""
+    if stream is not None:
+        return _on(stream, _native.gated_step, (x, r, i, A, state, slots), (x, r, i, A, state, slots))
+    return _native.gated_step(x, r, i, A, state, slots)
