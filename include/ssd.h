@@ -636,6 +636,57 @@ SSD_API int ssd_gated_step(int dtype, const void* x, const void* r, const void* 
                            cudaStream_t stream);
 
 /*
+ * The norm over groups of a token's channels (group norm, channels last) with its activation: the norm behind a scan.
+ * `width` channels are `groups` groups of neighbouring ones, each with its own statistics, of one row alone: a sequence
+ * model's norm may not look ahead.  With s(v) = v * sigmoid(v):
+ *     q    = x * s(z)  with SSD_GATE_BEFORE, else x
+ *     n    = (q - mean) * rstd * weight + bias,  rstd = 1 / sqrt(mean((q - mean)^2) + eps) over the group
+ *     y    = s(n) with SSD_GATE_SILU, n * s(z) with SSD_GATE_AFTER, else n
+ * rms leaves the mean out (it is taken as 0).
+ */
+typedef enum ssd_gate { SSD_GATE_NONE = 0, SSD_GATE_SILU = 1, SSD_GATE_AFTER = 2, SSD_GATE_BEFORE = 3 } ssd_gate;
+
+/*
+ * ssd_group_norm_forward
+ *   x, z         (rows, width) at row strides in elements; z exactly with SSD_GATE_AFTER and SSD_GATE_BEFORE
+ *   weight, bias (width) f32, NULL for ones and zeros; y (rows, width) dense
+ *   mean, rstd   (rows, groups) f32, NULL where they are not wanted (mean: NULL with rms)
+ * groups divides width and is at most 65535.
+ */
+SSD_API int ssd_group_norm_forward(int dtype, const void* x, long long x_row_stride, const void* z, long long z_row_stride,
+                                   const float* weight, const float* bias, float eps, int gate, int rms, long long rows,
+                                   int width, int groups, void* y, float* mean, float* rstd, cudaStream_t stream);
+
+/*
+ * ssd_group_norm_backward -- dx and, with z, dz (both dense), and dweight and dbias ((width) f32, or NULL) summed over the
+ * rows, from dy, the inputs and the forward pass's mean (NULL: rms) and rstd.
+ */
+SSD_API int ssd_group_norm_backward(int dtype, const void* x, long long x_row_stride, const void* z, long long z_row_stride,
+                                    const float* weight, const float* bias, int gate, const float* mean, const float* rstd,
+                                    const void* dy, long long dy_row_stride, long long rows, int width, int groups, void* dx,
+                                    void* dz, float* dweight, float* dbias, cudaStream_t stream);
+
+/*
+ * ssd_rotary -- rotary positions on one or two tensors of heads: a scan's B and C (C_t . B_s then turns with s - t, so that the
+ * scan's real decay exp(dt A) becomes the complex exp(dt A + i frequency)), or queries and keys.  Pair k of a head's
+ * first `turned` entries is (2 k, 2 k + 1) if interleaved, else (k, k + turned / 2):
+ *     (a, b) -> scale * (a cos w - b sin w, a sin w + b cos w),  w = position * frequency[k]
+ * and the other entries are copied.  inverse turns back (w -> -w): the gradient, as the turn is orthogonal.
+ *   x0, x1       (batch, seqlen, heads, dim), dense within a token, at the given strides; x1 NULL with heads1 = 0
+ *   table        (turned / 2): frequency[k] / (2 pi) in units of 2^-64, rounded (modulo 2^64), so that the product with a
+ *                position loses nothing but whole turns
+ *   positions    NULL: token t is at position t; (batch) int32: at positions[b] + t; with positions_each (batch,
+ *                seqlen) int32: at positions[b,t].  Negative positions turn the other way
+ *   y0, y1       dense, of the same type; tokens past a row's length are zero
+ * float32 tensors take accurate sines; those of 16 bits the special function unit's (absolute error below 2^-19).
+ */
+SSD_API int ssd_rotary(int dtype, const void* x0, long long x0_batch_stride, long long x0_token_stride, int heads0,
+                       const void* x1, long long x1_batch_stride, long long x1_token_stride, int heads1,
+                       const unsigned long long* table, int turned, const int* positions, int positions_each,
+                       const int* lengths, float scale, int interleaved, int inverse, int batch, int seqlen, int dim, void* y0,
+                       void* y1, cudaStream_t stream);
+
+/*
  * ssd_get_device_error -- reads and clears the library's device error words
  * on the current device (synchronizes with the device).  Returns SSD_OK;
  * SSD_ERR_TIMEOUT if a kernel's bounded wait gave up since the last read

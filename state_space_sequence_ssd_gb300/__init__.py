@@ -21,14 +21,17 @@ from __future__ import annotations
 
 from . import _ffi
 from .layer import (ssd_conv_backward, ssd_conv_forward, ssd_conv_step, ssd_gated_backward, ssd_gated_forward, ssd_gated_step,
-                    ssd_layer_norm_backward, ssd_layer_norm_forward, ssd_selective_backward, ssd_selective_forward, ssd_selective_step)
+                    ssd_group_norm_backward, ssd_group_norm_forward, ssd_layer_norm_backward, ssd_layer_norm_forward, ssd_rotary_backward,
+                    ssd_rotary_forward, ssd_rotary_step, ssd_rotary_table, ssd_selective_backward, ssd_selective_forward, ssd_selective_step)
 
 __all__ = ["ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan", "ssd_forward",
            "ssd_forward_noalloc", "ssd_forward_heads", "ssd_partition_heads", "ssd_forward_plan", "ssd_step",
            "ssd_step_multi", "ssd_forward_ex", "ssd_step_ex", "ssd_backward", "ssd_get_device_error", "SSDError", "library_path",
            "ssd_conv_forward", "ssd_conv_backward", "ssd_conv_step", "ssd_selective_forward", "ssd_selective_backward",
            "ssd_selective_step", "ssd_layer_norm_forward", "ssd_layer_norm_backward",
-           "ssd_gated_forward", "ssd_gated_backward", "ssd_gated_step"]
+           "ssd_gated_forward", "ssd_gated_backward", "ssd_gated_step",
+           "ssd_group_norm_forward", "ssd_group_norm_backward",
+           "ssd_rotary_table", "ssd_rotary_forward", "ssd_rotary_backward", "ssd_rotary_step"]
 
 SSDError = _ffi.SSDError
 library_path = _ffi.LIB_PATH

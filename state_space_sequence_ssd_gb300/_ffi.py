@@ -54,6 +54,9 @@ SIGNATURES = {
     "ssd_gated_forward": (_i, [_i] + [_p] * 7 + [_i] * 3 + [_p] * 4),
     "ssd_gated_backward": (_i, [_i] + [_p] * 7 + [_i] * 3 + [_p] * 9),
     "ssd_gated_step": (_i, [_i] + [_p] * 6 + [_i, _p] + [_i] * 2 + [_p] * 2),
+    "ssd_group_norm_forward": (_i, [_i, _p, _l, _p, _l, _p, _p, ctypes.c_float, _i, _i, _l, _i, _i] + [_p] * 4),
+    "ssd_group_norm_backward": (_i, [_i, _p, _l, _p, _l, _p, _p, _i, _p, _p, _p, _l, _l, _i, _i] + [_p] * 5),
+    "ssd_rotary": (_i, [_i] + [_p, _l, _l, _i] * 2 + [_p, _i, _p, _i, _p, ctypes.c_float] + [_i] * 5 + [_p] * 3),
     "ssd_get_device_error": (_i, []),
     "ssd_debug_set_wait_limit_ns": (_i, [ctypes.c_ulonglong]),
     "ssd_debug_stall": (_i, [_i]),

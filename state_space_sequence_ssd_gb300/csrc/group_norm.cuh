@@ -1,0 +1,441 @@
+// group_norm.cuh -- the norm over groups of a token's channels with its activation, and its gradient; compiled once per element
+// type by k_group_norm_{bf16,f16,f32}.cu.
+//
+//   q    = x silu(z)  where the gate comes first, else x
+//   xhat = (q - mean) rstd (the mean left out where rms),   n = xhat weight + bias
+//   y    = n, silu(n), or n silu(z) where the gate comes last
+//   backward, with g the gradient of n (dy, through the activation), gw = g weight:
+//   dq = rstd (gw - mean(gw) - xhat mean(gw xhat)),  dweight = sum g xhat,  dbias = sum g
+//   dx = dq (through silu(z) where it comes first), dz = dy n silu'(z) or dq x silu'(z)
+//
+// A unit is one group of one row.  `lanes` threads (a power of two, at most a block's) share it and hold it in registers, so that
+// everything is read once: up to 32 lanes, as for a group per head, the sums take shuffles alone.  Bound by HBM.
+#pragma once
+
+#include "norm.cuh"
+
+namespace ssd {
+namespace {
+
+// silu(v) = v sigmoid(v) and its slope
+__device__ __forceinline__ f32x2 slope_of(f32x2 v, f32x2 sig) {
+    const f32x2 one = pk(1.f, 1.f);
+    return mul2(sig, fma2(v, fma2(sig, pk(-1.f, -1.f), one), one));
+}
+
+// Row and group of unit u (units that fit 32 bits, as all but the longest do, are divided there).
+__device__ __forceinline__ void unit_of(int64_t u, int groups, int64_t& row, int& group) {
+    if (u <= 0xffffffffll) {
+        row = (uint32_t)u / (uint32_t)groups;
+        group = (int)((uint32_t)u - (uint32_t)row * (uint32_t)groups);
+    } else {
+        row = u / groups;
+        group = (int)(u - row * groups);
+    }
+}
+
+// Thread `lane` of a unit holds columns (lane + lanes i) V .. of its group.
+template <typename T, int V, int NV, int GATE>
+__global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g, int lanes, T* __restrict__ y, float* __restrict__ mean,
+                                                                 float* __restrict__ rstd, bool vecw) {
+    constexpr int P = (V + 1) / 2;
+    __shared__ float2 buf[2][kThreads / 32];
+    const int lane = threadIdx.x & (lanes - 1), per = g.width / g.groups;
+    const int64_t unit = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+    const bool live = unit < g.rows * g.groups;
+    int64_t row = 0;
+    int group = 0;
+    if (live) unit_of(unit, g.groups, row, group);
+    const int base = group * per;
+    const T* x = static_cast<const T*>(g.x) + row * g.x_row + base;
+    const T* z = static_cast<const T*>(g.z) + (GATE >= kGateAfter ? row * g.z_row + base : 0);
+    Vec<T, V> rx[NV], rz[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + lanes * i) * V;
+        rx[i] = load_vec<T, V>(x + c, live ? per - c : 0, true);
+        if (GATE >= kGateAfter) rz[i] = load_vec<T, V>(z + c, live ? per - c : 0, true);
+    }
+    f32x2 q[NV][P], s2 = 0ull, v2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            q[i][e] = rx[i].pair(e);
+            if (GATE == kGateBefore) {
+                const f32x2 zz = rz[i].pair(e);
+                q[i][e] = mul2(q[i][e], mul2(zz, sigmoid2(zz)));
+            }
+            s2 = add2(s2, q[i][e]);
+        }
+    const float inv = 1.f / (float)per;
+    const float m = g.rms ? 0.f : row_sum(sum2(s2), lanes, buf[0]) * inv;
+    const f32x2 m2 = pk(-m, V > 1 ? -m : 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((lane + lanes * i) * V < per) {
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                q[i][e] = add2(q[i][e], m2);
+                v2 = fma2(q[i][e], q[i][e], v2);
+            }
+        }
+    const float rs = rsqrtf(fmaf(row_sum(sum2(v2), lanes, buf[1]), inv, g.eps));
+    if (!live) return;
+    if (lane == 0) {
+        if (mean != nullptr) mean[unit] = m;
+        if (rstd != nullptr) rstd[unit] = rs;
+    }
+    T* o = y + row * g.width + base;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + lanes * i) * V;
+        if (c >= per) break;
+        f32x2 w[P], b[P], out[P];
+        load_columns<V>(g.weight == nullptr ? nullptr : g.weight + base, c, per, vecw, 1.f, w);
+        load_columns<V>(g.bias == nullptr ? nullptr : g.bias + base, c, per, vecw, 0.f, b);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            out[e] = fma2(mul2(q[i][e], pk(rs, rs)), w[e], b[e]);
+            if (GATE == kGateSilu) out[e] = mul2(out[e], sigmoid2(out[e]));
+            if (GATE == kGateAfter) {
+                const f32x2 zz = rz[i].pair(e);
+                out[e] = mul2(out[e], mul2(zz, sigmoid2(zz)));
+            }
+        }
+        store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), per - c, true);
+    }
+}
+
+// One value of q from memory.
+template <typename T>
+__device__ __forceinline__ float gated_value(const GroupNormArgs& g, int64_t row, int c) {
+    const float x = to_f32<T>(static_cast<const T*>(g.x)[row * g.x_row + c]);
+    if (g.gate != kGateBefore) return x;
+    const float z = to_f32<T>(static_cast<const T*>(g.z)[row * g.z_row + c]);
+    return x * (z * sigmoid(z));
+}
+
+// Groups that do not fit the registers, a block each: read again (from L2) for each sum and the output.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) group_forward_wide_kernel(GroupNormArgs g, T* __restrict__ y, float* __restrict__ mean,
+                                                                      float* __restrict__ rstd) {
+    __shared__ float2 buf[2][kThreads / 32];
+    const int per = g.width / g.groups;
+    int64_t row;
+    int group;
+    unit_of(blockIdx.x, g.groups, row, group);
+    const int base = group * per;
+    const float inv = 1.f / (float)per;
+    float s = 0.f, q = 0.f;
+    if (!g.rms) {
+#pragma unroll 4
+        for (int c = threadIdx.x; c < per; c += kThreads) s += gated_value<T>(g, row, base + c);
+    }
+    const float m = g.rms ? 0.f : row_sum(s, kThreads, buf[0]) * inv;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < per; c += kThreads) {
+        const float d = gated_value<T>(g, row, base + c) - m;
+        q = fmaf(d, d, q);
+    }
+    const float rs = rsqrtf(fmaf(row_sum(q, kThreads, buf[1]), inv, g.eps));
+    if (threadIdx.x == 0) {
+        if (mean != nullptr) mean[blockIdx.x] = m;
+        if (rstd != nullptr) rstd[blockIdx.x] = rs;
+    }
+#pragma unroll 4
+    for (int c = threadIdx.x; c < per; c += kThreads) {
+        float n = fmaf((gated_value<T>(g, row, base + c) - m) * rs, g.weight != nullptr ? g.weight[base + c] : 1.f, g.bias != nullptr ? g.bias[base + c] : 0.f);
+        if (g.gate == kGateSilu) n *= sigmoid(n);
+        if (g.gate == kGateAfter) {
+            const float z = to_f32<T>(static_cast<const T*>(g.z)[row * g.z_row + base + c]);
+            n *= z * sigmoid(z);
+        }
+        y[row * g.width + base + c] = from_f32<T>(n);
+    }
+}
+
+// A block holds `side` groups of a row next to one another and kThreads / lanes / side rows at once, and walks the rows a grid's
+// height apart; its columns' sums stay in registers, and the next rows' loads are in flight while a row is summed.
+template <typename T, int V, int NV, int GATE>
+__global__ void __launch_bounds__(kThreads) group_backward_kernel(GroupNormArgs g, int lanes, int side, const float* __restrict__ mean,
+                                                                  const float* __restrict__ rstd, const T* __restrict__ dy, int64_t dy_row,
+                                                                  T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ partial, bool vecw) {
+    constexpr int P = (V + 1) / 2;
+    constexpr bool Z = GATE >= kGateAfter;
+    extern __shared__ float sums[];  // rows at once x 2 x the block's columns
+    __shared__ float2 buf[2][kThreads / 32];
+    const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x / lanes, high = kThreads / lanes / side;
+    const int per = g.width / g.groups, group = blockIdx.x * side + sub % side, base = group * per;
+    const bool here = group < g.groups;
+    const float inv = 1.f / (float)per;
+    f32x2 w[NV][P], b[NV][P], dw[NV][P], db[NV][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + lanes * i) * V;
+        load_columns<V>(g.weight == nullptr ? nullptr : g.weight + (here ? base : 0), c, per, vecw, 1.f, w[i]);
+        if (GATE == kGateSilu || GATE == kGateAfter) load_columns<V>(g.bias == nullptr ? nullptr : g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
+#pragma unroll
+        for (int e = 0; e < P; ++e) dw[i][e] = db[i][e] = 0ull;
+    }
+    Vec<T, V> nx[NV], ng[NV], nz[NV];
+    float nm, nrs;
+    auto fetch = [&](int64_t row) {
+        const bool live = here && row < g.rows;
+        const int64_t at = live ? row : 0, off = live ? base : 0;
+        nm = live && mean != nullptr ? __ldg(mean + at * g.groups + group) : 0.f;
+        nrs = live ? __ldg(rstd + at * g.groups + group) : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + lanes * i) * V, left = live ? per - c : 0;
+            nx[i] = load_vec<T, V>(static_cast<const T*>(g.x) + at * g.x_row + off + c, left, true);
+            ng[i] = load_vec<T, V>(dy + at * dy_row + off + c, left, true);
+            if (Z) nz[i] = load_vec<T, V>(static_cast<const T*>(g.z) + at * g.z_row + off + c, left, true);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.y * high;
+    int64_t row = (int64_t)blockIdx.y * high + sub / side;
+    fetch(row);
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.y * high; r0 < g.rows; r0 += step, row += step, turn ^= 1) {
+        Vec<T, V> cx[NV], cg[NV], cz[NV];
+        const float rs = nrs;
+        const f32x2 rs2 = pk(rs, rs), shift = pk(-nm * rs, -nm * rs);
+        f32x2 s1 = 0ull, s2 = 0ull;
+        f32x2 sig[NV][P], gn[NV][P];  // sigmoid of the gate; the gradient of n
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            cx[i] = nx[i];
+            cg[i] = ng[i];
+            if (Z) cz[i] = nz[i];
+        }
+        if (r0 + step < g.rows) fetch(row + step);
+        auto xhat = [&](int i, int e) {
+            f32x2 q = cx[i].pair(e);
+            if (GATE == kGateBefore) q = mul2(q, mul2(cz[i].pair(e), sig[i][e]));
+            return fma2(q, rs2, shift);
+        };
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                if (Z) sig[i][e] = sigmoid2(cz[i].pair(e));
+                const f32x2 xh = xhat(i, e);
+                f32x2 gy = cg[i].pair(e);  // zero past the group's end
+                if (GATE == kGateSilu) {
+                    const f32x2 n = fma2(xh, w[i][e], b[i][e]);
+                    gy = mul2(gy, slope_of(n, sigmoid2(n)));
+                }
+                if (GATE == kGateAfter) gy = mul2(gy, mul2(cz[i].pair(e), sig[i][e]));
+                gn[i][e] = gy;
+                const f32x2 gw = mul2(gy, w[i][e]);
+                db[i][e] = add2(db[i][e], gy);
+                dw[i][e] = fma2(gy, xh, dw[i][e]);
+                s1 = add2(s1, gw);
+                s2 = fma2(gw, xh, s2);
+            }
+        const float2 s = row_sums(make_float2(sum2(s1), sum2(s2)), lanes, buf[turn]);
+        if (!here || row >= g.rows) continue;
+        const float k1 = g.rms ? 0.f : -s.x * inv * rs, k2 = -s.y * inv * rs;
+        T *ox = dx + row * g.width + base, *oz = Z ? dz + row * g.width + base : nullptr;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + lanes * i) * V;
+            if (c >= per) break;
+            f32x2 o1[P], o2[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const f32x2 xh = xhat(i, e), gw = mul2(gn[i][e], w[i][e]);
+                const f32x2 dq = fma2(gw, rs2, fma2(xh, pk(k2, k2), pk(k1, k1)));
+                o1[e] = dq;
+                if (GATE == kGateBefore) {
+                    const f32x2 zz = cz[i].pair(e);
+                    o1[e] = mul2(dq, mul2(zz, sig[i][e]));
+                    o2[e] = mul2(mul2(dq, cx[i].pair(e)), slope_of(zz, sig[i][e]));
+                }
+                if (GATE == kGateAfter) o2[e] = mul2(mul2(cg[i].pair(e), fma2(xh, w[i][e], b[i][e])), slope_of(cz[i].pair(e), sig[i][e]));
+            }
+            store_vec<T, V>(ox + c, Vec<T, V>::of_pairs(o1), per - c, true);
+            if (Z) store_vec<T, V>(oz + c, Vec<T, V>::of_pairs(o2), per - c, true);
+        }
+    }
+    if (partial == nullptr) return;
+    // the block's columns, one sum for all rows at once
+    const int columns = side * per, first = blockIdx.x * columns;
+    float* out = partial + (int64_t)blockIdx.y * 2 * g.width;
+    float* to = sums + (sub / side) * 2 * columns + (sub % side) * per;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int c = (lane + lanes * i) * V + e;
+            float p, q;
+            unpk(dw[i][e / 2], p, q);
+            const float a = e & 1 ? q : p;
+            unpk(db[i][e / 2], p, q);
+            const float d = e & 1 ? q : p;
+            if (c >= per || !here) continue;
+            if (high == 1) {
+                out[base + c] = a;
+                out[g.width + base + c] = d;
+            } else {
+                to[c] = a;
+                to[columns + c] = d;
+            }
+        }
+    if (high == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < columns; c += kThreads) {
+        if (first + c >= g.width) continue;
+        float p = 0.f, q = 0.f;
+        for (int k = 0; k < high; ++k) {
+            p += sums[k * 2 * columns + c];
+            q += sums[k * 2 * columns + columns + c];
+        }
+        out[first + c] = p;
+        out[g.width + first + c] = q;
+    }
+}
+
+// Groups wider than the registers hold: a block per row and group at a time, x, z and dy read twice (the second time from L2), the
+// columns' sums kept in the block's row of `partial`.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) group_backward_wide_kernel(GroupNormArgs g, const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                                       const T* __restrict__ dy, int64_t dy_row, T* __restrict__ dx,
+                                                                       T* __restrict__ dz, float* __restrict__ partial) {
+    __shared__ float2 buf[2][kThreads / 32];
+    const int per = g.width / g.groups, base = blockIdx.x * per;
+    const float inv = 1.f / (float)per;
+    int turn = 0;
+    float* sum = partial == nullptr ? nullptr : partial + (int64_t)blockIdx.y * 2 * g.width;
+    for (int64_t row = blockIdx.y; row < g.rows; row += gridDim.y) {
+        const float m = mean != nullptr ? mean[row * g.groups + blockIdx.x] : 0.f, rs = rstd[row * g.groups + blockIdx.x];
+        float n, z, sig;
+        auto parts = [&](int c, float& xh, float& gy) {
+            xh = (gated_value<T>(g, row, c) - m) * rs;
+            gy = to_f32<T>(dy[row * dy_row + c]);
+            n = fmaf(xh, g.weight != nullptr ? g.weight[c] : 1.f, g.bias != nullptr ? g.bias[c] : 0.f);
+            if (g.gate == kGateSilu) {
+                const float s = sigmoid(n);
+                gy *= s * fmaf(n, 1.f - s, 1.f);
+            }
+            if (g.gate >= kGateAfter) {
+                z = to_f32<T>(static_cast<const T*>(g.z)[row * g.z_row + c]);
+                sig = sigmoid(z);
+            }
+            if (g.gate == kGateAfter) gy *= z * sig;
+        };
+        float2 s = make_float2(0.f, 0.f);
+        for (int c = base + threadIdx.x; c < base + per; c += kThreads) {
+            float xh, gy;
+            parts(c, xh, gy);
+            const float gw = gy * (g.weight != nullptr ? g.weight[c] : 1.f);
+            if (sum != nullptr) {
+                const bool first = row == blockIdx.y;
+                sum[c] = first ? gy * xh : fmaf(gy, xh, sum[c]);
+                sum[g.width + c] = first ? gy : sum[g.width + c] + gy;
+            }
+            s.x += gw;
+            s.y = fmaf(gw, xh, s.y);
+        }
+        s = row_sums(s, kThreads, buf[turn]);
+        turn ^= 1;
+        const float s1 = g.rms ? 0.f : s.x * inv, s2 = s.y * inv;
+        for (int c = base + threadIdx.x; c < base + per; c += kThreads) {
+            float xh, gy;
+            parts(c, xh, gy);
+            const float gw = gy * (g.weight != nullptr ? g.weight[c] : 1.f);
+            float dq = rs * (gw - s1 - xh * s2);
+            const int64_t at = row * g.width + c;
+            if (g.gate >= kGateAfter) {
+                const float slope = sig * fmaf(z, 1.f - sig, 1.f);
+                const float other = g.gate == kGateAfter ? to_f32<T>(dy[row * dy_row + c]) * n : dq * to_f32<T>(static_cast<const T*>(g.x)[row * g.x_row + c]);
+                dz[at] = from_f32<T>(other * slope);
+                if (g.gate == kGateBefore) dq *= z * sig;
+            }
+            dx[at] = from_f32<T>(dq);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launches
+
+// Whether rows and groups are whole 16-byte vectors.
+template <typename T>
+bool in_vectors(const GroupNormArgs& g) {
+    constexpr int V = 16 / sizeof(T);
+    return g.width / g.groups % V == 0 && g.x_row % V == 0 && (g.z == nullptr || g.z_row % V == 0) && aligned_to(g.x, 16) && aligned_to(g.z, 16);
+}
+
+template <typename T, int V, int GATE>
+int group_forward_of(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s) {
+    constexpr int M = V == 1 ? 4 : 1;
+    const int64_t units = g.rows * g.groups;
+    const int vecs = ceil_div(g.width / g.groups, V), lanes = row_lanes(units, vecs, 2 * M, 1), nv = ceil_div(vecs, lanes);
+    const int64_t blocks = ceil_div64(units, kThreads / lanes);
+    const bool vecw = aligned_to(g.weight, 16) && aligned_to(g.bias, 16);
+    if (blocks > 2147483647) return SSD_ERR_UNSUPPORTED;
+    launch_begin(kKindGroupNorm, s);
+    auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, kThreads, 0, s>>>(g, lanes, static_cast<T*>(y), mean, rstd, vecw); };
+    if (nv <= 1 * M) go(group_forward_kernel<T, V, 1 * M, GATE>);
+    else if (nv <= 2 * M) go(group_forward_kernel<T, V, 2 * M, GATE>);
+    else if (nv <= 4 * M) go(group_forward_kernel<T, V, 4 * M, GATE>);
+    else group_forward_wide_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(g, static_cast<T*>(y), mean, rstd);
+    return launch_end(kKindGroupNorm, s);
+}
+
+template <typename T, int V, int GATE>
+int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
+    constexpr int M = V == 1 ? 4 : 1;
+    const int vecs = ceil_div(g.width / g.groups, V), lanes = row_lanes(g.rows * g.groups, vecs, 2 * M, 1), nv = ceil_div(vecs, lanes);
+    const int room = kThreads / lanes;
+    int side = 1;
+    while (side < room && side < g.groups) side *= 2;
+    const int high = room / side, smem = high == 1 || partial == nullptr ? 0 : high * 2 * side * (g.width / g.groups) * 4;
+    const bool vecw = aligned_to(g.weight, 16) && aligned_to(g.bias, 16);
+    const T* dy = static_cast<const T*>(d.dy);
+    T *dx = static_cast<T*>(d.dx), *dz = static_cast<T*>(d.dz);
+    launch_begin(kKindGroupNormBwd, s);
+    int r = SSD_OK;
+    auto go = [&](auto kernel) {
+        if (smem > 48 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 227 * 1024);
+        if (r == SSD_OK)
+            kernel<<<dim3(ceil_div(g.groups, side), parts), kThreads, smem, s>>>(g, lanes, side, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial, vecw);
+    };
+    if (nv <= 1 * M) go(group_backward_kernel<T, V, 1 * M, GATE>);
+    else if (nv <= 2 * M) go(group_backward_kernel<T, V, 2 * M, GATE>);
+    else
+        group_backward_wide_kernel<T><<<dim3(g.groups, parts), kThreads, 0, s>>>(g, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial);
+    const int e = launch_end(kKindGroupNormBwd, s);
+    return r != SSD_OK ? r : e;
+}
+
+template <typename T, int V>
+int group_forward_gate(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s) {
+    if (g.gate == kGateSilu) return group_forward_of<T, V, kGateSilu>(g, y, mean, rstd, s);
+    if (g.gate == kGateAfter) return group_forward_of<T, V, kGateAfter>(g, y, mean, rstd, s);
+    if (g.gate == kGateBefore) return group_forward_of<T, V, kGateBefore>(g, y, mean, rstd, s);
+    return group_forward_of<T, V, kGateNone>(g, y, mean, rstd, s);
+}
+template <typename T, int V>
+int group_backward_gate(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
+    if (g.gate == kGateSilu) return group_backward_of<T, V, kGateSilu>(g, d, partial, parts, s);
+    if (g.gate == kGateAfter) return group_backward_of<T, V, kGateAfter>(g, d, partial, parts, s);
+    if (g.gate == kGateBefore) return group_backward_of<T, V, kGateBefore>(g, d, partial, parts, s);
+    return group_backward_of<T, V, kGateNone>(g, d, partial, parts, s);
+}
+
+template <typename T>
+int group_forward_type(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s) {
+    if (in_vectors<T>(g) && aligned_to(y, 16)) return group_forward_gate<T, 16 / sizeof(T)>(g, y, mean, rstd, s);
+    return group_forward_gate<T, 1>(g, y, mean, rstd, s);
+}
+template <typename T>
+int group_backward_type(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
+    if (in_vectors<T>(g) && d.dy_row % (16 / sizeof(T)) == 0 && aligned_to(d.dy, 16) && aligned_to(d.dx, 16) && aligned_to(d.dz, 16))
+        return group_backward_gate<T, 16 / sizeof(T)>(g, d, partial, parts, s);
+    return group_backward_gate<T, 1>(g, d, partial, parts, s);
+}
+
+}  // namespace
+}  // namespace ssd

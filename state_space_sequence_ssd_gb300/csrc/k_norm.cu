@@ -9,63 +9,10 @@
 // block's; narrow rows share a block.  The backward kernel's blocks each walk rows a grid's width apart and
 // hold the columns' sums of their threads in registers; a block writes one row of partial sums and a second
 // kernel adds the blocks' rows in a fixed order.  All sums are float32; y and dx are rounded once.
-#include "ops.cuh"
+#include "norm.cuh"
 
 namespace ssd {
 namespace {
-
-constexpr int kThreads = 256;
-
-// Sums of two values over the `lanes` threads of one row (a power of two; at most kThreads).  Every thread of the
-// block calls it.  buf holds a pair per warp; calls that follow one another alternate between two of them, so that
-// one barrier a call is enough.
-__device__ __forceinline__ float2 row_sums(float2 v, int lanes, float2* buf) {
-    if (lanes >= 32) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        }
-    } else {
-        for (int o = lanes / 2; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        }
-    }
-    if (lanes <= 32) return v;
-    const int warp = threadIdx.x >> 5, per = lanes >> 5;
-    if ((threadIdx.x & 31) == 0) buf[warp] = v;
-    __syncthreads();
-    v = make_float2(0.f, 0.f);
-    for (int i = 0; i < per; ++i) {
-        const float2 q = buf[(warp / per) * per + i];
-        v.x += q.x;
-        v.y += q.y;
-    }
-    return v;
-}
-__device__ __forceinline__ float row_sum(float v, int lanes, float2* buf) { return row_sums(make_float2(v, 0.f), lanes, buf).x; }
-
-// V columns of a float32 row from column c on, as pairs (a null row: `otherwise`).  `vec`: 16-byte aligned groups of four.
-template <int V>
-__device__ __forceinline__ void load_columns(const float* p, int c, int width, bool vec, float otherwise,
-                                             f32x2 (&o)[(V + 1) / 2]) {
-    if (p == nullptr) {
-#pragma unroll
-        for (int e = 0; e < (V + 1) / 2; ++e) o[e] = pk(otherwise, otherwise);
-    } else if (V >= 4 && vec) {
-#pragma unroll
-        for (int e = 0; e + 3 < V; e += 4) {
-            const float4 q = c < width ? __ldg(reinterpret_cast<const float4*>(p + c + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            o[e / 2] = pk(q.x, q.y);
-            o[(e / 2 + 1) % ((V + 1) / 2)] = pk(q.z, q.w);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; e += 2)
-            o[e / 2] = pk(c + e < width ? __ldg(p + c + e) : 0.f, e + 1 < V && c + e + 1 < width ? __ldg(p + c + e + 1) : 0.f);
-    }
-}
 
 // NV vectors of V columns per thread: thread `lane` holds columns (lane + lanes i) V ..  A block takes its rows and ends.
 template <typename T, int V, int NV>
@@ -439,15 +386,6 @@ __global__ void __launch_bounds__(32 * kJoin) norm_reduce_kernel(const float* pa
     }
 }
 
-// Threads that share a row of `vecs` vectors, a power of two: enough that a thread holds at most `most` vectors, more
-// (down to one each) while the rows alone leave the SMs with less than about 1024 threads.
-int row_lanes(int64_t rows, int vecs, int most, int least) {
-    int lanes = least;
-    while (lanes < kThreads && (int64_t)lanes * most < vecs) lanes *= 2;
-    while (lanes < kThreads && lanes < vecs && rows * lanes < kSms * 1024) lanes *= 2;
-    return lanes;
-}
-
 template <typename T, int V>
 int forward_of(const void* x, int64_t x_row, const float* weight, const float* bias, float eps, int64_t rows, int width,
                void* y, float* mean, float* rstd, cudaStream_t s) {
@@ -548,6 +486,12 @@ int layer_norm_parts(int64_t rows, int sms) {
     return (int)(want < 2 * sms ? want : 2 * sms);
 }
 
+int launch_norm_sums(int kind, const float* partial, int parts, int width, float* dweight, float* dbias, cudaStream_t s) {
+    launch_begin(kind, s);
+    launch_dependent(norm_reduce_kernel, dim3(ceil_div(2 * width, 32)), dim3(32 * kJoin), 0, s, partial, parts, width, dweight, dbias);
+    return launch_end(kind, s);
+}
+
 int launch_layer_norm_backward(int dtype, const void* x, int64_t x_row, const float* weight, const float* mean,
                                const float* rstd, const void* dy, int64_t dy_row, int64_t rows, int width, void* dx,
                                float* dweight, float* dbias, float* partial, int parts, cudaStream_t s) {
@@ -559,9 +503,7 @@ int launch_layer_norm_backward(int dtype, const void* x, int64_t x_row, const fl
     else
         r = backward_type<float>(x, x_row, weight, mean, rstd, dy, dy_row, rows, width, dx, partial, parts, s);
     if (r != SSD_OK || partial == nullptr) return r;
-    launch_begin(kKindNormBwd, s);
-    launch_dependent(norm_reduce_kernel, dim3(ceil_div(2 * width, 32)), dim3(32 * kJoin), 0, s, partial, parts, width, dweight, dbias);
-    return launch_end(kKindNormBwd, s);
+    return launch_norm_sums(kKindNormBwd, partial, parts, width, dweight, dbias, s);
 }
 
 }  // namespace ssd

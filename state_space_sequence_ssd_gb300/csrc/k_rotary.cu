@@ -1,0 +1,137 @@
+// k_rotary.cu -- rotary positions: pairs of a head's entries turned by an angle that grows with the token's position.
+//
+//   (a, b) -> scale (a cos - b sin, a sin + b cos),   angle = position * frequency[pair]
+//
+// The table holds each pair's frequency as the part of a turn that one position adds, in units of 2^-64: the product with a position,
+// taken modulo 2^64, is the angle with its whole turns gone, exactly, at any position and without a float64 operation.  Its
+// upper 32 bits are the angle to 2^-32 of a turn.
+// Bound by HBM: every entry is read and written once.  A thread turns the same pairs of up to four heads, so that they share the
+// sine and cosine; the two tensors' heads (a scan's B and C) go side by side in one launch.
+#include "ops.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kRotaryThreads = 256;
+
+// cos and sin of `turns`, the signed fraction of a turn in units of 2^-32.  float32 tensors take the accurate functions, the others
+// the special function unit's, whose absolute error on [-pi, pi] of 2^-20 is far below half a step of their type (2^-11 and more).
+template <typename T>
+__device__ __forceinline__ void cos_sin(int turns, float& c, float& s) {
+    if constexpr (sizeof(T) == 4) {
+        sincospif((float)turns * 0x1p-31f, &s, &c);
+    } else {
+        const float v = (float)turns * (6.283185307179586f * 0x1p-32f);
+        asm("sin.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(v));
+        asm("cos.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(v));
+    }
+}
+
+// V: entries of a vector.  HALF: pairs (k, k + turned / 2), a thread holding V pairs of a head in two vectors; else (2 k, 2 k + 1), V / 2
+// pairs in one.  H: heads a thread.  `chunks` vectors (or pairs of vectors) a head, `blocks` groups of H heads.
+template <typename T, int V, bool HALF, int H>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(RotaryArgs g, int chunks, int blocks, int tokens, bool vec) {
+    constexpr int NP = HALF ? V : V / 2;
+    const int per = chunks * blocks, b = blockIdx.y;
+    const int share = per < kRotaryThreads ? per : kRotaryThreads;  // threads of a token
+    const int t = blockIdx.x * tokens + threadIdx.x / share;
+    if ((int)threadIdx.x >= tokens * share || t >= g.seqlen) return;
+    const bool live = t < row_length(g.lengths, b, g.seqlen);
+    int64_t position = t;
+    if (g.positions != nullptr) position = g.each ? g.positions[(int64_t)b * g.seqlen + t] : position + g.positions[b];
+    const int pairs = g.turned / 2, turning = HALF ? ceil_div(pairs, V) : chunks;
+    for (int unit = threadIdx.x % share; unit < per; unit += share) {
+        const int chunk = unit % chunks, head0 = unit / chunks * H;
+        const bool turn = chunk < turning;
+        const int c0 = turn ? chunk * V : g.turned + (chunk - turning) * V, c1 = c0 + pairs;
+        const int left0 = (HALF && turn ? pairs : g.dim) - c0, left1 = HALF && turn ? pairs - chunk * V : 0;
+        Vec<T, V> r0[H], r1[H];
+        const T* from[H];
+        T* to[H];
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            const int head = head0 + k, second = head >= g.heads[0], h = head - (second ? g.heads[0] : 0);
+            const bool in = head < g.heads[0] + g.heads[1];
+            from[k] = in ? static_cast<const T*>(g.in[second]) + b * g.batch_stride[second] + t * g.token_stride[second] + (int64_t)h * g.dim : nullptr;
+            to[k] = in ? static_cast<T*>(g.out[second]) + (((int64_t)b * g.seqlen + t) * g.heads[second] + h) * g.dim : nullptr;
+            const bool read = in && live;
+            r0[k] = load_vec<T, V>(read ? from[k] + c0 : nullptr, read ? left0 : 0, vec);
+            if (HALF) r1[k] = load_vec<T, V>(read ? from[k] + c1 : nullptr, read ? left1 : 0, vec);
+        }
+        float cs[NP], sn[NP];
+        if (turn) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const int k = (HALF ? chunk * V : chunk * V / 2) + p;
+                cs[p] = sn[p] = 0.f;
+                if (k < pairs) {
+                    cos_sin<T>((int)(((unsigned long long)position * __ldg(g.table + k)) >> 32), cs[p], sn[p]);
+                    cs[p] *= g.scale;
+                    sn[p] *= g.inverse ? -g.scale : g.scale;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            if (to[k] == nullptr) break;
+            if (turn) {
+                float o0[V], o1[V];
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    const float x = HALF ? r0[k].get(p) : r0[k].get(2 * p % V), y = HALF ? r1[k].get(p) : r0[k].get((2 * p + 1) % V);
+                    const bool in = HALF || chunk * V / 2 + p < pairs;  // a vector may hold entries that are copied
+                    const float first = in ? fmaf(x, cs[p], -y * sn[p]) : x, other = in ? fmaf(x, sn[p], y * cs[p]) : y;
+                    if (HALF) {
+                        o0[p] = first;
+                        o1[p] = other;
+                    } else {
+                        o0[2 * p % V] = first;
+                        o0[(2 * p + 1) % V] = other;
+                    }
+                }
+                r0[k] = Vec<T, V>::of(o0);
+                if (HALF) r1[k] = Vec<T, V>::of(o1);
+            }
+            store_vec<T, V>(to[k] + c0, r0[k], left0, vec);
+            if (HALF) store_vec<T, V>(to[k] + c1, r1[k], left1, vec);
+        }
+    }
+}
+
+template <typename T, int V, bool HALF>
+int rotary_of(const RotaryArgs& g, bool vec, cudaStream_t s) {
+    const int pairs = g.turned / 2, heads = g.heads[0] + g.heads[1];
+    const int chunks = HALF ? ceil_div(pairs, V) + ceil_div(g.dim - g.turned, V) : ceil_div(g.dim, V);
+    // Four heads a thread where that leaves every SM two thousand threads.
+    const bool many = (int64_t)g.batch * g.seqlen * chunks * ceil_div(heads, 4) >= (int64_t)kSms * 2048;
+    const int blocks = ceil_div(heads, many ? 4 : 1);
+    const int64_t per = (int64_t)chunks * blocks;
+    if (per > 2147483647) return SSD_ERR_UNSUPPORTED;
+    const int tokens = per >= kRotaryThreads ? 1 : kRotaryThreads / (int)per;
+    const dim3 grid(ceil_div(g.seqlen, tokens), g.batch);
+    launch_begin(kKindRotary, s);
+    if (many) rotary_kernel<T, V, HALF, 4><<<grid, kRotaryThreads, 0, s>>>(g, chunks, blocks, tokens, vec);
+    else rotary_kernel<T, V, HALF, 1><<<grid, kRotaryThreads, 0, s>>>(g, chunks, blocks, tokens, vec);
+    return launch_end(kKindRotary, s);
+}
+
+template <typename T>
+int rotary_type(const RotaryArgs& g, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    bool vec = g.dim % V == 0;
+    for (int k = 0; k < 2; ++k)
+        if (g.heads[k] > 0)
+            vec = vec && g.batch_stride[k] % V == 0 && g.token_stride[k] % V == 0 && aligned_to(g.in[k], 16) && aligned_to(g.out[k], 16);
+    if (g.interleaved) return vec ? rotary_of<T, V, false>(g, true, s) : rotary_of<T, 2, false>(g, false, s);
+    return vec && g.turned / 2 % V == 0 ? rotary_of<T, V, true>(g, true, s) : rotary_of<T, 1, true>(g, true, s);
+}
+
+}  // namespace
+
+int launch_rotary(const RotaryArgs& g, cudaStream_t s) {
+    if (g.dtype == SSD_BF16) return rotary_type<__nv_bfloat16>(g, s);
+    if (g.dtype == SSD_F16) return rotary_type<__half>(g, s);
+    return rotary_type<float>(g, s);
+}
+
+}  // namespace ssd

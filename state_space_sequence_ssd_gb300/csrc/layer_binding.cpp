@@ -573,6 +573,115 @@ PyObject* norm_backward(PyObject* const* a) {
     return dict_of({{"dx", &dx}, {"dweight", &dweight}, {"dbias", &dbias}});
 }
 
+// What the grouped norm's entries share, from x, groups, weight, bias, z, gate_first, silu.
+struct GroupNorm {
+    Lead l;
+    int64_t width, groups;
+    Flat x, z;
+    const void *px, *pz;
+    const float *weight, *bias;
+    int gate;
+    std::vector<int64_t> stats;  // shape of mean and rstd
+};
+GroupNorm group_norm(PyObject* ox, PyObject* ogroups, PyObject* oweight, PyObject* obias, PyObject* oz, PyObject* ofirst, PyObject* osilu) {
+    const Tensor& x = tensor(ox, "x");
+    GroupNorm s{lead(x, "x", 0)};
+    s.width = x.size(-1);
+    s.groups = PyLong_AsLongLong(ogroups);
+    if (PyErr_Occurred()) throw Raised();
+    if (s.groups < 1 || s.width % s.groups != 0)
+        refuse(PyExc_ValueError, "groups (" + std::to_string(s.groups) + ") must divide x's " + std::to_string(s.width) + " channels");
+    s.weight = dense<float>(oweight, "weight", at::kFloat, {s.width}, s.l);
+    s.bias = dense<float>(obias, "bias", at::kFloat, {s.width}, s.l);
+    const Tensor* z = optional(oz, "z");
+    const bool first = truth(ofirst), silu = truth(osilu);
+    if (silu && z != nullptr) refuse(PyExc_ValueError, "silu and a gate z exclude one another");
+    if (first && z == nullptr) refuse(PyExc_ValueError, "gate_first needs a gate z");
+    s.gate = z == nullptr ? (silu ? SSD_GATE_SILU : SSD_GATE_NONE) : first ? SSD_GATE_BEFORE : SSD_GATE_AFTER;
+    s.x = flat(x, "x");
+    s.z = {0, 0};
+    s.px = x.data_ptr();
+    s.pz = nullptr;
+    if (z != nullptr) {
+        check(*z, "z", s.l.type, x.sizes(), s.l);
+        s.z = flat(*z, "z");
+        s.pz = z->data_ptr();
+    }
+    s.stats = x.sizes().slice(0, x.dim() - 1).vec();
+    s.stats.push_back(s.groups);
+    return s;
+}
+
+// x, groups, weight, bias, z, gate_first, silu, rms, eps
+PyObject* group_norm_forward(PyObject* const* a) {
+    const GroupNorm s = group_norm(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
+    const bool rms = truth(a[7]);
+    const double eps = PyFloat_AsDouble(a[8]);
+    if (PyErr_Occurred()) throw Raised();
+    Tensor y = empty(tensor(a[0], "x").sizes(), s.l.type, s.l), mean, rstd = empty(s.stats, at::kFloat, s.l);
+    if (!rms) mean = empty(s.stats, at::kFloat, s.l);
+    done("ssd_group_norm_forward",
+         ssd_group_norm_forward(s.l.code, s.px, s.x.step, s.pz, s.z.step, s.weight, s.bias, (float)eps, s.gate, rms, s.x.rows, size_int(s.width),
+                                size_int(s.groups), y.data_ptr(), floats(mean), floats(rstd), s.l.stream));
+    return tuple_of({wrap(y), wrap(mean), wrap(rstd)});
+}
+
+// x, groups, weight, bias, mean, rstd, dy, z, gate_first, silu
+PyObject* group_norm_backward(PyObject* const* a) {
+    const GroupNorm s = group_norm(a[0], a[1], a[2], a[3], a[7], a[8], a[9]);
+    const auto shape = tensor(a[0], "x").sizes();
+    const float *mean = dense<float>(a[4], "mean", at::kFloat, s.stats, s.l), *rstd = dense<float>(tensor(a[5], "rstd"), "rstd", at::kFloat, s.stats, s.l);
+    const Tensor& dy = tensor(a[6], "dy");
+    check(dy, "dy", s.l.type, shape, s.l);
+    const Flat g = flat(dy, "dy");
+    Tensor dx = empty(shape, s.l.type, s.l), dz, dweight, dbias;
+    if (s.pz != nullptr) dz = empty(shape, s.l.type, s.l);
+    if (s.weight != nullptr) dweight = empty({s.width}, at::kFloat, s.l);
+    if (s.bias != nullptr) dbias = empty({s.width}, at::kFloat, s.l);
+    done("ssd_group_norm_backward",
+         ssd_group_norm_backward(s.l.code, s.px, s.x.step, s.pz, s.z.step, s.weight, s.bias, s.gate, mean, rstd, dy.data_ptr(), g.step, s.x.rows,
+                                 size_int(s.width), size_int(s.groups), dx.data_ptr(), dz.defined() ? dz.data_ptr() : nullptr, floats(dweight), floats(dbias),
+                                 s.l.stream));
+    if (dz.defined()) return dict_of({{"dx", &dx}, {"dz", &dz}, {"dweight", &dweight}, {"dbias", &dbias}});
+    return dict_of({{"dx", &dx}, {"dweight", &dweight}, {"dbias", &dbias}});
+}
+
+// B, C, table, positions, lengths, interleaved, scale, inverse, step
+PyObject* rotary(PyObject* const* a) {
+    const bool step = truth(a[8]);
+    const int ndim = step ? 3 : 4;
+    const Tensor& B = tensor(a[0], "B");
+    const Tensor* C = optional(a[1], "C");
+    const Lead l = lead(B, "B", ndim);
+    const int64_t b = B.size(0), L = step ? 1 : B.size(1), dim = B.size(ndim - 1), G = B.size(ndim - 2), G2 = C == nullptr ? 0 : C->dim() == ndim ? C->size(ndim - 2) : 0;
+    auto shape = [&](int64_t heads) { return step ? std::vector<int64_t>{b, heads, dim} : std::vector<int64_t>{b, L, heads, dim}; };
+    need_dense_end(B, "B", 2);
+    if (C != nullptr) {
+        check(*C, "C", l.type, shape(G2), l);
+        need_dense_end(*C, "C", 2);
+    }
+    const Tensor& table = tensor(a[2], "table");
+    if (table.dim() != 1) refuse(PyExc_ValueError, "table must have 1 dim, got " + shape_text(table.sizes()));
+    const void* turns = dense(table, "table", at::kLong, {table.size(0)}, l);
+    const Tensor* positions = optional(a[3], "positions");
+    const bool each = positions != nullptr && positions->dim() == 2;
+    const int* at = nullptr;
+    if (positions != nullptr) at = dense<int>(*positions, "positions", at::kInt, each ? std::vector<int64_t>{b, L} : std::vector<int64_t>{b}, l);
+    const int* lengths = dense<int>(a[4], "lengths", at::kInt, {b}, l);
+    const double scale = PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) throw Raised();
+    const Tensor y = empty(shape(G), l.type, l);
+    Tensor y2;
+    if (C != nullptr) y2 = empty(shape(G2), l.type, l);
+    auto token = [&](const Tensor& t) { return step ? 0 : stride(t, 1); };
+    done("ssd_rotary",
+         ssd_rotary(l.code, B.data_ptr(), stride(B, 0), token(B), size_int(G), C == nullptr ? nullptr : C->data_ptr(), C == nullptr ? 0 : stride(*C, 0),
+                    C == nullptr ? 0 : token(*C), size_int(G2), static_cast<const unsigned long long*>(turns), size_int(2 * table.size(0)), at, each, lengths,
+                    (float)scale, truth(a[5]), truth(a[7]), size_int(b), size_int(L), size_int(dim), y.data_ptr(), C == nullptr ? nullptr : y2.data_ptr(),
+                    l.stream));
+    return C == nullptr ? wrap(y) : tuple_of({wrap(y), wrap(y2)});
+}
+
 // For the tests without a GPU: (step, rows) of a tensor's rows, and the strides before its last `inner` dimensions.
 PyObject* flat_rows(PyObject* const* a) {
     const Flat f = flat(tensor(a[0], "t"), "t");
@@ -630,6 +739,9 @@ PyMethodDef g_methods[] = {
     method<gated_forward, 8>("gated_forward"),
     method<gated_backward, 10>("gated_backward"),
     method<gated_step, 6>("gated_step"),
+    method<group_norm_forward, 9>("group_norm_forward"),
+    method<group_norm_backward, 10>("group_norm_backward"),
+    method<rotary, 9>("rotary"),
     method<flat_rows, 1>("flat_rows"),
     method<row_strides, 2>("row_strides"),
     method<set_fail, 1>("set_fail"),

@@ -253,6 +253,9 @@ enum LayerKind {
     kKindGated,
     kKindGatedBwd,
     kKindGatedStep,
+    kKindGroupNorm,
+    kKindGroupNormBwd,
+    kKindRotary,
     kAllKinds
 };
 
@@ -340,6 +343,49 @@ size_t gated_sums_floats(const GatedArgs& g);
 int launch_gated_forward(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s);
 int launch_gated_backward(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s);
 int launch_gated_step(const GatedArgs& g, float* state, const int* slots, int nslots, void* y, int* err, cudaStream_t s);
+
+// The column sums of a norm's gradient: dweight and dbias (either may be nullptr) from `parts` rows of 2 x width.
+int launch_norm_sums(int kind, const float* partial, int parts, int width, float* dweight, float* dbias, cudaStream_t s);
+
+enum Gate { kGateNone = SSD_GATE_NONE, kGateSilu = SSD_GATE_SILU, kGateAfter = SSD_GATE_AFTER, kGateBefore = SSD_GATE_BEFORE };
+struct GroupNormArgs {
+    int dtype;
+    int64_t rows;
+    int width, groups, gate;
+    bool rms;
+    float eps;
+    const void *x, *z;  // z with kGateAfter and kGateBefore only
+    int64_t x_row, z_row;
+    const float *weight, *bias;  // (width) or nullptr
+};
+struct GroupNormGrads {
+    const float *mean, *rstd;  // (rows, groups); mean is nullptr where rms
+    const void* dy;
+    int64_t dy_row;
+    void *dx, *dz;
+};
+int group_norm_forward_bf16(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);
+int group_norm_forward_f16(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);
+int group_norm_forward_f32(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);
+// partial: parts x 2 x width float32, or nullptr where no column sums are wanted
+int group_norm_backward_bf16(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s);
+int group_norm_backward_f16(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s);
+int group_norm_backward_f32(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s);
+
+struct RotaryArgs {
+    int dtype, batch, seqlen, dim, turned;
+    bool interleaved, inverse;
+    float scale;
+    int heads[2];  // the second may be 0
+    const void* in[2];
+    int64_t batch_stride[2], token_stride[2];
+    void* out[2];  // dense
+    const unsigned long long* table;  // (turned / 2)
+    const int* positions;             // (batch), (batch, seqlen) where `each`, or nullptr
+    bool each;
+    const int* lengths;
+};
+int launch_rotary(const RotaryArgs& g, cudaStream_t s);
 
 // Workspace, error words and device size, implemented in ssd_api.cu.
 int take_workspace(void** ptr, size_t bytes, cudaStream_t s);

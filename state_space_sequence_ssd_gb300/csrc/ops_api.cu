@@ -112,6 +112,20 @@ int read_gated(int dtype, const void* x, const void* r, const void* i, const flo
     return SSD_OK;
 }
 
+int read_group_norm(int dtype, const void* x, int64_t x_row, const void* z, int64_t z_row, const float* weight, const float* bias, float eps, int gate,
+                    bool rms, int64_t rows, int width, int groups, GroupNormArgs* a) {
+    if (!x || !known(dtype) || rows <= 0 || width <= 0 || groups <= 0 || width % groups != 0 || x_row < 0 || gate < SSD_GATE_NONE ||
+        gate > SSD_GATE_BEFORE || !(eps >= 0.f) || std::isinf(eps))
+        return SSD_ERR_INVALID_ARG;
+    const bool gated = gate >= SSD_GATE_AFTER;
+    if (gated != (z != nullptr) || (gated && z_row < 0)) return SSD_ERR_INVALID_ARG;
+    if (width > kMaxChannels || groups > kMaxGrid || rows > ((int64_t)1 << 40)) return SSD_ERR_UNSUPPORTED;
+    const uintptr_t size = size_of(dtype);
+    if (!aligned_to(x, size) || !aligned_to(z, size) || !aligned_to(weight, 4) || !aligned_to(bias, 4)) return SSD_ERR_INVALID_ARG;
+    *a = GroupNormArgs{dtype, rows, width, groups, gate, rms, eps, x, z, x_row, gated ? z_row : 0, weight, bias};
+    return SSD_OK;
+}
+
 // Gives `ws` back to the pool in stream order; an error of the launches comes first.
 int give_back(void* ws, cudaStream_t s, int r) {
     if (ws != nullptr && cudaFreeAsync(ws, s) != cudaSuccess && r == SSD_OK) r = SSD_ERR_CUDA;
@@ -315,6 +329,62 @@ int ssd_gated_step(int dtype, const void* x, const void* r, const void* i, const
     int* err = error_words();
     if (err == nullptr) return SSD_ERR_CUDA;
     return launch_gated_step(a, state, slots, nslots, y, err, stream);
+}
+
+int ssd_group_norm_forward(int dtype, const void* x, long long x_row_stride, const void* z, long long z_row_stride, const float* weight,
+                           const float* bias, float eps, int gate, int rms, long long rows, int width, int groups, void* y,
+                           float* mean, float* rstd, cudaStream_t stream) {
+    GroupNormArgs a;
+    const int e = read_group_norm(dtype, x, x_row_stride, z, z_row_stride, weight, bias, eps, gate, rms != 0, rows, width, groups, &a);
+    if (e != SSD_OK) return e;
+    if (!y || !aligned_to(y, size_of(dtype)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || (a.rms && mean != nullptr)) return SSD_ERR_INVALID_ARG;
+    if (dtype == SSD_BF16) return group_norm_forward_bf16(a, y, mean, rstd, stream);
+    if (dtype == SSD_F16) return group_norm_forward_f16(a, y, mean, rstd, stream);
+    return group_norm_forward_f32(a, y, mean, rstd, stream);
+}
+
+int ssd_group_norm_backward(int dtype, const void* x, long long x_row_stride, const void* z, long long z_row_stride, const float* weight,
+                            const float* bias, int gate, const float* mean, const float* rstd, const void* dy, long long dy_row_stride,
+                            long long rows, int width, int groups, void* dx, void* dz, float* dweight, float* dbias,
+                            cudaStream_t stream) {
+    GroupNormArgs a;
+    int e = read_group_norm(dtype, x, x_row_stride, z, z_row_stride, weight, bias, 0.f, gate, mean == nullptr, rows, width, groups, &a);
+    if (e != SSD_OK) return e;
+    const uintptr_t size = size_of(dtype);
+    if (!rstd || !dy || !dx || dy_row_stride < 0 || (a.z != nullptr) != (dz != nullptr) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) ||
+        !aligned_to(dy, size) || !aligned_to(dx, size) || !aligned_to(dz, size) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
+        return SSD_ERR_INVALID_ARG;
+    const GroupNormGrads d = {mean, rstd, dy, dy_row_stride, dx, dz};
+    const int parts = layer_norm_parts(rows, multiprocessors());
+    void* ws = nullptr;
+    if ((dweight != nullptr || dbias != nullptr) && take_workspace(&ws, (size_t)parts * 2 * width * sizeof(float), stream) != SSD_OK)
+        return SSD_ERR_NO_MEMORY;
+    float* partial = static_cast<float*>(ws);
+    if (dtype == SSD_BF16) e = group_norm_backward_bf16(a, d, partial, parts, stream);
+    else if (dtype == SSD_F16) e = group_norm_backward_f16(a, d, partial, parts, stream);
+    else e = group_norm_backward_f32(a, d, partial, parts, stream);
+    if (e == SSD_OK && partial != nullptr) e = launch_norm_sums(kKindGroupNormBwd, partial, parts, width, dweight, dbias, stream);
+    return give_back(ws, stream, e);
+}
+
+int ssd_rotary(int dtype, const void* x0, long long x0_batch_stride, long long x0_token_stride, int heads0, const void* x1,
+               long long x1_batch_stride, long long x1_token_stride, int heads1, const unsigned long long* table, int turned,
+               const int* positions, int positions_each, const int* lengths, float scale, int interleaved, int inverse, int batch,
+               int seqlen, int dim, void* y0, void* y1, cudaStream_t stream) {
+    if (!x0 || !y0 || !table || !known(dtype) || batch <= 0 || seqlen <= 0 || dim <= 0 || heads0 <= 0 || heads1 < 0 || turned <= 0 ||
+        turned % 2 != 0 || turned > dim || x0_batch_stride < 0 || x0_token_stride < 0 || !std::isfinite(scale) ||
+        (positions_each != 0 && positions == nullptr))
+        return SSD_ERR_INVALID_ARG;
+    if ((heads1 > 0) != (x1 != nullptr) || (heads1 > 0) != (y1 != nullptr) || (heads1 > 0 && (x1_batch_stride < 0 || x1_token_stride < 0)))
+        return SSD_ERR_INVALID_ARG;
+    if (batch > kMaxBatch || seqlen > kMaxTokens || (int64_t)heads0 * dim > kMaxChannels || (int64_t)heads1 * dim > kMaxChannels) return SSD_ERR_UNSUPPORTED;
+    const uintptr_t size = size_of(dtype);
+    if (!aligned_to(x0, size) || !aligned_to(x1, size) || !aligned_to(y0, size) || !aligned_to(y1, size) || !aligned_to(table, 8) ||
+        !aligned_to(positions, 4) || !aligned_to(lengths, 4))
+        return SSD_ERR_INVALID_ARG;
+    RotaryArgs a = {dtype, batch, seqlen, dim, turned, interleaved != 0, inverse != 0, scale, {heads0, heads1}, {x0, x1},
+                    {x0_batch_stride, x1_batch_stride}, {x0_token_stride, x1_token_stride}, {y0, y1}, table, positions, positions_each != 0, lengths};
+    return launch_rotary(a, stream);
 }
 
 }  // extern "C"

@@ -49,7 +49,7 @@ const char* const kKindNames[kAllKinds] = {"chunk_cumsum", "chunk_state", "state
                                            "bc_to_f16", "step", "bwd_chunk", "bwd_reduce",
                                            "conv", "conv_bwd", "conv_step", "selective", "selective_bwd",
                                            "selective_step", "layer_norm", "layer_norm_bwd",
-                                           "gated", "gated_bwd", "gated_step"};
+                                           "gated", "gated_bwd", "gated_step", "group_norm", "group_norm_bwd", "rotary"};
 
 }  // namespace
 

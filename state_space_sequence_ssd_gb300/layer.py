@@ -185,3 +185,91 @@ def ssd_gated_step(x, r, i, A, state, slots=None, stream=None):
     if stream is not None:
         return _on(stream, _native.gated_step, (x, r, i, A, state, slots), (x, r, i, A, state, slots))
     return _native.gated_step(x, r, i, A, state, slots)
+
+
+def ssd_group_norm_forward(x, groups, weight=None, bias=None, z=None, gate_first=False, silu=False, rms=False, eps=1e-5, stream=None):
+    """Norm over groups of the last dimension's channels, with its activation -> (y, mean or None, rstd).
+
+    x (..., width) with a dense last dimension and evenly spaced rows, z like it (strides of its own); weight, bias (width,)
+    f32 or None; mean (None with ``rms``, which takes it as 0) and rstd are (..., groups) f32.  With a gate z the output is
+    norm(x * silu(z)) if ``gate_first``, else norm(x) * silu(z); without one silu(norm(x)) if ``silu``."""
+    if stream is not None:
+        return _on(stream, _native.group_norm_forward, (x, groups, weight, bias, z, gate_first, silu, rms, eps), (x, weight, bias, z))
+    return _native.group_norm_forward(x, groups, weight, bias, z, gate_first, silu, rms, eps)
+
+
+def ssd_group_norm_backward(x, groups, weight, bias, mean, rstd, dy, z=None, gate_first=False, silu=False, stream=None):
+    """Gradients through ssd_group_norm_forward -> dict of dx (dense), dz (absent without a gate), dweight and dbias ((width,)
+    f32, None without a weight or a bias), from the forward pass's mean (None: ``rms``) and rstd."""
+    if stream is not None:
+        return _on(stream, _native.group_norm_backward, (x, groups, weight, bias, mean, rstd, dy, z, gate_first, silu),
+                   (x, weight, bias, mean, rstd, dy, z))
+    return _native.group_norm_backward(x, groups, weight, bias, mean, rstd, dy, z, gate_first, silu)
+
+
+def ssd_rotary_table(turned, base=10000.0, scaling=None, factor=1.0, original=None, slow=1.0, fast=32.0, frequencies=None, device="cuda"):
+    """The table of the rotary calls for ``turned`` entries of a head -> (turned // 2,) int64 on ``device``: pair k's frequency
+    base ** (-2 k / turned) in radians a position, as the part of a turn in units of 2^-64.
+
+    For contexts longer than the ``original`` by ``factor``: scaling "linear" divides every frequency by it, "base" raises the base
+    by factor ** (turned / (turned - 2)) (the slowest pair is divided by factor, the fastest kept), "parts" divides those that
+    turn less than ``slow`` times over the original context, keeps those that turn more than ``fast`` times, and blends linearly
+    between.  ``frequencies`` gives them instead (a sequence of turned // 2 numbers).  The computation is on the host."""
+    import math
+
+    import torch
+    if turned < 2 or turned % 2:
+        raise ValueError(f"turned must be even and at least 2, got {turned}")
+    pairs = turned // 2
+    if frequencies is None:
+        if not base > 0:
+            raise ValueError(f"base must be positive, got {base}")
+        if not (factor > 0 and math.isfinite(factor)):
+            raise ValueError(f"factor must be positive, got {factor}")
+        if scaling not in (None, "linear", "base", "parts"):
+            raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', got {scaling!r}")
+        if scaling == "base" and turned > 2:
+            base = base * factor ** (turned / (turned - 2))
+        frequencies = [base ** (-k / pairs) for k in range(pairs)]
+        if scaling == "linear" or scaling == "base" and turned == 2:
+            frequencies = [f / factor for f in frequencies]
+        elif scaling == "parts":
+            if original is None or not original > 0 or not fast > slow:
+                raise ValueError("scaling 'parts' needs the original context, and fast above slow")
+            for k, f in enumerate(frequencies):
+                keep = min(max((original * f / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0)
+                frequencies[k] = f * keep + f / factor * (1 - keep)
+    else:
+        frequencies = [float(f) for f in frequencies]
+    if len(frequencies) != pairs or not all(math.isfinite(f) for f in frequencies):
+        raise ValueError(f"frequencies must be {pairs} finite numbers")
+    turns = [round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in frequencies]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _rotary(args, stream):
+    if stream is not None:
+        return _on(stream, _native.rotary, args, args[:5])
+    return _native.rotary(*args)
+
+
+def ssd_rotary_forward(B, C, table, positions=None, lengths=None, interleaved=False, scale=1.0, stream=None):
+    """Rotary positions on a scan's B and C (or queries and keys) -> (B, C) turned, or B alone where C is None.
+
+    B, C (batch, L, groups, dstate), each with a number of groups of its own; the first 2 * len(table) entries of a group are turned,
+    as pairs (2 k, 2 k + 1) if ``interleaved``, else (k, k + len(table)), and multiplied by ``scale``; the others are copied.
+    table is ssd_rotary_table's.  Token t is at position t, at positions[b] + t with positions (batch,) int32, or at
+    positions[b, t] with (batch, L) int32 (rows of packed documents)."""
+    return _rotary((B, C, table, positions, lengths, interleaved, scale, False, False), stream)
+
+
+def ssd_rotary_backward(dB, dC, table, positions=None, lengths=None, interleaved=False, scale=1.0, stream=None):
+    """Gradients through ssd_rotary_forward: (dB, dC) turned back, or dB alone where dC is None."""
+    return _rotary((dB, dC, table, positions, lengths, interleaved, scale, True, False), stream)
+
+
+def ssd_rotary_step(B, C, table, positions, interleaved=False, scale=1.0, stream=None):
+    """ssd_rotary_forward for one token of every row: B, C (batch, groups, dstate), positions (batch,) int32."""
+    if positions is None:
+        raise ValueError("positions is required")
+    return _rotary((B, C, table, positions, None, interleaved, scale, False, True), stream)

@@ -88,3 +88,91 @@ def gated(x, r, i, A, init=None, lengths=None, dy=None, dfinal=None):
     out["dA"] = (q.sum((0, 1)) / A, (e_q.sum((0, 1)) + terms * (L / 8 + 16 + 8 * b) * U) / A.abs())
     out["dinit"] = (a[:, 0] * lam[:, 0], a[:, 0] * (lam_err[:, 0] + lam_mag[:, 0] * (e_a[:, 0] + 2 * U)))
     return out
+
+
+def _silu(v):
+    """silu and its slope, each with the bound of its error."""
+    s = torch.sigmoid(v)
+    slope = s * (1 + v * (1 - s))
+    return s, v * s, (v * s).abs() * (12 + v.abs()) * U, slope, s * (1 + v.abs() * (1 - s)) * (30 + 2 * v.abs()) * U
+
+
+def group_norm(x, groups, weight=None, bias=None, z=None, gate_first=False, silu=False, rms=False, eps=1e-5, stats=None, dy=None):
+    """{name: (value, bound)} of y, mean and rstd; with stats (mean, rstd), which are taken as they are, and dy of the gradients."""
+    rows, width = x.shape
+    per = width // groups
+    # a thread adds at most 32 values, or one in 256 of a wide group's; then the threads' sums
+    k = (per / 256 + 60) * U
+    split = lambda t: t.unflatten(-1, (groups, per))  # noqa: E731
+    w = torch.ones_like(x[0]) if weight is None else weight
+    b = torch.zeros_like(w) if bias is None else bias
+    if z is not None:
+        sz, gz, e_gz, slope_z, e_slope_z = _silu(z)
+    q, e_q = (x * gz, x.abs() * e_gz + (x * gz).abs() * 2 * U) if gate_first else (x, torch.zeros_like(x))
+    q, e_q = split(q), split(e_q)
+    if stats is None:
+        mean = q.mean(-1, keepdim=True) * (not rms)
+        e_mean = (q.abs().mean(-1, keepdim=True) * k + e_q.mean(-1, keepdim=True)) * (not rms)
+        off = q - mean
+        e_off = e_q + e_mean + off.abs() * U
+        var = off.square().mean(-1, keepdim=True)
+        rstd = 1 / torch.sqrt(var + eps)
+        e_rstd = (off.abs() * e_off).mean(-1, keepdim=True) / (var + eps) + (k + 8 * U)
+        n = (off * rstd).flatten(1) * w
+        e_n = (e_off * rstd + (off * rstd).abs() * (e_rstd + 4 * U)).flatten(1) * w.abs() + 2 * U * (n.abs() + b.abs())
+        n = n + b
+        if silu:
+            _, y, e_y, *_ = _silu(n)
+            e_y = e_y + 1.1 * e_n
+        elif z is not None and not gate_first:
+            y, e_y = n * gz, e_n * gz.abs() + n.abs() * (e_gz + 2 * U * gz.abs())
+        else:
+            y, e_y = n, e_n
+        return {"y": (y, e_y), "mean": (mean[..., 0], e_mean[..., 0]), "rstd": (rstd[..., 0], (rstd * e_rstd)[..., 0])}
+    mean, rstd = (torch.zeros_like(q[..., :1]) if v is None else v[..., None] for v in stats)
+    xh = ((q - mean) * rstd).flatten(1)
+    e_xh = (e_q * rstd + (q.abs() + mean.abs()) * rstd * 4 * U).flatten(1)
+    n, e_n = xh * w + b, e_xh * w.abs() + 2 * U * (xh * w).abs() + U * b.abs()
+    out, g, e_g = {}, dy, torch.zeros_like(dy)
+    if silu:
+        _, _, _, slope, e_slope = _silu(n)
+        g, e_g = dy * slope, dy.abs() * (e_slope + 0.6 * e_n + U)  # the slope's own slope is at most 0.5
+    if z is not None and not gate_first:
+        out["dz"] = dy * n * slope_z, dy.abs() * (e_n * slope_z.abs() + n.abs() * (e_slope_z + 3 * U * slope_z.abs()))
+        g, e_g = dy * gz, dy.abs() * (e_gz + 2 * U * gz.abs())
+    gw, e_gw, xs, e_xs = split(g * w), split(e_g * w.abs() + U * (g * w).abs()), split(xh), split(e_xh)
+    s1, m1 = gw.mean(-1, keepdim=True) * (not rms), gw.abs().mean(-1, keepdim=True) * (not rms)
+    s2, m2 = (gw * xs).mean(-1, keepdim=True), (gw * xs).abs().mean(-1, keepdim=True)
+    e_s1 = m1 * k + e_gw.mean(-1, keepdim=True) * (not rms)
+    e_s2 = m2 * k + (e_gw * xs.abs() + gw.abs() * e_xs).mean(-1, keepdim=True)
+    dq = (rstd * (gw - s1 - xs * s2)).flatten(1)
+    e_dq = (rstd * (e_gw + e_s1 + xs.abs() * e_s2 + e_xs * s2.abs() + 6 * U * (gw.abs() + m1 + xs.abs() * m2))).flatten(1)
+    if gate_first:
+        out["dz"] = dq * x * slope_z, x.abs() * (e_dq * slope_z.abs() + dq.abs() * (e_slope_z + 3 * U * slope_z.abs()))
+        dq, e_dq = dq * gz, e_dq * gz.abs() + dq.abs() * (e_gz + 2 * U * gz.abs())
+    out["dx"] = dq, e_dq
+    # a block adds its rows, up to 256 of them at once, then 32 sums of the blocks' rows
+    terms = (rows / 300 + 320) * U
+    out["dweight"] = (g * xh).sum(0), (e_g * xh.abs() + g.abs() * e_xh).sum(0) + (g * xh).abs().sum(0) * terms
+    out["dbias"] = g.sum(0), e_g.sum(0) + g.abs().sum(0) * terms
+    return out
+
+
+def rotary(x, frequencies, positions=None, lengths=None, interleaved=False, scale=1.0, inverse=False, fast=False):
+    """(value, bound) of x (batch, L, heads, dim) turned; fast: the sines of 16-bit tensors."""
+    b, L = x.shape[:2]
+    at = torch.arange(L, device=x.device).expand(b, L)
+    if positions is not None:
+        at = positions.long() if positions.dim() == 2 else at + positions.long()[:, None]
+    angle = at[..., None, None].double() * frequencies
+    cos, sin = scale * torch.cos(angle), scale * torch.sin(angle) * (-1 if inverse else 1)
+    n = 2 * len(frequencies)
+    one, two = (slice(0, n, 2), slice(1, n, 2)) if interleaved else (slice(0, n // 2), slice(n // 2, n))
+    y, bound = x.clone(), torch.zeros_like(x)
+    p, q = x[..., one], x[..., two]
+    y[..., one], y[..., two] = p * cos - q * sin, p * sin + q * cos
+    # the angle to 2^-32 of a turn and a float32 rounding of it, the functions' error, the products and their sum
+    e = (2.0 ** -19 if fast else 14 * U) * abs(scale) + 3 * U * abs(scale)
+    bound[..., one] = bound[..., two] = (p.abs() + q.abs()) * e
+    keep = kept(b, L, lengths, x)[..., None]
+    return torch.where(keep, y, 0.0), torch.where(keep, bound, 0.0)
