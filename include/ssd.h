@@ -608,7 +608,7 @@ typedef struct ssd_gated_strides {
  *   y            (batch, seqlen, channels) dense
  *   states       (batch, ceil(seqlen / SSD_GATED_SPAN), channels) f32 or NULL: the state in front of every
  *                SSD_GATED_SPAN-th token (the final state past a row's length), for ssd_gated_backward
- * Value domain: A < 0; a token's decay, gate or 1 - a^2 below 2^-126 is zero.  An infinity or a NaN in a live place reaches what the
+ * Value domain: A < 0; a token's decay below 2^-126 is taken as that, a gate or 1 - a^2 below it as zero.  An infinity or a NaN in a live place reaches what the
  * recurrence carries it to and nothing else.  One launch, no workspace.
  */
 SSD_API int ssd_gated_forward(int dtype, const void* x, const void* r, const void* i, const float* A,
@@ -705,7 +705,8 @@ SSD_API int ssd_get_device_error(void);
  * Test hooks of the failure path (no counterpart in the pages; process-wide,
  * they affect every later launch until reset).
  * ssd_debug_set_wait_limit_ns(ns) sets the time after which a pipeline wait
- * inside the tensor-core kernels (chunk_state, chunk_scan) gives up; 0
+ * inside the tensor-core kernels (chunk_state, chunk_scan), or between the
+ * blocks of a cluster (gated, gated_bwd), gives up; 0
  * restores the default of one second.  The teardown drains that let every
  * copy and product already issued complete before a kernel releases shared
  * memory and TMEM keep their own one-second limit.

@@ -6,14 +6,20 @@
 
 namespace ssd {
 
-// Two channels a lane, 64 a block; eight warps of eight consecutive tokens each, SSD_GATED_SPAN a block and step.
-constexpr int kGatedWarps = 8, kGatedRun = 8, kGatedThreads = 32 * kGatedWarps, kGatedTile = 64;
-constexpr int kGatedSpan = kGatedWarps * kGatedRun;
-static_assert(kGatedSpan == SSD_GATED_SPAN, "a kept state is the one in front of a block's step");
+// Two channels a lane, 64 a block; a block's warps hold SSD_GATED_SPAN consecutive tokens between them.
+constexpr int kGatedTile = 64, kGatedSpan = SSD_GATED_SPAN;
+
+constexpr int kGatedRanks = 8;  // blocks of a cluster at most
+constexpr int kGatedWait = 61;  // a cluster's wait that gave up, in the device error words
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ float sqrt_fast(float v) {
@@ -30,61 +36,80 @@ __device__ __forceinline__ float rsqrt_fast(float v) {
 // e^-v of two channels.
 __device__ __forceinline__ f32x2 exp_neg(f32x2 v) { return exp2_2(mul2(v, pk(-kLog2e, -kLog2e))); }
 
-// v = 1 / (1 + er) and g = 1 / (1 + ei), er = e^-r and ei = e^-i.  One reciprocal serves both: 1 / ((1 + er) (1 + ei)) times the
-// other's denominator.  Where an exponential passes 2^60 the product could overflow, and a NaN of one gate would reach the
-// other: there each has its own.  REST: also 1 - v = er v and 1 - g = ei g, which cancel nothing where v and g are near one.
-template <bool REST>
-__device__ __forceinline__ void two_gates(f32x2 er, f32x2 ei, f32x2& v, f32x2& g, f32x2& v_rest, f32x2& g_rest) {
+// v = 1 / (1 + er) and g = 1 / (1 + ei), er = e^-r and ei = e^-i.  ONE: one reciprocal serves both, 1 / ((1 + er) (1 + ei)) times the
+// other's denominator.  The product may then not overflow, nor one of them be a NaN, which would reach the other: `top` is the
+// largest product so far, or a NaN, and the values stand where it is at most kShared.
+constexpr float kShared = 0x1p120f;
+template <bool ONE>
+__device__ __forceinline__ void two_gates(f32x2 er, f32x2 ei, f32x2& v, f32x2& g, float& top) {
     const f32x2 one = pk(1.f, 1.f), p = add2(er, one), q = add2(ei, one);
-    float r0, r1, i0, i1, a, b;
-    unpk(er, r0, r1);
-    unpk(ei, i0, i1);
-    if (max_nan(max_nan(r0, r1), max_nan(i0, i1)) <= 0x1p60f) {
+    float a, b;
+    if (ONE) {
         unpk(mul2(p, q), a, b);
+        top = max_nan(top, a, b);
         const f32x2 inv = pk(rcp_fast(a), rcp_fast(b));
         v = mul2(q, inv);
         g = mul2(p, inv);
-        if (REST) {
-            v_rest = mul2(er, v);
-            g_rest = mul2(ei, g);
-        }
     } else {
         unpk(p, a, b);
         v = pk(rcp_fast(a), rcp_fast(b));
         unpk(q, a, b);
         g = pk(rcp_fast(a), rcp_fast(b));
-        if (REST) {  // past 2^60 the rest is one
-            unpk(mul2(er, v), a, b);
-            v_rest = pk(r0 > 0x1p60f ? 1.f : a, r1 > 0x1p60f ? 1.f : b);
-            unpk(mul2(ei, g), a, b);
-            g_rest = pk(i0 > 0x1p60f ? 1.f : a, i1 > 0x1p60f ? 1.f : b);
-        }
     }
 }
+template <bool ONE>
 __device__ __forceinline__ void two_gates(f32x2 er, f32x2 ei, f32x2& v, f32x2& g) {
-    f32x2 none;
-    two_gates<false>(er, ei, v, g, none, none);
+    float none = 0.f;
+    two_gates<ONE>(er, ei, v, g, none);
+}
+// 1 - v = er v, which cancels nothing where v is near one; past 2^60 it is one.
+template <bool ONE>
+__device__ __forceinline__ f32x2 gate_rest(f32x2 er, f32x2 v) {
+    if (ONE) return mul2(er, v);
+    float r0, r1, a, b;
+    unpk(er, r0, r1);
+    unpk(mul2(er, v), a, b);
+    return pk(r0 > 0x1p60f ? 1.f : a, r1 > 0x1p60f ? 1.f : b);
+}
+// Whether one reciprocal may serve both gates of all of R tokens.
+template <int R>
+__device__ __forceinline__ bool gates_share(const f32x2 (&er)[R], const f32x2 (&ei)[R]) {
+    float m = 0.f, a, b;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        unpk(er[k], a, b);
+        m = max_nan(m, max_nan(a, b));
+        unpk(ei[k], a, b);
+        m = max_nan(m, max_nan(a, b));
+    }
+    return m <= 0x1p60f;
 }
 
-// a = e^u and w = 1 - a^2 for u <= 0.  Near zero 1 - a^2 cancels: there e^u - 1 is Taylor's polynomial of degree 6 (what it
-// leaves out is below 2^-24 of it for |u| < 1/4), and w = -(a - 1)(a + 1).  Beyond, e^u is the special function unit's,
-// and 1 - a is at least 0.22, so that its error stays below 2^-19.
+// a = e^u and w = 1 - a^2 for u <= 0.  With n the whole number next to u / ln 2 and f = u - n ln 2, |f| <= ln 2 / 2, e^u - 1 is
+// 2^n (e^f - 1) + (2^n - 1); e^f - 1 is Taylor's polynomial of degree 7 (what it leaves out is below 2^-25 of it).  Near u = 0 n is 0
+// and nothing cancels: w = -(a - 1)(a + 1) is right to 3 and a to 2 roundings there, and within 5 everywhere (every step of
+// 2^-24 checked over [-87, 0] in samples).  Adding 1.5 2^23 rounds to n and leaves it in the low bits, from where it goes to the exponent.
+// In packed arithmetic this takes fewer instructions than the special function unit's exponential with a polynomial beside it
+// for small u, and leaves that unit, which the gates keep busy, one call less of five.  a is 2^-126 for all u below its logarithm.
 __device__ __forceinline__ void decay_terms(f32x2 u, f32x2& a, f32x2& w) {
-    f32x2 t = fma2(u, pk(1.f / 720, 1.f / 720), pk(1.f / 120, 1.f / 120));
-    t = fma2(t, u, pk(1.f / 24, 1.f / 24));
-    t = fma2(t, u, pk(1.f / 6, 1.f / 6));
-    t = fma2(t, u, pk(0.5f, 0.5f));
-    t = fma2(t, u, pk(1.f, 1.f));
-    t = mul2(t, u);
-    float u0, u1, m0, m1, a0, a1;
+    float u0, u1;
     unpk(u, u0, u1);
-    unpk(t, m0, m1);
-    unpk(add2(t, pk(1.f, 1.f)), a0, a1);
-    const float e0 = exp2_fast(u0 * kLog2e), e1 = exp2_fast(u1 * kLog2e);
-    const bool near0 = u0 > -0.25f, near1 = u1 > -0.25f;
-    a = pk(near0 ? a0 : e0, near1 ? a1 : e1);
-    const f32x2 m = pk(near0 ? m0 : e0 - 1.f, near1 ? m1 : e1 - 1.f);
-    w = mul2(mul2(m, pk(-1.f, -1.f)), add2(m, pk(2.f, 2.f)));
+    u = pk(max_nan(u0, -87.33f), max_nan(u1, -87.33f));
+    const f32x2 magic = pk(12582912.f, 12582912.f), t = fma2(u, pk(kLog2e, kLog2e), magic);
+    const f32x2 n = add2(t, pk(-12582912.f, -12582912.f)), f = fma2(n, pk(-0.6931471805599453f, -0.6931471805599453f), u);
+    f32x2 p = fma2(f, pk(1.f / 5040, 1.f / 5040), pk(1.f / 720, 1.f / 720));
+    p = fma2(p, f, pk(1.f / 120, 1.f / 120));
+    p = fma2(p, f, pk(1.f / 24, 1.f / 24));
+    p = fma2(p, f, pk(1.f / 6, 1.f / 6));
+    p = fma2(p, f, pk(0.5f, 0.5f));
+    p = fma2(p, f, pk(1.f, 1.f));
+    p = mul2(p, f);
+    float t0, t1;
+    unpk(t, t0, t1);
+    const f32x2 scale = pk(__uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u), __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u));
+    const f32x2 m = fma2(p, scale, add2(scale, pk(-1.f, -1.f)));
+    a = fma2(p, scale, scale);
+    w = mul2(m, fma2(m, pk(-1.f, -1.f), pk(-2.f, -2.f)));
 }
 
 // The state h after tokens that multiply it by p and add own.  p may have rounded to zero where no single decay is: an infinite
@@ -102,59 +127,149 @@ __device__ __forceinline__ float2 unpk(f32x2 v) {
     return r;
 }
 
-// A warp's part of a step: its kGatedRun rows of the block's channels, one after another in shared memory.
-template <typename T>
-constexpr int kGatedRow = kGatedTile * (int)sizeof(T);  // bytes of a row
-template <typename T>
-constexpr int kGatedPart = kGatedRun * kGatedRow<T>;  // of a warp's rows of one tensor
+// h after a run that multiplies it by q.xy and adds q.zw.  SAFE: as above; else a product that rounded to zero may make a NaN
+// of an infinity, which the caller looks for (a composition without infinities is an instruction for both channels).
+template <bool SAFE>
+__device__ __forceinline__ float2 run_after(float2 h, float2 p, float2 own) {
+    return SAFE ? onward(p, h, own) : unpk(fma2(pk(p), pk(h), pk(own)));
+}
+template <bool SAFE>
+__device__ __forceinline__ float2 run_after(float2 h, float4 q) {
+    return run_after<SAFE>(h, make_float2(q.x, q.y), make_float2(q.z, q.w));
+}
+__device__ __forceinline__ float2 times(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ bool has_nan(float2 v) { return !(v.x == v.x && v.y == v.y); }
 
-// Copies tokens t0 .. t0 + kGatedRun - 1 of one tensor into the warp's part; tokens from n on and channels past the tensor's
-// are zeros.  `p` is the row's first token at channel c0, `left` its channels from there.  vec: whole 16-byte vectors.
-template <typename T>
-__device__ __forceinline__ void gated_fetch(unsigned char* to, const T* p, int64_t token, int t0, int n, int left, bool vec) {
-    constexpr int V = 16 / sizeof(T), PER = kGatedTile / V, ROWS = 32 / PER;
-    const int lane = threadIdx.x & 31;
-    if (vec) {
-        const int c = (lane % PER) * V, r0 = lane / PER;
-#pragma unroll
-        for (int k = 0; k < kGatedRun / ROWS; ++k) {
-            const int r = k * ROWS + r0;
-            const bool in = t0 + r < n && c < left;
-            copy16(to + r * kGatedRow<T> + c * (int)sizeof(T), in ? p + (t0 + r) * token + c : p, in);
+// A warp's R rows (tokens) of one tensor, 64 channels each, on their way through shared memory.  VEC: rows are whole 16-byte vectors,
+// and lie there as they are.  Else a row's aligned 16-byte chunks are copied, the first with what lies in front of the row in it,
+// into rows that are one chunk longer; where such a chunk is not within the tensor's own row, its elements are copied one by one.
+template <typename T, int R, bool VEC>
+struct GatedRows {
+    static constexpr int PITCH = kGatedTile * (int)sizeof(T) + (VEC ? 0 : 16), BYTES = R * PITCH, V = 16 / (int)sizeof(T);
+    const T* p;       // VEC: this lane's vector of the row's first token; else that token at the block's first channel
+    int phase, pitch; // !VEC: bytes of its address past a multiple of 16, and what a token adds
+
+    __device__ __forceinline__ void begin(const void* tensor, int64_t batch, int64_t token, int c0) {
+        p = static_cast<const T*>(tensor) + batch + c0;
+        if (VEC) {
+            const int lane = threadIdx.x & 31;
+            p += lane / (kGatedTile / V) * token + lane % (kGatedTile / V) * V;
+        } else {
+            phase = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+            pitch = (int)((uint64_t)token * sizeof(T) & 15);
         }
-    } else {
-        T* s = reinterpret_cast<T*>(to) + lane * 2;
-        T v[kGatedRun][2];
-#pragma unroll
-        for (int r = 0; r < kGatedRun; ++r)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                v[r][e] = t0 + r < n && lane * 2 + e < left ? p[(t0 + r) * token + lane * 2 + e] : from_f32<T>(0.f);
-#pragma unroll
-        for (int r = 0; r < kGatedRun; ++r)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s[r * kGatedTile + e] = v[r][e];
     }
-}
-template <typename T>
-__device__ __forceinline__ f32x2 gated_at(const unsigned char* part, int r) {
-    Vec<T, 2> q;
-    const unsigned char* p = part + r * kGatedRow<T> + (threadIdx.x & 31) * 2 * (int)sizeof(T);
-    if constexpr (sizeof(T) == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        q.w[0] = u.x;
-        q.w[1] = u.y;
-    } else {
-        q.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    // Tokens t0 .. t0 + R - 1 to `to`; those from n on and channels past the tensor's (`left` from the block's first) are zeros, or,
+    // without VEC, not written.
+    __device__ __forceinline__ void fetch(unsigned char* to, int64_t token, int t0, int n, int c0, int left) const {
+        const int lane = threadIdx.x & 31;
+        if constexpr (VEC) {
+            constexpr int PER = kGatedTile / V, ROWS = 32 / PER;
+            const bool in = lane % PER * V < left;
+            const int r0 = lane / PER;
+            const T* q = p + t0 * token;
+            to += lane * 16;
+            if (t0 + R <= n) {
+#pragma unroll
+                for (int k = 0; k < R / ROWS; ++k, q += ROWS * token) copy16(to + k * 32 * 16, q, in);
+            } else {
+#pragma unroll
+                for (int k = 0; k < R / ROWS; ++k, q += ROWS * token) copy16(to + k * 32 * 16, q, in && t0 + k * ROWS + r0 < n);
+            }
+        } else {
+            constexpr int PER = kGatedTile / V + 1;
+            for (int k = lane; k < R * PER; k += 32) {
+                const int r = k / PER, j = k - r * PER;
+                if (t0 + r >= n) continue;
+                const T* row = p + (t0 + r) * token;  // aligned down: the chunks; its own channels are row - c0 .. row + left
+                const int off = (phase + (t0 + r) * pitch) & 15;
+                const int first = (j * 16 - off) / (int)sizeof(T);  // the chunk's first channel (off is a multiple of the element)
+                if (first >= (left < kGatedTile ? left : kGatedTile)) continue;
+                if (first >= -c0 && first + V <= left) {
+                    copy16(to + r * PITCH + j * 16, row + first, true);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (first + e >= 0 && first + e < left) reinterpret_cast<T*>(to + r * PITCH + j * 16)[e] = row[first + e];
+                }
+            }
+        }
     }
-    return q.pair(0);
-}
+    // This lane's two channels of row r, which is token t.
+    __device__ __forceinline__ f32x2 at(const unsigned char* part, int r, int t) const {
+        const unsigned char* q = part + r * PITCH + (threadIdx.x & 31) * 2 * (int)sizeof(T);
+        if constexpr (VEC) {
+            Vec<T, 2> v;
+            if constexpr (sizeof(T) == 4) {
+                const uint2 u = *reinterpret_cast<const uint2*>(q);
+                v.w[0] = u.x;
+                v.w[1] = u.y;
+            } else {
+                v.w[0] = *reinterpret_cast<const uint32_t*>(q);
+            }
+            return v.pair(0);
+        } else {
+            const T* e = reinterpret_cast<const T*>(q + ((phase + t * pitch) & 15));
+            return pk(to_f32<T>(e[0]), to_f32<T>(e[1]));
+        }
+    }
+};
 
-// One float4 of a lane into the same place of the shared memory of the cluster's block `rank`.
-__device__ __forceinline__ void give(uint32_t saddr, uint32_t rank, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(sm100::map_shared_rank(saddr, rank)), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
-                 : "memory");
+// The exchange of a cluster's blocks: every step each block gives all of them (itself too) one float4 a lane, with asynchronous stores
+// that complete a barrier of the receiver, so that nobody waits for its own stores to global memory, as a cluster barrier's
+// release would (gradient of 2 x 4096 x 4096: 183 us with one, 170 without).  Two places take turns: a block gives step s + 2 only
+// when it has everyone's step s + 1, which they give after they have read step s.  Waits have a limit (Ctl).  A block whose wait
+// ran out neither gives nor waits from then on, so that every barrier is armed only behind a phase that completed; the
+// others' waits run out in turn.
+struct Cluster {
+    uint64_t full[2];
+    int abort, pad[3];
+    // behind it float4 by turn, rank and lane
+    __device__ __forceinline__ float4* pair(int turn, int rank, int ranks) {
+        return reinterpret_cast<float4*>(this + 1) + (turn * ranks + rank) * 32 + (threadIdx.x & 31);
+    }
+};
+constexpr int cluster_bytes(int ranks) { return (int)sizeof(Cluster) + (ranks > 1 ? 2 * ranks * 32 * (int)sizeof(float4) : 0); }
+__device__ __forceinline__ void cluster_begin(Cluster* cl, int ranks) {
+    if (ranks == 1) return;
+    if (threadIdx.x == 0) {
+        cl->abort = 0;
+        sm100::mbar_init(&cl->full[0], 1);
+        sm100::mbar_init(&cl->full[1], 1);
+        sm100::fence_barrier_init();
+    }
+    sm100::cluster_sync();
+}
+// Called by one warp: the block's float4 of a step.
+__device__ __forceinline__ void cluster_give(Cluster* cl, int step, int rank, int ranks, float4 v, const Ctl& ctl) {
+    if (*static_cast<volatile int*>(&cl->abort)) return;  // set in front of the block's last barrier
+    const int turn = step & 1, lane = threadIdx.x & 31;
+    if (lane == 0 && !(ctl.stall && step == 0)) sm100::mbar_arrive_expect_tx(&cl->full[turn], ranks * 32 * (uint32_t)sizeof(float4));
+    const uint32_t place = sm100::smem_u32(cl->pair(turn, rank, ranks)), bar = sm100::smem_u32(&cl->full[turn]);
+    for (int k = 0; k < ranks; ++k)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                         sm100::map_shared_rank(place, k)),
+                     "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(sm100::map_shared_rank(bar, k))
+                     : "memory");
+}
+__device__ __forceinline__ void cluster_take(Cluster* cl, int step, const Ctl& ctl) {
+    sm100::mbar_wait_bounded(&cl->full[step & 1], (step >> 1) & 1, &cl->abort, ctl.err, kGatedWait, ctl.wait_ns);
+}
+// No block ends while another may still write to its shared memory: all that is given to it has come, and nobody gives more.  Where a
+// wait ran out that cannot be waited for; then a millisecond lets the stores on their way arrive.
+__device__ __forceinline__ void cluster_end(Cluster* cl, int steps, int ranks, const Ctl& ctl) {
+    if (ranks == 1) return;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (*static_cast<volatile int*>(&cl->abort)) {
+            const uint64_t t0 = sm100::globaltimer_ns();
+            while (sm100::globaltimer_ns() - t0 < 1000000ull) {}
+        } else {
+            if (steps > 1) sm100::mbar_wait_drain(&cl->full[steps & 1], ((steps - 2) >> 1) & 1, ctl.err, kGatedWait, kDrainNs);
+            if (steps > 0) sm100::mbar_wait_drain(&cl->full[(steps - 1) & 1], ((steps - 1) >> 1) & 1, ctl.err, kGatedWait, kDrainNs);
+        }
+    }
+    sm100::cluster_sync();
 }
 
 }  // namespace ssd

@@ -3,60 +3,94 @@
 //   v = sigmoid(r), g = sigmoid(i), u = A v, a = exp(u), s = sqrt(1 - a^2)
 //   h_t = a_t h_{t-1} + s_t g_t x_t,   y_t = h_t
 //
-// A scan over composed pairs: a run of tokens takes h to P h + H with P the product of its decays.  A block holds 64
-// channels; its eight warps take eight tokens each at once: every warp composes its own run in registers, the pairs go
-// through shared memory, and each warp then walks its tokens again from the state in front of them, with the decays and
-// inputs that it still holds.  The blocks of a cluster take neighbouring steps of the sequence and give each other their
-// pairs through distributed shared memory, so that one pass over the data serves sequences of any length, with as many blocks
-// as fill the SMs.  The inputs come through cp.async two steps ahead.
+// A scan over composed pairs: a run of tokens takes h to P h + H with P the product of its decays.  A block holds 64 channels, two a
+// lane; its warps take 16 consecutive tokens each at once: every warp composes its own run in registers, the pairs go through
+// shared memory, and each warp then walks its tokens again from the state in front of them, with the decays and inputs that it
+// still holds.  The blocks of a cluster take neighbouring steps of the sequence and give each other their pairs through
+// distributed shared memory, so that one pass over the data serves sequences of any length, with as many blocks as fill the SMs.
+// The next step's inputs come through cp.async while this step's pairs are exchanged and its outputs written.
+//
+// 2 x 4096 x 4096 of bfloat16 takes 68 us (4.0 TB/s; the bytes' floor is 40), of float32 85 (6.4 TB/s; 80), 65536 x 2048 of
+// bfloat16 299 (159): of 16-bit elements the instructions bind, 36 a warp and element pair of the special function unit's five, the
+// polynomial and conversions, at half the issue slots; and 256 blocks on 152 SMs leave some with one where others have two.
+// Runs of 8 tokens take 85 us at the first size (more exchange for the work), copies two steps ahead as long as one.
 #include "gated.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kStages = 2;
+constexpr int R = 16;  // consecutive tokens of a warp
 
-struct Cluster {
-    float4 pair[2][8][32];  // by turn, rank and lane: P and H of two channels
-};
-
+// The gradient's blocks: four warps.  With 16-bit tensors two of them an SM, with up to 255 registers a thread, and two steps of
+// input on their way; three with 168 registers, which a 32-bit type's single step of input leaves room for, take 146 us
+// where these take 139 (2 x 4096 x 4096 of bfloat16), and 169 where two take 199 (float32).
+constexpr int kBackWarps = 4;
 template <typename T>
-constexpr int forward_smem() {
-    return kStages * 3 * kGatedWarps * kGatedPart<T> + 2 * kGatedWarps * 32 * 16 + (int)sizeof(Cluster);
+constexpr int kBackResident = sizeof(T) == 4 ? 3 : 2;
+template <typename T>
+constexpr int kBackStages = sizeof(T) == 4 ? 1 : 2;
+
+template <typename T, int W, bool VEC>
+int forward_smem(int ranks) {
+    return 3 * W * GatedRows<T, R, VEC>::BYTES + 2 * W * 32 * 16 + cluster_bytes(ranks);
+}
+
+// The state behind `count` of a block's runs, and the product of their decays, from h in front of them.
+template <bool SAFE>
+__device__ __forceinline__ void through_runs(const float4* pairs, int count, float2& h, float2& p) {
+#pragma unroll 4
+    for (int k = 0; k < count; ++k) {
+        const float4 q = pairs[k * 32];
+        h = run_after<SAFE>(h, q);
+        p = times(p, make_float2(q.x, q.y));
+    }
+}
+// What the blocks of a cluster gave: on from h in front of block `first` through the blocks to `last` (exclusive; backwards if it is smaller).
+template <bool SAFE>
+__device__ __forceinline__ float2 through_blocks(Cluster* cl, int turn, int ranks, int first, int last, float2 h) {
+    const int way = last < first ? -1 : 1;
+#pragma unroll 2
+    for (int k = first; k != last; k += way) h = run_after<SAFE>(h, *cl->pair(turn, k, ranks));
+    return h;
 }
 
 // states: (batch, ceil(seqlen / span), channels), the state in front of each span; y, final_state, states may be null.
-template <typename T>
-__global__ void __launch_bounds__(kGatedThreads, 2)
-gated_forward_kernel(GatedArgs g, int ranks, bool vec, bool vecy, T* __restrict__ y, float* __restrict__ final_state,
-                     float* __restrict__ states) {
+template <typename T, int W, bool VEC>
+__global__ void __launch_bounds__(32 * W, 16 / W)
+gated_forward_kernel(GatedArgs g, Ctl ctl, int ranks, bool vecy, T* __restrict__ y, float* __restrict__ final_state, float* __restrict__ states) {
+    using Rows = GatedRows<T, R, VEC>;
+    constexpr int SPAN = W * R, STAGE = 3 * W * Rows::BYTES;
     extern __shared__ __align__(16) unsigned char smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int rank = blockIdx.x % ranks, b = blockIdx.y, c0 = blockIdx.x / ranks * kGatedTile, c = c0 + lane * 2;
     const int left = g.channels - c0;
-    unsigned char* mine = smem + warp * 3 * kGatedPart<T>;
-    constexpr int STAGE = 3 * kGatedWarps * kGatedPart<T>;
-    float4* pairs = reinterpret_cast<float4*>(smem + kStages * STAGE);  // [turn][warp][lane]
-    Cluster* cl = reinterpret_cast<Cluster*>(pairs + 2 * kGatedWarps * 32);
+    unsigned char* mine = smem + warp * 3 * Rows::BYTES;
+    float4* pairs = reinterpret_cast<float4*>(smem + STAGE);  // [turn][warp][lane]
+    Cluster* cl = reinterpret_cast<Cluster*>(pairs + 2 * W * 32);
     const int n = row_length(g.lengths, b, g.seqlen);
-    const int steps = ceil_div(n, kGatedSpan * ranks);
-    const T* x = static_cast<const T*>(g.x) + b * g.x_batch + c0;
-    const T* r = static_cast<const T*>(g.r) + b * g.r_batch + c0;
-    const T* i = static_cast<const T*>(g.i) + b * g.i_batch + c0;
-    auto fetch = [&](int step) {
-        if (step < steps) {
-            const int t0 = (step * ranks + rank) * kGatedSpan + warp * kGatedRun;
-            unsigned char* to = mine + (step % kStages) * STAGE;
-            gated_fetch<T>(to, x, g.x_token, t0, n, left, vec);
-            gated_fetch<T>(to + kGatedPart<T>, r, g.r_token, t0, n, left, vec);
-            gated_fetch<T>(to + 2 * kGatedPart<T>, i, g.i_token, t0, n, left, vec);
+    const int steps = ceil_div(n, SPAN * ranks);
+    int ahead = rank * SPAN + warp * R;  // the first token that is not on its way
+    Rows x, r, i;
+    x.begin(g.x, b * g.x_batch, g.x_token, c0);
+    r.begin(g.r, b * g.r_batch, g.r_token, c0);
+    i.begin(g.i, b * g.i_batch, g.i_token, c0);
+    if (!VEC) {  // what no copy writes is finite
+        for (int k = threadIdx.x; k < STAGE / 4; k += 32 * W) reinterpret_cast<uint32_t*>(smem)[k] = 0u;
+        __syncthreads();
+    }
+    auto fetch = [&] {
+        if (ahead < n) {
+            x.fetch(mine, g.x_token, ahead, n, c0, left);
+            r.fetch(mine + Rows::BYTES, g.r_token, ahead, n, c0, left);
+            i.fetch(mine + 2 * Rows::BYTES, g.i_token, ahead, n, c0, left);
         }
+        ahead += SPAN * ranks;
         copies_commit();
     };
-#pragma unroll
-    for (int k = 0; k < kStages; ++k) fetch(k);
+    fetch();
+    cluster_begin(cl, ranks);
     const bool in0 = c < g.channels, in1 = c + 1 < g.channels;
-    const f32x2 A = pk(in0 ? g.A[c] : 0.f, in1 ? g.A[c + 1] : 0.f);
+    const f32x2 A = pk(in0 ? g.A[c] : -1.f, in1 ? g.A[c + 1] : -1.f);
     float2 h = make_float2(0.f, 0.f);  // in front of the cluster's step
     if (g.init != nullptr) {
         const float* p = g.init + (int64_t)b * g.channels + c;
@@ -69,81 +103,100 @@ gated_forward_kernel(GatedArgs g, int ranks, bool vec, bool vecy, T* __restrict_
         if (in0) p[0] = v.x;
         if (in1) p[1] = v.y;
     };
-    for (int step = 0; step < steps; ++step) {
-        const int turn = step & 1, span = step * ranks + rank;
-        const int t0 = span * kGatedSpan + warp * kGatedRun;
-        const unsigned char* from = mine + (step % kStages) * STAGE;
-        copies_wait<kStages - 1>();
+    int t0 = rank * SPAN + warp * R;
+    for (int step = 0; step < steps; ++step, t0 += SPAN * ranks) {
+        const int turn = step & 1;
+        copies_wait<0>();
         __syncwarp();
-        f32x2 a[kGatedRun], bx[kGatedRun], P = pk(1.f, 1.f), H = pk(0.f, 0.f);
+        f32x2 a[R], bx[R], P = pk(1.f, 1.f), H = pk(0.f, 0.f);  // a and bx hold the gates' exponentials first
 #pragma unroll
-        for (int k = 0; k < kGatedRun; ++k) {
-            f32x2 v, gi, w;
-            two_gates(exp_neg(gated_at<T>(from + kGatedPart<T>, k)), exp_neg(gated_at<T>(from + 2 * kGatedPart<T>, k)), v, gi);
-            decay_terms(mul2(A, v), a[k], w);
-            float w0, w1;
-            unpk(w, w0, w1);
-            bx[k] = mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), gated_at<T>(from, k));
+        for (int k = 0; k < R; ++k) {
+            a[k] = exp_neg(r.at(mine + Rows::BYTES, k, t0 + k));
+            bx[k] = exp_neg(i.at(mine + 2 * Rows::BYTES, k, t0 + k));
         }
-        if (t0 + kGatedRun > n) {  // tokens past the length keep the state
+        auto terms = [&](auto one) {
+            constexpr bool ONE = decltype(one)::value;
 #pragma unroll
-            for (int k = 0; k < kGatedRun; ++k)
-                if (t0 + k >= n) {
+            for (int k = 0; k < R; ++k) {
+                f32x2 v, gi, w;
+                two_gates<ONE>(a[k], bx[k], v, gi);
+                decay_terms(mul2(A, v), a[k], w);
+                float w0, w1;
+                unpk(w, w0, w1);
+                bx[k] = mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.at(mine, k, t0 + k));
+                if (!ONE && t0 + k >= n) {  // tokens past the length keep the state
                     a[k] = pk(1.f, 1.f);
                     bx[k] = pk(0.f, 0.f);
                 }
-        }
+            }
+        };
+        const bool whole = t0 + R <= n;
+        if (whole && gates_share(a, bx)) terms(std::true_type());
+        else terms(std::false_type());
 #pragma unroll
-        for (int k = 0; k < kGatedRun; ++k) {
+        for (int k = 0; k < R; ++k) {
             P = mul2(P, a[k]);
             H = fma2(a[k], H, bx[k]);
         }
         __syncwarp();
-        fetch(step + kStages);
+        fetch();
         {
             const float2 p2 = unpk(P), h2 = unpk(H);
-            pairs[(turn * kGatedWarps + warp) * 32 + lane] = make_float4(p2.x, p2.y, h2.x, h2.y);
+            pairs[(turn * W + warp) * 32 + lane] = make_float4(p2.x, p2.y, h2.x, h2.y);
         }
         __syncthreads();
-        float2 start = h;  // in front of this warp's tokens
-        if (ranks == 1) {
-#pragma unroll
-            for (int k = 0; k < kGatedWarps; ++k) {
-                const float4 q = pairs[(turn * kGatedWarps + k) * 32 + lane];
-                if (k == warp) start = h;
-                if (k == 0 && warp == 0 && states != nullptr) keep(span, h);
-                h = onward(make_float2(q.x, q.y), h, make_float2(q.z, q.w));
+        const float4* q = pairs + turn * W * 32 + lane;
+        auto exchange = [&](auto safe) {  // h in front of this warp's tokens; h becomes the state behind the cluster's step
+            constexpr bool SAFE = decltype(safe)::value;
+            const float2 zero = make_float2(0.f, 0.f), one = make_float2(1.f, 1.f);
+            float2 at = ranks == 1 ? h : zero, p = one;
+            through_runs<SAFE>(q, warp, at, p);
+            if (ranks == 1) {
+                float2 end = at;
+                through_runs<SAFE>(q + warp * 32, W - warp, end, p);
+                h = end;
+                return at;
             }
-        } else {
-            float2 own_p = make_float2(1.f, 1.f), own_h = make_float2(0.f, 0.f), all_p = own_p, all_h = own_h;
-#pragma unroll
-            for (int k = 0; k < kGatedWarps; ++k) {
-                const float4 q = pairs[(turn * kGatedWarps + k) * 32 + lane];
-                if (k == warp) {
-                    own_p = all_p;
-                    own_h = all_h;
+            const float2 before = through_blocks<SAFE>(cl, turn, ranks, 0, rank, h);
+            h = through_blocks<SAFE>(cl, turn, ranks, rank, ranks, before);
+            return run_after<SAFE>(before, p, at);
+        };
+        if (ranks > 1) {
+            if (warp == W - 1) {  // the block's runs composed, for the cluster
+                float2 end = make_float2(0.f, 0.f), p = make_float2(1.f, 1.f);
+                through_runs<false>(q, W, end, p);
+                if (has_nan(end)) {
+                    end = make_float2(0.f, 0.f), p = make_float2(1.f, 1.f);
+                    through_runs<true>(q, W, end, p);
                 }
-                all_h = onward(make_float2(q.x, q.y), all_h, make_float2(q.z, q.w));
-                all_p = make_float2(all_p.x * q.x, all_p.y * q.y);
+                cluster_give(cl, step, rank, ranks, make_float4(p.x, p.y, end.x, end.y), ctl);
             }
-            if (warp < ranks) give((uint32_t)__cvta_generic_to_shared(&cl->pair[turn][rank][lane]), warp, make_float4(all_p.x, all_p.y, all_h.x, all_h.y));
-            sm100::cluster_sync();
-            for (int k = 0; k < ranks; ++k) {
-                const float4 q = cl->pair[turn][k][lane];
-                if (k == rank) {
-                    if (warp == 0 && states != nullptr && span < kept) keep(span, h);
-                    start = onward(own_p, h, own_h);
-                }
-                h = onward(make_float2(q.x, q.y), h, make_float2(q.z, q.w));
-            }
+            cluster_take(cl, step, ctl);
         }
+        const float2 before = h;
+        float2 start = exchange(std::false_type());
+        if (has_nan(start) || has_nan(h)) {
+            h = before;
+            start = exchange(std::true_type());
+        }
+        if (states != nullptr && warp * R % kGatedSpan == 0 && t0 < g.seqlen) keep(t0 / kGatedSpan, start);
         if (y == nullptr) continue;
         f32x2 hs = pk(start);
-        T* o = y + ((int64_t)b * g.seqlen + t0) * g.channels + c;
+        T* to = y + ((int64_t)b * g.seqlen + t0) * g.channels;  // the same for all lanes
+        if (whole && vecy) {
+            if (in0) {
 #pragma unroll
-        for (int k = 0; k < kGatedRun; ++k) {
-            hs = fma2(a[k], hs, bx[k]);
-            if (t0 + k < n) store_vec<T, 2>(o + (int64_t)k * g.channels, Vec<T, 2>::of_pairs({hs}), g.channels - c, vecy);
+                for (int k = 0; k < R; ++k, to += g.channels) {
+                    hs = fma2(a[k], hs, bx[k]);
+                    store_vec<T, 2>(to + (uint32_t)c, Vec<T, 2>::of_pairs({hs}), 2, true);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < R; ++k, to += g.channels) {
+                hs = fma2(a[k], hs, bx[k]);
+                if (t0 + k < n) store_vec<T, 2>(to + (uint32_t)c, Vec<T, 2>::of_pairs({hs}), g.channels - c, vecy);
+            }
         }
     }
     copies_wait<0>();
@@ -153,59 +206,79 @@ gated_forward_kernel(GatedArgs g, int ranks, bool vec, bool vecy, T* __restrict_
         if (in1) p[1] = h.y;
     }
     if (states != nullptr)
-        for (int span = steps * ranks + rank + warp * ranks; span < kept; span += ranks * kGatedWarps) keep(span, h);
+        for (int span = steps * ranks * (SPAN / kGatedSpan) + rank + warp * ranks; span < kept; span += ranks * W) keep(span, h);
     if (y != nullptr)
-        for (int t = n + rank * kGatedWarps + warp; t < g.seqlen; t += ranks * kGatedWarps)
+        for (int t = n + rank * W + warp; t < g.seqlen; t += ranks * W)
             store_vec<T, 2>(y + ((int64_t)b * g.seqlen + t) * g.channels + c, Vec<T, 2>::zero(), g.channels - c, vecy);
-    if (ranks > 1) sm100::cluster_sync();  // no block ends while another may still write to its shared memory
+    cluster_end(cl, steps, ranks, ctl);
 }
 
 // ------------------------------------------------------------------ gradient
 //
 //   lam_t = dy_t + a_{t+1} lam_{t+1}  (dfinal behind the last token)
-//   dx = lam s g,   di = lam s x g (1 - g),   dr = q (1 - v),   q = lam (u a h_{t-1} - (u a^2 / s) g x)
+//   dx = lam s g,   di = lam s x g (1 - g),   dr = q (1 - v),   q = lam u a (h_{t-1} - (a / s) g x)
 //   dA = sum(q) / A,   dinit = a_0 lam_0
 //
 // The same blocks walk the steps from the last to the first.  The state in front of a step is one that the forward pass kept,
 // so that only lam crosses blocks; within the step the pairs of h go forwards and those of lam backwards through
-// the same exchange.  u a^2 / s has the limit 0 at u = 0.
-template <typename T>
-constexpr int backward_smem() {
-    return kStages * 4 * kGatedWarps * kGatedPart<T> + 2 * kGatedWarps * 32 * (16 + 8) + (int)sizeof(Cluster);
+// the same exchange.  u a / s has the limit 0 at u = 0.
+template <typename T, int W, int STAGES, bool VEC>
+int backward_smem(int ranks) {
+    return STAGES * 4 * W * GatedRows<T, R, VEC>::BYTES + 2 * W * 32 * (16 + 8) + cluster_bytes(ranks);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kGatedThreads, 2)
-gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy, const float* __restrict__ dfinal, int ranks, bool vec, bool vecy,
+// As through_runs, for lam: from the last run to the first.
+template <bool SAFE>
+__device__ __forceinline__ void back_through_runs(const float4* pairs, const float2* ends, int from, int to, float2& mu, float2& p) {
+#pragma unroll 4
+    for (int k = from; k > to; --k) {
+        const float2 q = *reinterpret_cast<const float2*>(&pairs[k * 32]);
+        mu = run_after<SAFE>(mu, q, ends[k * 32]);
+        p = times(p, q);
+    }
+}
+
+template <typename T, int W, int STAGES, bool VEC>
+__global__ void __launch_bounds__(32 * W, kBackResident<T>)
+gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy, const float* __restrict__ dfinal, Ctl ctl, int ranks, bool vecy,
                       T* __restrict__ dx, T* __restrict__ dr, T* __restrict__ di, float* __restrict__ dinit, float* __restrict__ partial) {
+    using Rows = GatedRows<T, R, VEC>;
+    constexpr bool FIRST = sizeof(T) == 4;
+    constexpr int SPAN = W * R, STAGE = 4 * W * Rows::BYTES;
     extern __shared__ __align__(16) unsigned char smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int rank = blockIdx.x % ranks, b = blockIdx.y, c0 = blockIdx.x / ranks * kGatedTile, c = c0 + lane * 2;
     const int left = g.channels - c0;
-    unsigned char* mine = smem + warp * 4 * kGatedPart<T>;
-    constexpr int STAGE = 4 * kGatedWarps * kGatedPart<T>;
-    float4* pairs = reinterpret_cast<float4*>(smem + kStages * STAGE);          // [turn][warp][lane]: P and H
-    float2* ends = reinterpret_cast<float2*>(pairs + 2 * kGatedWarps * 32);     // what lam's run adds
-    Cluster* cl = reinterpret_cast<Cluster*>(ends + 2 * kGatedWarps * 32);
+    unsigned char* mine = smem + warp * 4 * Rows::BYTES;
+    float4* pairs = reinterpret_cast<float4*>(smem + STAGES * STAGE);  // [turn][warp][lane]: P and H
+    float2* ends = reinterpret_cast<float2*>(pairs + 2 * W * 32);       // what lam's run adds
+    Cluster* cl = reinterpret_cast<Cluster*>(ends + 2 * W * 32);
     const int n = row_length(g.lengths, b, g.seqlen);
-    const int steps = ceil_div(n, kGatedSpan * ranks), kept = ceil_div(g.seqlen, kGatedSpan);
-    const T* x = static_cast<const T*>(g.x) + b * g.x_batch + c0;
-    const T* r = static_cast<const T*>(g.r) + b * g.r_batch + c0;
-    const T* i = static_cast<const T*>(g.i) + b * g.i_batch + c0;
-    const T* y = dy + (int64_t)b * g.seqlen * g.channels + c0;
-    auto fetch = [&](int step) {
-        if (step >= 0) {
-            const int t0 = (step * ranks + rank) * kGatedSpan + warp * kGatedRun;
-            unsigned char* to = mine + (step % kStages) * STAGE;
-            gated_fetch<T>(to, x, g.x_token, t0, n, left, vec);
-            gated_fetch<T>(to + kGatedPart<T>, r, g.r_token, t0, n, left, vec);
-            gated_fetch<T>(to + 2 * kGatedPart<T>, i, g.i_token, t0, n, left, vec);
-            gated_fetch<T>(to + 3 * kGatedPart<T>, y, g.channels, t0, n, left, vec);
+    const int steps = ceil_div(n, SPAN * ranks), kept = ceil_div(g.seqlen, kGatedSpan);
+    int t0 = ((steps - 1) * ranks + rank) * SPAN + warp * R, ahead = t0;
+    Rows x, r, i, gy;
+    x.begin(g.x, b * g.x_batch, g.x_token, c0);
+    r.begin(g.r, b * g.r_batch, g.r_token, c0);
+    i.begin(g.i, b * g.i_batch, g.i_token, c0);
+    gy.begin(dy, (int64_t)b * g.seqlen * g.channels, g.channels, c0);
+    if (!VEC) {  // what no copy writes is finite
+        for (int k = threadIdx.x; k < STAGES * STAGE / 4; k += 32 * W) reinterpret_cast<uint32_t*>(smem)[k] = 0u;
+        __syncthreads();
+    }
+    auto fetch = [&](int stage) {
+        unsigned char* to = mine + stage * STAGE;
+        if (ahead >= 0) {
+            x.fetch(to, g.x_token, ahead, n, c0, left);
+            r.fetch(to + Rows::BYTES, g.r_token, ahead, n, c0, left);
+            i.fetch(to + 2 * Rows::BYTES, g.i_token, ahead, n, c0, left);
+            gy.fetch(to + 3 * Rows::BYTES, g.channels, ahead, n, c0, left);
         }
+        ahead -= SPAN * ranks;
         copies_commit();
     };
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) fetch(steps - 1 - k);
+    for (int k = 0; k < STAGES; ++k) fetch(k);
+    cluster_begin(cl, ranks);
     const bool in0 = c < g.channels, in1 = c + 1 < g.channels;
     const f32x2 A = pk(in0 ? g.A[c] : -1.f, in1 ? g.A[c + 1] : -1.f);
     float2 mu = make_float2(0.f, 0.f);  // the gradient of the state behind the cluster's step
@@ -214,111 +287,166 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
         if (in0) mu.x = p[0];
         if (in1) mu.y = p[1];
     }
-    if (states != nullptr && steps == 0) states = nullptr;
-    f32x2 dA = pk(0.f, 0.f);
-    for (int step = steps - 1; step >= 0; --step) {
-        const int turn = step & 1, span = step * ranks + rank;
-        const int t0 = span * kGatedSpan + warp * kGatedRun;
-        const unsigned char* from = mine + (step % kStages) * STAGE;
-        float2 h = make_float2(0.f, 0.f);  // in front of this block's step
-        if (span < kept) {
+    auto kept_state = [&](int span) {  // in front of this block's tokens
+        float2 v = make_float2(0.f, 0.f);
+        if (span >= 0 && span < kept) {
             const float* p = states + ((int64_t)b * kept + span) * g.channels + c;
-            if (in0) h.x = p[0];
-            if (in1) h.y = p[1];
+            if (in0) v.x = p[0];
+            if (in1) v.y = p[1];
         }
-        copies_wait<kStages - 1>();
+        return v;
+    };
+    float2 next = kept_state((steps - 1) * ranks + rank);
+    f32x2 dA = pk(0.f, 0.f);
+    for (int step = 0; step < steps; ++step, t0 -= SPAN * ranks) {
+        const int turn = step & 1, span = (steps - 1 - step) * ranks + rank;
+        const unsigned char* from = mine + (step % STAGES) * STAGE;
+        const float2 before = next;
+        copies_wait<STAGES - 1>();
         __syncwarp();
-        f32x2 a[kGatedRun], er[kGatedRun], ei[kGatedRun], w[kGatedRun], hs[kGatedRun];
+        f32x2 a[R], w[R], hs[R];
         f32x2 P = pk(1.f, 1.f), H = pk(0.f, 0.f), Q = pk(0.f, 0.f);
+        const bool whole = t0 + R <= n;
+        // VEC: x and dy are zero past the length already
+        auto x_at = [&](int k) { return VEC || whole || t0 + k < n ? x.at(from, k, t0 + k) : pk(0.f, 0.f); };
+        auto dy_at = [&](int k) { return VEC || whole || t0 + k < n ? gy.at(from + 3 * Rows::BYTES, k, t0 + k) : pk(0.f, 0.f); };
+        float top = 0.f;
+        auto terms = [&](auto one) {
+            constexpr bool ONE = decltype(one)::value;
 #pragma unroll
-        for (int k = 0; k < kGatedRun; ++k) {
-            f32x2 v, gi;
-            er[k] = exp_neg(gated_at<T>(from + kGatedPart<T>, k));
-            ei[k] = exp_neg(gated_at<T>(from + 2 * kGatedPart<T>, k));
-            two_gates(er[k], ei[k], v, gi);
-            decay_terms(mul2(A, v), a[k], w[k]);
-            if (t0 + k >= n) {  // tokens past the length keep the state
-                a[k] = pk(1.f, 1.f);
-                w[k] = pk(0.f, 0.f);
+            for (int k = 0; k < R; ++k) {
+                f32x2 v, gi;
+                if (FIRST) two_gates<ONE>(a[k], w[k], v, gi);
+                else two_gates<ONE>(exp_neg(r.at(from + Rows::BYTES, k, t0 + k)), exp_neg(i.at(from + 2 * Rows::BYTES, k, t0 + k)), v, gi, top);
+                decay_terms(mul2(A, v), a[k], w[k]);
+                if (!ONE && t0 + k >= n) {  // tokens past the length keep the state
+                    a[k] = pk(1.f, 1.f);
+                    w[k] = pk(0.f, 0.f);
+                }
+                float w0, w1;
+                unpk(w[k], w0, w1);
+                hs[k] = H;  // what this run's tokens in front of k make of a zero state
+                H = fma2(a[k], H, mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x_at(k)));
+                P = mul2(P, a[k]);
             }
-            float w0, w1;
-            unpk(w[k], w0, w1);
-            hs[k] = H;  // what this run's tokens in front of k make of a zero state
-            H = fma2(a[k], H, mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), gated_at<T>(from, k)));
-            P = mul2(P, a[k]);
+        };
+        bool share = whole;
+        if (FIRST) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                a[k] = exp_neg(r.at(from + Rows::BYTES, k, t0 + k));
+                w[k] = exp_neg(i.at(from + 2 * Rows::BYTES, k, t0 + k));
+            }
+            share = whole && gates_share(a, w);
+            if (share) terms(std::true_type());
+        } else if (whole) {
+            terms(std::true_type());
+            share = top <= kShared;
+        }
+        if (!share) {
+            P = pk(1.f, 1.f);
+            H = pk(0.f, 0.f);
+            terms(std::false_type());
         }
 #pragma unroll
-        for (int k = kGatedRun - 1; k >= 0; --k) Q = mul2(a[k], add2(Q, gated_at<T>(from + 3 * kGatedPart<T>, k)));
+        for (int k = R - 1; k >= 0; --k) Q = mul2(a[k], add2(Q, dy_at(k)));
         {
             const float2 p2 = unpk(P), h2 = unpk(H);
-            pairs[(turn * kGatedWarps + warp) * 32 + lane] = make_float4(p2.x, p2.y, h2.x, h2.y);
-            ends[(turn * kGatedWarps + warp) * 32 + lane] = unpk(Q);
+            pairs[(turn * W + warp) * 32 + lane] = make_float4(p2.x, p2.y, h2.x, h2.y);
+            ends[(turn * W + warp) * 32 + lane] = unpk(Q);
         }
         __syncthreads();
-        float2 behind = mu, own_p = make_float2(1.f, 1.f), own_q = make_float2(0.f, 0.f), all_p = own_p, all_q = own_q;
-#pragma unroll
-        for (int k = 0; k < kGatedWarps; ++k)
-            if (k < warp) {
-                const float4 q = pairs[(turn * kGatedWarps + k) * 32 + lane];
-                h = onward(make_float2(q.x, q.y), h, make_float2(q.z, q.w));
+        const float4* pq = pairs + turn * W * 32 + lane;
+        const float2* eq = ends + turn * W * 32 + lane;
+        if (ranks > 1) {
+            if (warp == 0) {
+                float2 all = make_float2(0.f, 0.f), p = make_float2(1.f, 1.f);
+                back_through_runs<false>(pq, eq, W - 1, -1, all, p);
+                if (has_nan(all)) {
+                    all = make_float2(0.f, 0.f), p = make_float2(1.f, 1.f);
+                    back_through_runs<true>(pq, eq, W - 1, -1, all, p);
+                }
+                cluster_give(cl, step, rank, ranks, make_float4(p.x, p.y, all.x, all.y), ctl);
             }
-#pragma unroll
-        for (int k = kGatedWarps - 1; k >= 0; --k) {
-            const float4 q = pairs[(turn * kGatedWarps + k) * 32 + lane];
-            const float2 e = ends[(turn * kGatedWarps + k) * 32 + lane], p = make_float2(q.x, q.y);
-            if (k == warp) {
-                own_p = all_p;
-                own_q = all_q;
-            }
-            all_q = onward(p, all_q, e);
-            all_p = make_float2(all_p.x * p.x, all_p.y * p.y);
         }
-        if (ranks == 1) {
-            behind = onward(own_p, mu, own_q);
-            mu = onward(all_p, mu, all_q);
-        } else {
-            if (warp < ranks) give((uint32_t)__cvta_generic_to_shared(&cl->pair[turn][rank][lane]), warp, make_float4(all_p.x, all_p.y, all_q.x, all_q.y));
-            sm100::cluster_sync();
-            for (int k = ranks - 1; k >= 0; --k) {
-                const float4 q = cl->pair[turn][k][lane];
-                if (k == rank) behind = onward(own_p, mu, own_q);
-                mu = onward(make_float2(q.x, q.y), mu, make_float2(q.z, q.w));
+        float2 h, behind;  // the state in front of this warp's tokens, the gradient of the one behind them
+        auto exchange = [&](auto safe) {
+            constexpr bool SAFE = decltype(safe)::value;
+            const float2 zero = make_float2(0.f, 0.f);
+            float2 p = make_float2(1.f, 1.f), own_p = p, own = ranks == 1 ? mu : zero;
+            h = before;
+            through_runs<SAFE>(pq, warp, h, p);
+            back_through_runs<SAFE>(pq, eq, W - 1, warp, own, own_p);
+            if (ranks == 1) {
+                behind = mu = own;
+                back_through_runs<SAFE>(pq, eq, warp, -1, mu, own_p);
+            } else {
+                const float2 from_others = through_blocks<SAFE>(cl, turn, ranks, ranks - 1, rank, mu);
+                mu = through_blocks<SAFE>(cl, turn, ranks, rank, -1, from_others);
+                behind = run_after<SAFE>(from_others, own_p, own);
             }
+        };
+        next = kept_state(span - ranks);
+        if (ranks > 1) cluster_take(cl, step, ctl);
+        const float2 mu0 = mu;
+        exchange(std::false_type());
+        if (has_nan(h) || has_nan(behind) || has_nan(mu)) {
+            mu = mu0;
+            exchange(std::true_type());
         }
         {  // the states in front of the tokens
-            float2 p = make_float2(1.f, 1.f);
+            f32x2 p = pk(1.f, 1.f);
+            const f32x2 h2 = pk(h);
+            if (fabsf(h.x) < __int_as_float(0x7f800000) && fabsf(h.y) < __int_as_float(0x7f800000)) {
 #pragma unroll
-            for (int k = 0; k < kGatedRun; ++k) {
-                hs[k] = pk(onward(p, h, unpk(hs[k])));
-                const float2 ak = unpk(a[k]);
-                p = make_float2(p.x * ak.x, p.y * ak.y);
+                for (int k = 0; k < R; ++k) {
+                    hs[k] = fma2(p, h2, hs[k]);
+                    p = mul2(p, a[k]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    hs[k] = pk(onward(unpk(p), h, unpk(hs[k])));
+                    p = mul2(p, a[k]);
+                }
             }
         }
         f32x2 m = pk(behind);
-        const int64_t o = ((int64_t)b * g.seqlen + t0) * g.channels + c;
+        auto gradients = [&](auto one) {
+            constexpr bool ONE = decltype(one)::value;
+            int64_t at = ((int64_t)b * g.seqlen + t0 + R - 1) * g.channels;  // the same for all lanes
 #pragma unroll
-        for (int k = kGatedRun - 1; k >= 0; --k) {
-            const f32x2 xk = gated_at<T>(from, k), lam = add2(m, gated_at<T>(from + 3 * kGatedPart<T>, k));
-            f32x2 v, gi, v_rest, g_rest;
-            two_gates<true>(er[k], ei[k], v, gi, v_rest, g_rest);
-            float w0, w1;
-            unpk(w[k], w0, w1);
-            const f32x2 rs = pk(w0 < 0x1p-126f ? 0.f : rsqrt_fast(w0), w1 < 0x1p-126f ? 0.f : rsqrt_fast(w1));
-            const f32x2 ox = mul2(lam, mul2(mul2(w[k], rs), gi)), oi = mul2(mul2(ox, xk), g_rest);
-            // q = lam u a (h - (a / s) g x)
-            const f32x2 q = mul2(mul2(lam, mul2(mul2(A, v), a[k])), fma2(mul2(mul2(a[k], rs), mul2(gi, xk)), pk(-1.f, -1.f), hs[k]));
-            const f32x2 orr = mul2(q, v_rest);
-            m = mul2(a[k], lam);
-            if (t0 + k < n) {
-                dA = add2(dA, q);
-                const int64_t at = o + (int64_t)k * g.channels;
-                store_vec<T, 2>(dx + at, Vec<T, 2>::of_pairs({ox}), g.channels - c, vecy);
-                store_vec<T, 2>(dr + at, Vec<T, 2>::of_pairs({orr}), g.channels - c, vecy);
-                store_vec<T, 2>(di + at, Vec<T, 2>::of_pairs({oi}), g.channels - c, vecy);
+            for (int k = R - 1; k >= 0; --k, at -= g.channels) {
+                const f32x2 xk = x_at(k), lam = add2(m, dy_at(k));
+                f32x2 v, gi;
+                const f32x2 er = exp_neg(r.at(from + Rows::BYTES, k, t0 + k)), ei = exp_neg(i.at(from + 2 * Rows::BYTES, k, t0 + k));
+                two_gates<ONE>(er, ei, v, gi);
+                float w0, w1;
+                unpk(w[k], w0, w1);
+                const f32x2 rs = pk(rsqrt_fast(fmaxf(w0, 0x1p-126f)), rsqrt_fast(fmaxf(w1, 0x1p-126f)));  // s = w rs is 0 at w = 0
+                const f32x2 gx = mul2(lam, mul2(mul2(w[k], rs), gi)), gi_x = mul2(gi, xk);
+                const f32x2 q = mul2(mul2(lam, mul2(mul2(A, v), a[k])), fma2(mul2(mul2(a[k], rs), gi_x), pk(-1.f, -1.f), hs[k]));
+                m = mul2(a[k], lam);
+                const f32x2 gr = mul2(q, gate_rest<ONE>(er, v)), gi2 = mul2(mul2(gx, xk), gate_rest<ONE>(ei, gi));
+                if (ONE) {
+                    dA = add2(dA, q);
+                    if (in0) {
+                        store_vec<T, 2>(dx + at + (uint32_t)c, Vec<T, 2>::of_pairs({gx}), 2, true);
+                        store_vec<T, 2>(dr + at + (uint32_t)c, Vec<T, 2>::of_pairs({gr}), 2, true);
+                        store_vec<T, 2>(di + at + (uint32_t)c, Vec<T, 2>::of_pairs({gi2}), 2, true);
+                    }
+                } else if (t0 + k < n) {
+                    dA = add2(dA, q);
+                    store_vec<T, 2>(dx + at + (uint32_t)c, Vec<T, 2>::of_pairs({gx}), g.channels - c, vecy);
+                    store_vec<T, 2>(dr + at + (uint32_t)c, Vec<T, 2>::of_pairs({gr}), g.channels - c, vecy);
+                    store_vec<T, 2>(di + at + (uint32_t)c, Vec<T, 2>::of_pairs({gi2}), g.channels - c, vecy);
+                }
             }
-        }
+        };
+        if (share && vecy) gradients(std::true_type());
+        else gradients(std::false_type());
         __syncwarp();
-        fetch(step - kStages);
+        fetch(step % STAGES);
     }
     copies_wait<0>();
     if (rank == 0 && warp == 0 && dinit != nullptr) {
@@ -326,7 +454,7 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
         if (in0) p[0] = mu.x;
         if (in1) p[1] = mu.y;
     }
-    for (int t = n + rank * kGatedWarps + warp; t < g.seqlen; t += ranks * kGatedWarps) {
+    for (int t = n + rank * W + warp; t < g.seqlen; t += ranks * W) {
         const int64_t at = ((int64_t)b * g.seqlen + t) * g.channels + c;
         store_vec<T, 2>(dx + at, Vec<T, 2>::zero(), g.channels - c, vecy);
         store_vec<T, 2>(dr + at, Vec<T, 2>::zero(), g.channels - c, vecy);
@@ -338,7 +466,7 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
     if (warp == 0) {
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kGatedWarps; ++k) {
+        for (int k = 0; k < W; ++k) {
             const float2 e = ends[k * 32 + lane];
             s.x += e.x;
             s.y += e.y;
@@ -347,7 +475,7 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
         if (in0) p[0] = s.x;
         if (in1) p[1] = s.y;
     }
-    if (ranks > 1) sm100::cluster_sync();
+    cluster_end(cl, steps, ranks, ctl);
 }
 
 // dA: the blocks' sums of q, added in a fixed order, over A.  (`partial` is written while this kernel may already run.)
@@ -379,43 +507,53 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g, float* sta
     const auto r = load_vec<T, V>(static_cast<const T*>(g.r) + b * g.r_batch + c, left, vec);
     const auto i = load_vec<T, V>(static_cast<const T*>(g.i) + b * g.i_batch + c, left, vec);
     const int slot = row_slot(slots, b, nslots, threadIdx.x == 0 ? err : nullptr);
-    f32x2 out[(V + 1) / 2];
+    constexpr int N = (V + 1) / 2;
+    f32x2 out[N], h[N];
+    float top = 0.f;
     float* p = state + (int64_t)(slot < 0 ? 0 : slot) * g.channels + c;
 #pragma unroll
-    for (int e = 0; e < (V + 1) / 2; ++e) {
-        const bool in0 = 2 * e < left && slot >= 0, in1 = 2 * e + 1 < V && 2 * e + 1 < left && slot >= 0;
-        const f32x2 A = pk(in0 ? g.A[c + 2 * e] : 0.f, in1 ? g.A[c + 2 * e + 1] : 0.f);
-        f32x2 v, gi, a, w;
-        two_gates(exp_neg(r.pair(e)), exp_neg(i.pair(e)), v, gi);
-        decay_terms(mul2(A, v), a, w);
-        float w0, w1;
-        unpk(w, w0, w1);
-        const f32x2 h = pk(in0 ? p[2 * e] : 0.f, in1 ? p[2 * e + 1] : 0.f);
-        out[e] = fma2(a, h, mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.pair(e)));
+    for (int e = 0; e < N; ++e)
+        h[e] = pk(slot >= 0 && 2 * e < left ? p[2 * e] : 0.f, slot >= 0 && 2 * e + 1 < V && 2 * e + 1 < left ? p[2 * e + 1] : 0.f);
+    auto token = [&](auto one) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const f32x2 A = pk(2 * e < left ? g.A[c + 2 * e] : -1.f, 2 * e + 1 < V && 2 * e + 1 < left ? g.A[c + 2 * e + 1] : -1.f);
+            f32x2 v, gi, a, w;
+            two_gates<decltype(one)::value>(exp_neg(r.pair(e)), exp_neg(i.pair(e)), v, gi, top);
+            decay_terms(mul2(A, v), a, w);
+            float w0, w1;
+            unpk(w, w0, w1);
+            out[e] = fma2(a, h[e], mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.pair(e)));
+        }
+    };
+    token(std::true_type());
+    if (!(top <= kShared)) token(std::false_type());
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
         const float2 o = unpk(out[e]);
-        if (in0) p[2 * e] = o.x;
-        if (in1) p[2 * e + 1] = o.y;
+        if (slot >= 0 && 2 * e < left) p[2 * e] = o.x;
+        if (slot >= 0 && 2 * e + 1 < V && 2 * e + 1 < left) p[2 * e + 1] = o.y;
         if (slot < 0) out[e] = pk(0.f, 0.f);
     }
     store_vec<T, V>(y + (int64_t)b * g.channels + c, Vec<T, V>::of_pairs(out), left, vec);
 }
 
-// Blocks of a cluster, a power of two: enough that about three blocks are there for every SM, none without a step.
-int gated_ranks(const GatedArgs& g) {
-    const int64_t blocks = (int64_t)ceil_div(g.channels, kGatedTile) * g.batch;
-    const int most = ceil_div(g.seqlen, kGatedSpan);
-    int k = 1;
-    while (k < 8 && 2 * k <= most && blocks * k * 2 <= 3 * kSms) k *= 2;
-    return k;
+// Blocks of a cluster: as many as keep `resident` blocks on every SM, none without a step.
+int gated_ranks(const GatedArgs& g, int resident, int span) {
+    const int64_t blocks = (int64_t)ceil_div(g.channels, kGatedTile) * g.batch, want = (int64_t)resident * kSms / blocks;
+    const int most = ceil_div(g.seqlen, span), k = want < kGatedRanks ? (int)want : kGatedRanks;
+    return k < 1 ? 1 : k < most ? k : most;
 }
+template <typename T>
+int back_ranks(const GatedArgs& g) { return gated_ranks(g, kBackResident<T>, kBackWarps * R); }
 
 template <typename K, typename... Args>
-int launch_cluster(K kernel, dim3 grid, int ranks, int smem, cudaStream_t s, Args... args) {
-    const int r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+int launch_cluster(K kernel, dim3 grid, int threads, int ranks, int smem, cudaStream_t s, Args... args) {
+    const int r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 227 * 1024);
     if (r != SSD_OK) return r;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kGatedThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
@@ -437,30 +575,47 @@ bool rows_in_vectors(const GatedArgs& g) {
     return aligned_to(g.x, 16) && aligned_to(g.r, 16) && aligned_to(g.i, 16);
 }
 
-template <typename T>
-int forward_of(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
-    const int ranks = gated_ranks(g);
+template <typename T, int W, bool VEC>
+int forward_rows(const GatedArgs& g, int ranks, void* y, float* final_state, float* states, cudaStream_t s) {
     launch_begin(kKindGated, s);
-    const int r = launch_cluster(gated_forward_kernel<T>, dim3(ceil_div(g.channels, kGatedTile) * ranks, g.batch), ranks, forward_smem<T>(), s, g, ranks,
-                                 rows_in_vectors<T>(g), g.channels % 2 == 0 && aligned_to(y, 2 * sizeof(T)), static_cast<T*>(y), final_state, states);
+    const int r = launch_cluster(gated_forward_kernel<T, W, VEC>, dim3(ceil_div(g.channels, kGatedTile) * ranks, g.batch), 32 * W, ranks,
+                                 forward_smem<T, W, VEC>(ranks), s, g, wait_control(kKindGated), ranks,
+                                 g.channels % 2 == 0 && aligned_to(y, 2 * sizeof(T)), static_cast<T*>(y), final_state, states);
     const int e = launch_end(kKindGated, s);
     return r != SSD_OK ? r : e;
 }
-
+// Eight warps a block; four, and so twice the blocks, where rows are too short for the clusters that would fill the SMs (512 tokens of
+// 256 channels of float32: 4.7 us with four, 5.5 with eight; 65536 of 2048 of bfloat16: 324 and 299; 2 x 4096 of 4096: 71 and 68).
+template <typename T, bool VEC>
+int forward_warps(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
+    const int eight = gated_ranks(g, 2, 8 * R);
+    if (eight == ceil_div(g.seqlen, 8 * R)) return forward_rows<T, 4, VEC>(g, gated_ranks(g, 4, 4 * R), y, final_state, states, s);
+    return forward_rows<T, 8, VEC>(g, eight, y, final_state, states, s);
+}
 template <typename T>
-int backward_of(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
-    const int ranks = gated_ranks(g);
+int forward_of(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
+    return rows_in_vectors<T>(g) ? forward_warps<T, true>(g, y, final_state, states, s) : forward_warps<T, false>(g, y, final_state, states, s);
+}
+
+template <typename T, bool VEC>
+int backward_rows(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
+    constexpr int W = kBackWarps, S = kBackStages<T>;
+    const int ranks = back_ranks<T>(g);
     const bool vecy = g.channels % 2 == 0 && aligned_to(d.dx, 2 * sizeof(T)) && aligned_to(d.dr, 2 * sizeof(T)) && aligned_to(d.di, 2 * sizeof(T));
     launch_begin(kKindGatedBwd, s);
-    int r = launch_cluster(gated_backward_kernel<T>, dim3(ceil_div(g.channels, kGatedTile) * ranks, g.batch), ranks, backward_smem<T>(), s, g, states,
-                           static_cast<const T*>(d.dy), d.dfinal, ranks, rows_in_vectors<T>(g) && aligned_to(d.dy, 16), vecy, static_cast<T*>(d.dx),
+    int r = launch_cluster(gated_backward_kernel<T, W, S, VEC>, dim3(ceil_div(g.channels, kGatedTile) * ranks, g.batch), 32 * W, ranks,
+                           backward_smem<T, W, S, VEC>(ranks), s, g, states, static_cast<const T*>(d.dy), d.dfinal, wait_control(kKindGatedBwd), ranks, vecy, static_cast<T*>(d.dx),
                            static_cast<T*>(d.dr), static_cast<T*>(d.di), d.dinit, partial);
-    int e = launch_end(kKindGatedBwd, s);
+    const int e = launch_end(kKindGatedBwd, s);
     r = r != SSD_OK ? r : e;
     if (r != SSD_OK) return r;
     launch_begin(kKindGatedBwd, s);
     launch_dependent(gated_sums_kernel, dim3(ceil_div(g.channels, 32)), dim3(256), 0, s, (const float*)partial, ranks * g.batch, g.channels, g.A, d.dA);
     return launch_end(kKindGatedBwd, s);
+}
+template <typename T>
+int backward_of(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
+    return rows_in_vectors<T>(g) && aligned_to(d.dy, 16) ? backward_rows<T, true>(g, d, states, partial, s) : backward_rows<T, false>(g, d, states, partial, s);
 }
 
 template <typename T>
@@ -476,7 +631,10 @@ int step_of(const GatedArgs& g, float* state, const int* slots, int nslots, void
 }  // namespace
 
 size_t gated_states_floats(const GatedArgs& g) { return (size_t)g.batch * ceil_div(g.seqlen, kGatedSpan) * g.channels; }
-size_t gated_sums_floats(const GatedArgs& g) { return (size_t)g.batch * gated_ranks(g) * g.channels; }
+size_t gated_sums_floats(const GatedArgs& g) {
+    const int ranks = g.dtype == SSD_BF16 ? back_ranks<__nv_bfloat16>(g) : g.dtype == SSD_F16 ? back_ranks<__half>(g) : back_ranks<float>(g);
+    return (size_t)g.batch * ranks * g.channels;
+}
 
 int launch_gated_forward(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
     if (g.dtype == SSD_BF16) return forward_of<__nv_bfloat16>(g, y, final_state, states, s);

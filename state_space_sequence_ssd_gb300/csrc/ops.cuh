@@ -390,6 +390,7 @@ int launch_rotary(const RotaryArgs& g, cudaStream_t s);
 // Workspace, error words and device size, implemented in ssd_api.cu.
 int take_workspace(void** ptr, size_t bytes, cudaStream_t s);
 int* error_words();
+Ctl wait_control(int kind);  // of a kernel of this kind: its error words, wait limit and test hook
 int multiprocessors();
 
 }  // namespace ssd

@@ -461,6 +461,7 @@ namespace ssd {
 
 int take_workspace(void** ptr, size_t bytes, cudaStream_t s) { return workspace_alloc(ptr, bytes, s); }
 int* error_words() { return device_error_ptr(); }
+Ctl wait_control(int kind) { return make_ctl(device_error_ptr(), kind); }
 int multiprocessors() { return device_sms(); }
 
 }  // namespace ssd

@@ -58,10 +58,13 @@ CASES = [("f32", 1, 1, 1, True, None, (0, 0), 1.0, (0.01, 1.0)),
          ("f32", 1, 512, 256, True, None, (0, 0), 1.0, (0.008, 0.84)),
          ("bf16", 2, 1000, 200, True, [999, 1000], (8, 8), 1.0, (0.008, 0.84)),
          ("f16", 2, 3001, 16, False, None, (0, 0), 1.0, (0.0001, 0.1)),
-         ("f32", 40, 300, 130, True, None, (2, 0), 30.0, (0.01, 10.0)),     # clusters of four
-         ("bf16", 75, 200, 128, False, None, (0, 0), 1.0, (0.01, 1.0)),     # clusters of two
-         ("bf16", 300, 70, 72, True, None, (0, 0), 1.0, (0.01, 1.0)),       # no clusters
-         ("f16", 260, 129, 65, True, None, (1, 1), 1.0, (0.01, 1.0))]
+         # (warps a block and blocks a cluster of the forward pass; blocks a cluster of the gradient)
+         ("f32", 40, 300, 130, True, None, (2, 0), 30.0, (0.01, 10.0)),     # 8 and 2; 3
+         ("bf16", 75, 200, 128, False, None, (0, 0), 1.0, (0.01, 1.0)),     # 4 and 4; 2
+         ("bf16", 300, 70, 72, True, None, (0, 0), 1.0, (0.01, 1.0)),       # 4 and 1; 1
+         ("f16", 260, 129, 65, True, None, (1, 1), 1.0, (0.01, 1.0)),       # 8 and 1; 1
+         ("bf16", 50, 1300, 64, True, None, (8, 0), 1.0, (0.01, 1.0)),      # 8 and 6; 6
+         ("f16", 1, 5000, 40, False, [4242], (0, 0), 1.0, (0.001, 0.1))]    # 8 and 8; 8
 
 
 def make(c, seed=5):
@@ -239,3 +242,27 @@ def test_a_slot_past_the_pool_is_reported(ssd):
     y = ssd.ssd_gated_step(x, x, x, A, state, torch.tensor([3, 1], dtype=torch.int32, device="cuda"))
     assert ssd.ssd_get_device_error() == 8 and ssd.ssd_get_device_error() == 0
     assert bool((y[0] == 0).all()) and bool((y[1] != 0).all()) and bool((state[[0, 2]] == 0).all())
+
+
+def test_a_wait_that_runs_out_is_reported(ssd):
+    """A cluster's exchange that never completes: the kernel gives up, says so, and the next call is right."""
+    from state_space_sequence_ssd_gb300 import _ffi
+    lib = _ffi.lib()
+    kinds = {lib.ssd_kernel_name(k).decode(): k for k in range(32)}
+    d, b, L, ch = Draw(13), 2, 1000, 64
+    x, r, i, A, dy = d.normal(b, L, ch), d.normal(b, L, ch), d.normal(b, L, ch), -d.normal(ch).abs() - 0.1, d.normal(b, L, ch)
+    want, _, states = ssd.ssd_gated_forward(x, r, i, A, want_states=True)
+    grads = ssd.ssd_gated_backward(x, r, i, A, dy, states=states)
+    for name, call in (("gated", lambda: ssd.ssd_gated_forward(x, r, i, A)[0]), ("gated_bwd", lambda: ssd.ssd_gated_backward(x, r, i, A, dy, states=states)["dx"])):
+        lib.ssd_debug_set_wait_limit_ns(2_000_000)
+        lib.ssd_debug_stall(1 << kinds[name])
+        try:
+            call()
+            torch.cuda.synchronize()
+            assert ssd.ssd_get_device_error() == _ffi.SSD_ERR_TIMEOUT
+        finally:
+            lib.ssd_debug_stall(0)
+            lib.ssd_debug_set_wait_limit_ns(0)
+        assert ssd.ssd_get_device_error() == 0
+        assert torch.equal(call(), want if name == "gated" else grads["dx"])
+    assert ssd.ssd_get_device_error() == 0
