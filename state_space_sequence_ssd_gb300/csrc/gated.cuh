@@ -140,23 +140,31 @@ __device__ __forceinline__ float2 run_after(float2 h, float4 q) {
 __device__ __forceinline__ float2 times(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
 __device__ __forceinline__ bool has_nan(float2 v) { return !(v.x == v.x && v.y == v.y); }
 
+// Four bytes from global to shared memory without a register between.
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
 // A warp's R rows (tokens) of one tensor, 64 channels each, on their way through shared memory.  VEC: rows are whole 16-byte vectors,
-// and lie there as they are.  Else a row's aligned 16-byte chunks are copied, the first with what lies in front of the row in it,
-// into rows that are one chunk longer; where such a chunk is not within the tensor's own row, its elements are copied one by one.
+// and lie there as they are.  Else they are copied in words of four bytes, a word a lane; a row of 16-bit elements that begins in the
+// middle of a word lies there shifted by an element, and its words that are not within the tensor's own row are copied
+// as the one element that is.
 template <typename T, int R, bool VEC>
 struct GatedRows {
-    static constexpr int PITCH = kGatedTile * (int)sizeof(T) + (VEC ? 0 : 16), BYTES = R * PITCH, V = 16 / (int)sizeof(T);
-    const T* p;       // VEC: this lane's vector of the row's first token; else that token at the block's first channel
-    int phase, pitch; // !VEC: bytes of its address past a multiple of 16, and what a token adds
+    static constexpr bool HALF = sizeof(T) == 2;
+    static constexpr int PITCH = kGatedTile * (int)sizeof(T) + (VEC || !HALF ? 0 : 4), BYTES = R * PITCH, V = 16 / (int)sizeof(T);
+    const T* p;  // VEC: this lane's vector of the row's first token; else that token at the block's first channel
+    // 16-bit elements without VEC: whether even and odd tokens' rows begin in the middle of a word, 0 or 1.  (A run begins at an even token.)
+    int shift[2];
 
     __device__ __forceinline__ void begin(const void* tensor, int64_t batch, int64_t token, int c0) {
         p = static_cast<const T*>(tensor) + batch + c0;
         if (VEC) {
             const int lane = threadIdx.x & 31;
             p += lane / (kGatedTile / V) * token + lane % (kGatedTile / V) * V;
-        } else {
-            phase = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-            pitch = (int)((uint64_t)token * sizeof(T) & 15);
+        } else if (HALF) {
+            shift[0] = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+            shift[1] = (shift[0] + (int)token) & 1;
         }
     }
     // Tokens t0 .. t0 + R - 1 to `to`; those from n on and channels past the tensor's (`left` from the block's first) are zeros, or,
@@ -177,41 +185,53 @@ struct GatedRows {
                 for (int k = 0; k < R / ROWS; ++k, q += ROWS * token) copy16(to + k * 32 * 16, q, in && t0 + k * ROWS + r0 < n);
             }
         } else {
-            constexpr int PER = kGatedTile / V + 1;
-            for (int k = lane; k < R * PER; k += 32) {
-                const int r = k / PER, j = k - r * PER;
-                if (t0 + r >= n) continue;
-                const T* row = p + (t0 + r) * token;  // aligned down: the chunks; its own channels are row - c0 .. row + left
-                const int off = (phase + (t0 + r) * pitch) & 15;
-                const int first = (j * 16 - off) / (int)sizeof(T);  // the chunk's first channel (off is a multiple of the element)
-                if (first >= (left < kGatedTile ? left : kGatedTile)) continue;
-                if (first >= -c0 && first + V <= left) {
-                    copy16(to + r * PITCH + j * 16, row + first, true);
-                } else {
+            const int rows = n - t0 < R ? n - t0 : R;
+            const T* q = p + t0 * token;
+            if constexpr (HALF) {
+                // element e of row r lies at T number e + shift[r & 1] of its place
+                const bool even = 2 * lane - shift[0] >= -c0 && 2 * lane - shift[0] + 1 < left;
+                const bool odd = 2 * lane - shift[1] >= -c0 && 2 * lane - shift[1] + 1 < left;
+                const T *from0 = q + 2 * lane - shift[0], *from1 = q + token + 2 * lane - shift[1];
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (first + e >= 0 && first + e < left) reinterpret_cast<T*>(to + r * PITCH + j * 16)[e] = row[first + e];
+                for (int r = 0; r < R; r += 2, from0 += 2 * token, from1 += 2 * token) {
+                    if (even && r < rows) copy4(to + r * PITCH + lane * 4, from0);
+                    if (odd && r + 1 < rows) copy4(to + (r + 1) * PITCH + lane * 4, from1);
+                }
+                // a lane a row: a shifted row's last channel, which begins one more word, and the elements whose word is only half the row's
+                if (lane < rows) {
+                    const int off = shift[lane & 1], last = left - 1;
+                    const T* row = q + lane * token;
+                    T* place = reinterpret_cast<T*>(to + lane * PITCH) + off;
+                    if (off && left > kGatedTile) copy4(place + kGatedTile - 1, row + kGatedTile - 1);
+                    if (off && c0 == 0) place[0] = row[0];
+                    if (last < kGatedTile && (last + off) % 2 == 0) place[last] = row[last];
+                }
+            } else {
+                const T* from = q + lane;
+                to += lane * 4;
+#pragma unroll
+                for (int r = 0; r < R; ++r, from += token) {
+                    if (lane < left && r < rows) copy4(to + r * PITCH, from);
+                    if (lane + 32 < left && r < rows) copy4(to + r * PITCH + 128, from + 32);
                 }
             }
         }
     }
-    // This lane's two channels of row r, which is token t.
-    __device__ __forceinline__ f32x2 at(const unsigned char* part, int r, int t) const {
+    // This lane's two channels of row r.
+    __device__ __forceinline__ f32x2 at(const unsigned char* part, int r) const {
         const unsigned char* q = part + r * PITCH + (threadIdx.x & 31) * 2 * (int)sizeof(T);
-        if constexpr (VEC) {
-            Vec<T, 2> v;
-            if constexpr (sizeof(T) == 4) {
-                const uint2 u = *reinterpret_cast<const uint2*>(q);
-                v.w[0] = u.x;
-                v.w[1] = u.y;
-            } else {
-                v.w[0] = *reinterpret_cast<const uint32_t*>(q);
-            }
-            return v.pair(0);
+        Vec<T, 2> v;
+        if constexpr (!HALF) {
+            const uint2 u = *reinterpret_cast<const uint2*>(q);
+            v.w[0] = u.x;
+            v.w[1] = u.y;
+        } else if constexpr (VEC) {
+            v.w[0] = *reinterpret_cast<const uint32_t*>(q);
         } else {
-            const T* e = reinterpret_cast<const T*>(q + ((phase + t * pitch) & 15));
+            const T* e = reinterpret_cast<const T*>(q) + shift[r & 1];
             return pk(to_f32<T>(e[0]), to_f32<T>(e[1]));
         }
+        return v.pair(0);
     }
 };
 

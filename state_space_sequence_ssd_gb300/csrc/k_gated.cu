@@ -111,8 +111,8 @@ gated_forward_kernel(GatedArgs g, Ctl ctl, int ranks, bool vecy, T* __restrict__
         f32x2 a[R], bx[R], P = pk(1.f, 1.f), H = pk(0.f, 0.f);  // a and bx hold the gates' exponentials first
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            a[k] = exp_neg(r.at(mine + Rows::BYTES, k, t0 + k));
-            bx[k] = exp_neg(i.at(mine + 2 * Rows::BYTES, k, t0 + k));
+            a[k] = exp_neg(r.at(mine + Rows::BYTES, k));
+            bx[k] = exp_neg(i.at(mine + 2 * Rows::BYTES, k));
         }
         auto terms = [&](auto one) {
             constexpr bool ONE = decltype(one)::value;
@@ -123,7 +123,7 @@ gated_forward_kernel(GatedArgs g, Ctl ctl, int ranks, bool vecy, T* __restrict__
                 decay_terms(mul2(A, v), a[k], w);
                 float w0, w1;
                 unpk(w, w0, w1);
-                bx[k] = mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.at(mine, k, t0 + k));
+                bx[k] = mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.at(mine, k));
                 if (!ONE && t0 + k >= n) {  // tokens past the length keep the state
                     a[k] = pk(1.f, 1.f);
                     bx[k] = pk(0.f, 0.f);
@@ -308,8 +308,8 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
         f32x2 P = pk(1.f, 1.f), H = pk(0.f, 0.f), Q = pk(0.f, 0.f);
         const bool whole = t0 + R <= n;
         // VEC: x and dy are zero past the length already
-        auto x_at = [&](int k) { return VEC || whole || t0 + k < n ? x.at(from, k, t0 + k) : pk(0.f, 0.f); };
-        auto dy_at = [&](int k) { return VEC || whole || t0 + k < n ? gy.at(from + 3 * Rows::BYTES, k, t0 + k) : pk(0.f, 0.f); };
+        auto x_at = [&](int k) { return VEC || whole || t0 + k < n ? x.at(from, k) : pk(0.f, 0.f); };
+        auto dy_at = [&](int k) { return VEC || whole || t0 + k < n ? gy.at(from + 3 * Rows::BYTES, k) : pk(0.f, 0.f); };
         float top = 0.f;
         auto terms = [&](auto one) {
             constexpr bool ONE = decltype(one)::value;
@@ -317,7 +317,7 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
             for (int k = 0; k < R; ++k) {
                 f32x2 v, gi;
                 if (FIRST) two_gates<ONE>(a[k], w[k], v, gi);
-                else two_gates<ONE>(exp_neg(r.at(from + Rows::BYTES, k, t0 + k)), exp_neg(i.at(from + 2 * Rows::BYTES, k, t0 + k)), v, gi, top);
+                else two_gates<ONE>(exp_neg(r.at(from + Rows::BYTES, k)), exp_neg(i.at(from + 2 * Rows::BYTES, k)), v, gi, top);
                 decay_terms(mul2(A, v), a[k], w[k]);
                 if (!ONE && t0 + k >= n) {  // tokens past the length keep the state
                     a[k] = pk(1.f, 1.f);
@@ -334,8 +334,8 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
         if (FIRST) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                a[k] = exp_neg(r.at(from + Rows::BYTES, k, t0 + k));
-                w[k] = exp_neg(i.at(from + 2 * Rows::BYTES, k, t0 + k));
+                a[k] = exp_neg(r.at(from + Rows::BYTES, k));
+                w[k] = exp_neg(i.at(from + 2 * Rows::BYTES, k));
             }
             share = whole && gates_share(a, w);
             if (share) terms(std::true_type());
@@ -419,7 +419,7 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
             for (int k = R - 1; k >= 0; --k, at -= g.channels) {
                 const f32x2 xk = x_at(k), lam = add2(m, dy_at(k));
                 f32x2 v, gi;
-                const f32x2 er = exp_neg(r.at(from + Rows::BYTES, k, t0 + k)), ei = exp_neg(i.at(from + 2 * Rows::BYTES, k, t0 + k));
+                const f32x2 er = exp_neg(r.at(from + Rows::BYTES, k)), ei = exp_neg(i.at(from + 2 * Rows::BYTES, k));
                 two_gates<ONE>(er, ei, v, gi);
                 float w0, w1;
                 unpk(w[k], w0, w1);
