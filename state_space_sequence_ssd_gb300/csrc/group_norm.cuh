@@ -17,10 +17,22 @@
 namespace ssd {
 namespace {
 
+// sigmoid of two values.  Packed where it can be: its two constants stay in registers over a thread's many values.
+__device__ __forceinline__ f32x2 sigmoid_pair(f32x2 v) {
+    float a, b;
+    unpk(add2(exp2_2(mul2(v, pk(-kLog2e, -kLog2e))), pk(1.f, 1.f)), a, b);
+    return pk(rcp_fast(a), rcp_fast(b));
+}
 // silu(v) = v sigmoid(v) and its slope
 __device__ __forceinline__ f32x2 slope_of(f32x2 v, f32x2 sig) {
     const f32x2 one = pk(1.f, 1.f);
     return mul2(sig, fma2(v, fma2(sig, pk(-1.f, -1.f), one), one));
+}
+
+__device__ __forceinline__ float unpk_low(f32x2 v) {
+    float a, b;
+    unpk(v, a, b);
+    return a;
 }
 
 // Row and group of unit u (units that fit 32 bits, as all but the longest do, are divided there).
@@ -33,6 +45,10 @@ __device__ __forceinline__ void unit_of(int64_t u, int groups, int64_t& row, int
         group = (int)(u - row * groups);
     }
 }
+
+// Rows and groups that are whole 16-byte vectors are read in those (V = 8 or 4); others in pairs, an element at a time.
+template <int V>
+constexpr bool kWhole = V > 2;
 
 // Thread `lane` of a unit holds columns (lane + lanes i) V .. of its group.
 template <typename T, int V, int NV, int GATE>
@@ -53,8 +69,8 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + lanes * i) * V;
-        rx[i] = load_vec<T, V>(x + c, live ? per - c : 0, true);
-        if (GATE >= kGateAfter) rz[i] = load_vec<T, V>(z + c, live ? per - c : 0, true);
+        rx[i] = load_vec<T, V>(x + c, live ? per - c : 0, kWhole<V>);
+        if (GATE >= kGateAfter) rz[i] = load_vec<T, V>(z + c, live ? per - c : 0, kWhole<V>);
     }
     f32x2 q[NV][P], s2 = 0ull, v2 = 0ull;
 #pragma unroll
@@ -64,19 +80,20 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
             q[i][e] = rx[i].pair(e);
             if (GATE == kGateBefore) {
                 const f32x2 zz = rz[i].pair(e);
-                q[i][e] = mul2(q[i][e], mul2(zz, sigmoid2(zz)));
+                q[i][e] = mul2(q[i][e], mul2(zz, sigmoid_pair(zz)));
             }
             s2 = add2(s2, q[i][e]);
         }
     const float inv = 1.f / (float)per;
     const float m = g.rms ? 0.f : row_sum(sum2(s2), lanes, buf[0]) * inv;
-    const f32x2 m2 = pk(-m, V > 1 ? -m : 0.f);
+    const f32x2 m2 = pk(-m, -m);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if ((lane + lanes * i) * V < per) {
 #pragma unroll
             for (int e = 0; e < P; ++e) {
                 q[i][e] = add2(q[i][e], m2);
+                if (!kWhole<V> && (lane + lanes * i) * V + 1 >= per) q[i][e] = pk(unpk_low(q[i][e]), 0.f);  // half a pair
                 v2 = fma2(q[i][e], q[i][e], v2);
             }
         }
@@ -97,13 +114,13 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
 #pragma unroll
         for (int e = 0; e < P; ++e) {
             out[e] = fma2(mul2(q[i][e], pk(rs, rs)), w[e], b[e]);
-            if (GATE == kGateSilu) out[e] = mul2(out[e], sigmoid2(out[e]));
+            if (GATE == kGateSilu) out[e] = mul2(out[e], sigmoid_pair(out[e]));
             if (GATE == kGateAfter) {
                 const f32x2 zz = rz[i].pair(e);
-                out[e] = mul2(out[e], mul2(zz, sigmoid2(zz)));
+                out[e] = mul2(out[e], mul2(zz, sigmoid_pair(zz)));
             }
         }
-        store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), per - c, true);
+        store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), per - c, kWhole<V>);
     }
 }
 
@@ -156,80 +173,116 @@ __global__ void __launch_bounds__(kThreads) group_forward_wide_kernel(GroupNormA
 }
 
 // A block holds `side` groups of a row next to one another and kThreads / lanes / side rows at once, and walks the rows a grid's
-// height apart; its columns' sums stay in registers, and the next rows' loads are in flight while a row is summed.
-template <typename T, int V, int NV, int GATE>
-__global__ void __launch_bounds__(kThreads) group_backward_kernel(GroupNormArgs g, int lanes, int side, const float* __restrict__ mean,
-                                                                  const float* __restrict__ rstd, const T* __restrict__ dy, int64_t dy_row,
-                                                                  T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ partial, bool vecw) {
-    constexpr int P = (V + 1) / 2;
-    constexpr bool Z = GATE >= kGateAfter;
-    extern __shared__ float sums[];  // rows at once x 2 x the block's columns
+// height apart; its columns' sums stay in registers.  Whole vectors of the next rows are copied to shared memory that their thread
+// alone reads, so that they need neither registers nor barriers on their way.
+constexpr int kRowsAhead = 2;
+template <typename T, int V, int NV, int GATE, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormArgs g, int lanes, int side, const float* __restrict__ mean,
+                                                                     const float* __restrict__ rstd, const T* __restrict__ dy, int64_t dy_row,
+                                                                     T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ partial, bool vecw) {
+    constexpr int P = (V + 1) / 2, TENSORS = GATE >= kGateAfter ? 3 : 2;
+    constexpr bool Z = GATE >= kGateAfter, PRE = GATE == kGateSilu || GATE == kGateAfter;
+    extern __shared__ __align__(16) unsigned char smem[];  // copies; at the end rows at once x 2 x the block's columns
     __shared__ float2 buf[2][kThreads / 32];
     const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x / lanes, high = kThreads / lanes / side;
     const int per = g.width / g.groups, group = blockIdx.x * side + sub % side, base = group * per;
     const bool here = group < g.groups;
     const float inv = 1.f / (float)per;
-    f32x2 w[NV][P], b[NV][P], dw[NV][P], db[NV][P];
+    f32x2 w[NV][P], b[PRE && BIAS ? NV : 1][P], dw[NV][P], db[BIAS ? NV : 1][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + lanes * i) * V;
         load_columns<V>(g.weight == nullptr ? nullptr : g.weight + (here ? base : 0), c, per, vecw, 1.f, w[i]);
-        if (GATE == kGateSilu || GATE == kGateAfter) load_columns<V>(g.bias == nullptr ? nullptr : g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
+        if (PRE && BIAS) load_columns<V>(g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
 #pragma unroll
-        for (int e = 0; e < P; ++e) dw[i][e] = db[i][e] = 0ull;
+        for (int e = 0; e < P; ++e) dw[i][e] = db[BIAS ? i : 0][e] = 0ull;
     }
-    Vec<T, V> nx[NV], ng[NV], nz[NV];
-    float nm, nrs;
-    auto fetch = [&](int64_t row) {
+    const T *x = static_cast<const T*>(g.x), *z = static_cast<const T*>(g.z);
+    uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+    float nm[kRowsAhead], nrs[kRowsAhead];
+    auto fetch = [&](int64_t row, int turn) {
         const bool live = here && row < g.rows;
-        const int64_t at = live ? row : 0, off = live ? base : 0;
-        nm = live && mean != nullptr ? __ldg(mean + at * g.groups + group) : 0.f;
-        nrs = live ? __ldg(rstd + at * g.groups + group) : 0.f;
+        if (kWhole<V>) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + lanes * i) * V, left = live ? per - c : 0;
-            nx[i] = load_vec<T, V>(static_cast<const T*>(g.x) + at * g.x_row + off + c, left, true);
-            ng[i] = load_vec<T, V>(dy + at * dy_row + off + c, left, true);
-            if (Z) nz[i] = load_vec<T, V>(static_cast<const T*>(g.z) + at * g.z_row + off + c, left, true);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + lanes * i) * V;
+                const bool in = live && c < per;
+                uint4* to = ring + (turn * NV + i) * TENSORS * kThreads;
+                copy16(to, in ? x + row * g.x_row + base + c : x, in);
+                copy16(to + kThreads, in ? dy + row * dy_row + base + c : dy, in);
+                if (Z) copy16(to + 2 * kThreads, in ? z + row * g.z_row + base + c : z, in);
+            }
+            copies_commit();
         }
+        const float m = live && mean != nullptr ? __ldg(mean + row * g.groups + group) : 0.f, r = live ? __ldg(rstd + row * g.groups + group) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kRowsAhead; ++k)
+            if (k == turn) {
+                nm[k] = m;
+                nrs[k] = r;
+            }
     };
     const int64_t step = (int64_t)gridDim.y * high;
     int64_t row = (int64_t)blockIdx.y * high + sub / side;
-    fetch(row);
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k) fetch(row + k * step, k);
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.y * high; r0 < g.rows; r0 += step, row += step, turn ^= 1) {
+        static_assert(kRowsAhead == 2, "two turns");
         Vec<T, V> cx[NV], cg[NV], cz[NV];
-        const float rs = nrs;
-        const f32x2 rs2 = pk(rs, rs), shift = pk(-nm * rs, -nm * rs);
+        const float rs = turn ? nrs[1] : nrs[0], mn = turn ? nm[1] : nm[0];
+        const f32x2 rs2 = pk(rs, rs), shift = pk(-mn * rs, -mn * rs);
         f32x2 s1 = 0ull, s2 = 0ull;
-        f32x2 sig[NV][P], gn[NV][P];  // sigmoid of the gate; the gradient of n
+        f32x2 sig[Z ? NV : 1][P];  // of the gate
+        if (kWhole<V>) {
+            copies_wait<kRowsAhead - 1>();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            cx[i] = nx[i];
-            cg[i] = ng[i];
-            if (Z) cz[i] = nz[i];
+            for (int i = 0; i < NV; ++i) {
+                const uint4* from = ring + (turn * NV + i) * TENSORS * kThreads;
+                auto take = [&](Vec<T, V>& v, const uint4& u) {
+                    v.w[0] = u.x;
+                    v.w[1 % Vec<T, V>::WORDS] = u.y;
+                    v.w[2 % Vec<T, V>::WORDS] = u.z;
+                    v.w[3 % Vec<T, V>::WORDS] = u.w;
+                };
+                take(cx[i], from[0]);
+                take(cg[i], from[kThreads]);
+                if (Z) take(cz[i], from[2 * kThreads]);
+            }
+        } else {
+            const bool live = here && row < g.rows;
+            const int64_t at = live ? row : 0, off = live ? base : 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + lanes * i) * V, left = live ? per - c : 0;
+                cx[i] = load_vec<T, V>(x + at * g.x_row + off + c, left, false);
+                cg[i] = load_vec<T, V>(dy + at * dy_row + off + c, left, false);
+                if (Z) cz[i] = load_vec<T, V>(z + at * g.z_row + off + c, left, false);
+            }
         }
-        if (r0 + step < g.rows) fetch(row + step);
+        fetch(row + kRowsAhead * step, turn);
         auto xhat = [&](int i, int e) {
             f32x2 q = cx[i].pair(e);
             if (GATE == kGateBefore) q = mul2(q, mul2(cz[i].pair(e), sig[i][e]));
             return fma2(q, rs2, shift);
         };
+        auto pre = [&](int i, int e, f32x2 xh) { return BIAS ? fma2(xh, w[i][e], b[PRE && BIAS ? i : 0][e]) : mul2(xh, w[i][e]); };
+        auto gradient = [&](int i, int e, f32x2 xh) {  // of n; zero past the group's end
+            f32x2 gy = cg[i].pair(e);
+            if (GATE == kGateSilu) {
+                const f32x2 n = pre(i, e, xh);
+                gy = mul2(gy, slope_of(n, sigmoid_pair(n)));
+            }
+            if (GATE == kGateAfter) gy = mul2(gy, mul2(cz[i].pair(e), sig[i][e]));
+            return gy;
+        };
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                if (Z) sig[i][e] = sigmoid2(cz[i].pair(e));
-                const f32x2 xh = xhat(i, e);
-                f32x2 gy = cg[i].pair(e);  // zero past the group's end
-                if (GATE == kGateSilu) {
-                    const f32x2 n = fma2(xh, w[i][e], b[i][e]);
-                    gy = mul2(gy, slope_of(n, sigmoid2(n)));
-                }
-                if (GATE == kGateAfter) gy = mul2(gy, mul2(cz[i].pair(e), sig[i][e]));
-                gn[i][e] = gy;
-                const f32x2 gw = mul2(gy, w[i][e]);
-                db[i][e] = add2(db[i][e], gy);
+                if (Z) sig[Z ? i : 0][e] = sigmoid_pair(cz[i].pair(e));
+                const f32x2 xh = xhat(i, e), gy = gradient(i, e, xh), gw = mul2(gy, w[i][e]);
+                if (BIAS) db[BIAS ? i : 0][e] = add2(db[BIAS ? i : 0][e], gy);
                 dw[i][e] = fma2(gy, xh, dw[i][e]);
                 s1 = add2(s1, gw);
                 s2 = fma2(gw, xh, s2);
@@ -245,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) group_backward_kernel(GroupNormArgs 
             f32x2 o1[P], o2[P];
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                const f32x2 xh = xhat(i, e), gw = mul2(gn[i][e], w[i][e]);
+                const f32x2 xh = xhat(i, e), gw = mul2(gradient(i, e, xh), w[i][e]);
                 const f32x2 dq = fma2(gw, rs2, fma2(xh, pk(k2, k2), pk(k1, k1)));
                 o1[e] = dq;
                 if (GATE == kGateBefore) {
@@ -253,14 +306,17 @@ __global__ void __launch_bounds__(kThreads) group_backward_kernel(GroupNormArgs 
                     o1[e] = mul2(dq, mul2(zz, sig[i][e]));
                     o2[e] = mul2(mul2(dq, cx[i].pair(e)), slope_of(zz, sig[i][e]));
                 }
-                if (GATE == kGateAfter) o2[e] = mul2(mul2(cg[i].pair(e), fma2(xh, w[i][e], b[i][e])), slope_of(cz[i].pair(e), sig[i][e]));
+                if (GATE == kGateAfter) o2[e] = mul2(mul2(cg[i].pair(e), pre(i, e, xh)), slope_of(cz[i].pair(e), sig[i][e]));
             }
-            store_vec<T, V>(ox + c, Vec<T, V>::of_pairs(o1), per - c, true);
-            if (Z) store_vec<T, V>(oz + c, Vec<T, V>::of_pairs(o2), per - c, true);
+            store_vec<T, V>(ox + c, Vec<T, V>::of_pairs(o1), per - c, kWhole<V>);
+            if (Z) store_vec<T, V>(oz + c, Vec<T, V>::of_pairs(o2), per - c, kWhole<V>);
         }
     }
+    copies_wait<0>();
     if (partial == nullptr) return;
     // the block's columns, one sum for all rows at once
+    __syncthreads();  // the copies' place is the sums' now
+    float* sums = reinterpret_cast<float*>(smem);
     const int columns = side * per, first = blockIdx.x * columns;
     float* out = partial + (int64_t)blockIdx.y * 2 * g.width;
     float* to = sums + (sub / side) * 2 * columns + (sub % side) * per;
@@ -272,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) group_backward_kernel(GroupNormArgs 
             float p, q;
             unpk(dw[i][e / 2], p, q);
             const float a = e & 1 ? q : p;
-            unpk(db[i][e / 2], p, q);
+            unpk(db[BIAS ? i : 0][e / 2], p, q);
             const float d = e & 1 ? q : p;
             if (c >= per || !here) continue;
             if (high == 1) {
@@ -369,7 +425,7 @@ bool in_vectors(const GroupNormArgs& g) {
 
 template <typename T, int V, int GATE>
 int group_forward_of(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s) {
-    constexpr int M = V == 1 ? 4 : 1;
+    constexpr int M = kWhole<V> ? 1 : 4;
     const int64_t units = g.rows * g.groups;
     const int vecs = ceil_div(g.width / g.groups, V), lanes = row_lanes(units, vecs, 2 * M, 1), nv = ceil_div(vecs, lanes);
     const int64_t blocks = ceil_div64(units, kThreads / lanes);
@@ -386,24 +442,25 @@ int group_forward_of(const GroupNormArgs& g, void* y, float* mean, float* rstd, 
 
 template <typename T, int V, int GATE>
 int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
-    constexpr int M = V == 1 ? 4 : 1;
+    constexpr int M = kWhole<V> ? 1 : 4;
     const int vecs = ceil_div(g.width / g.groups, V), lanes = row_lanes(g.rows * g.groups, vecs, 2 * M, 1), nv = ceil_div(vecs, lanes);
     const int room = kThreads / lanes;
     int side = 1;
     while (side < room && side < g.groups) side *= 2;
-    const int high = room / side, smem = high == 1 || partial == nullptr ? 0 : high * 2 * side * (g.width / g.groups) * 4;
+    const int high = room / side, sums = high == 1 || partial == nullptr ? 0 : high * 2 * side * (g.width / g.groups) * 4;
     const bool vecw = aligned_to(g.weight, 16) && aligned_to(g.bias, 16);
     const T* dy = static_cast<const T*>(d.dy);
     T *dx = static_cast<T*>(d.dx), *dz = static_cast<T*>(d.dz);
     launch_begin(kKindGroupNormBwd, s);
     int r = SSD_OK;
-    auto go = [&](auto kernel) {
-        if (smem > 48 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 227 * 1024);
+    auto go = [&](auto kernel, int held) {
+        const int copies = kWhole<V> ? kRowsAhead * held * (GATE >= kGateAfter ? 3 : 2) * kThreads * 16 : 0, smem = copies > sums ? copies : sums;
+        if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 100 * 1024);  // beside static memory
         if (r == SSD_OK)
             kernel<<<dim3(ceil_div(g.groups, side), parts), kThreads, smem, s>>>(g, lanes, side, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial, vecw);
     };
-    if (nv <= 1 * M) go(group_backward_kernel<T, V, 1 * M, GATE>);
-    else if (nv <= 2 * M) go(group_backward_kernel<T, V, 2 * M, GATE>);
+    if (nv <= 1 * M) g.bias != nullptr ? go(group_backward_kernel<T, V, 1 * M, GATE, true>, 1) : go(group_backward_kernel<T, V, 1 * M, GATE, false>, 1);
+    else if (nv <= 2 * M) g.bias != nullptr ? go(group_backward_kernel<T, V, 2 * M, GATE, true>, 2) : go(group_backward_kernel<T, V, 2 * M, GATE, false>, 2);
     else
         group_backward_wide_kernel<T><<<dim3(g.groups, parts), kThreads, 0, s>>>(g, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial);
     const int e = launch_end(kKindGroupNormBwd, s);
@@ -428,13 +485,13 @@ int group_backward_gate(const GroupNormArgs& g, const GroupNormGrads& d, float* 
 template <typename T>
 int group_forward_type(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s) {
     if (in_vectors<T>(g) && aligned_to(y, 16)) return group_forward_gate<T, 16 / sizeof(T)>(g, y, mean, rstd, s);
-    return group_forward_gate<T, 1>(g, y, mean, rstd, s);
+    return group_forward_gate<T, 2>(g, y, mean, rstd, s);
 }
 template <typename T>
 int group_backward_type(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
     if (in_vectors<T>(g) && d.dy_row % (16 / sizeof(T)) == 0 && aligned_to(d.dy, 16) && aligned_to(d.dx, 16) && aligned_to(d.dz, 16))
         return group_backward_gate<T, 16 / sizeof(T)>(g, d, partial, parts, s);
-    return group_backward_gate<T, 1>(g, d, partial, parts, s);
+    return group_backward_gate<T, 2>(g, d, partial, parts, s);
 }
 
 }  // namespace

@@ -18,6 +18,9 @@ SIZES = [("f32", 1, 1, 1, (0, 0), True, True),
          ("f16", 4, 1, 16384, (0, 0), True, True),          # wider than the registers
          ("f32", 3, 2, 4999, (1, 0), True, False),          # the same, odd
          ("bf16", 6000, 4, 64, (0, 0), True, True),
+         ("f32", 2, 1, 9001, (0, 0), True, True),           # odd and wider than the registers
+         ("bf16", 4000, 2, 40, (8, 8), True, True),
+         ("f32", 3000, 1, 130, (0, 0), True, False),
          ("bf16", 1, 1, 4096, (0, 0), False, False),
          ("f16", 2, 7, 1, (2, 1), True, True)]
 GATES = ["none", "silu", "after", "before"]
