@@ -140,11 +140,6 @@ __device__ __forceinline__ float2 run_after(float2 h, float4 q) {
 __device__ __forceinline__ float2 times(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
 __device__ __forceinline__ bool has_nan(float2 v) { return !(v.x == v.x && v.y == v.y); }
 
-// Four bytes from global to shared memory without a register between.
-__device__ __forceinline__ void copy4(void* to, const void* from) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
-
 // A warp's R rows (tokens) of one tensor, 64 channels each, on their way through shared memory.  VEC: rows are whole 16-byte vectors,
 // and lie there as they are.  Else they are copied in words of four bytes, a word a lane; a row of 16-bit elements that begins in the
 // middle of a word lies there shifted by an element, and its words that are not within the tensor's own row are copied

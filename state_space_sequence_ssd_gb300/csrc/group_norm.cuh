@@ -124,6 +124,120 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
     }
 }
 
+// The same for many rows of whole vectors: a resident grid whose blocks walk the rows.  A thread keeps its columns, and with them their
+// weights; a block holds `side` groups of a row next to one another and kThreads / lanes / side rows at once.  A thread's
+// pieces of the next rows are copied to shared memory that it alone reads.  8192 x 4096 of bfloat16 in 8 groups, gated in front:
+// 33.7 us (6.0 TB/s; 41.0 with the kernel above, whose threads spend half their instructions on addresses and weights); copies three rows
+// ahead 36.2, four blocks an SM 36.4.
+constexpr int kForwardAhead = 2;
+constexpr int kWalkers = 3;  // blocks of an SM
+template <typename T, int V, int NV, int GATE>
+__global__ void __launch_bounds__(kThreads, kWalkers) group_walk_kernel(GroupNormArgs g, int lanes, int side, T* __restrict__ y, float* __restrict__ mean,
+                                                                 float* __restrict__ rstd, bool vecw) {
+    constexpr int P = V / 2, TENSORS = GATE >= kGateAfter ? 2 : 1;
+    constexpr bool Z = GATE >= kGateAfter;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float2 buf[2][kThreads / 32];
+    const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x / lanes, high = kThreads / lanes / side;
+    const int per = g.width / g.groups, group = blockIdx.x * side + sub % side, base = group * per;
+    const bool here = group < g.groups;
+    const float inv = 1.f / (float)per;
+    f32x2 w[NV][P], b[NV][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + lanes * i) * V;
+        load_columns<V>(g.weight == nullptr ? nullptr : g.weight + (here ? base : 0), c, per, vecw, 1.f, w[i]);
+        load_columns<V>(g.bias == nullptr ? nullptr : g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
+    }
+    uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+    const T *x = static_cast<const T*>(g.x) + (here ? base : 0), *z = Z ? static_cast<const T*>(g.z) + (here ? base : 0) : nullptr;
+    auto fetch = [&](int64_t row, int turn) {
+        const bool live = here && row < g.rows;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + lanes * i) * V;
+            const bool in = live && c < per;
+            uint4* to = ring + (turn * NV + i) * TENSORS * kThreads;
+            copy16(to, in ? x + row * g.x_row + c : x, in);
+            if (Z) copy16(to + kThreads, in ? z + row * g.z_row + c : z, in);
+        }
+        copies_commit();
+    };
+    const int64_t step = (int64_t)gridDim.y * high;
+    int64_t row = (int64_t)blockIdx.y * high + sub / side;
+#pragma unroll
+    for (int k = 0; k < kForwardAhead; ++k) fetch(row + k * step, k);
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.y * high; r0 < g.rows; r0 += step, row += step) {
+        Vec<T, V> cz[NV];
+        f32x2 q[NV][P], s2 = 0ull, v2 = 0ull;
+        copies_wait<kForwardAhead - 1>();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint4* from = ring + (turn * NV + i) * TENSORS * kThreads;
+            Vec<T, V> cx;
+            const uint4 u = from[0];
+            cx.w[0] = u.x; cx.w[1] = u.y; cx.w[2] = u.z; cx.w[3] = u.w;
+            if (Z) {
+                const uint4 u2 = from[kThreads];
+                cz[i].w[0] = u2.x; cz[i].w[1] = u2.y; cz[i].w[2] = u2.z; cz[i].w[3] = u2.w;
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                q[i][e] = cx.pair(e);
+                if (GATE == kGateBefore) {
+                    const f32x2 zz = cz[i].pair(e);
+                    q[i][e] = mul2(q[i][e], mul2(zz, sigmoid_pair(zz)));
+                }
+            }
+        }
+        fetch(row + kForwardAhead * step, turn);
+        if (++turn == kForwardAhead) turn = 0;
+        float m = 0.f;
+        if (!g.rms) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < P; ++e) s2 = add2(s2, q[i][e]);
+            m = row_sum(sum2(s2), lanes, buf[0]) * inv;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < P; ++e) q[i][e] = add2(q[i][e], pk(-m, -m));
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((lane + lanes * i) * V < per) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) v2 = fma2(q[i][e], q[i][e], v2);
+            }
+        const float rs = rsqrtf(fmaf(row_sum(sum2(v2), lanes, buf[1]), inv, g.eps));
+        if (!here || row >= g.rows) continue;
+        if (lane == 0) {
+            if (mean != nullptr) mean[row * g.groups + group] = m;
+            if (rstd != nullptr) rstd[row * g.groups + group] = rs;
+        }
+        T* o = y + row * g.width + base;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + lanes * i) * V;
+            if (c >= per) break;
+            f32x2 out[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                out[e] = fma2(mul2(q[i][e], pk(rs, rs)), w[i][e], b[i][e]);
+                if (GATE == kGateSilu) out[e] = mul2(out[e], sigmoid_pair(out[e]));
+                if (GATE == kGateAfter) {
+                    const f32x2 zz = cz[i].pair(e);
+                    out[e] = mul2(out[e], mul2(zz, sigmoid_pair(zz)));
+                }
+            }
+            store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), per - c, true);
+        }
+    }
+    copies_wait<0>();
+}
+
 // One value of q from memory.
 template <typename T>
 __device__ __forceinline__ float gated_value(const GroupNormArgs& g, int64_t row, int c) {
@@ -174,7 +288,9 @@ __global__ void __launch_bounds__(kThreads) group_forward_wide_kernel(GroupNormA
 
 // A block holds `side` groups of a row next to one another and kThreads / lanes / side rows at once, and walks the rows a grid's
 // height apart; its columns' sums stay in registers.  Whole vectors of the next rows are copied to shared memory that their thread
-// alone reads, so that they need neither registers nor barriers on their way.
+// alone reads, so that they need neither registers nor barriers on their way.  8192 x 4096 of bfloat16 in 8 groups, gated in front, with
+// the sums of the blocks 61 us (5.5 TB/s; floor 49.5); values held between the two passes over a row instead of computed twice
+// 74, three rows ahead 68, three blocks an SM 68.
 constexpr int kRowsAhead = 2;
 template <typename T, int V, int NV, int GATE, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormArgs g, int lanes, int side, const float* __restrict__ mean,
@@ -193,13 +309,13 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + lanes * i) * V;
         load_columns<V>(g.weight == nullptr ? nullptr : g.weight + (here ? base : 0), c, per, vecw, 1.f, w[i]);
-        if (PRE && BIAS) load_columns<V>(g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
+        if (PRE && BIAS) load_columns<V>(g.bias == nullptr ? nullptr : g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
 #pragma unroll
         for (int e = 0; e < P; ++e) dw[i][e] = db[BIAS ? i : 0][e] = 0ull;
     }
     const T *x = static_cast<const T*>(g.x), *z = static_cast<const T*>(g.z);
     uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;
-    float nm[kRowsAhead], nrs[kRowsAhead];
+    float* stats = reinterpret_cast<float*>(smem + (kWhole<V> ? kRowsAhead * NV * TENSORS * kThreads * 16 : 0)) + threadIdx.x;
     auto fetch = [&](int64_t row, int turn) {
         const bool live = here && row < g.rows;
         if (kWhole<V>) {
@@ -212,105 +328,109 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
                 copy16(to + kThreads, in ? dy + row * dy_row + base + c : dy, in);
                 if (Z) copy16(to + 2 * kThreads, in ? z + row * g.z_row + base + c : z, in);
             }
-            copies_commit();
         }
-        const float m = live && mean != nullptr ? __ldg(mean + row * g.groups + group) : 0.f, r = live ? __ldg(rstd + row * g.groups + group) : 0.f;
-#pragma unroll
-        for (int k = 0; k < kRowsAhead; ++k)
-            if (k == turn) {
-                nm[k] = m;
-                nrs[k] = r;
-            }
+        if (live) {
+            copy4(stats + turn * 2 * kThreads, rstd + row * g.groups + group);
+            if (mean != nullptr) copy4(stats + (turn * 2 + 1) * kThreads, mean + row * g.groups + group);
+        }
+        copies_commit();
     };
     const int64_t step = (int64_t)gridDim.y * high;
     int64_t row = (int64_t)blockIdx.y * high + sub / side;
 #pragma unroll
     for (int k = 0; k < kRowsAhead; ++k) fetch(row + k * step, k);
-    int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.y * high; r0 < g.rows; r0 += step, row += step, turn ^= 1) {
-        static_assert(kRowsAhead == 2, "two turns");
-        Vec<T, V> cx[NV], cg[NV], cz[NV];
-        const float rs = turn ? nrs[1] : nrs[0], mn = turn ? nm[1] : nm[0];
+    int turn = 0, flip = 0;
+    for (int64_t r0 = (int64_t)blockIdx.y * high; r0 < g.rows; r0 += step, row += step, turn = turn + 1 == kRowsAhead ? 0 : turn + 1) {
+        copies_wait<kRowsAhead - 1>();
+        const bool current = here && row < g.rows;
+        const float rs = current ? stats[turn * 2 * kThreads] : 0.f, mn = current && mean != nullptr ? stats[(turn * 2 + 1) * kThreads] : 0.f;
         const f32x2 rs2 = pk(rs, rs), shift = pk(-mn * rs, -mn * rs);
-        f32x2 s1 = 0ull, s2 = 0ull;
-        f32x2 sig[Z ? NV : 1][P];  // of the gate
-        if (kWhole<V>) {
-            copies_wait<kRowsAhead - 1>();
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
+        // Both passes over the row read it from shared memory (or L1) and compute the same from it: what the sums stand between would
+        // not fit the registers.
+        struct Part {
+            Vec<T, V> x, dy, z;
+        };
+        auto part = [&](int i) {
+            Part p;
+            if constexpr (kWhole<V>) {
                 const uint4* from = ring + (turn * NV + i) * TENSORS * kThreads;
                 auto take = [&](Vec<T, V>& v, const uint4& u) {
                     v.w[0] = u.x;
-                    v.w[1 % Vec<T, V>::WORDS] = u.y;
-                    v.w[2 % Vec<T, V>::WORDS] = u.z;
-                    v.w[3 % Vec<T, V>::WORDS] = u.w;
+                    v.w[1] = u.y;
+                    v.w[2] = u.z;
+                    v.w[3] = u.w;
                 };
-                take(cx[i], from[0]);
-                take(cg[i], from[kThreads]);
-                if (Z) take(cz[i], from[2 * kThreads]);
+                take(p.x, from[0]);
+                take(p.dy, from[kThreads]);
+                if (Z) take(p.z, from[2 * kThreads]);
+            } else {
+                const int64_t at = current ? row : 0, off = current ? base : 0;
+                const int c = (lane + lanes * i) * V, left = current ? per - c : 0;
+                p.x = load_vec<T, V>(x + at * g.x_row + off + c, left, false);
+                p.dy = load_vec<T, V>(dy + at * dy_row + off + c, left, false);
+                if (Z) p.z = load_vec<T, V>(z + at * g.z_row + off + c, left, false);
             }
-        } else {
-            const bool live = here && row < g.rows;
-            const int64_t at = live ? row : 0, off = live ? base : 0;
+            return p;
+        };
+        struct Value {
+            f32x2 xhat, g, n, silu, sig;  // n with an activation behind the norm; the last two of the gate
+        };
+        auto value = [&](const Part& p, int i, int e) {
+            Value v;
+            f32x2 q = p.x.pair(e);
+            if constexpr (Z) {
+                const f32x2 zz = p.z.pair(e);
+                v.sig = sigmoid_pair(zz);
+                v.silu = mul2(zz, v.sig);
+                if constexpr (GATE == kGateBefore) q = mul2(q, v.silu);
+            }
+            v.xhat = fma2(q, rs2, shift);
+            v.g = p.dy.pair(e);  // zero past the group's end
+            if constexpr (PRE) v.n = BIAS ? fma2(v.xhat, w[i][e], b[BIAS ? i : 0][e]) : mul2(v.xhat, w[i][e]);
+            if constexpr (GATE == kGateSilu) v.g = mul2(v.g, slope_of(v.n, sigmoid_pair(v.n)));
+            if constexpr (GATE == kGateAfter) v.g = mul2(v.g, v.silu);
+            return v;
+        };
+        f32x2 s1 = 0ull, s2 = 0ull;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Part p = part(i);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const Value v = value(p, i, e);
+                const f32x2 gw = mul2(v.g, w[i][e]);
+                if (BIAS) db[BIAS ? i : 0][e] = add2(db[BIAS ? i : 0][e], v.g);
+                dw[i][e] = fma2(v.g, v.xhat, dw[i][e]);
+                s1 = add2(s1, gw);
+                s2 = fma2(gw, v.xhat, s2);
+            }
+        }
+        const float2 s = row_sums(make_float2(sum2(s1), sum2(s2)), lanes, buf[flip ^= 1]);
+        asm volatile("" ::: "memory");  // the second pass reads again
+        if (current) {
+            const float k1 = g.rms ? 0.f : -s.x * inv * rs, k2 = -s.y * inv * rs;
+            T *ox = dx + row * g.width + base, *oz = Z ? dz + row * g.width + base : nullptr;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (lane + lanes * i) * V, left = live ? per - c : 0;
-                cx[i] = load_vec<T, V>(x + at * g.x_row + off + c, left, false);
-                cg[i] = load_vec<T, V>(dy + at * dy_row + off + c, left, false);
-                if (Z) cz[i] = load_vec<T, V>(z + at * g.z_row + off + c, left, false);
+                const int c = (lane + lanes * i) * V;
+                if (c >= per) break;
+                const Part p = part(i);
+                f32x2 o1[P], o2[P];
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const Value v = value(p, i, e);
+                    o1[e] = fma2(mul2(v.g, w[i][e]), rs2, fma2(v.xhat, pk(k2, k2), pk(k1, k1)));
+                    if constexpr (GATE == kGateBefore) {
+                        o2[e] = mul2(mul2(o1[e], p.x.pair(e)), slope_of(p.z.pair(e), v.sig));
+                        o1[e] = mul2(o1[e], v.silu);
+                    }
+                    if constexpr (GATE == kGateAfter) o2[e] = mul2(mul2(p.dy.pair(e), v.n), slope_of(p.z.pair(e), v.sig));
+                }
+                store_vec<T, V>(ox + c, Vec<T, V>::of_pairs(o1), per - c, kWhole<V>);
+                if constexpr (Z) store_vec<T, V>(oz + c, Vec<T, V>::of_pairs(o2), per - c, kWhole<V>);
             }
         }
         fetch(row + kRowsAhead * step, turn);
-        auto xhat = [&](int i, int e) {
-            f32x2 q = cx[i].pair(e);
-            if (GATE == kGateBefore) q = mul2(q, mul2(cz[i].pair(e), sig[i][e]));
-            return fma2(q, rs2, shift);
-        };
-        auto pre = [&](int i, int e, f32x2 xh) { return BIAS ? fma2(xh, w[i][e], b[PRE && BIAS ? i : 0][e]) : mul2(xh, w[i][e]); };
-        auto gradient = [&](int i, int e, f32x2 xh) {  // of n; zero past the group's end
-            f32x2 gy = cg[i].pair(e);
-            if (GATE == kGateSilu) {
-                const f32x2 n = pre(i, e, xh);
-                gy = mul2(gy, slope_of(n, sigmoid_pair(n)));
-            }
-            if (GATE == kGateAfter) gy = mul2(gy, mul2(cz[i].pair(e), sig[i][e]));
-            return gy;
-        };
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-                if (Z) sig[Z ? i : 0][e] = sigmoid_pair(cz[i].pair(e));
-                const f32x2 xh = xhat(i, e), gy = gradient(i, e, xh), gw = mul2(gy, w[i][e]);
-                if (BIAS) db[BIAS ? i : 0][e] = add2(db[BIAS ? i : 0][e], gy);
-                dw[i][e] = fma2(gy, xh, dw[i][e]);
-                s1 = add2(s1, gw);
-                s2 = fma2(gw, xh, s2);
-            }
-        const float2 s = row_sums(make_float2(sum2(s1), sum2(s2)), lanes, buf[turn]);
-        if (!here || row >= g.rows) continue;
-        const float k1 = g.rms ? 0.f : -s.x * inv * rs, k2 = -s.y * inv * rs;
-        T *ox = dx + row * g.width + base, *oz = Z ? dz + row * g.width + base : nullptr;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + lanes * i) * V;
-            if (c >= per) break;
-            f32x2 o1[P], o2[P];
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-                const f32x2 xh = xhat(i, e), gw = mul2(gradient(i, e, xh), w[i][e]);
-                const f32x2 dq = fma2(gw, rs2, fma2(xh, pk(k2, k2), pk(k1, k1)));
-                o1[e] = dq;
-                if (GATE == kGateBefore) {
-                    const f32x2 zz = cz[i].pair(e);
-                    o1[e] = mul2(dq, mul2(zz, sig[i][e]));
-                    o2[e] = mul2(mul2(dq, cx[i].pair(e)), slope_of(zz, sig[i][e]));
-                }
-                if (GATE == kGateAfter) o2[e] = mul2(mul2(cg[i].pair(e), pre(i, e, xh)), slope_of(cz[i].pair(e), sig[i][e]));
-            }
-            store_vec<T, V>(ox + c, Vec<T, V>::of_pairs(o1), per - c, kWhole<V>);
-            if (Z) store_vec<T, V>(oz + c, Vec<T, V>::of_pairs(o2), per - c, kWhole<V>);
-        }
     }
     copies_wait<0>();
     if (partial == nullptr) return;
@@ -333,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
             if (c >= per || !here) continue;
             if (high == 1) {
                 out[base + c] = a;
-                out[g.width + base + c] = d;
+                if (BIAS) out[g.width + base + c] = d;
             } else {
                 to[c] = a;
                 to[columns + c] = d;
@@ -349,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
             q += sums[k * 2 * columns + columns + c];
         }
         out[first + c] = p;
-        out[g.width + first + c] = q;
+        if (BIAS) out[g.width + first + c] = q;
     }
 }
 
@@ -431,6 +551,27 @@ int group_forward_of(const GroupNormArgs& g, void* y, float* mean, float* rstd, 
     const int64_t blocks = ceil_div64(units, kThreads / lanes);
     const bool vecw = aligned_to(g.weight, 16) && aligned_to(g.bias, 16);
     if (blocks > 2147483647) return SSD_ERR_UNSUPPORTED;
+    if constexpr (kWhole<V>) {
+        // The walk pays from two rows a block (gated in front, bfloat16, one row a thread's group and walk: 608 x 4096 in 8 groups 4.6 and
+        // 5.3 us, 1216 7.1 and 6.9, 2432 12.1 and 10.2; in one group 912 x 4096 6.7 and 6.5; 8192 x 4096 in 8 41.0 and 33.7).
+        int side = 1;
+        while (side < kThreads / lanes && side < g.groups) side *= 2;
+        const int slabs = ceil_div(g.groups, side);
+        const int64_t high = kThreads / lanes / side, most = ceil_div64(g.rows, high), parts = kWalkers * kSms / slabs;
+        if (nv <= 2 && parts > 0 && most >= 2 * parts) {
+            int r = SSD_OK;
+            launch_begin(kKindGroupNorm, s);
+            auto walk = [&](auto kernel, int held) {
+                const int smem = kForwardAhead * held * (GATE >= kGateAfter ? 2 : 1) * kThreads * 16;
+                if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);  // beside static memory
+                if (r == SSD_OK) kernel<<<dim3(slabs, (unsigned)parts), kThreads, smem, s>>>(g, lanes, side, static_cast<T*>(y), mean, rstd, vecw);
+            };
+            if (nv == 1) walk(group_walk_kernel<T, V, 1, GATE>, 1);
+            else walk(group_walk_kernel<T, V, 2, GATE>, 2);
+            const int e = launch_end(kKindGroupNorm, s);
+            return r != SSD_OK ? r : e;
+        }
+    }
     launch_begin(kKindGroupNorm, s);
     auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, kThreads, 0, s>>>(g, lanes, static_cast<T*>(y), mean, rstd, vecw); };
     if (nv <= 1 * M) go(group_forward_kernel<T, V, 1 * M, GATE>);
@@ -454,13 +595,14 @@ int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* pa
     launch_begin(kKindGroupNormBwd, s);
     int r = SSD_OK;
     auto go = [&](auto kernel, int held) {
-        const int copies = kWhole<V> ? kRowsAhead * held * (GATE >= kGateAfter ? 3 : 2) * kThreads * 16 : 0, smem = copies > sums ? copies : sums;
-        if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 100 * 1024);  // beside static memory
+        const int copies = kRowsAhead * kThreads * ((kWhole<V> ? held * (GATE >= kGateAfter ? 3 : 2) * 16 : 0) + 8), smem = copies > sums ? copies : sums;
+        if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);  // beside static memory
         if (r == SSD_OK)
             kernel<<<dim3(ceil_div(g.groups, side), parts), kThreads, smem, s>>>(g, lanes, side, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial, vecw);
     };
-    if (nv <= 1 * M) g.bias != nullptr ? go(group_backward_kernel<T, V, 1 * M, GATE, true>, 1) : go(group_backward_kernel<T, V, 1 * M, GATE, false>, 1);
-    else if (nv <= 2 * M) g.bias != nullptr ? go(group_backward_kernel<T, V, 2 * M, GATE, true>, 2) : go(group_backward_kernel<T, V, 2 * M, GATE, false>, 2);
+    const bool bias = g.bias != nullptr || d.want_dbias;
+    if (nv <= 1 * M) bias ? go(group_backward_kernel<T, V, 1 * M, GATE, true>, 1) : go(group_backward_kernel<T, V, 1 * M, GATE, false>, 1);
+    else if (nv <= 2 * M) bias ? go(group_backward_kernel<T, V, 2 * M, GATE, true>, 2) : go(group_backward_kernel<T, V, 2 * M, GATE, false>, 2);
     else
         group_backward_wide_kernel<T><<<dim3(g.groups, parts), kThreads, 0, s>>>(g, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial);
     const int e = launch_end(kKindGroupNormBwd, s);

@@ -369,19 +369,20 @@ __global__ void __launch_bounds__(32 * kJoin) norm_reduce_kernel(const float* pa
     const int i = blockIdx.x * 32 + lane;
     grid_dep_wait();
     float s = 0.f;
-    if (i < 2 * width) {
+    const int columns = dbias != nullptr ? 2 * width : width;  // of a row that are wanted
+    if (i < columns) {
 #pragma unroll 8
         for (int r = warp; r < parts; r += kJoin) s += partial[(int64_t)r * 2 * width + i];
     }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp != 0 || i >= 2 * width) return;
+    if (warp != 0 || i >= columns) return;
     s = 0.f;
 #pragma unroll
     for (int q = 0; q < kJoin; ++q) s += part[q][lane];
     if (i < width) {
         if (dweight != nullptr) dweight[i] = s;
-    } else if (dbias != nullptr) {
+    } else {
         dbias[i - width] = s;
     }
 }
@@ -488,7 +489,7 @@ int layer_norm_parts(int64_t rows, int sms) {
 
 int launch_norm_sums(int kind, const float* partial, int parts, int width, float* dweight, float* dbias, cudaStream_t s) {
     launch_begin(kind, s);
-    launch_dependent(norm_reduce_kernel, dim3(ceil_div(2 * width, 32)), dim3(32 * kJoin), 0, s, partial, parts, width, dweight, dbias);
+    launch_dependent(norm_reduce_kernel, dim3(ceil_div(dbias != nullptr ? 2 * width : width, 32)), dim3(32 * kJoin), 0, s, partial, parts, width, dweight, dbias);
     return launch_end(kind, s);
 }
 

@@ -210,6 +210,10 @@ __device__ __forceinline__ void copy16(void* to, const void* from, bool live) {
     const int bytes = live ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
 }
+// Four bytes from global to shared memory without a register between.
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
 __device__ __forceinline__ void copies_wait() {
@@ -344,7 +348,8 @@ int launch_gated_forward(const GatedArgs& g, void* y, float* final_state, float*
 int launch_gated_backward(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s);
 int launch_gated_step(const GatedArgs& g, float* state, const int* slots, int nslots, void* y, int* err, cudaStream_t s);
 
-// The column sums of a norm's gradient: dweight and dbias (either may be nullptr) from `parts` rows of 2 x width.
+// The column sums of a norm's gradient: dweight and dbias (either may be nullptr) from `parts` rows of 2 x width, whose
+// second halves are not read without a dbias.
 int launch_norm_sums(int kind, const float* partial, int parts, int width, float* dweight, float* dbias, cudaStream_t s);
 
 enum Gate { kGateNone = SSD_GATE_NONE, kGateSilu = SSD_GATE_SILU, kGateAfter = SSD_GATE_AFTER, kGateBefore = SSD_GATE_BEFORE };
@@ -363,6 +368,7 @@ struct GroupNormGrads {
     const void* dy;
     int64_t dy_row;
     void *dx, *dz;
+    bool want_dbias;
 };
 int group_norm_forward_bf16(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);
 int group_norm_forward_f16(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);

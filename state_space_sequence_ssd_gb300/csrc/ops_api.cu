@@ -354,7 +354,7 @@ int ssd_group_norm_backward(int dtype, const void* x, long long x_row_stride, co
     if (!rstd || !dy || !dx || dy_row_stride < 0 || (a.z != nullptr) != (dz != nullptr) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) ||
         !aligned_to(dy, size) || !aligned_to(dx, size) || !aligned_to(dz, size) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
         return SSD_ERR_INVALID_ARG;
-    const GroupNormGrads d = {mean, rstd, dy, dy_row_stride, dx, dz};
+    const GroupNormGrads d = {mean, rstd, dy, dy_row_stride, dx, dz, dbias != nullptr};
     const int parts = layer_norm_parts(rows, multiprocessors());
     void* ws = nullptr;
     if ((dweight != nullptr || dbias != nullptr) && take_workspace(&ws, (size_t)parts * 2 * width * sizeof(float), stream) != SSD_OK)

@@ -139,3 +139,22 @@ def test_streams_and_graphs(ssd):  # noqa: F811
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(out[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("width", [64, 30])
+def test_the_c_entry_gives_dbias_without_a_bias(ssd, width):  # noqa: F811
+    """dbias is the sum of n's gradient whether or not a bias was added."""
+    from state_space_sequence_ssd_gb300 import _ffi
+    d, rows = Draw(14), 50
+    x, w, dy = d.normal(rows, width), d.normal(width), d.normal(rows, width)
+    _, mean, rstd = ssd.ssd_group_norm_forward(x, 2, w)
+    want = ssd.ssd_group_norm_backward(x, 2, w, torch.zeros(width, device="cuda"), mean, rstd, dy)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.full_like(w, float("nan"))
+    p = lambda t: t.data_ptr()  # noqa: E731
+    assert _ffi.lib().ssd_group_norm_backward(_ffi.SSD_F32, p(x), width, None, 0, p(w), None, 0, p(mean), p(rstd), p(dy), width, rows, width, 2, p(dx), None,
+                                              p(dw), p(db), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dweight"]) and torch.equal(db, want["dbias"])
+    db.fill_(float("nan"))  # and alone
+    assert _ffi.lib().ssd_group_norm_backward(_ffi.SSD_F32, p(x), width, None, 0, p(w), None, 0, p(mean), p(rstd), p(dy), width, rows, width, 2, p(dx), None,
+                                              None, p(db), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(db, want["dbias"])
