@@ -78,29 +78,33 @@ __device__ __forceinline__ bool gates_share(const f32x2 (&er)[R], const f32x2 (&
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         unpk(er[k], a, b);
-        m = max_nan(m, max_nan(a, b));
+        m = max_nan(m, a, b);
         unpk(ei[k], a, b);
-        m = max_nan(m, max_nan(a, b));
+        m = max_nan(m, a, b);
     }
     return m <= 0x1p60f;
 }
 
 // a = e^u and w = 1 - a^2 for u <= 0.  With n the whole number next to u / ln 2 and f = u - n ln 2, |f| <= ln 2 / 2, e^u - 1 is
-// 2^n (e^f - 1) + (2^n - 1); e^f - 1 is Taylor's polynomial of degree 7 (what it leaves out is below 2^-25 of it).  Near u = 0 n is 0
-// and nothing cancels: w = -(a - 1)(a + 1) is right to 3 and a to 2 roundings there, and within 5 everywhere (every step of
-// 2^-24 checked over [-87, 0] in samples).  Adding 1.5 2^23 rounds to n and leaves it in the low bits, from where it goes to the exponent.
-// In packed arithmetic this takes fewer instructions than the special function unit's exponential with a polynomial beside it
-// for small u, and leaves that unit, which the gates keep busy, one call less of five.  a is 2^-126 for all u below its logarithm.
+// 2^n (e^f - 1) + (2^n - 1).  (e^f - 1) / f is fitted by a polynomial of degree 5 through the Chebyshev expansion (largest error
+// 0.42 2^-24, 2.2 with its float32 evaluation).  Near u = 0 n is 0 and nothing cancels: w = -(a - 1)(a + 1) is right to 4 roundings
+// and a to 2 there, and within 6 everywhere (samples over [-87, 0]).  Adding 1.5 2^23 rounds to n and leaves it in the low bits,
+// from where it goes to the exponent.  In packed arithmetic this takes fewer instructions than the special function unit's
+// exponential with a polynomial beside it for small u, and leaves that unit, which the gates keep busy, one call less of five.
+// CLAMP: u may be below kDeepest; a is about 2^-126 for all of those.
+constexpr float kDeepest = -87.f;
+template <bool CLAMP>
 __device__ __forceinline__ void decay_terms(f32x2 u, f32x2& a, f32x2& w) {
-    float u0, u1;
-    unpk(u, u0, u1);
-    u = pk(max_nan(u0, -87.33f), max_nan(u1, -87.33f));
-    const f32x2 magic = pk(12582912.f, 12582912.f), t = fma2(u, pk(kLog2e, kLog2e), magic);
-    const f32x2 n = add2(t, pk(-12582912.f, -12582912.f)), f = fma2(n, pk(-0.6931471805599453f, -0.6931471805599453f), u);
-    f32x2 p = fma2(f, pk(1.f / 5040, 1.f / 5040), pk(1.f / 720, 1.f / 720));
-    p = fma2(p, f, pk(1.f / 120, 1.f / 120));
-    p = fma2(p, f, pk(1.f / 24, 1.f / 24));
-    p = fma2(p, f, pk(1.f / 6, 1.f / 6));
+    if (CLAMP) {
+        float u0, u1;
+        unpk(u, u0, u1);
+        u = pk(max_nan(u0, kDeepest), max_nan(u1, kDeepest));
+    }
+    const f32x2 t = fma2(u, pk(kLog2e, kLog2e), pk(12582912.f, 12582912.f)), n = add2(t, pk(-12582912.f, -12582912.f));
+    const f32x2 f = fma2(n, pk(-0.6931471805599453f, -0.6931471805599453f), u);
+    f32x2 p = fma2(f, pk(0.0013933649752289057f, 0.0013933649752289057f), pk(0.00836915522813797f, 0.00836915522813797f));
+    p = fma2(p, f, pk(0.04166646674275398f, 0.04166646674275398f));
+    p = fma2(p, f, pk(0.16666504740715027f, 0.16666504740715027f));
     p = fma2(p, f, pk(0.5f, 0.5f));
     p = fma2(p, f, pk(1.f, 1.f));
     p = mul2(p, f);

@@ -90,7 +90,9 @@ gated_forward_kernel(GatedArgs g, Ctl ctl, int ranks, bool vecy, T* __restrict__
     fetch();
     cluster_begin(cl, ranks);
     const bool in0 = c < g.channels, in1 = c + 1 < g.channels;
-    const f32x2 A = pk(in0 ? g.A[c] : -1.f, in1 ? g.A[c + 1] : -1.f);
+    const float A0 = in0 ? g.A[c] : -1.f, A1 = in1 ? g.A[c + 1] : -1.f;
+    const f32x2 A = pk(A0, A1);
+    const bool shallow = A0 > kDeepest && A1 > kDeepest;  // no decay needs holding (its gate is at most one)
     float2 h = make_float2(0.f, 0.f);  // in front of the cluster's step
     if (g.init != nullptr) {
         const float* p = g.init + (int64_t)b * g.channels + c;
@@ -120,7 +122,7 @@ gated_forward_kernel(GatedArgs g, Ctl ctl, int ranks, bool vecy, T* __restrict__
             for (int k = 0; k < R; ++k) {
                 f32x2 v, gi, w;
                 two_gates<ONE>(a[k], bx[k], v, gi);
-                decay_terms(mul2(A, v), a[k], w);
+                decay_terms<!ONE>(mul2(A, v), a[k], w);
                 float w0, w1;
                 unpk(w, w0, w1);
                 bx[k] = mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.at(mine, k));
@@ -131,7 +133,7 @@ gated_forward_kernel(GatedArgs g, Ctl ctl, int ranks, bool vecy, T* __restrict__
             }
         };
         const bool whole = t0 + R <= n;
-        if (whole && gates_share(a, bx)) terms(std::true_type());
+        if (whole && shallow && gates_share(a, bx)) terms(std::true_type());
         else terms(std::false_type());
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -280,7 +282,9 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
     for (int k = 0; k < STAGES; ++k) fetch(k);
     cluster_begin(cl, ranks);
     const bool in0 = c < g.channels, in1 = c + 1 < g.channels;
-    const f32x2 A = pk(in0 ? g.A[c] : -1.f, in1 ? g.A[c + 1] : -1.f);
+    const float A0 = in0 ? g.A[c] : -1.f, A1 = in1 ? g.A[c + 1] : -1.f;
+    const f32x2 A = pk(A0, A1);
+    const bool shallow = A0 > kDeepest && A1 > kDeepest;  // no decay needs holding (its gate is at most one)
     float2 mu = make_float2(0.f, 0.f);  // the gradient of the state behind the cluster's step
     if (dfinal != nullptr) {
         const float* p = dfinal + (int64_t)b * g.channels + c;
@@ -318,7 +322,7 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
                 f32x2 v, gi;
                 if (FIRST) two_gates<ONE>(a[k], w[k], v, gi);
                 else two_gates<ONE>(exp_neg(r.at(from + Rows::BYTES, k)), exp_neg(i.at(from + 2 * Rows::BYTES, k)), v, gi, top);
-                decay_terms(mul2(A, v), a[k], w[k]);
+                decay_terms<!ONE>(mul2(A, v), a[k], w[k]);
                 if (!ONE && t0 + k >= n) {  // tokens past the length keep the state
                     a[k] = pk(1.f, 1.f);
                     w[k] = pk(0.f, 0.f);
@@ -330,16 +334,16 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
                 P = mul2(P, a[k]);
             }
         };
-        bool share = whole;
+        bool share = false;
         if (FIRST) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
                 a[k] = exp_neg(r.at(from + Rows::BYTES, k));
                 w[k] = exp_neg(i.at(from + 2 * Rows::BYTES, k));
             }
-            share = whole && gates_share(a, w);
+            share = whole && shallow && gates_share(a, w);
             if (share) terms(std::true_type());
-        } else if (whole) {
+        } else if (whole && shallow) {
             terms(std::true_type());
             share = top <= kShared;
         }
@@ -520,7 +524,7 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g, float* sta
             const f32x2 A = pk(2 * e < left ? g.A[c + 2 * e] : -1.f, 2 * e + 1 < V && 2 * e + 1 < left ? g.A[c + 2 * e + 1] : -1.f);
             f32x2 v, gi, a, w;
             two_gates<decltype(one)::value>(exp_neg(r.pair(e)), exp_neg(i.pair(e)), v, gi, top);
-            decay_terms(mul2(A, v), a, w);
+            decay_terms<true>(mul2(A, v), a, w);
             float w0, w1;
             unpk(w, w0, w1);
             out[e] = fma2(a, h[e], mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.pair(e)));
