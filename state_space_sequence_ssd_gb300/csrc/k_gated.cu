@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(256) gated_sums_kernel(const float* partial, i
 // ------------------------------------------------------------------ one token
 template <typename T, int V>
 __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g, float* state, const int* __restrict__ slots, int nslots, T* __restrict__ y,
-                                                         int* err, bool vec) {
+                                                         int* err, bool vec, bool vecs) {
     const int c = (blockIdx.x * 128 + threadIdx.x) * V, b = blockIdx.y;
     if (c >= g.channels) return;
     const int left = g.channels - c;
@@ -511,33 +511,29 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g, float* sta
     const auto r = load_vec<T, V>(static_cast<const T*>(g.r) + b * g.r_batch + c, left, vec);
     const auto i = load_vec<T, V>(static_cast<const T*>(g.i) + b * g.i_batch + c, left, vec);
     const int slot = row_slot(slots, b, nslots, threadIdx.x == 0 ? err : nullptr);
-    constexpr int N = (V + 1) / 2;
-    f32x2 out[N], h[N];
-    float top = 0.f;
+    static_assert(V % 2 == 0, "whole pairs");
     float* p = state + (int64_t)(slot < 0 ? 0 : slot) * g.channels + c;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        h[e] = pk(slot >= 0 && 2 * e < left ? p[2 * e] : 0.f, slot >= 0 && 2 * e + 1 < V && 2 * e + 1 < left ? p[2 * e + 1] : 0.f);
+    const auto A = load_vec<float, V>(g.A + c, left, vecs);
+    const auto h = load_vec<float, V, true>(p, slot < 0 ? 0 : left, vecs);
+    f32x2 out[V / 2];
+    float top = 0.f;
     auto token = [&](auto one) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const f32x2 A = pk(2 * e < left ? g.A[c + 2 * e] : -1.f, 2 * e + 1 < V && 2 * e + 1 < left ? g.A[c + 2 * e + 1] : -1.f);
+        for (int e = 0; e < V / 2; ++e) {
             f32x2 v, gi, a, w;
             two_gates<decltype(one)::value>(exp_neg(r.pair(e)), exp_neg(i.pair(e)), v, gi, top);
-            decay_terms<true>(mul2(A, v), a, w);
+            decay_terms<true>(mul2(A.pair(e), v), a, w);
             float w0, w1;
             unpk(w, w0, w1);
-            out[e] = fma2(a, h[e], mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.pair(e)));
+            out[e] = fma2(a, h.pair(e), mul2(mul2(pk(sqrt_fast(w0), sqrt_fast(w1)), gi), x.pair(e)));
         }
     };
     token(std::true_type());
     if (!(top <= kShared)) token(std::false_type());
+    if (slot >= 0) store_vec<float, V>(p, Vec<float, V>::of_pairs(out), left, vecs);
+    if (slot < 0) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const float2 o = unpk(out[e]);
-        if (slot >= 0 && 2 * e < left) p[2 * e] = o.x;
-        if (slot >= 0 && 2 * e + 1 < V && 2 * e + 1 < left) p[2 * e + 1] = o.y;
-        if (slot < 0) out[e] = pk(0.f, 0.f);
+        for (int e = 0; e < V / 2; ++e) out[e] = pk(0.f, 0.f);
     }
     store_vec<T, V>(y + (int64_t)b * g.channels + c, Vec<T, V>::of_pairs(out), left, vec);
 }
@@ -626,9 +622,9 @@ template <typename T>
 int step_of(const GatedArgs& g, float* state, const int* slots, int nslots, void* y, int* err, cudaStream_t s) {
     constexpr int V = 8 / sizeof(T);
     const bool vec = g.channels % V == 0 && g.x_batch % V == 0 && g.r_batch % V == 0 && g.i_batch % V == 0 && aligned_to(g.x, 8) && aligned_to(g.r, 8) &&
-                     aligned_to(g.i, 8) && aligned_to(y, 8);
+                     aligned_to(g.i, 8) && aligned_to(y, 8), vecs = g.channels % V == 0 && aligned_to(state, 4 * V) && aligned_to(g.A, 4 * V);
     launch_begin(kKindGatedStep, s);
-    gated_step_kernel<T, V><<<dim3(ceil_div(g.channels, 128 * V), g.batch), 128, 0, s>>>(g, state, slots, nslots, static_cast<T*>(y), err, vec);
+    gated_step_kernel<T, V><<<dim3(ceil_div(g.channels, 128 * V), g.batch), 128, 0, s>>>(g, state, slots, nslots, static_cast<T*>(y), err, vec, vecs);
     return launch_end(kKindGatedStep, s);
 }
 

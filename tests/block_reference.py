@@ -58,8 +58,10 @@ def gated(x, r, i, A, init=None, lengths=None, dy=None, dfinal=None):
     h = _walk(a, bx, h0)
     mag = _walk(a, bx.abs(), h0.abs())
     mag_before, h_before = _before(mag, h0.abs()), _before(h, h0)
+    # a decay below 2^-126 is taken as that
+    off_a = e_a * a + torch.where(u < -86, LEAST, 0.0)
     # a token's decay enters a term of the state once, with its error and a rounding of its product and of its sum
-    err = _walk(a, (e_a + 4 * U) * a * mag_before + (e_b + 4 * U) * bx.abs(), torch.zeros_like(h0))
+    err = _walk(a, (off_a + 4 * U * a) * mag_before + (e_b + 4 * U) * bx.abs(), torch.zeros_like(h0))
     if dy is None:
         at = torch.arange(0, L, SPAN, device=x.device)
         return {"y": tuple(torch.where(keep, q, 0.0) for q in (h, err)), "final": (h[:, -1], err[:, -1]),
@@ -70,23 +72,25 @@ def gated(x, r, i, A, init=None, lengths=None, dy=None, dfinal=None):
     back = lambda q, first: _walk(_before(a.flip(1), torch.ones_like(h0)), q.flip(1), first).flip(1)  # noqa: E731
     lam, lam_mag = back(gy, last), back(gy.abs(), last.abs())
     after = lambda q: torch.cat([q[:, 1:], torch.zeros_like(q[:, :1])], 1)  # noqa: E731
-    lam_err = back((after(e_a) + 6 * U) * after(a * lam_mag) + 2 * U * gy.abs(), torch.zeros_like(h0)) + 2 * U * lam_mag
+    lam_err = back(after((off_a + 6 * U * a) * lam_mag) + 2 * U * gy.abs(), torch.zeros_like(h0)) + 2 * U * lam_mag
     live = lambda val, e: (torch.where(keep, val, 0.0), torch.where(keep, e, 0.0))  # noqa: E731
     out = {"dx": live(lam * s * g, lam_err * s * g + lam_mag * s * g * (e_b + 2 * U))}
     # 1 - v and 1 - g are e^-r v and e^-i g: zero, with a relative error of one, below 2^-126
     e_vr, e_gr = (torch.where(q < LEAST, 1.0, e) for q, e in ((v_rest, e_v + r.abs() * U + 10 * U), (g_rest, e_g + i.abs() * U + 10 * U)))
     n = s * x.abs() * g * g_rest
     out["di"] = live(lam * s * x * g * g_rest, (lam_err + lam_mag * (e_b + e_gr + 4 * U)) * n)
-    ratio = torch.where(w > 0, a * g / s.clamp(min=1e-300), 0.0)
+    per_s = torch.where(w > 0, g / s.clamp(min=1e-300), 0.0)
+    ratio = a * per_s
     size = mag_before + ratio * x.abs()
     q = lam * u * a * (h_before - ratio * x)
-    e_q = lam_err * u.abs() * a * size + lam_mag * u.abs() * a * (e_before + ratio * x.abs() * (e_a + e_b + 8 * U) + size * (e_u + e_a + 6 * U))
+    e_size = e_before + (per_s * off_a + ratio * (e_b + 8 * U)) * x.abs() + size * (e_u + 6 * U)
+    e_q = lam_err * u.abs() * a * size + lam_mag * u.abs() * (off_a * size + (a + off_a) * e_size)
     out["dr"] = live(q * v_rest, (e_q + lam_mag * u.abs() * a * size * e_vr) * v_rest)
     q, e_q = live(q, e_q)
     # a thread adds a token in eight of each step's 64, then 8 warps, the blocks of a row and the rows
     terms = (lam_mag * u.abs() * a * size * keep).sum((0, 1))
     out["dA"] = (q.sum((0, 1)) / A, (e_q.sum((0, 1)) + terms * (L / 8 + 16 + 8 * b) * U) / A.abs())
-    out["dinit"] = (a[:, 0] * lam[:, 0], a[:, 0] * (lam_err[:, 0] + lam_mag[:, 0] * (e_a[:, 0] + 2 * U)))
+    out["dinit"] = (a[:, 0] * lam[:, 0], a[:, 0] * (lam_err[:, 0] + lam_mag[:, 0] * 2 * U) + off_a[:, 0] * lam_mag[:, 0])
     return out
 
 

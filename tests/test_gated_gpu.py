@@ -58,6 +58,7 @@ CASES = [("f32", 1, 1, 1, True, None, (0, 0), 1.0, (0.01, 1.0)),
          ("f32", 1, 512, 256, True, None, (0, 0), 1.0, (0.008, 0.84)),
          ("bf16", 2, 1000, 200, True, [999, 1000], (8, 8), 1.0, (0.008, 0.84)),
          ("f16", 2, 3001, 16, False, None, (0, 0), 1.0, (0.0001, 0.1)),
+         ("f32", 2, 140, 10, True, None, (0, 0), 3.0, (60.0, 300.0)),       # decays below the smallest float32
          # (warps a block and blocks a cluster of the forward pass; blocks a cluster of the gradient)
          ("f32", 40, 300, 130, True, None, (2, 0), 30.0, (0.01, 10.0)),     # 8 and 2; 3
          ("bf16", 75, 200, 128, False, None, (0, 0), 1.0, (0.01, 1.0)),     # 4 and 4; 2
