@@ -21,10 +21,7 @@ namespace {
 
 constexpr int R = 16;  // consecutive tokens of a warp
 
-// The gradient's blocks: four warps.  With 16-bit tensors two of them an SM, with up to 255 registers a thread, and two steps of
-// input on their way; three with 168 registers, which a 32-bit type's single step of input leaves room for, take 146 us
-// where these take 139 (2 x 4096 x 4096 of bfloat16), and 169 where two take 199 (float32).
-constexpr int kBackWarps = 4;
+// The gradient's blocks of four warps on an SM, and steps of input on their way (see back_plan).
 template <typename T>
 constexpr int kBackResident = sizeof(T) == 4 ? 3 : 2;
 template <typename T>
@@ -241,7 +238,7 @@ __device__ __forceinline__ void back_through_runs(const float4* pairs, const flo
 }
 
 template <typename T, int W, int STAGES, bool VEC>
-__global__ void __launch_bounds__(32 * W, kBackResident<T>)
+__global__ void __launch_bounds__(32 * W, W == 4 ? kBackResident<T> : 1)
 gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy, const float* __restrict__ dfinal, Ctl ctl, int ranks, bool vecy,
                       T* __restrict__ dx, T* __restrict__ dr, T* __restrict__ di, float* __restrict__ dinit, float* __restrict__ partial) {
     using Rows = GatedRows<T, R, VEC>;
@@ -293,8 +290,9 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
     }
     auto kept_state = [&](int span) {  // in front of this block's tokens
         float2 v = make_float2(0.f, 0.f);
-        if (span >= 0 && span < kept) {
-            const float* p = states + ((int64_t)b * kept + span) * g.channels + c;
+        const int at = span * (SPAN / kGatedSpan);
+        if (at >= 0 && at < kept) {
+            const float* p = states + ((int64_t)b * kept + at) * g.channels + c;
             if (in0) v.x = p[0];
             if (in1) v.y = p[1];
         }
@@ -544,8 +542,19 @@ int gated_ranks(const GatedArgs& g, int resident, int span) {
     const int most = ceil_div(g.seqlen, span), k = want < kGatedRanks ? (int)want : kGatedRanks;
     return k < 1 ? 1 : k < most ? k : most;
 }
+// The gradient's blocks.  Four warps: with 16-bit tensors two of them an SM, with up to 255 registers a thread, and two steps of input on
+// their way; three with 168 registers, which a 32-bit type's single step of input leaves room for, take 146 us where these take
+// 139 (2 x 4096 x 4096 of bfloat16), and 169 where two take 199 (float32).  Eight warps, and so half as many steps, where even the largest
+// clusters leave half the SMs idle and take more than a step (4096 tokens of 96 channels of bfloat16: 35.6 us with four, 22.9 with eight; 2048 of 256 20.0
+// and 13.7; 2 x 4096 of 512, whose 16 clusters of eight whole SMs do not all find room at once, 37.9 and 42.9).
+struct BackPlan {
+    int warps, ranks;
+};
 template <typename T>
-int back_ranks(const GatedArgs& g) { return gated_ranks(g, kBackResident<T>, kBackWarps * R); }
+BackPlan back_plan(const GatedArgs& g) {
+    if ((int64_t)ceil_div(g.channels, kGatedTile) * g.batch * kGatedRanks <= kSms / 2 && g.seqlen > 4 * R * kGatedRanks) return {8, gated_ranks(g, 1, 8 * R)};
+    return {4, gated_ranks(g, kBackResident<T>, 4 * R)};
+}
 
 template <typename K, typename... Args>
 int launch_cluster(K kernel, dim3 grid, int threads, int ranks, int smem, cudaStream_t s, Args... args) {
@@ -584,28 +593,27 @@ int forward_rows(const GatedArgs& g, int ranks, void* y, float* final_state, flo
     const int e = launch_end(kKindGated, s);
     return r != SSD_OK ? r : e;
 }
-// Eight warps a block; four, and so twice the blocks, where rows are too short for the clusters that would fill the SMs (512 tokens of
-// 256 channels of float32: 4.7 us with four, 5.5 with eight; 65536 of 2048 of bfloat16: 324 and 299; 2 x 4096 of 4096: 71 and 68).
+// Eight warps a block; four, and so more blocks, where one step of theirs holds the rows (512 tokens of 256 channels of bfloat16: 5.1 us with
+// four, 5.7 with eight; 1024: 7.3 and 6.0; 2 x 4096 of 4096: 71 and 68; 65536 of 2048: 324 and 299).
 template <typename T, bool VEC>
 int forward_warps(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
-    const int eight = gated_ranks(g, 2, 8 * R);
-    if (eight == ceil_div(g.seqlen, 8 * R)) return forward_rows<T, 4, VEC>(g, gated_ranks(g, 4, 4 * R), y, final_state, states, s);
-    return forward_rows<T, 8, VEC>(g, eight, y, final_state, states, s);
+    const int four = gated_ranks(g, 4, 4 * R);
+    if ((int64_t)four * 4 * R >= g.seqlen) return forward_rows<T, 4, VEC>(g, four, y, final_state, states, s);
+    return forward_rows<T, 8, VEC>(g, gated_ranks(g, 2, 8 * R), y, final_state, states, s);
 }
 template <typename T>
 int forward_of(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
     return rows_in_vectors<T>(g) ? forward_warps<T, true>(g, y, final_state, states, s) : forward_warps<T, false>(g, y, final_state, states, s);
 }
 
-template <typename T, bool VEC>
-int backward_rows(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
-    constexpr int W = kBackWarps, S = kBackStages<T>;
-    const int ranks = back_ranks<T>(g);
+template <typename T, int W, bool VEC>
+int backward_rows(const GatedArgs& g, int ranks, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
+    constexpr int S = kBackStages<T>;
     const bool vecy = g.channels % 2 == 0 && aligned_to(d.dx, 2 * sizeof(T)) && aligned_to(d.dr, 2 * sizeof(T)) && aligned_to(d.di, 2 * sizeof(T));
     launch_begin(kKindGatedBwd, s);
     int r = launch_cluster(gated_backward_kernel<T, W, S, VEC>, dim3(ceil_div(g.channels, kGatedTile) * ranks, g.batch), 32 * W, ranks,
-                           backward_smem<T, W, S, VEC>(ranks), s, g, states, static_cast<const T*>(d.dy), d.dfinal, wait_control(kKindGatedBwd), ranks, vecy, static_cast<T*>(d.dx),
-                           static_cast<T*>(d.dr), static_cast<T*>(d.di), d.dinit, partial);
+                           backward_smem<T, W, S, VEC>(ranks), s, g, states, static_cast<const T*>(d.dy), d.dfinal, wait_control(kKindGatedBwd), ranks,
+                           vecy, static_cast<T*>(d.dx), static_cast<T*>(d.dr), static_cast<T*>(d.di), d.dinit, partial);
     const int e = launch_end(kKindGatedBwd, s);
     r = r != SSD_OK ? r : e;
     if (r != SSD_OK) return r;
@@ -613,9 +621,14 @@ int backward_rows(const GatedArgs& g, const GatedGrads& d, const float* states, 
     launch_dependent(gated_sums_kernel, dim3(ceil_div(g.channels, 32)), dim3(256), 0, s, (const float*)partial, ranks * g.batch, g.channels, g.A, d.dA);
     return launch_end(kKindGatedBwd, s);
 }
+template <typename T, bool VEC>
+int backward_warps(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
+    const BackPlan p = back_plan<T>(g);
+    return p.warps == 8 ? backward_rows<T, 8, VEC>(g, p.ranks, d, states, partial, s) : backward_rows<T, 4, VEC>(g, p.ranks, d, states, partial, s);
+}
 template <typename T>
 int backward_of(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
-    return rows_in_vectors<T>(g) && aligned_to(d.dy, 16) ? backward_rows<T, true>(g, d, states, partial, s) : backward_rows<T, false>(g, d, states, partial, s);
+    return rows_in_vectors<T>(g) && aligned_to(d.dy, 16) ? backward_warps<T, true>(g, d, states, partial, s) : backward_warps<T, false>(g, d, states, partial, s);
 }
 
 template <typename T>
@@ -632,7 +645,7 @@ int step_of(const GatedArgs& g, float* state, const int* slots, int nslots, void
 
 size_t gated_states_floats(const GatedArgs& g) { return (size_t)g.batch * ceil_div(g.seqlen, kGatedSpan) * g.channels; }
 size_t gated_sums_floats(const GatedArgs& g) {
-    const int ranks = g.dtype == SSD_BF16 ? back_ranks<__nv_bfloat16>(g) : g.dtype == SSD_F16 ? back_ranks<__half>(g) : back_ranks<float>(g);
+    const int ranks = (g.dtype == SSD_BF16 ? back_plan<__nv_bfloat16>(g) : g.dtype == SSD_F16 ? back_plan<__half>(g) : back_plan<float>(g)).ranks;
     return (size_t)g.batch * ranks * g.channels;
 }
 

@@ -59,13 +59,15 @@ CASES = [("f32", 1, 1, 1, True, None, (0, 0), 1.0, (0.01, 1.0)),
          ("bf16", 2, 1000, 200, True, [999, 1000], (8, 8), 1.0, (0.008, 0.84)),
          ("f16", 2, 3001, 16, False, None, (0, 0), 1.0, (0.0001, 0.1)),
          ("f32", 2, 140, 10, True, None, (0, 0), 3.0, (60.0, 300.0)),       # decays below the smallest float32
-         # (warps a block and blocks a cluster of the forward pass; blocks a cluster of the gradient)
-         ("f32", 40, 300, 130, True, None, (2, 0), 30.0, (0.01, 10.0)),     # 8 and 2; 3
-         ("bf16", 75, 200, 128, False, None, (0, 0), 1.0, (0.01, 1.0)),     # 4 and 4; 2
-         ("bf16", 300, 70, 72, True, None, (0, 0), 1.0, (0.01, 1.0)),       # 4 and 1; 1
-         ("f16", 260, 129, 65, True, None, (1, 1), 1.0, (0.01, 1.0)),       # 8 and 1; 1
-         ("bf16", 50, 1300, 64, True, None, (8, 0), 1.0, (0.01, 1.0)),      # 8 and 6; 6
-         ("f16", 1, 5000, 40, False, [4242], (0, 0), 1.0, (0.001, 0.1))]    # 8 and 8; 8
+         # (warps a block and blocks a cluster of the forward pass; of the gradient)
+         ("f32", 40, 300, 130, True, None, (2, 0), 30.0, (0.01, 10.0)),     # 4 and 5; 4 and 3
+         ("bf16", 75, 200, 128, False, None, (0, 0), 1.0, (0.01, 1.0)),     # 4 and 4; 4 and 2
+         ("bf16", 300, 70, 72, True, None, (0, 0), 1.0, (0.01, 1.0)),       # 8 and 1; 4 and 1
+         ("f16", 260, 129, 65, True, None, (1, 1), 1.0, (0.01, 1.0)),       # 8 and 1; 4 and 1
+         ("bf16", 50, 1300, 64, True, None, (8, 0), 1.0, (0.01, 1.0)),      # 8 and 6; 4 and 6
+         ("f32", 24, 1100, 64, True, [(97 * k) % 1101 for k in range(24)], (4, 0), 1.0, (0.01, 1.0)),  # 8 and 8; 4 and 8
+         ("f16", 1, 5000, 40, False, [4242], (0, 0), 1.0, (0.001, 0.1)),    # 8 and 8; 8 and 8
+         ("f32", 2, 2500, 70, True, [2500, 1030], (1, 0), 1.0, (0.001, 0.1))]  # 8 and 8; 8 and 8
 
 
 def make(c, seed=5):
