@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, kWalkers) group_walk_kernel(GroupNor
     int64_t row = (int64_t)blockIdx.y * high + sub / side;
 #pragma unroll
     for (int k = 0; k < kForwardAhead; ++k) fetch(row + k * step, k);
-    int turn = 0;
+    int turn = 0, flip = 0;  // sums that follow one another take turns in buf, with a mean or without
     for (int64_t r0 = (int64_t)blockIdx.y * high; r0 < g.rows; r0 += step, row += step) {
         Vec<T, V> cz[NV];
         f32x2 q[NV][P], s2 = 0ull, v2 = 0ull;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, kWalkers) group_walk_kernel(GroupNor
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < P; ++e) s2 = add2(s2, q[i][e]);
-            m = row_sum(sum2(s2), lanes, buf[0]) * inv;
+            m = row_sum(sum2(s2), lanes, buf[flip ^= 1]) * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kWalkers) group_walk_kernel(GroupNor
 #pragma unroll
                 for (int e = 0; e < P; ++e) v2 = fma2(q[i][e], q[i][e], v2);
             }
-        const float rs = rsqrtf(fmaf(row_sum(sum2(v2), lanes, buf[1]), inv, g.eps));
+        const float rs = rsqrtf(fmaf(row_sum(sum2(v2), lanes, buf[flip ^= 1]), inv, g.eps));
         if (!here || row >= g.rows) continue;
         if (lane == 0) {
             if (mean != nullptr) mean[row * g.groups + group] = m;
@@ -563,7 +563,7 @@ int group_forward_of(const GroupNormArgs& g, void* y, float* mean, float* rstd, 
             launch_begin(kKindGroupNorm, s);
             auto walk = [&](auto kernel, int held) {
                 const int smem = kForwardAhead * held * (GATE >= kGateAfter ? 2 : 1) * kThreads * 16;
-                if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);  // beside static memory
+                if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 100 * 1024);  // beside static memory
                 if (r == SSD_OK) kernel<<<dim3(slabs, (unsigned)parts), kThreads, smem, s>>>(g, lanes, side, static_cast<T*>(y), mean, rstd, vecw);
             };
             if (nv == 1) walk(group_walk_kernel<T, V, 1, GATE>, 1);
@@ -596,7 +596,7 @@ int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* pa
     int r = SSD_OK;
     auto go = [&](auto kernel, int held) {
         const int copies = kRowsAhead * kThreads * ((kWhole<V> ? held * (GATE >= kGateAfter ? 3 : 2) * 16 : 0) + 8), smem = copies > sums ? copies : sums;
-        if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);  // beside static memory
+        if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 100 * 1024);  // beside static memory
         if (r == SSD_OK)
             kernel<<<dim3(ceil_div(g.groups, side), parts), kThreads, smem, s>>>(g, lanes, side, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial, vecw);
     };

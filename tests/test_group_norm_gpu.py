@@ -21,6 +21,8 @@ SIZES = [("f32", 1, 1, 1, (0, 0), True, True),
          ("f32", 2, 1, 9001, (0, 0), True, True),           # odd and wider than the registers
          ("bf16", 4000, 2, 40, (8, 8), True, True),
          ("f32", 3000, 1, 130, (0, 0), True, False),
+         ("f32", 1500, 2, 1024, (0, 0), True, True),        # several warps a group, many rows a block
+         ("bf16", 2500, 1, 2048, (0, 8), True, False),
          ("bf16", 1, 1, 4096, (0, 0), False, False),
          ("f16", 2, 7, 1, (2, 1), True, True)]
 GATES = ["none", "silu", "after", "before"]
@@ -158,3 +160,19 @@ def test_the_c_entry_gives_dbias_without_a_bias(ssd, width):  # noqa: F811
     assert _ffi.lib().ssd_group_norm_backward(_ffi.SSD_F32, p(x), width, None, 0, p(w), None, 0, p(mean), p(rstd), p(dy), width, rows, width, 2, p(dx), None,
                                               None, p(db), torch.cuda.current_stream().cuda_stream) == 0
     assert torch.equal(db, want["dbias"])
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_groups_of_several_warps_over_many_rows(ssd, rms):  # noqa: F811
+    """Rows that follow one another in a block do not meet in the sums: rows of sizes far apart, many times."""
+    d = Draw(15)
+    x = d.normal(6000, 4096, dtype=torch.bfloat16) * torch.exp2((torch.arange(6000, device="cuda") % 13 - 6.0))[:, None].to(torch.bfloat16)
+    q = x.double()
+    mean = q.mean(-1, keepdim=True) * (not rms)
+    want = 1 / torch.sqrt((q - mean).square().mean(-1, keepdim=True) + 1e-5)
+    first = ssd.ssd_group_norm_forward(x, 1, rms=rms)
+    # as block_reference: 16 + 60 additions of 2^-24 and the root's
+    assert float(((first[2].double() - want).abs() / want).max()) <= 90 * R.U
+    for _ in range(20):
+        again = ssd.ssd_group_norm_forward(x, 1, rms=rms)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[2], first[2])
