@@ -10,10 +10,15 @@
 // distributed shared memory, so that one pass over the data serves sequences of any length, with as many blocks as fill the SMs.
 // The next step's inputs come through cp.async while this step's pairs are exchanged and its outputs written.
 //
-// 2 x 4096 x 4096 of bfloat16 takes 68 us (4.0 TB/s; the bytes' floor is 40), of float32 85 (6.4 TB/s; 80), 65536 x 2048 of
-// bfloat16 299 (159): of 16-bit elements the instructions bind, 36 a warp and element pair of the special function unit's five, the
-// polynomial and conversions, at half the issue slots; and 256 blocks on 152 SMs leave some with one where others have two.
+// 2 x 4096 x 4096 of bfloat16 takes 68 us (4.0 TB/s; the bytes' floor is 40), of float32 86 (6.3 TB/s; 80), 65536 x 2048 of
+// bfloat16 295 (159).  With 16-bit elements the instructions bind: about 70 a warp and token of its 64 channels, for the gates' four calls of the
+// special function unit an element, the polynomial, conversions and the exchange, at 52% of the issue slots with 13 warps an SM, which
+// the registers allow.  Beside that, 256 blocks on 152 SMs leave some with one where others have two (2 x 4096 x 4864, 304 blocks, takes
+// 69), and the exchange between blocks takes a tenth (2 x 4096 x 9728, without clusters, 124: 5.2 TB/s).
 // Runs of 8 tokens take 85 us at the first size (more exchange for the work), copies two steps ahead as long as one.
+#include <mutex>
+#include <vector>
+
 #include "gated.cuh"
 
 namespace ssd {
@@ -21,7 +26,7 @@ namespace {
 
 constexpr int R = 16;  // consecutive tokens of a warp
 
-// The gradient's blocks of four warps on an SM, and steps of input on their way (see back_plan).
+// The gradient's blocks of four warps on an SM, and steps of input on their way (see backward_warps).
 template <typename T>
 constexpr int kBackResident = sizeof(T) == 4 ? 3 : 2;
 template <typename T>
@@ -536,42 +541,65 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g, float* sta
     store_vec<T, V>(y + (int64_t)b * g.channels + c, Vec<T, V>::of_pairs(out), left, vec);
 }
 
-// Blocks of a cluster: as many as keep `resident` blocks on every SM, none without a step.
-int gated_ranks(const GatedArgs& g, int resident, int span) {
-    const int64_t blocks = (int64_t)ceil_div(g.channels, kGatedTile) * g.batch, want = (int64_t)resident * kSms / blocks;
-    const int most = ceil_div(g.seqlen, span), k = want < kGatedRanks ? (int)want : kGatedRanks;
-    return k < 1 ? 1 : k < most ? k : most;
+cudaLaunchConfig_t cluster_launch(dim3 grid, int threads, int ranks, int smem, cudaStream_t s, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = ranks;
+    attr->val.clusterDim.y = 1;
+    attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
-// The gradient's blocks.  Four warps: with 16-bit tensors two of them an SM, with up to 255 registers a thread, and two steps of input on
-// their way; three with 168 registers, which a 32-bit type's single step of input leaves room for, take 146 us where these take
-// 139 (2 x 4096 x 4096 of bfloat16), and 169 where two take 199 (float32).  Eight warps, and so half as many steps, where even the largest
-// clusters leave half the SMs idle and take more than a step (4096 tokens of 96 channels of bfloat16: 35.6 us with four, 22.9 with eight; 2048 of 256 20.0
-// and 13.7; 2 x 4096 of 512, whose 16 clusters of eight whole SMs do not all find room at once, 37.9 and 42.9).
-struct BackPlan {
-    int warps, ranks;
-};
-template <typename T>
-BackPlan back_plan(const GatedArgs& g) {
-    if ((int64_t)ceil_div(g.channels, kGatedTile) * g.batch * kGatedRanks <= kSms / 2 && g.seqlen > 4 * R * kGatedRanks) return {8, gated_ranks(g, 1, 8 * R)};
-    return {4, gated_ranks(g, kBackResident<T>, 4 * R)};
+
+// Clusters of `ranks` blocks that the device holds at once; asked for once per kernel, size and device.
+template <typename K>
+int cluster_room(K kernel, int threads, int ranks, int smem) {
+    struct Known {
+        const void* kernel;
+        int device, ranks, room;
+    };
+    static std::mutex mu;
+    static std::vector<Known> known;
+    const void* k = reinterpret_cast<const void*>(kernel);
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || ensure_smem_limit(k, 227 * 1024) != SSD_OK) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const Known& e : known)
+        if (e.kernel == k && e.device == device && e.ranks == ranks) return e.room;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = cluster_launch(dim3(ranks), threads, ranks, smem, nullptr, &attr);
+    int room = 0;
+    if (cudaOccupancyMaxActiveClusters(&room, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        room = 0;
+    }
+    known.push_back({k, device, ranks, room});
+    return room;
+}
+
+// Blocks of a cluster: the most, none without a step, with which all clusters run at once.  (They need room within one part of the device
+// each, so that fewer fit than blocks do: 1 x 4096 x 4864 of bfloat16 takes 57 us in 76 clusters of four, two of which wait for a second
+// turn, and 50 in clusters of three, its gradient 123 and 80.)
+template <typename K>
+int gated_ranks(K kernel, const GatedArgs& g, int warps, int (*smem)(int)) {
+    const int64_t blocks = (int64_t)ceil_div(g.channels, kGatedTile) * g.batch;
+    const int most = ceil_div(g.seqlen, warps * R);
+    for (int k = most < kGatedRanks ? most : kGatedRanks; k > 1; --k)
+        if (blocks <= 4 * kSms / k && blocks <= cluster_room(kernel, 32 * warps, k, smem(k))) return k;
+    return 1;
 }
 
 template <typename K, typename... Args>
 int launch_cluster(K kernel, dim3 grid, int threads, int ranks, int smem, cudaStream_t s, Args... args) {
     const int r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 227 * 1024);
     if (r != SSD_OK) return r;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ranks;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    const cudaLaunchConfig_t cfg = cluster_launch(grid, threads, ranks, smem, s, &attr);
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -597,9 +625,11 @@ int forward_rows(const GatedArgs& g, int ranks, void* y, float* final_state, flo
 // four, 5.7 with eight; 1024: 7.3 and 6.0; 2 x 4096 of 4096: 71 and 68; 65536 of 2048: 324 and 299).
 template <typename T, bool VEC>
 int forward_warps(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
-    const int four = gated_ranks(g, 4, 4 * R);
-    if ((int64_t)four * 4 * R >= g.seqlen) return forward_rows<T, 4, VEC>(g, four, y, final_state, states, s);
-    return forward_rows<T, 8, VEC>(g, gated_ranks(g, 2, 8 * R), y, final_state, states, s);
+    if (g.seqlen <= 4 * R * kGatedRanks) {
+        const int four = gated_ranks(gated_forward_kernel<T, 4, VEC>, g, 4, forward_smem<T, 4, VEC>);
+        if (four * 4 * R >= g.seqlen) return forward_rows<T, 4, VEC>(g, four, y, final_state, states, s);
+    }
+    return forward_rows<T, 8, VEC>(g, gated_ranks(gated_forward_kernel<T, 8, VEC>, g, 8, forward_smem<T, 8, VEC>), y, final_state, states, s);
 }
 template <typename T>
 int forward_of(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
@@ -621,10 +651,20 @@ int backward_rows(const GatedArgs& g, int ranks, const GatedGrads& d, const floa
     launch_dependent(gated_sums_kernel, dim3(ceil_div(g.channels, 32)), dim3(256), 0, s, (const float*)partial, ranks * g.batch, g.channels, g.A, d.dA);
     return launch_end(kKindGatedBwd, s);
 }
+// Four warps: with 16-bit tensors two blocks an SM, with up to 255 registers a thread, and two steps of input on their way; three
+// with 168 registers, which a 32-bit type's single step of input leaves room for, take 146 us where these take 139 (2 x 4096 x 4096 of
+// bfloat16), and 169 where two take 199 (float32).  Eight warps where their clusters, of one block an SM, take in more tokens a step
+// (4096 tokens of 96 channels of bfloat16: 35.6 us with four, 22.9 with eight; 2048 of 256 20.0 and 13.7; 2 x 4096 of 512, in clusters of
+// six, 37.9 and 32.9; without clusters 8 x 4096 of 4096 474 and 511), and rows take more than one.
 template <typename T, bool VEC>
 int backward_warps(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
-    const BackPlan p = back_plan<T>(g);
-    return p.warps == 8 ? backward_rows<T, 8, VEC>(g, p.ranks, d, states, partial, s) : backward_rows<T, 4, VEC>(g, p.ranks, d, states, partial, s);
+    constexpr int S = kBackStages<T>;
+    const int four = gated_ranks(gated_backward_kernel<T, 4, S, VEC>, g, 4, backward_smem<T, 4, S, VEC>);
+    if (g.seqlen > four * 4 * R) {
+        const int eight = gated_ranks(gated_backward_kernel<T, 8, S, VEC>, g, 8, backward_smem<T, 8, S, VEC>);
+        if (eight > 1 && 2 * eight > four) return backward_rows<T, 8, VEC>(g, eight, d, states, partial, s);
+    }
+    return backward_rows<T, 4, VEC>(g, four, d, states, partial, s);
 }
 template <typename T>
 int backward_of(const GatedArgs& g, const GatedGrads& d, const float* states, float* partial, cudaStream_t s) {
@@ -644,10 +684,7 @@ int step_of(const GatedArgs& g, float* state, const int* slots, int nslots, void
 }  // namespace
 
 size_t gated_states_floats(const GatedArgs& g) { return (size_t)g.batch * ceil_div(g.seqlen, kGatedSpan) * g.channels; }
-size_t gated_sums_floats(const GatedArgs& g) {
-    const int ranks = (g.dtype == SSD_BF16 ? back_plan<__nv_bfloat16>(g) : g.dtype == SSD_F16 ? back_plan<__half>(g) : back_plan<float>(g)).ranks;
-    return (size_t)g.batch * ranks * g.channels;
-}
+size_t gated_sums_floats(const GatedArgs& g) { return (size_t)g.batch * kGatedRanks * g.channels; }
 
 int launch_gated_forward(const GatedArgs& g, void* y, float* final_state, float* states, cudaStream_t s) {
     if (g.dtype == SSD_BF16) return forward_of<__nv_bfloat16>(g, y, final_state, states, s);
