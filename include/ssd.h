@@ -97,7 +97,8 @@ typedef enum {
     SSD_ERR_SLOT = 8         /* a slot index past its state pool (see ssd_get_device_error) */
 } ssd_status;
 
-/* Element types of the layer operators (ssd_conv_*, ssd_selective_*, ssd_layer_norm_*). */
+/* Element types of the layer operators (ssd_conv_*, ssd_selective_*, ssd_layer_norm_*, ssd_gated_*, ssd_group_norm_*,
+ * ssd_rotary). */
 typedef enum { SSD_BF16 = 0, SSD_F16 = 1, SSD_F32 = 2 } ssd_dtype;
 
 /* Size in bytes of the fixed device scratch array used by ssd_forward_noalloc. */
@@ -431,9 +432,10 @@ SSD_API int ssd_step_ex(const void* x, const float* dt, const float* A, const vo
 /*
  * ------------------------------------------------------------------------
  * The layer operators around a scan: a short causal convolution, the selective
- * scan with one decay per channel and state entry, and the layer norm.  The
- * pages describe none of them; they are what a layer runs next to the scan
- * (and, for the second, in its place).  Common to all:
+ * scan with one decay per channel and state entry, the layer norm; further down
+ * the gated linear recurrence, the grouped norm with its gate, and rotary
+ * positions.  The pages describe none of them; they are what a layer runs next
+ * to the scan (and, for the scan and the recurrence, in its place).  Common to all:
  *
  *  * `dtype` is the element type of the tensors declared as void* (x, y, their
  *    gradients, B, C, dt, z, the convolution's states); everything else is

@@ -14,8 +14,9 @@ CUDA kernels.  Inputs must be contiguous CUDA tensors:
 ``stream`` is a torch.cuda.Stream (default: the current stream).
 
 The operators that a layer runs around the scan (short convolution, selective
-scan with one decay per channel, layer norm) are in layer.py; they also take
-strided rows and other element types.
+scan with one decay per channel, layer norm, gated recurrence, grouped norm,
+rotary positions) are in layer.py; they also take strided rows and other
+element types.
 """
 from __future__ import annotations
 

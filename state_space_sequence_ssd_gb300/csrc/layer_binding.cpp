@@ -1,5 +1,5 @@
-// layer_binding.cpp -- the Python side of the layer operators (ssd_conv_*, ssd_selective_*, ssd_layer_norm_*): checks of
-// tensors, allocation of outputs, and the call of the C entry.  layer.py holds the public functions with their
+// layer_binding.cpp -- the Python side of the layer operators (ssd_conv_*, ssd_selective_*, ssd_layer_norm_*, ssd_gated_*,
+// ssd_group_norm_*, ssd_rotary_*): checks of tensors, allocation of outputs, and the call of the C entry.  layer.py holds the public functions with their
 // documentation; what is here was Python there, and took 22 us of a call that launches one small kernel (one token of
 // 256 sequences: 4.7 us on the device).  Nothing is computed here.
 #include <Python.h>

@@ -1,4 +1,4 @@
-// ops.cuh -- what the layer operators (k_conv.cu, k_selective*.cu, k_norm.cu) share: the element types
+// ops.cuh -- what the layer operators (k_conv.cu, k_selective*.cu, k_norm.cu, k_gated.cu, k_group_norm*.cu, k_rotary.cu) share: the element types
 // of their tensors, vector loads that fall back to single elements, and the launchers' declarations.
 #pragma once
 

@@ -1,6 +1,6 @@
 // ops_api.cu -- the C entries of the layer operators around the scan (short convolution, selective scan with one
-// decay per channel and state entry, layer norm): argument validation, workspace and launch order.  Every exported
-// function is declared and documented in include/ssd.h.
+// decay per channel and state entry, layer norm, gated recurrence, grouped norm, rotary positions): argument
+// validation, workspace and launch order.  Every exported function is declared and documented in include/ssd.h.
 #include <cmath>
 
 #include "ops.cuh"

@@ -1,6 +1,7 @@
 """The layer operators around a scan: the short causal convolution, the selective scan with one decay per channel
-and state entry, and the layer norm (binding of the ssd_conv_*, ssd_selective_* and ssd_layer_norm_* entries of
-include/ssd.h; the checks of the tensors and the allocation of the outputs are in csrc/layer_binding.cpp).
+and state entry, the layer norm, the gated linear recurrence, the norm over groups of channels with its gate, and rotary
+positions (binding of the ssd_conv_*, ssd_selective_*, ssd_layer_norm_*, ssd_gated_*, ssd_group_norm_* and ssd_rotary
+entries of include/ssd.h; the checks of the tensors and the allocation of the outputs are in csrc/layer_binding.cpp).
 
 x, dt, z, B, C and the convolution's states are bfloat16, float16 or float32, one type per call; weights, A, D, the
 scan's states and every summed gradient are float32.  Inputs may be column slices of a wider tensor: only the last
