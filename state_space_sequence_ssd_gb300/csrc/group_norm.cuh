@@ -582,13 +582,18 @@ int group_forward_of(const GroupNormArgs& g, void* y, float* mean, float* rstd, 
 }
 
 template <typename T, int V, int GATE>
-int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
+int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int* parts, cudaStream_t s) {
     constexpr int M = kWhole<V> ? 1 : 4;
     const int vecs = ceil_div(g.width / g.groups, V), lanes = row_lanes(g.rows * g.groups, vecs, 2 * M, 1), nv = ceil_div(vecs, lanes);
     const int room = kThreads / lanes;
     int side = 1;
     while (side < room && side < g.groups) side *= 2;
-    const int high = room / side, sums = high == 1 || partial == nullptr ? 0 : high * 2 * side * (g.width / g.groups) * 4;
+    // Blocks that walk the rows: two an SM over all slabs, none without a row.
+    const int high = nv <= 2 * M ? room / side : 1, slabs = nv <= 2 * M ? ceil_div(g.groups, side) : g.groups;
+    const int64_t most = ceil_div64(g.rows, high);
+    const int want = ceil_div(2 * kSms, slabs), walkers = most < want ? (int)most : want;
+    *parts = walkers < *parts ? walkers : *parts;
+    const int sums = high == 1 || partial == nullptr ? 0 : high * 2 * side * (g.width / g.groups) * 4;
     const bool vecw = aligned_to(g.weight, 16) && aligned_to(g.bias, 16);
     const T* dy = static_cast<const T*>(d.dy);
     T *dx = static_cast<T*>(d.dx), *dz = static_cast<T*>(d.dz);
@@ -598,13 +603,13 @@ int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* pa
         const int copies = kRowsAhead * kThreads * ((kWhole<V> ? held * (GATE >= kGateAfter ? 3 : 2) * 16 : 0) + 8), smem = copies > sums ? copies : sums;
         if (smem > 32 * 1024) r = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 100 * 1024);  // beside static memory
         if (r == SSD_OK)
-            kernel<<<dim3(ceil_div(g.groups, side), parts), kThreads, smem, s>>>(g, lanes, side, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial, vecw);
+            kernel<<<dim3(slabs, *parts), kThreads, smem, s>>>(g, lanes, side, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial, vecw);
     };
     const bool bias = g.bias != nullptr || d.want_dbias;
     if (nv <= 1 * M) bias ? go(group_backward_kernel<T, V, 1 * M, GATE, true>, 1) : go(group_backward_kernel<T, V, 1 * M, GATE, false>, 1);
     else if (nv <= 2 * M) bias ? go(group_backward_kernel<T, V, 2 * M, GATE, true>, 2) : go(group_backward_kernel<T, V, 2 * M, GATE, false>, 2);
     else
-        group_backward_wide_kernel<T><<<dim3(g.groups, parts), kThreads, 0, s>>>(g, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial);
+        group_backward_wide_kernel<T><<<dim3(slabs, *parts), kThreads, 0, s>>>(g, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial);
     const int e = launch_end(kKindGroupNormBwd, s);
     return r != SSD_OK ? r : e;
 }
@@ -617,7 +622,7 @@ int group_forward_gate(const GroupNormArgs& g, void* y, float* mean, float* rstd
     return group_forward_of<T, V, kGateNone>(g, y, mean, rstd, s);
 }
 template <typename T, int V>
-int group_backward_gate(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
+int group_backward_gate(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int* parts, cudaStream_t s) {
     if (g.gate == kGateSilu) return group_backward_of<T, V, kGateSilu>(g, d, partial, parts, s);
     if (g.gate == kGateAfter) return group_backward_of<T, V, kGateAfter>(g, d, partial, parts, s);
     if (g.gate == kGateBefore) return group_backward_of<T, V, kGateBefore>(g, d, partial, parts, s);
@@ -630,7 +635,7 @@ int group_forward_type(const GroupNormArgs& g, void* y, float* mean, float* rstd
     return group_forward_gate<T, 2>(g, y, mean, rstd, s);
 }
 template <typename T>
-int group_backward_type(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s) {
+int group_backward_type(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int* parts, cudaStream_t s) {
     if (in_vectors<T>(g) && d.dy_row % (16 / sizeof(T)) == 0 && aligned_to(d.dy, 16) && aligned_to(d.dx, 16) && aligned_to(d.dz, 16))
         return group_backward_gate<T, 16 / sizeof(T)>(g, d, partial, parts, s);
     return group_backward_gate<T, 2>(g, d, partial, parts, s);

@@ -373,10 +373,10 @@ struct GroupNormGrads {
 int group_norm_forward_bf16(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);
 int group_norm_forward_f16(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);
 int group_norm_forward_f32(const GroupNormArgs& g, void* y, float* mean, float* rstd, cudaStream_t s);
-// partial: parts x 2 x width float32, or nullptr where no column sums are wanted
-int group_norm_backward_bf16(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s);
-int group_norm_backward_f16(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s);
-int group_norm_backward_f32(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int parts, cudaStream_t s);
+// partial: *parts x 2 x width float32, or nullptr where no column sums are wanted; *parts becomes the number of them that are written
+int group_norm_backward_bf16(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int* parts, cudaStream_t s);
+int group_norm_backward_f16(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int* parts, cudaStream_t s);
+int group_norm_backward_f32(const GroupNormArgs& g, const GroupNormGrads& d, float* partial, int* parts, cudaStream_t s);
 
 struct RotaryArgs {
     int dtype, batch, seqlen, dim, turned;

@@ -355,14 +355,14 @@ int ssd_group_norm_backward(int dtype, const void* x, long long x_row_stride, co
         !aligned_to(dy, size) || !aligned_to(dx, size) || !aligned_to(dz, size) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
         return SSD_ERR_INVALID_ARG;
     const GroupNormGrads d = {mean, rstd, dy, dy_row_stride, dx, dz, dbias != nullptr};
-    const int parts = layer_norm_parts(rows, multiprocessors());
+    int parts = (int)(rows < 2 * kSms ? rows : 2 * kSms);
     void* ws = nullptr;
     if ((dweight != nullptr || dbias != nullptr) && take_workspace(&ws, (size_t)parts * 2 * width * sizeof(float), stream) != SSD_OK)
         return SSD_ERR_NO_MEMORY;
     float* partial = static_cast<float*>(ws);
-    if (dtype == SSD_BF16) e = group_norm_backward_bf16(a, d, partial, parts, stream);
-    else if (dtype == SSD_F16) e = group_norm_backward_f16(a, d, partial, parts, stream);
-    else e = group_norm_backward_f32(a, d, partial, parts, stream);
+    if (dtype == SSD_BF16) e = group_norm_backward_bf16(a, d, partial, &parts, stream);
+    else if (dtype == SSD_F16) e = group_norm_backward_f16(a, d, partial, &parts, stream);
+    else e = group_norm_backward_f32(a, d, partial, &parts, stream);
     if (e == SSD_OK && partial != nullptr) e = launch_norm_sums(kKindGroupNormBwd, partial, parts, width, dweight, dbias, stream);
     return give_back(ws, stream, e);
 }
