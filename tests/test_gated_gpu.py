@@ -269,3 +269,77 @@ def test_a_wait_that_runs_out_is_reported(ssd):
         assert ssd.ssd_get_device_error() == 0
         assert torch.equal(call(), want if name == "gated" else grads["dx"])
     assert ssd.ssd_get_device_error() == 0
+
+
+def test_the_same_bits_every_time(ssd):
+    """Clusters of every size, and none: what the blocks of one give each other does not depend on who is first."""
+    for b, L, ch, T in ((1, 9000, 128, torch.bfloat16), (2, 3000, 1088, torch.bfloat16), (2, 2100, 3200, torch.float32), (9, 700, 4096, torch.bfloat16)):
+        d = Draw(21)
+        x, r, i, dy = (d.normal(b, L, ch, dtype=T) for _ in range(4))
+        A = -d.normal(ch).abs() - 0.01
+        y, final, states = ssd.ssd_gated_forward(x, r, i, A, want_states=True)
+        g = ssd.ssd_gated_backward(x, r, i, A, dy, states=states, want_dinit=True)
+        for _ in range(15):
+            y2, final2, states2 = ssd.ssd_gated_forward(x, r, i, A, want_states=True)
+            g2 = ssd.ssd_gated_backward(x, r, i, A, dy, states=states, want_dinit=True)
+            assert torch.equal(y, y2) and torch.equal(final, final2) and torch.equal(states, states2)
+            assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+def test_strides_and_pools_past_32_bits(ssd):
+    """A batch stride, and a pool of states, of more than 2^31 elements."""
+    d, T = Draw(22), torch.bfloat16
+    big = torch.empty(2, (1 << 31) + 64, device="cuda", dtype=T)
+    x = big[:, :40 * 32].unflatten(1, (40, 32))
+    x.copy_(d.normal(2, 40, 32, dtype=T))
+    A = -d.normal(32).abs() - 0.1
+    y, _, _ = ssd.ssd_gated_forward(x, x, x, A)
+    c = x.contiguous()
+    assert torch.equal(y, ssd.ssd_gated_forward(c, c, c, A)[0])
+    del big, x
+    pool = torch.zeros((1 << 20) + 2, 2052, device="cuda")
+    at = torch.tensor([(1 << 20) + 1, 5], dtype=torch.int32, device="cuda")
+    v, A = d.normal(2, 2052), -d.normal(2052).abs() - 0.1
+    small = torch.zeros(2, 2052, device="cuda")
+    y, want = ssd.ssd_gated_step(v, v, v, A, pool, at), ssd.ssd_gated_step(v, v, v, A, small)
+    assert torch.equal(y, want) and torch.equal(pool[at.long()], small) and float(pool.sum(dtype=torch.float64)) == float(small.sum(dtype=torch.float64))
+
+
+def test_a_row_of_more_than_32_bits_of_elements(ssd):
+    """The end of a row of 2^31 elements and more is the end of the same row cut short in front, from the state there."""
+    d, L, ch, T = Draw(23), (1 << 19) + 200, 4104, torch.bfloat16
+    x = d.normal(1, 1 << 12, ch, dtype=T).repeat(1, 129, 1)[:, :L]
+    A = -d.normal(ch).abs() - 0.05
+    y, final, states = ssd.ssd_gated_forward(x, x, x, A, want_states=True)
+    start = L - L % 64 - 640
+    part = x[:, start:].contiguous()
+    want, wfinal, _ = ssd.ssd_gated_forward(part, part, part, A, states[:, start // 64].contiguous())
+    # the runs are composed in another order: roundings of float32, then at most one of bfloat16 apart
+    assert float((y[:, start:].float() - want.float()).abs().max()) <= 2.0 ** -7 * float(want.float().abs().max())
+    assert float((final - wfinal).abs().max()) <= 1e-5 * float(wfinal.abs().max())
+    g = ssd.ssd_gated_backward(x, x, x, A, y, states=states)
+    tail = ssd.ssd_gated_backward(part, part, part, A, y[:, start:].contiguous(), states[:, start // 64].contiguous())
+    for k in ("dx", "dr", "di"):
+        assert float((g[k][:, start:].float() - tail[k].float()).abs().max()) <= 2.0 ** -7 * float(tail[k].float().abs().max()), k
+
+
+def test_refusals(ssd):
+    x, A = torch.zeros(2, 5, 16, device="cuda"), -torch.ones(16, device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        ssd.ssd_gated_forward(x, x[..., :8], x, A)
+    with pytest.raises(TypeError):
+        ssd.ssd_gated_forward(x, x.half(), x, A)
+    with pytest.raises(ValueError, match="shape"):
+        ssd.ssd_gated_forward(x, x, x, A[:8])
+    with pytest.raises(ValueError, match="dims"):
+        ssd.ssd_gated_forward(x[0], x[0], x[0], A)
+    with pytest.raises(ValueError, match="dense"):
+        ssd.ssd_gated_forward(x, x, torch.zeros(2, 16, 5, device="cuda").transpose(1, 2), A)
+    with pytest.raises(TypeError):
+        ssd.ssd_gated_forward(x, x, x, A, lengths=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="states"):
+        ssd.ssd_gated_backward(x, x, x, A, x, states=torch.zeros(2, 2, 16, device="cuda"))
+    with pytest.raises(ValueError, match="holds 1 rows"):
+        ssd.ssd_gated_step(x[:, 0], x[:, 0], x[:, 0], A, torch.zeros(1, 16, device="cuda"))
+    with pytest.raises(ssd.SSDError):
+        ssd.ssd_gated_forward(x[:, :0], x[:, :0], x[:, :0], A)

@@ -176,3 +176,31 @@ def test_groups_of_several_warps_over_many_rows(ssd, rms):  # noqa: F811
     for _ in range(20):
         again = ssd.ssd_group_norm_forward(x, 1, rms=rms)
         assert torch.equal(again[0], first[0]) and torch.equal(again[2], first[2])
+
+
+def test_one_row_as_a_vector(ssd):  # noqa: F811
+    d = Draw(16)
+    x, z, w, dy = d.normal(96), d.normal(96), d.normal(96), d.normal(96)
+    y, mean, rstd = ssd.ssd_group_norm_forward(x, 3, w, z=z)
+    want = ssd.ssd_group_norm_forward(x[None], 3, w, z=z[None])
+    assert y.shape == (96,) and mean.shape == rstd.shape == (3,) and all(torch.equal(a, b[0]) for a, b in zip((y, mean, rstd), want))
+    g = ssd.ssd_group_norm_backward(x, 3, w, None, mean, rstd, dy, z=z)
+    assert g["dx"].shape == g["dz"].shape == (96,) and g["dweight"].shape == (96,) and g["dbias"] is None
+
+
+def test_refusals(ssd):  # noqa: F811
+    x = torch.zeros(4, 96, device="cuda")
+    with pytest.raises(ValueError, match="divide"):
+        ssd.ssd_group_norm_forward(x, 5)
+    with pytest.raises(ValueError, match="exclude"):
+        ssd.ssd_group_norm_forward(x, 3, z=x, silu=True)
+    with pytest.raises(ValueError, match="gate"):
+        ssd.ssd_group_norm_forward(x, 3, gate_first=True)
+    with pytest.raises(ValueError, match="shape"):
+        ssd.ssd_group_norm_forward(x, 3, z=x[:, :48])
+    with pytest.raises(TypeError):
+        ssd.ssd_group_norm_forward(x, 3, z=x.half())
+    with pytest.raises(ValueError, match="evenly"):
+        ssd.ssd_group_norm_forward(torch.zeros(3, 4, 96, device="cuda")[:, :2], 3)
+    with pytest.raises(ssd.SSDError):
+        ssd.ssd_group_norm_forward(x, 3, eps=-1.0)

@@ -166,3 +166,26 @@ def test_a_layer_whose_state_turns(ssd):  # noqa: F811
     dB, dC = ssd.ssd_rotary_backward(s["dB"], s["dC"], table)
     for got, turned in ((dB, s["dB"]), (dC, s["dC"])):
         close("turned back", got, R.rotary(turned.double(), f, inverse=True))
+
+
+def test_refusals(ssd):  # noqa: F811
+    x, table = torch.zeros(2, 5, 3, 16, device="cuda"), ssd.ssd_rotary_table(16)
+    int32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError, match="shape"):
+        ssd.ssd_rotary_forward(x, x[..., :8], table)
+    with pytest.raises(ValueError, match="dims"):
+        ssd.ssd_rotary_forward(x[0], None, table)
+    with pytest.raises(TypeError):
+        ssd.ssd_rotary_forward(x, x.half(), table)
+    with pytest.raises(TypeError):
+        ssd.ssd_rotary_forward(x, x, table, int32(2).long())
+    with pytest.raises(ValueError, match="positions"):
+        ssd.ssd_rotary_forward(x, x, table, int32(2, 4))
+    with pytest.raises(ValueError, match="table"):
+        ssd.ssd_rotary_forward(x, x, table.cpu())
+    with pytest.raises(ssd.SSDError):
+        ssd.ssd_rotary_forward(x, x, ssd.ssd_rotary_table(18))
+    with pytest.raises(ssd.SSDError):
+        ssd.ssd_rotary_forward(x, x, table, scale=float("inf"))
+    with pytest.raises(ValueError, match="dense"):
+        ssd.ssd_rotary_forward(x.transpose(1, 2), None, table)
