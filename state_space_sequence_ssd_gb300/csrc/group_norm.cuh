@@ -49,9 +49,34 @@ __device__ __forceinline__ void unit_of(int64_t u, int groups, int64_t& row, int
 // Rows and groups that are whole 16-byte vectors are read in those (V = 8 or 4); others in pairs, an element at a time.
 template <int V>
 constexpr bool kWhole = V > 2;
+// EVEN, for the others: groups are whole pairs, and outputs and weights aligned to pairs.
+template <typename T, int V, bool EVEN>
+__device__ __forceinline__ Vec<T, V> load_part(const T* p, int valid) {
+    if constexpr (!kWhole<V> && EVEN) {
+        Vec<T, V> r = Vec<T, V>::zero();
+        if (valid > 0) {
+            r.w[0] = bits_at(p);
+            if constexpr (sizeof(T) == 4) r.w[1] = bits_at(p + 1);
+            else r.w[0] |= bits_at(p + 1) << 16;
+        }
+        return r;
+    } else {
+        return load_vec<T, V>(p, valid, kWhole<V>);
+    }
+}
+template <int V, bool EVEN>
+__device__ __forceinline__ void load_weights(const float* p, int c, int per, bool vecw, float otherwise, f32x2 (&o)[(V + 1) / 2]) {
+    if constexpr (!kWhole<V> && EVEN) {
+        float2 q = make_float2(otherwise, otherwise);
+        if (p != nullptr && c < per) q = __ldg(reinterpret_cast<const float2*>(p + c));
+        o[0] = pk(q.x, q.y);
+    } else {
+        load_columns<V>(p, c, per, vecw, otherwise, o);
+    }
+}
 
 // Thread `lane` of a unit holds columns (lane + lanes i) V .. of its group.
-template <typename T, int V, int NV, int GATE>
+template <typename T, int V, int NV, int GATE, bool EVEN>
 __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g, int lanes, T* __restrict__ y, float* __restrict__ mean,
                                                                  float* __restrict__ rstd, bool vecw) {
     constexpr int P = (V + 1) / 2;
@@ -69,8 +94,8 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + lanes * i) * V;
-        rx[i] = load_vec<T, V>(x + c, live ? per - c : 0, kWhole<V>);
-        if (GATE >= kGateAfter) rz[i] = load_vec<T, V>(z + c, live ? per - c : 0, kWhole<V>);
+        rx[i] = load_part<T, V, EVEN>(x + c, live ? per - c : 0);
+        if (GATE >= kGateAfter) rz[i] = load_part<T, V, EVEN>(z + c, live ? per - c : 0);
     }
     f32x2 q[NV][P], s2 = 0ull, v2 = 0ull;
 #pragma unroll
@@ -93,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
 #pragma unroll
             for (int e = 0; e < P; ++e) {
                 q[i][e] = add2(q[i][e], m2);
-                if (!kWhole<V> && (lane + lanes * i) * V + 1 >= per) q[i][e] = pk(unpk_low(q[i][e]), 0.f);  // half a pair
+                if (!kWhole<V> && !EVEN && (lane + lanes * i) * V + 1 >= per) q[i][e] = pk(unpk_low(q[i][e]), 0.f);  // half a pair
                 v2 = fma2(q[i][e], q[i][e], v2);
             }
         }
@@ -109,8 +134,8 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
         const int c = (lane + lanes * i) * V;
         if (c >= per) break;
         f32x2 w[P], b[P], out[P];
-        load_columns<V>(g.weight == nullptr ? nullptr : g.weight + base, c, per, vecw, 1.f, w);
-        load_columns<V>(g.bias == nullptr ? nullptr : g.bias + base, c, per, vecw, 0.f, b);
+        load_weights<V, EVEN>(g.weight == nullptr ? nullptr : g.weight + base, c, per, vecw, 1.f, w);
+        load_weights<V, EVEN>(g.bias == nullptr ? nullptr : g.bias + base, c, per, vecw, 0.f, b);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
             out[e] = fma2(mul2(q[i][e], pk(rs, rs)), w[e], b[e]);
@@ -120,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) group_forward_kernel(GroupNormArgs g
                 out[e] = mul2(out[e], mul2(zz, sigmoid_pair(zz)));
             }
         }
-        store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), per - c, kWhole<V>);
+        store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), per - c, kWhole<V> || EVEN);
     }
 }
 
@@ -574,9 +599,15 @@ int group_forward_of(const GroupNormArgs& g, void* y, float* mean, float* rstd, 
     }
     launch_begin(kKindGroupNorm, s);
     auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, kThreads, 0, s>>>(g, lanes, static_cast<T*>(y), mean, rstd, vecw); };
-    if (nv <= 1 * M) go(group_forward_kernel<T, V, 1 * M, GATE>);
-    else if (nv <= 2 * M) go(group_forward_kernel<T, V, 2 * M, GATE>);
-    else if (nv <= 4 * M) go(group_forward_kernel<T, V, 4 * M, GATE>);
+    auto held = [&](auto even) {
+        constexpr bool EVEN = decltype(even)::value;
+        if (nv <= 1 * M) go(group_forward_kernel<T, V, 1 * M, GATE, EVEN>);
+        else if (nv <= 2 * M) go(group_forward_kernel<T, V, 2 * M, GATE, EVEN>);
+        else go(group_forward_kernel<T, V, 4 * M, GATE, EVEN>);
+    };
+    const bool even = !kWhole<V> && g.width / g.groups % 2 == 0 && aligned_to(g.weight, 8) && aligned_to(g.bias, 8) && aligned_to(y, 2 * sizeof(T));
+    if (nv <= 4 * M && even) held(std::integral_constant<bool, !kWhole<V>>());
+    else if (nv <= 4 * M) held(std::false_type());
     else group_forward_wide_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(g, static_cast<T*>(y), mean, rstd);
     return launch_end(kKindGroupNorm, s);
 }
