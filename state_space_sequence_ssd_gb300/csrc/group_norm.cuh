@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) group_forward_wide_kernel(GroupNormA
 // the sums of the blocks 61 us (5.5 TB/s; floor 49.5); values held between the two passes over a row instead of computed twice
 // 74, three rows ahead 68, three blocks an SM 68.
 constexpr int kRowsAhead = 2;
-template <typename T, int V, int NV, int GATE, bool BIAS>
+template <typename T, int V, int NV, int GATE, bool BIAS, bool EVEN>
 __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormArgs g, int lanes, int side, const float* __restrict__ mean,
                                                                      const float* __restrict__ rstd, const T* __restrict__ dy, int64_t dy_row,
                                                                      T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ partial, bool vecw) {
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + lanes * i) * V;
-        load_columns<V>(g.weight == nullptr ? nullptr : g.weight + (here ? base : 0), c, per, vecw, 1.f, w[i]);
-        if (PRE && BIAS) load_columns<V>(g.bias == nullptr ? nullptr : g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
+        load_weights<V, EVEN>(g.weight == nullptr ? nullptr : g.weight + (here ? base : 0), c, per, vecw, 1.f, w[i]);
+        if (PRE && BIAS) load_weights<V, EVEN>(g.bias == nullptr ? nullptr : g.bias + (here ? base : 0), c, per, vecw, 0.f, b[i]);
 #pragma unroll
         for (int e = 0; e < P; ++e) dw[i][e] = db[BIAS ? i : 0][e] = 0ull;
     }
@@ -360,6 +360,9 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
         }
         copies_commit();
     };
+    struct Part {
+        Vec<T, V> x, dy, z;
+    };
     const int64_t step = (int64_t)gridDim.y * high;
     int64_t row = (int64_t)blockIdx.y * high + sub / side;
 #pragma unroll
@@ -370,11 +373,8 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
         const bool current = here && row < g.rows;
         const float rs = current ? stats[turn * 2 * kThreads] : 0.f, mn = current && mean != nullptr ? stats[(turn * 2 + 1) * kThreads] : 0.f;
         const f32x2 rs2 = pk(rs, rs), shift = pk(-mn * rs, -mn * rs);
-        // Both passes over the row read it from shared memory (or L1) and compute the same from it: what the sums stand between would
-        // not fit the registers.
-        struct Part {
-            Vec<T, V> x, dy, z;
-        };
+        // Both passes over the row take it from shared memory (pairs: from L1) and compute the same from it: what the sums stand
+        // between would not fit the registers.
         auto part = [&](int i) {
             Part p;
             if constexpr (kWhole<V>) {
@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
             } else {
                 const int64_t at = current ? row : 0, off = current ? base : 0;
                 const int c = (lane + lanes * i) * V, left = current ? per - c : 0;
-                p.x = load_vec<T, V>(x + at * g.x_row + off + c, left, false);
-                p.dy = load_vec<T, V>(dy + at * dy_row + off + c, left, false);
-                if (Z) p.z = load_vec<T, V>(z + at * g.z_row + off + c, left, false);
+                p.x = load_part<T, V, EVEN>(x + at * g.x_row + off + c, left);
+                p.dy = load_part<T, V, EVEN>(dy + at * dy_row + off + c, left);
+                if (Z) p.z = load_part<T, V, EVEN>(z + at * g.z_row + off + c, left);
             }
             return p;
         };
@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
                     }
                     if constexpr (GATE == kGateAfter) o2[e] = mul2(mul2(p.dy.pair(e), v.n), slope_of(p.z.pair(e), v.sig));
                 }
-                store_vec<T, V>(ox + c, Vec<T, V>::of_pairs(o1), per - c, kWhole<V>);
-                if constexpr (Z) store_vec<T, V>(oz + c, Vec<T, V>::of_pairs(o2), per - c, kWhole<V>);
+                store_vec<T, V>(ox + c, Vec<T, V>::of_pairs(o1), per - c, kWhole<V> || EVEN);
+                if constexpr (Z) store_vec<T, V>(oz + c, Vec<T, V>::of_pairs(o2), per - c, kWhole<V> || EVEN);
             }
         }
         fetch(row + kRowsAhead * step, turn);
@@ -637,8 +637,15 @@ int group_backward_of(const GroupNormArgs& g, const GroupNormGrads& d, float* pa
             kernel<<<dim3(slabs, *parts), kThreads, smem, s>>>(g, lanes, side, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial, vecw);
     };
     const bool bias = g.bias != nullptr || d.want_dbias;
-    if (nv <= 1 * M) bias ? go(group_backward_kernel<T, V, 1 * M, GATE, true>, 1) : go(group_backward_kernel<T, V, 1 * M, GATE, false>, 1);
-    else if (nv <= 2 * M) bias ? go(group_backward_kernel<T, V, 2 * M, GATE, true>, 2) : go(group_backward_kernel<T, V, 2 * M, GATE, false>, 2);
+    auto held = [&](auto even) {
+        constexpr bool EVEN = decltype(even)::value;
+        if (nv <= 1 * M) bias ? go(group_backward_kernel<T, V, 1 * M, GATE, true, EVEN>, 1) : go(group_backward_kernel<T, V, 1 * M, GATE, false, EVEN>, 1);
+        else bias ? go(group_backward_kernel<T, V, 2 * M, GATE, true, EVEN>, 2) : go(group_backward_kernel<T, V, 2 * M, GATE, false, EVEN>, 2);
+    };
+    const bool even = !kWhole<V> && g.width / g.groups % 2 == 0 && aligned_to(g.weight, 8) && aligned_to(g.bias, 8) && aligned_to(dx, 2 * sizeof(T)) &&
+                      aligned_to(dz, 2 * sizeof(T));
+    if (nv <= 2 * M && even) held(std::integral_constant<bool, !kWhole<V>>());
+    else if (nv <= 2 * M) held(std::false_type());
     else
         group_backward_wide_kernel<T><<<dim3(slabs, *parts), kThreads, 0, s>>>(g, d.mean, d.rstd, dy, d.dy_row, dx, dz, partial);
     const int e = launch_end(kKindGroupNormBwd, s);
