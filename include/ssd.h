@@ -623,6 +623,7 @@ SSD_API int ssd_gated_forward(int dtype, const void* x, const void* r, const voi
  * NULL: they are computed again from the inputs into a workspace.  Outputs, dense and fully written:
  *   dx, dr, di   (batch, seqlen, channels): dr and di are those of the gates in front of their sigmoid
  *   dA           (channels) f32; dinit (batch, channels) f32 or NULL
+ * Its workspace is 32 bytes a row and channel, and without states 4 more for every SSD_GATED_SPAN-th token.
  */
 SSD_API int ssd_gated_backward(int dtype, const void* x, const void* r, const void* i, const float* A,
                                const float* init_state, const int* lengths, const ssd_gated_strides* strides, int batch,
@@ -661,7 +662,8 @@ SSD_API int ssd_group_norm_forward(int dtype, const void* x, long long x_row_str
 
 /*
  * ssd_group_norm_backward -- dx and, with z, dz (both dense), and dweight and dbias ((width) f32, or NULL) summed over the
- * rows, from dy, the inputs and the forward pass's mean (NULL: rms) and rstd.
+ * rows, from dy, the inputs and the forward pass's mean (NULL: rms) and rstd.  Its workspace is at most 2432 bytes a
+ * channel (8 for each of up to 304 rows), none without dweight and dbias.
  */
 SSD_API int ssd_group_norm_backward(int dtype, const void* x, long long x_row_stride, const void* z, long long z_row_stride,
                                     const float* weight, const float* bias, int gate, const float* mean, const float* rstd,

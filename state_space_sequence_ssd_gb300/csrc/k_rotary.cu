@@ -117,17 +117,29 @@ int rotary_of(const RotaryArgs& g, bool vec, cudaStream_t s) {
     return launch_end(kKindRotary, s);
 }
 
+template <typename T, int V>
+int rotary_vectors(const RotaryArgs& g, cudaStream_t s) {
+    return g.interleaved ? rotary_of<T, V, false>(g, true, s) : rotary_of<T, V, true>(g, true, s);
+}
+
+// The widest vectors of which rows, heads and (half layout) halves are whole and aligned; else an element at a time, two pairs a thread
+// (B and C of 8 x 2560 tokens of float16: 8 x 48 in vectors of eight 14 us, 8 x 44 interleaved of four 19, half layout of two 23; 8 x 46
+// of odd rows an element at a time, half layout: one pair a thread 41, two 32, four 46; interleaved one pair 37, two 31, and one as
+// a vector where rows allow it 35).
 template <typename T>
 int rotary_type(const RotaryArgs& g, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-    bool vec = g.dim % V == 0;
-    for (int k = 0; k < 2; ++k)
-        if (g.heads[k] > 0)
-            vec = vec && g.batch_stride[k] % V == 0 && g.token_stride[k] % V == 0 && aligned_to(g.in[k], 16) && aligned_to(g.out[k], 16);
-    // Rows that are no whole vectors: two pairs a thread, an element at a time (8 x 2560 tokens of 2 x 8 x 46 of float16, half layout:
-    // one pair a thread 41 us, two 32, four 46; interleaved one 37, two 31).
-    if (g.interleaved) return vec ? rotary_of<T, V, false>(g, true, s) : rotary_of<T, 4, false>(g, false, s);
-    return vec && g.turned / 2 % V == 0 ? rotary_of<T, V, true>(g, true, s) : rotary_of<T, 2, true>(g, false, s);
+    constexpr int FULL = 16 / sizeof(T);
+    auto fits = [&](int V) {
+        bool whole = g.dim % V == 0 && (g.interleaved || g.turned / 2 % V == 0);
+        for (int k = 0; k < 2; ++k)
+            if (g.heads[k] > 0)
+                whole = whole && g.batch_stride[k] % V == 0 && g.token_stride[k] % V == 0 && aligned_to(g.in[k], V * sizeof(T)) && aligned_to(g.out[k], V * sizeof(T));
+        return whole;
+    };
+    if (fits(FULL)) return rotary_vectors<T, FULL>(g, s);
+    if (FULL > 4 && fits(4)) return rotary_vectors<T, 4>(g, s);
+    if (!g.interleaved && fits(2)) return rotary_of<T, 2, true>(g, true, s);
+    return g.interleaved ? rotary_of<T, 4, false>(g, false, s) : rotary_of<T, 2, true>(g, false, s);
 }
 
 }  // namespace

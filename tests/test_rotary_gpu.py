@@ -17,7 +17,12 @@ CASES = [("bf16", 2, 33, (1, 1), 128, 128, False, None, None, 0, 1.0),
          ("bf16", 1, 5000, (8, 8), 256, 256, False, "start", None, 128, 1.0),   # four heads a thread
          ("f16", 2, 3000, (5, 6), 80, 36, True, None, [3000, 17], 0, 1.1),       # a vector across the turned entries' end
          ("f32", 1, 2000, (32, 8), 128, 128, True, "each", None, 0, 1.0),
-         ("bf16", 1, 7, (300, 1), 24, 8, False, None, None, 0, 1.0)]
+         ("bf16", 1, 7, (300, 1), 24, 8, False, None, None, 0, 1.0),
+         ("f16", 2, 90, (3, 2), 44, 40, False, "start", None, 4, 1.0),           # vectors of four, of two, none
+         ("bf16", 2, 90, (3, 2), 46, 44, True, "start", [90, 3], 2, 1.0),
+         ("f32", 2, 90, (3, 2), 46, 44, False, "each", None, 2, 1.0),
+         ("f16", 2, 900, (9, 2), 46, 46, False, None, None, 2, 1.0),
+         ("bf16", 2, 900, (9, 2), 44, 44, True, None, None, 4, 1.0)]
 
 
 def make(c, seed=4):
