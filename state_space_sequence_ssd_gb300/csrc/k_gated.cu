@@ -419,8 +419,8 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
             }
         }
         f32x2 m = pk(behind);
-        auto gradients = [&](auto one) {
-            constexpr bool ONE = decltype(one)::value;
+        auto gradients = [&](auto one, auto packed) {
+            constexpr bool ONE = decltype(one)::value, PACKED = decltype(packed)::value;
             int64_t at = ((int64_t)b * g.seqlen + t0 + R - 1) * g.channels;  // the same for all lanes
 #pragma unroll
             for (int k = R - 1; k >= 0; --k, at -= g.channels) {
@@ -435,23 +435,25 @@ gated_backward_kernel(GatedArgs g, const float* states, const T* __restrict__ dy
                 const f32x2 q = mul2(mul2(lam, mul2(mul2(A, v), a[k])), fma2(mul2(mul2(a[k], rs), gi_x), pk(-1.f, -1.f), hs[k]));
                 m = mul2(a[k], lam);
                 const f32x2 gr = mul2(q, gate_rest<ONE>(er, v)), gi2 = mul2(mul2(gx, xk), gate_rest<ONE>(ei, gi));
-                if (ONE) {
+                if (ONE && PACKED) {
                     dA = add2(dA, q);
                     if (in0) {
                         store_vec<T, 2>(dx + at + (uint32_t)c, Vec<T, 2>::of_pairs({gx}), 2, true);
                         store_vec<T, 2>(dr + at + (uint32_t)c, Vec<T, 2>::of_pairs({gr}), 2, true);
                         store_vec<T, 2>(di + at + (uint32_t)c, Vec<T, 2>::of_pairs({gi2}), 2, true);
                     }
-                } else if (t0 + k < n) {
+                } else if (ONE || t0 + k < n) {
                     dA = add2(dA, q);
-                    store_vec<T, 2>(dx + at + (uint32_t)c, Vec<T, 2>::of_pairs({gx}), g.channels - c, vecy);
-                    store_vec<T, 2>(dr + at + (uint32_t)c, Vec<T, 2>::of_pairs({gr}), g.channels - c, vecy);
-                    store_vec<T, 2>(di + at + (uint32_t)c, Vec<T, 2>::of_pairs({gi2}), g.channels - c, vecy);
+                    const bool whole_pairs = !ONE && vecy;  // ONE without PACKED: they are not
+                    store_vec<T, 2>(dx + at + (uint32_t)c, Vec<T, 2>::of_pairs({gx}), g.channels - c, whole_pairs);
+                    store_vec<T, 2>(dr + at + (uint32_t)c, Vec<T, 2>::of_pairs({gr}), g.channels - c, whole_pairs);
+                    store_vec<T, 2>(di + at + (uint32_t)c, Vec<T, 2>::of_pairs({gi2}), g.channels - c, whole_pairs);
                 }
             }
         };
-        if (share && vecy) gradients(std::true_type());
-        else gradients(std::false_type());
+        if (share && vecy) gradients(std::true_type(), std::true_type());
+        else if (!VEC && share) gradients(std::true_type(), std::false_type());
+        else gradients(std::false_type(), std::false_type());
         __syncwarp();
         fetch(step % STAGES);
     }
