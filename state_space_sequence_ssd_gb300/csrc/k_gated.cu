@@ -17,7 +17,6 @@
 // 69), and the exchange between blocks takes a tenth (2 x 4096 x 9728, without clusters, 124: 5.2 TB/s).
 // Runs of 8 tokens take 85 us at the first size (more exchange for the work), copies two steps ahead as long as one.
 #include <mutex>
-#include <vector>
 
 #include "gated.cuh"
 
@@ -566,13 +565,14 @@ int cluster_room(K kernel, int threads, int ranks, int smem) {
         int device, ranks, room;
     };
     static std::mutex mu;
-    static std::vector<Known> known;
+    static Known known[256];  // of one signature: its types, warps and kinds of rows, by sizes and devices; asked for again where it is full
+    static int count = 0;
     const void* k = reinterpret_cast<const void*>(kernel);
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess || ensure_smem_limit(k, 227 * 1024) != SSD_OK) return 0;
     std::lock_guard<std::mutex> lock(mu);
-    for (const Known& e : known)
-        if (e.kernel == k && e.device == device && e.ranks == ranks) return e.room;
+    for (int i = 0; i < count; ++i)
+        if (known[i].kernel == k && known[i].device == device && known[i].ranks == ranks) return known[i].room;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_launch(dim3(ranks), threads, ranks, smem, nullptr, &attr);
     int room = 0;
@@ -580,7 +580,7 @@ int cluster_room(K kernel, int threads, int ranks, int smem) {
         cudaGetLastError();
         room = 0;
     }
-    known.push_back({k, device, ranks, room});
+    if (count < 256) known[count++] = {k, device, ranks, room};
     return room;
 }
 
