@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
         copies_wait<kRowsAhead - 1>();
         const bool current = here && row < g.rows;
         const float rs = current ? stats[turn * 2 * kThreads] : 0.f, mn = current && mean != nullptr ? stats[(turn * 2 + 1) * kThreads] : 0.f;
-        const f32x2 rs2 = pk(rs, rs), shift = pk(-mn * rs, -mn * rs);
+        const f32x2 rs2 = pk(rs, rs);
         // Both passes over the row take it from shared memory (pairs: from L1) and compute the same from it: what the sums stand
         // between would not fit the registers.
         auto part = [&](int i) {
@@ -402,14 +402,14 @@ __global__ void __launch_bounds__(kThreads, 2) group_backward_kernel(GroupNormAr
         };
         auto value = [&](const Part& p, int i, int e) {
             Value v;
-            f32x2 q = p.x.pair(e);
             if constexpr (Z) {
                 const f32x2 zz = p.z.pair(e);
                 v.sig = sigmoid_pair(zz);
                 v.silu = mul2(zz, v.sig);
-                if constexpr (GATE == kGateBefore) q = mul2(q, v.silu);
             }
-            v.xhat = fma2(q, rs2, shift);
+            // The difference first: q rstd - (mean rstd) would shift the whole group by that product's rounding.
+            if constexpr (GATE == kGateBefore) v.xhat = mul2(add2(mul2(p.x.pair(e), v.silu), pk(-mn, -mn)), rs2);
+            else v.xhat = mul2(pair_plus(p.x, e, -mn), rs2);
             v.g = p.dy.pair(e);  // zero past the group's end
             if constexpr (PRE) v.n = BIAS ? fma2(v.xhat, w[i][e], b[BIAS ? i : 0][e]) : mul2(v.xhat, w[i][e]);
             if constexpr (GATE == kGateSilu) v.g = mul2(v.g, slope_of(v.n, sigmoid_pair(v.n)));

@@ -39,6 +39,20 @@ __device__ __forceinline__ float2 row_sums(float2 v, int lanes, float2* buf) {
 }
 __device__ __forceinline__ float row_sum(float v, int lanes, float2* buf) { return row_sums(make_float2(v, 0.f), lanes, buf).x; }
 
+// Elements 2 i and 2 i + 1 of a vector plus c.  16-bit elements are widened by the addition itself, an instruction each instead of one
+// each and a packed addition (8192 x 4096 of float16 in 2 groups, silu of the output, gradient: 72 us; widened first 76).
+template <typename T, int V>
+__device__ __forceinline__ f32x2 pair_plus(const Vec<T, V>& v, int i, float c) {
+    static_assert(V % 2 == 0, "whole pairs");
+    if constexpr (sizeof(T) == 4) return add2(v.pair(i), pk(c, c));
+    float lo, hi;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.f16 %0, l, %3;\nadd.rn.f32.f16 %1, h, %3;\n}" : "=f"(lo), "=f"(hi) : "r"(v.w[i]), "f"(c));
+    else if constexpr (sizeof(T) == 2)
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.bf16 %0, l, %3;\nadd.rn.f32.bf16 %1, h, %3;\n}" : "=f"(lo), "=f"(hi) : "r"(v.w[i]), "f"(c));
+    return pk(lo, hi);
+}
+
 // V columns of a float32 row from column c on, as pairs (a null row: `otherwise`).  `vec`: 16-byte aligned groups of four.
 template <int V>
 __device__ __forceinline__ void load_columns(const float* p, int c, int width, bool vec, float otherwise,
