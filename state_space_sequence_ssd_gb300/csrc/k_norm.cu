@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __rest
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += step, row += step, turn ^= 1) {
         Vec<T, V> cx[NV], cg[NV];
-        const float rs = nrs;
-        const f32x2 rs2 = pk(rs, rs), shift = pk(-nm * rs, -nm * rs);  // xhat = x rstd - mean rstd
+        const float rs = nrs, minus = -nm;  // xhat = (x - mean) rstd: x rstd - (mean rstd) would shift the whole row by that product's rounding
+        const f32x2 rs2 = pk(rs, rs);
         f32x2 s1 = 0ull, s2 = 0ull;
 #pragma unroll
         for (int i = 0; i < NV; ++i) { cx[i] = nx[i]; cg[i] = ng[i]; }
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __rest
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                const f32x2 gy = cg[i].pair(e), xh = fma2(cx[i].pair(e), rs2, shift);  // gy is zero past the row's end
+                const f32x2 gy = cg[i].pair(e), xh = mul2(pair_plus(cx[i], e, minus), rs2);  // gy is zero past the row's end
                 const f32x2 g = mul2(gy, w[i][e]);
                 db[i][e] = add2(db[i][e], gy);
                 dw[i][e] = fma2(gy, xh, dw[i][e]);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const T* __rest
             f32x2 out[P];
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                const f32x2 xh = fma2(cx[i].pair(e), rs2, shift), g = mul2(cg[i].pair(e), w[i][e]);
+                const f32x2 xh = mul2(pair_plus(cx[i], e, minus), rs2), g = mul2(cg[i].pair(e), w[i][e]);
                 out[e] = fma2(g, rs2, fma2(xh, pk(k2, k2), pk(k1, k1)));
             }
             store_vec<T, V>(o + c, Vec<T, V>::of_pairs(out), width - c, true);

@@ -43,14 +43,16 @@ __device__ __forceinline__ float row_sum(float v, int lanes, float2* buf) { retu
 // each and a packed addition (8192 x 4096 of float16 in 2 groups, silu of the output, gradient: 72 us; widened first 76).
 template <typename T, int V>
 __device__ __forceinline__ f32x2 pair_plus(const Vec<T, V>& v, int i, float c) {
-    static_assert(V % 2 == 0, "whole pairs");
-    if constexpr (sizeof(T) == 4) return add2(v.pair(i), pk(c, c));
-    float lo, hi;
-    if constexpr (std::is_same<T, __half>::value)
-        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.f16 %0, l, %3;\nadd.rn.f32.f16 %1, h, %3;\n}" : "=f"(lo), "=f"(hi) : "r"(v.w[i]), "f"(c));
-    else if constexpr (sizeof(T) == 2)
-        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.bf16 %0, l, %3;\nadd.rn.f32.bf16 %1, h, %3;\n}" : "=f"(lo), "=f"(hi) : "r"(v.w[i]), "f"(c));
-    return pk(lo, hi);
+    if constexpr (sizeof(T) == 4 || V == 1) {
+        return add2(v.pair(i), pk(c, c));
+    } else {
+        float lo, hi;
+        if constexpr (std::is_same<T, __half>::value)
+            asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.f16 %0, l, %3;\nadd.rn.f32.f16 %1, h, %3;\n}" : "=f"(lo), "=f"(hi) : "r"(v.w[i]), "f"(c));
+        else
+            asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.bf16 %0, l, %3;\nadd.rn.f32.bf16 %1, h, %3;\n}" : "=f"(lo), "=f"(hi) : "r"(v.w[i]), "f"(c));
+        return pk(lo, hi);
+    }
 }
 
 // V columns of a float32 row from column c on, as pairs (a null row: `otherwise`).  `vec`: 16-byte aligned groups of four.

@@ -1,4 +1,4 @@
-"""The grouped norm's gradient of rows whose mean is many deviations from zero.
+"""The grouped norm's and the layer norm's gradient of rows whose mean is many deviations from zero.
 
 The gradient gets the mean and takes (q - mean) rstd.  That difference is rounded to a float32 of its own size and the product once more,
 so xhat is off by at most 2 U of itself (U = 2^-24) however far the mean lies; a form that rounds mean * rstd first is off by up to half
@@ -86,3 +86,24 @@ def test_16_bits(ssd, T, per):  # noqa: F811
         close("dweight", got["dweight"], want["dweight"])
         if row == 0:
             assert not bool(got["dweight"].any())
+
+
+@pytest.mark.parametrize("mean", [0.0, 10.0, 1000.0, 10000.0])
+@pytest.mark.parametrize("rows, per, front", [(2, 64, 0), (70, 512, 4), (2, 30, 1), (3, 33, 1), (2, 20000, 0)])  # the last wider than the registers
+def test_layer_norm(ssd, rows, per, front, mean):  # noqa: F811
+    d, x, m, r = rows_and_stats(rows, 1, per, front, mean)
+    w, dy = d.normal(per), d.normal(*x.shape)
+    want, _, _ = gradients(x, w, dy, m, r)
+    got = ssd.ssd_layer_norm_backward(x, w, m[:, 0].contiguous(), r[:, 0].contiguous(), dy)
+    for name, value in want.items():
+        close(name, got[name], value)
+
+
+@pytest.mark.parametrize("T", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("per", [64, 33])
+def test_layer_norm_of_one_value(ssd, per, T):  # noqa: F811
+    """Rows of one value only have an xhat of zero, whatever 1 / sqrt(eps) is."""
+    x, dy = torch.full((3, per), 1000.5, device="cuda").to(T), Draw(per).normal(3, per, dtype=T)
+    m, r = x[:, 0].float(), torch.full((3,), 316.227766, device="cuda")
+    got = ssd.ssd_layer_norm_backward(x, torch.ones(per, device="cuda"), m, r, dy)
+    assert not bool(got["dweight"].any())
