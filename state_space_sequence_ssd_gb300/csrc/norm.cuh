@@ -39,6 +39,13 @@ __device__ __forceinline__ float2 row_sums(float2 v, int lanes, float2* buf) {
 }
 __device__ __forceinline__ float row_sum(float v, int lanes, float2* buf) { return row_sums(make_float2(v, 0.f), lanes, buf).x; }
 
+// The mean of n values from their sum, inv = 1 / n rounded: a plain product is off by up to a unit and a half, which would shift the whole
+// group, times rstd; with inv's own error put back the result is the rounded quotient.  An infinite sum stays one.
+__device__ __forceinline__ float mean_of(float sum, int n, float inv) {
+    const float low = fmaf(-inv, (float)n, 1.f) * inv;
+    return fmaf(sum, inv, fminf(fmaxf(sum, -3.4028235e38f), 3.4028235e38f) * low);
+}
+
 // Elements 2 i and 2 i + 1 of a vector plus c.  16-bit elements are widened by the addition itself, an instruction each instead of one
 // each and a packed addition (8192 x 4096 of float16 in 2 groups, silu of the output, gradient: 72 us; widened first 76).
 template <typename T, int V>
