@@ -682,7 +682,8 @@ SSD_API int ssd_group_norm_backward(int dtype, const void* x, long long x_row_st
  *   positions    NULL: token t is at position t; (batch) int32: at positions[b] + t; with positions_each (batch,
  *                seqlen) int32: at positions[b,t].  Negative positions turn the other way
  *   y0, y1       dense, of the same type; tokens past a row's length are zero
- * float32 tensors take accurate sines; those of 16 bits the special function unit's (absolute error below 2^-19).
+ * The angle is taken to 2^-32 of a turn.  float32 tensors take accurate sines of it (relative error below 2^-22); those of 16
+ * bits the special function unit's (absolute error below 2^-19).
  */
 SSD_API int ssd_rotary(int dtype, const void* x0, long long x0_batch_stride, long long x0_token_stride, int heads0,
                        const void* x1, long long x1_batch_stride, long long x1_token_stride, int heads1,
