@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, !kWhole<V> && NV == 8 ? 4 : 0) group
 // The same for many rows of whole vectors: a resident grid whose blocks walk the rows.  A thread keeps its columns, and with them their
 // weights; a block holds `side` groups of a row next to one another and kThreads / lanes / side rows at once.  A thread's
 // pieces of the next rows are copied to shared memory that it alone reads.  8192 x 4096 of bfloat16 in 8 groups, gated in front:
-// 33.7 us (6.0 TB/s; 41.0 with the kernel above, whose threads spend half their instructions on addresses and weights); copies three rows
-// ahead 36.2, four blocks an SM 36.4.
+// 35.0 us (5.8 TB/s; floor 29.7).  On one set of inputs, part of it in L2, 33.7; 41.0 with the kernel above, whose threads spend half their
+// instructions on addresses and weights; copies three rows ahead 36.2, four blocks an SM 36.4.
 constexpr int kForwardAhead = 2;
 constexpr int kWalkers = 3;  // blocks of an SM
 template <typename T, int V, int NV, int GATE>
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) group_forward_wide_kernel(GroupNormA
 // A block holds `side` groups of a row next to one another and kThreads / lanes / side rows at once, and walks the rows a grid's
 // height apart; its columns' sums stay in registers.  Whole vectors of the next rows are copied to shared memory that their thread
 // alone reads, so that they need neither registers nor barriers on their way.  8192 x 4096 of bfloat16 in 8 groups, gated in front, with
-// the sums of the blocks 61 us (5.5 TB/s; floor 49.5); values held between the two passes over a row instead of computed twice
+// the sums of the blocks 59 us (5.7 TB/s; floor 49.5); values held between the two passes over a row instead of computed twice
 // 74, three rows ahead 68, three blocks an SM 68.
 constexpr int kRowsAhead = 2;
 template <typename T, int V, int NV, int GATE, bool BIAS, bool EVEN>

@@ -10,11 +10,12 @@
 // distributed shared memory, so that one pass over the data serves sequences of any length, with as many blocks as fill the SMs.
 // The next step's inputs come through cp.async while this step's pairs are exchanged and its outputs written.
 //
-// 2 x 4096 x 4096 of bfloat16 takes 68 us (4.0 TB/s; the bytes' floor is 40), of float32 86 (6.3 TB/s; 80), 65536 x 2048 of
-// bfloat16 295 (159).  With 16-bit elements the instructions bind: about 70 a warp and token of its 64 channels, for the gates' four calls of the
-// special function unit an element, the polynomial, conversions and the exchange, at 52% of the issue slots with 13 warps an SM, which
-// the registers allow.  Beside that, 256 blocks on 152 SMs leave some with one where others have two (2 x 4096 x 4864, 304 blocks, takes
-// 69), and the exchange between blocks takes a tenth (2 x 4096 x 9728, without clusters, 124: 5.2 TB/s).
+// 2 x 4096 x 4096 of bfloat16 takes 68 us (4.0 TB/s; the bytes' floor is 40), of float32 85 (6.3 TB/s; 80), 65536 x 2048 of
+// bfloat16 294 (158).  With 16-bit elements latency binds: 13 warps an SM, which the registers allow, use 52% of the issue slots, and no
+// pipe is full (the multiplier 38%, the special function unit, which gives four results an element, 29%; about 70 instructions a warp and
+// token of its 64 channels would issue in 31 us).  Beside that, 256 blocks on 152 SMs leave some with one where others have two
+// (2 x 4096 x 4864, 304 blocks, takes 69), and the exchange between blocks, during which nothing else is issued, takes a tenth
+// (2 x 4096 x 9728, without clusters, 123: 5.2 TB/s).
 // Runs of 8 tokens take 85 us at the first size (more exchange for the work), copies two steps ahead as long as one.
 #include <mutex>
 

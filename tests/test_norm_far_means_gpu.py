@@ -107,3 +107,20 @@ def test_layer_norm_of_one_value(ssd, per, T):  # noqa: F811
     m, r = x[:, 0].float(), torch.full((3,), 316.227766, device="cuda")
     got = ssd.ssd_layer_norm_backward(x, torch.ones(per, device="cuda"), m, r, dy)
     assert not bool(got["dweight"].any())
+
+
+@pytest.mark.parametrize("per", [64, 30, 33])
+@pytest.mark.parametrize("T", [torch.bfloat16, torch.float16, torch.float32])
+def test_infinities_and_nans(ssd, T, per):  # noqa: F811
+    """With a mean of 0 and an rstd of 1 dweight is dy x: an infinity keeps its sign, a NaN stays one, and the other group is as without."""
+    d, groups = Draw(per), 2
+    x, dy, one = d.normal(1, groups * per, dtype=T), d.normal(1, groups * per, dtype=T), torch.ones(groups * per, device="cuda")
+    m, r = torch.zeros(1, groups, device="cuda"), torch.ones(1, groups, device="cuda")
+    clean = ssd.ssd_group_norm_backward(x, groups, one, None, m, r, dy)
+    x[0, 4], x[0, 7], x[0, 9] = float("inf"), -float("inf"), float("nan")
+    got = ssd.ssd_group_norm_backward(x, groups, one, None, m, r, dy)
+    want = dy[0].double() * x[0].double()
+    assert got["dweight"][4] == want[4] and got["dweight"][7] == want[7] and bool(got["dweight"][9].isnan())
+    finite = torch.isfinite(want)
+    assert torch.equal(got["dweight"][finite], clean["dweight"][finite])
+    assert torch.equal(got["dx"][:, per:], clean["dx"][:, per:]) and not bool(torch.isfinite(got["dx"][:, :per]).any())
